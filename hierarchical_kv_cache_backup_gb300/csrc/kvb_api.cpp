@@ -14,6 +14,7 @@
 #include "kvb.h"
 #include "kvb_internal.h"
 #include "kvb_ring_internal.h"
+#include "kvb_vec_internal.h"
 
 #include <cuda.h>   // CUresult / CUdeviceptr types only; the function comes from the runtime
 #include <cuda_runtime.h>
@@ -345,6 +346,8 @@ kv_status init_device(int d) {
     // kernel (gate, resident server) would wait for that kernel to end
     cudaError_t e0 = preload_kernels();
     if (e0 == cudaSuccess) e0 = preload_ring_kernels();
+    if (e0 == cudaSuccess) e0 = preload_vector_kernels();
+    if (e0 == cudaSuccess) e0 = preload_attend_kernels();
     if (e0 != cudaSuccess) return cuda_fail(e0, "loading the library's kernels");
     // mapped pinned table: kRing fence words, kRing status words, the error word
     const size_t table = 2 * kRing * sizeof(unsigned long long) + 64;
@@ -1606,6 +1609,52 @@ int enqueue_staged_backup_noalloc(const void *pool_handle, const void *host_hand
     if (e != cudaSuccess) return cuda_fail(e, "launch of the move kernel");
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return staged_copies(*host, (char *)staging, slots, n, g.pb, 0, true, stream);
+}
+
+// --------------------------------------------------- head-vector operators
+
+int vec_cuda_error(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+
+void vec_count(int launches) { g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed); }
+
+int vec_enter_device(int device, void *stream, bool *pdl) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    const kv_status st = init_device(device);
+    if (st != KV_OK) return st;
+    forget_stream(g_dev[device], stream);
+    *pdl = (g_cfg.flags & KV_CFG_NO_PDL) == 0;
+    return KV_OK;
+}
+
+int vec_enter_pool(const void *pool_handle, uint32_t layer, void *stream, bool launch, VecPool *out) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (pool_handle == nullptr) return fail(KV_ERR_INVALID_ARG, "pool handle is NULL");
+    PoolObj *pool = find_pool((kv_pool)pool_handle);
+    if (pool == nullptr) return fail(KV_ERR_CLOSED, "pool handle is closed or unknown");
+    auto fl = g_floor.find(pool->instance_id);
+    if (fl != g_floor.end() && pool->generation < fl->second)
+        return fail(KV_ERR_STALE, "pool generation %llu of instance %llu is retired",
+                    (unsigned long long)pool->generation, (unsigned long long)pool->instance_id);
+    const Geo &g = pool->g;
+    if (layer >= g.L)
+        return fail(KV_ERR_OUT_OF_RANGE, "layer %u is outside [0, %llu)", layer, (unsigned long long)g.L);
+    const int d = pool->device;
+    DeviceGuard guard(d);
+    const kv_status st = init_device(d);
+    if (st != KV_OK) return st;
+    if (launch) forget_stream(g_dev[d], stream);
+    const Side s = pool_side(*pool);
+    out->layout = pool->layout;
+    out->s_page = s.s_id;
+    for (uint64_t c = 0; c < 2; ++c) {
+        const uint64_t k = std::min(c, g.C - 1);   // C = 1 is refused by the caller
+        out->base[c] = pool->table_dev != nullptr ? pool->table_host[layer * g.C + k]
+                                                  : s.base + layer * s.s_l + k * s.s_c;
+    }
+    out->device = d;
+    out->sms = g_dev[d].sms;
+    out->pdl = (g_cfg.flags & KV_CFG_NO_PDL) == 0;
+    return KV_OK;
 }
 
 int fence_gate_word(kv_fence f, const unsigned long long **word, unsigned long long *tag) {

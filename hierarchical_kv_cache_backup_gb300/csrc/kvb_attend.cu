@@ -1,0 +1,703 @@
+// kvb_attend.cu -- attention of new tokens over one layer of a 4-bit pool.
+//
+// Mathematics.  A cached value is (code - z) s with one step s and zero point z
+// for each 32 values of a vector (a group).  With codes re-centred to code - 8
+// (small integers, exact in fp16),
+//   q . k_t   = sum_groups s_t (q_g . (code_t - 8)_g - (z_t - 8) sum q_g)
+//   out[dim]  = sum_t p_t s_t (code_t[dim] - 8) - sum_t p_t s_t (z_t - 8)
+// so the matrix instructions multiply exact codes, steps scale float32 sums on
+// the key side and the probabilities on the value side, and zero points are one
+// float32 correction a group.  p_t = 2^(x_t - m) with a running maximum m.
+#include "kvb_vec.h"
+#include "kvb_vec_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+namespace kvb {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 32;        // cached tokens a warp takes at a time
+constexpr int kStages = 2;       // tiles in shared memory per warp
+constexpr float kNoMax = -3.0e38f;
+
+__host__ __device__ constexpr int vec_bytes(int D) { return (D / 2 + D / 8 + 15) / 16 * 16; }
+// Bytes between vectors in shared memory: an odd multiple of 16, so that the 8
+// rows of a fragment start 4 banks apart and no load has a bank conflict.
+__host__ __device__ constexpr int vec_stride(int D) {
+    return vec_bytes(D) / 16 % 2 ? vec_bytes(D) : vec_bytes(D) + 16;
+}
+__host__ __device__ constexpr int ring_bytes(int D) { return kStages * 2 * kTile * vec_stride(D); }
+__host__ __device__ constexpr int merge_floats(int D, int NT) { return 8 * NT * (D + 4); }
+__host__ __device__ constexpr int warp_bytes(int D, int NT) {
+    return ring_bytes(D) > 4 * merge_floats(D, NT) ? ring_bytes(D) : 4 * merge_floats(D, NT);
+}
+
+__device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Four pairs of codes (nibbles i of both 16-bit halves) as fp16 pairs code - 8.
+// 0x6400 | n is 1024 + n in fp16, and 0x6400 | n << 4 is 1024 + 16 n.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t *p) {
+    const __half2 k1032 = __half2half2(__ushort_as_half(0x6408));   // 1032
+    const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
+    const __half2 k72 = __half2half2(__ushort_as_half(0xd480));     // -72
+    const uint32_t v = w >> 8;
+    uint32_t t[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
+                     (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __half2 h = *reinterpret_cast<__half2 *>(&t[i]);
+        h = i & 1 ? __hfma2(h, k16, k72) : __hsub2(h, k1032);
+        p[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+// z - 8 of a scale word (0x4b000000 | z is 2^23 + z).
+__device__ __forceinline__ float zero8(uint32_t word) {
+    return __uint_as_float((word & 15u) | 0x4b000000u) - 8388616.0f;
+}
+
+__device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+
+template <int kRows>
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool *bad) {
+    return row_span(a.q_start[r], a.q_start[r + 1], a.lens[r], (int)a.tokens, (int)a.max_q,
+                    (int)a.max_len, (int)a.group, (int)a.window, rt, kRows, bad);
+}
+
+// --------------------------------------------------------- few rows a request
+//
+// A block takes one KV head of one request, a tile of 8 NT query rows (new
+// tokens x the head's group) and a chunk of the cached tokens; its 8 warps
+// take tiles of 32 tokens in turn, each with a private ring in shared memory
+// (no barrier in the loop), and join their maxima, sums and accumulators at the
+// end.  Cached tokens are the 16-row side of m16n8k16 and query rows its
+// 8-column side, so a GQA group of up to 8 heads fills the instruction.
+// Scores come out with a token a row; movmatrix turns the probabilities of an
+// 8 x 8 block for the second product.
+//
+// Bound: issue slots.  About 380 instructions a warp per 16 tokens of 128
+// values (2,560 B): unpacking is 10 instructions for 8 values.
+template <int D, int NT, bool kHalf, bool kMany>
+__global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
+    kv_attend_rows_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int NG = D / 32;                 // groups of a vector
+    constexpr int SV = vec_stride(D), PV = vec_bytes(D) / 16;
+    constexpr int kRows = 8 * NT;
+    constexpr int WB = warp_bytes(D, NT);
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float join_m[kWarps][kRows], join_l[kWarps][kRows];
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int H = (int)a.pool.H;
+    int bx = blockIdx.x;
+    const int head = bx % H;
+    bx /= H;
+    const int rt = bx % (int)a.row_tiles;
+    const int ci = bx / (int)a.row_tiles;
+    const int r = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    bool bad;
+    const Span s = span_of<kRows>(a, r, rt, &bad);
+    if (bad && a.status != nullptr && threadIdx.x == 0 && blockIdx.x == 0)
+        atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+    const int row0 = rt * kRows, rows = min(kRows, s.n * (int)a.group - row0);
+    if (rows <= 0) return;
+    const int c0 = s.lo + ci * (int)a.chunk, c1 = min(s.hi, c0 + (int)a.chunk);
+    if (c0 >= c1 && ci > 0) return;
+    const bool whole = s.hi - s.lo <= (int)a.chunk;   // this block sees all the rows see
+
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * WB;
+    const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
+    const int64_t head_off = (int64_t)head * a.pool.s_head;
+
+    uint32_t bad_page[kStages];
+    auto load = [&](int stage, int t0) {
+        const int t = t0 + lane;
+        bool ok = t < c1;
+        int64_t off = 0;
+        bool wrong = false;
+        if (ok) {
+            off = token_offset(a.pool, table, (uint32_t)t, &wrong) + head_off;
+            ok = !wrong;
+        }
+        bad_page[stage] = __ballot_sync(0xffffffffu, wrong);
+        const uint32_t at = ring + stage * (2 * kTile * SV);
+        if (!ok) off = -1;
+#pragma unroll
+        for (int k = 0; k < PV; ++k) {
+            const int idx = lane + 32 * k, tok = idx / PV, piece = idx - tok * PV;
+            const int64_t o = __shfl_sync(0xffffffffu, off, tok);
+            const bool on = o >= 0;
+            const uint64_t from = (on ? (uint64_t)o : 0) + piece * 16;
+            const uint32_t to = at + tok * SV + piece * 16;
+            copy16(to, a.pool.base[0] + from, on);
+            copy16(to + kTile * SV, a.pool.base[1] + from, on);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int t0 = c0 + warp * kTile;
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) {
+        bad_page[st] = 0;
+        if (t0 + st * kWarps * kTile < c1) load(st, t0 + st * kWarps * kTile);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    // Query rows as B fragments.  Each row is scaled by a power of two that
+    // brings its largest value near 2^8, so that bf16 queries are exact in fp16
+    // (but for values 2^-30 of the row's largest); the scores undo it.
+    uint32_t qf[NT][NG][4];
+    float qsum[NT][NG][2], qs[NT][2];
+    int lim[NT][2], low[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + g;
+        const bool on = row < rows;
+        const int i = on ? (row0 + row) / (int)a.group : 0;
+        const int j = on ? (row0 + row) - i * (int)a.group : 0;
+        const uint64_t src = a.q.data + (int64_t)(s.q0 + i) * a.q.s_tok +
+                             (int64_t)(head * (int)a.group + j) * a.q.s_head;
+        float x[NG][8], top = 0.0f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (on) u = *reinterpret_cast<const uint4 *>(src + (gr * 32 + c * 8) * 2);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (kHalf) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                    x[gr][2 * e] = f.x;
+                    x[gr][2 * e + 1] = f.y;
+                } else {
+                    x[gr][2 * e] = __uint_as_float(w[e] << 16);
+                    x[gr][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                }
+                top = fmaxf(top, fmaxf(fabsf(x[gr][2 * e]), fabsf(x[gr][2 * e + 1])));
+            }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(8 - exponent of top), and its inverse; 1 for zeros and infinities
+        const uint32_t ex = __float_as_uint(top) >> 23;
+        const bool scaled = ex >= 10 && ex < 255;
+        const float up = scaled ? __uint_as_float((262u - ex) << 23) : 1.0f;
+        const float back = scaled ? __uint_as_float((ex - 8u) << 23) : 1.0f;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            float y[8], sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = __half2float(__float2half_rn(x[gr][e] * up));
+                sum += y[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qf[nt][gr][e] = half2_bits(y[e], y[e + 4]);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            qsum[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+            qsum[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            qs[nt][e] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) * a.scale_log2;
+            const int col = 8 * nt + 2 * c + e;
+            const int pos = s.len - s.n + (row0 + col) / (int)a.group;
+            lim[nt][e] = min(pos, s.len - 1);
+            low[nt][e] = a.window ? pos - (int)a.window + 1 : 0;
+        }
+    }
+    // a tile wholly inside [safe_lo, safe_hi) is seen by every row of the block
+    const int safe_hi = min(c1, s.len - s.n + row0 / (int)a.group + 1);
+    const int safe_lo = a.window ? s.len - s.n + (row0 + rows - 1) / (int)a.group - (int)a.window + 1 : 0;
+
+    float o[NG][2][NT][4], corr[NT][NG][2], f[NG], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        f[gr] = __uint_as_float(227u << 23);   // 2^100: set by the first step that is not 0
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            corr[nt][gr][0] = corr[nt][gr][1] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[gr][0][nt][e] = o[gr][1][nt][e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = kNoMax;
+        l[nt][0] = l[nt][1] = 0.0f;
+    }
+
+    for (int stage = 0; t0 < c1; t0 += kWarps * kTile, stage ^= 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        const unsigned char *ks = smem + warp * WB + stage * (2 * kTile * SV);
+        const unsigned char *vs = ks + kTile * SV;
+
+        // scores: x[sub][nt][e] for token 16 sub + g (+ 8 for e >= 2), row 8 nt + 2 c + (e & 1)
+        float x[2][NT][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[sub][nt][e] = 0.0f;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const unsigned char *k0 = ks + (16 * sub + g) * SV, *k1 = k0 + 8 * SV;
+            uint4 w0, w1;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                if (gr % 4 == 0) {
+                    w0 = *reinterpret_cast<const uint4 *>(k0 + D / 2 + gr * 4);
+                    w1 = *reinterpret_cast<const uint4 *>(k1 + D / 2 + gr * 4);
+                }
+                const uint32_t s0 = gr % 4 == 0 ? w0.x : gr % 4 == 1 ? w0.y : gr % 4 == 2 ? w0.z : w0.w;
+                const uint32_t s1 = gr % 4 == 0 ? w1.x : gr % 4 == 1 ? w1.y : gr % 4 == 2 ? w1.z : w1.w;
+                uint32_t p0[4], p1[4];
+                codes4(*reinterpret_cast<const uint32_t *>(k0 + gr * 16 + c * 4), p0);
+                codes4(*reinterpret_cast<const uint32_t *>(k1 + gr * 16 + c * 4), p1);
+                const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]};
+                const uint32_t a1[4] = {p0[2], p1[2], p0[3], p1[3]};
+                const float d0 = q4_step(s0), d1 = q4_step(s1), z0 = zero8(s0), z1 = zero8(s1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma(acc, a0, qf[nt][gr][0], qf[nt][gr][1]);
+                    mma(acc, a1, qf[nt][gr][2], qf[nt][gr][3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[sub][nt][e] += (e < 2 ? d0 : d1) *
+                                         (acc[e] - (e < 2 ? z0 : z1) * qsum[nt][gr][e & 1]);
+                }
+            }
+        }
+        // x in units of log2, masked
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[sub][nt][e] *= qs[nt][e & 1];
+        if (t0 < safe_lo || t0 + kTile > safe_hi || bad_page[stage] != 0) {
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int in = 16 * sub + g + (e >= 2 ? 8 : 0), t = t0 + in;
+                        if (bad_page[stage] >> in & 1) x[sub][nt][e] = __uint_as_float(kNanWord);
+                        if (t >= c1 || t > lim[nt][e & 1] || t < low[nt][e & 1])
+                            x[sub][nt][e] = -INFINITY;
+                    }
+            if (bad_page[stage] != 0 && a.status != nullptr && lane == 0)
+                atomicOr(a.status, KV_STATUS_BAD_PAGE);
+        }
+        // The maximum moves only when a score passes it by more than 2^8: until
+        // then probabilities reach up to 2^8, which costs no precision.
+        float over = kNoMax;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) over = fmaxf(over, x[sub][nt][e] - m[nt][e & 1]);
+        if (__any_sync(0xffffffffu, over > 8.0f)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float t = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]),
+                                    fmaxf(x[1][nt][e], x[1][nt][e + 2]));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    t = fmaxf(t, m[nt][e]);
+                    const float k = exp2f(m[nt][e] - t);
+                    m[nt][e] = t;
+                    l[nt][e] *= k;
+#pragma unroll
+                    for (int gr = 0; gr < NG; ++gr) {
+                        corr[nt][gr][e] *= k;
+                        o[gr][0][nt][e] *= k;
+                        o[gr][0][nt][e + 2] *= k;
+                        o[gr][1][nt][e] *= k;
+                        o[gr][1][nt][e + 2] *= k;
+                    }
+                }
+        }
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[sub][nt][e] = exp2f(x[sub][nt][e] - m[nt][e & 1]);
+                    l[nt][e & 1] += x[sub][nt][e];
+                }
+
+        // Steps of the values, in units of 1/f: f is a power of two a group that
+        // keeps p x step inside fp16 (p <= 2^8, step x f <= 2^6).
+        uint4 vw[2][2][(NG + 3) / 4];
+        float most[NG];
+        bool raise = false;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int q = 0; q < (NG + 3) / 4; ++q) {
+                vw[sub][0][q] = *reinterpret_cast<const uint4 *>(vs + (16 * sub + g) * SV + D / 2 + q * 16);
+                vw[sub][1][q] = *reinterpret_cast<const uint4 *>(vs + (16 * sub + g + 8) * SV + D / 2 + q * 16);
+            }
+        auto word = [&](int sub, int k, int gr) {
+            const uint4 &u = vw[sub][k][gr / 4];
+            return gr % 4 == 0 ? u.x : gr % 4 == 1 ? u.y : gr % 4 == 2 ? u.z : u.w;
+        };
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            most[gr] = fmaxf(fmaxf(__uint_as_float(word(0, 0, gr)), __uint_as_float(word(0, 1, gr))),
+                             fmaxf(__uint_as_float(word(1, 0, gr)), __uint_as_float(word(1, 1, gr))));
+            raise |= most[gr] * f[gr] > 64.0f;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                float t = most[gr];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                const uint32_t ex = min(__float_as_uint(t) >> 23, 252u);
+                if (t * f[gr] > 64.0f) {
+                    const float to = __uint_as_float((254u - ex) << 23), k = to / f[gr];
+                    f[gr] = to;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        corr[nt][gr][0] *= k;
+                        corr[nt][gr][1] *= k;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[gr][0][nt][e] *= k;
+                            o[gr][1][nt][e] *= k;
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const unsigned char *v0 = vs + (16 * sub + 2 * c) * SV + 2 * g;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                const uint32_t s0 = word(sub, 0, gr), s1 = word(sub, 1, gr);
+                const float d0 = q4_step(s0) * f[gr], d1 = q4_step(s1) * f[gr];
+                const float z0 = zero8(s0), z1 = zero8(s1);
+                uint32_t b[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = x[sub][nt][e] * (e < 2 ? d0 : d1);
+                        // a token that a row does not see may hold NaN for another
+                        if (kMany && x[sub][nt][e] == 0.0f) p[e] = 0.0f;
+                    }
+                    corr[nt][gr][0] += p[0] * z0 + p[2] * z1;
+                    corr[nt][gr][1] += p[1] * z0 + p[3] * z1;
+                    b[nt][0] = transpose8x8(half2_bits(p[0], p[1]));
+                    b[nt][1] = transpose8x8(half2_bits(p[2], p[3]));
+                }
+                const unsigned char *v = v0 + gr * 16;
+                const uint32_t t0w = *reinterpret_cast<const unsigned short *>(v);
+                const uint32_t t1w = *reinterpret_cast<const unsigned short *>(v + SV);
+                const uint32_t t2w = *reinterpret_cast<const unsigned short *>(v + 8 * SV);
+                const uint32_t t3w = *reinterpret_cast<const unsigned short *>(v + 9 * SV);
+                uint32_t p0[4], p1[4];
+                codes4(__byte_perm(t0w, t1w, 0x5410), p0);
+                codes4(__byte_perm(t2w, t3w, 0x5410), p1);
+                const uint32_t a0[4] = {p0[0], p0[1], p1[0], p1[1]};
+                const uint32_t a1[4] = {p0[2], p0[3], p1[2], p1[3]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(o[gr][0][nt], a0, b[nt][0], b[nt][1]);
+                    mma(o[gr][1][nt], a1, b[nt][0], b[nt][1]);
+                }
+            }
+        }
+        __syncwarp();
+        const int next = t0 + kStages * kWarps * kTile;
+        if (next < c1) load(stage, next);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+
+    // Join the warps.  A warp's accumulators go to its own ring as [row][D + 4].
+    float *mine = reinterpret_cast<float *>(smem + warp * WB);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float t = l[nt][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+            const int row = 8 * nt + 2 * c + e;
+            if (g == 0) {
+                join_m[warp][row] = m[nt][e];
+                join_l[warp][row] = t;
+            }
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                float k = corr[nt][gr][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
+                const float back = 1.0f / f[gr];
+                *reinterpret_cast<float4 *>(mine + row * (D + 4) + gr * 32 + 4 * g) =
+                    make_float4((o[gr][0][nt][e] - k) * back, (o[gr][0][nt][e + 2] - k) * back,
+                                (o[gr][1][nt][e] - k) * back, (o[gr][1][nt][e + 2] - k) * back);
+            }
+        }
+    __syncthreads();
+    const int D4 = D / 4;
+    for (int it = threadIdx.x; it < rows * D4; it += kWarps * 32) {
+        const int row = it / D4, d4 = it - row * D4;
+        float top = kNoMax, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            top = fmaxf(top, join_l[w][row] != 0.0f ? join_m[w][row] : kNoMax);
+        float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float lw = join_l[w][row];
+            if (lw == 0.0f) continue;          // this warp saw nothing of the row
+            const float k = exp2f(join_m[w][row] - top);
+            const float4 v = *reinterpret_cast<const float4 *>(
+                reinterpret_cast<const float *>(smem + w * WB) + row * (D + 4) + d4 * 4);
+            sum += lw * k;
+            acc.x += v.x * k;
+            acc.y += v.y * k;
+            acc.z += v.z * k;
+            acc.w += v.w * k;
+        }
+        const int i = (row0 + row) / (int)a.group, j = (row0 + row) - i * (int)a.group;
+        const int64_t tok = s.q0 + i;
+        const int qh = head * (int)a.group + j;
+        if (whole) {
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head + d4 * 8;
+            uint2 u;
+            if (kHalf) {
+                u = make_uint2(half2_bits(acc.x * inv, acc.y * inv), half2_bits(acc.z * inv, acc.w * inv));
+            } else {
+                __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                u = make_uint2(*reinterpret_cast<uint32_t *>(&h0), *reinterpret_cast<uint32_t *>(&h1));
+            }
+            *reinterpret_cast<uint2 *>(dst) = u;
+            if (d4 == 0 && a.lse != nullptr)
+                a.lse[tok * a.q_heads + qh] =
+                    sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
+        } else {
+            const int64_t at = ((int64_t)ci * a.tokens + tok) * a.q_heads + qh;
+            *reinterpret_cast<float4 *>(a.part_o + at * D + d4 * 4) = acc;
+            if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + at * 2) = make_float2(top, sum);
+        }
+    }
+}
+
+// Joins the chunks of a row: one block a query head and token, 4 warps over the
+// chunks, a lane 4 values (twice for D > 128).
+template <int D, int kRows, bool kHalf>
+__global__ void __launch_bounds__(128) kv_attend_join_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int kW = 4, NV = (D + 127) / 128;
+    __shared__ __align__(16) float acc_s[kW][D];
+    __shared__ float m_s[kW], l_s[kW];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int qh = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = blockIdx.y, r = blockIdx.z;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool bad;
+    const int j = qh % (int)a.group;
+    const Span s = span_of<kRows>(a, r, (i * (int)a.group + j) / kRows, &bad);
+    const int n = (s.hi - s.lo + (int)a.chunk - 1) / (int)a.chunk;
+    if (i >= s.n || n <= 1) return;
+    const int64_t tok = s.q0 + i;
+    float top = kNoMax, sum = 0.0f;
+    float4 acc[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int k = warp; k < n; k += kW) {
+        const int64_t at = ((int64_t)k * a.tokens + tok) * a.q_heads + qh;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+        float4 x[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (v * 128 + lane * 4 < D)
+                x[v] = *reinterpret_cast<const float4 *>(a.part_o + at * D + v * 128 + lane * 4);
+        if (ml.y == 0.0f) continue;
+        const float t = fmaxf(top, ml.x), u = exp2f(top - t), w = exp2f(ml.x - t);
+        top = t;
+        sum = sum * u + ml.y * w;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            acc[v].x = acc[v].x * u + x[v].x * w;
+            acc[v].y = acc[v].y * u + x[v].y * w;
+            acc[v].z = acc[v].z * u + x[v].z * w;
+            acc[v].w = acc[v].w * u + x[v].w * w;
+        }
+    }
+    if (lane == 0) {
+        m_s[warp] = top;
+        l_s[warp] = sum;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (v * 128 + lane * 4 < D)
+            *reinterpret_cast<float4 *>(&acc_s[warp][v * 128 + lane * 4]) = acc[v];
+    __syncthreads();
+    float most = kNoMax, all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) most = fmaxf(most, l_s[w] != 0.0f ? m_s[w] : kNoMax);
+    float k[kW];
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        k[w] = l_s[w] != 0.0f ? exp2f(m_s[w] - most) : 0.0f;
+        all += l_s[w] * k[w];
+    }
+    const float inv = all != 0.0f ? 1.0f / all : 0.0f;
+    const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head;
+    for (int d = threadIdx.x; d < D; d += 128) {
+        float y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) y += acc_s[w][d] * k[w];
+        y *= inv;
+        if (kHalf) *reinterpret_cast<__half *>(dst + 2 * d) = __float2half_rn(y);
+        else *reinterpret_cast<__nv_bfloat16 *>(dst + 2 * d) = __float2bfloat16_rn(y);
+    }
+    if (threadIdx.x == 0 && a.lse != nullptr)
+        a.lse[tok * a.q_heads + qh] =
+            all != 0.0f ? (most + log2f(all)) * 0.693147180559945f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ launches
+
+template <typename Fn>
+cudaError_t launch(Fn *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl,
+                   const AttendArgs &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+typedef void(AttendFn)(AttendArgs);
+struct Variant {
+    uint32_t D, rows;
+    bool fp16, many;
+    AttendFn *rows_fn, *join_fn;
+    int smem;
+};
+
+template <int D, int NT, bool kHalf, bool kMany>
+constexpr Variant variant() {
+    return Variant{(uint32_t)D, 8u * NT, kHalf, kMany, kv_attend_rows_kernel<D, NT, kHalf, kMany>,
+                   kv_attend_join_kernel<D, 8 * NT, kHalf>, kWarps * warp_bytes(D, NT)};
+}
+
+#define KVB_VARIANTS(D, NT)                                                                       \
+    variant<D, NT, false, false>(), variant<D, NT, true, false>(), variant<D, NT, false, true>(), \
+        variant<D, NT, true, true>()
+const Variant kVariants[] = {KVB_VARIANTS(64, 1),  KVB_VARIANTS(64, 2),  KVB_VARIANTS(96, 1),
+                             KVB_VARIANTS(96, 2),  KVB_VARIANTS(128, 1), KVB_VARIANTS(128, 2),
+                             KVB_VARIANTS(192, 1), KVB_VARIANTS(256, 1)};
+
+}  // namespace
+
+AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
+                       uint32_t window, uint32_t q_heads, uint32_t kv_heads, uint32_t D, int sms) {
+    AttendPlan p{};
+    const uint64_t rows = (uint64_t)max_q * (q_heads / kv_heads);
+    p.rows = rows > 8 && D <= 128 ? 16 : 8;
+    p.row_tiles = (uint32_t)((rows + p.rows - 1) / p.rows);
+    // the most cached tokens a row tile sees: its queries' windows overlap
+    uint64_t span = max_len;
+    if (window) span = std::min<uint64_t>(span, (uint64_t)window + p.rows);
+    // about four blocks an SM, in chunks of at least a tile for each warp
+    const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
+    const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
+    uint64_t chunk = (span + want - 1) / want;
+    chunk = std::max<uint64_t>(kWarps * kTile, (chunk + kWarps * kTile - 1) / (kWarps * kTile) * (kWarps * kTile));
+    p.chunk = (uint32_t)chunk;
+    p.chunks = (uint32_t)std::max<uint64_t>(1, (span + chunk - 1) / chunk);
+    if (p.chunks > 1) p.bytes = (uint64_t)p.chunks * tokens * q_heads * (D + 2) * sizeof(float);
+    return p;
+}
+
+cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
+                          cudaStream_t stream, int *launches) {
+    (void)cudaGetLastError();
+    const bool many = a.max_q > 1;
+    for (const Variant &v : kVariants) {
+        if (v.D != D || v.rows != p.rows || v.fp16 != fp16 || v.many != many) continue;
+        const dim3 grid(a.pool.H * p.row_tiles * p.chunks, a.requests);
+        cudaError_t e = launch(v.rows_fn, grid, kWarps * 32, v.smem, stream, pdl, a);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        if (p.chunks > 1) {
+            e = launch(v.join_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
+            if (e == cudaSuccess) ++*launches;
+        }
+        return e;
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t preload_attend_kernels() {
+    cudaFuncAttributes at;
+    for (const Variant &v : kVariants) {
+        cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.rows_fn);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute((const void *)v.rows_fn,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvb

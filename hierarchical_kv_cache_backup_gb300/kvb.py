@@ -42,6 +42,12 @@ KV_CFG_NO_BULK = 1
 KV_CFG_NO_PDL = 2
 KV_CFG_OVERLAP_RESTORES = 4
 KV_CFG_OVERLAP_BACKUPS = 8
+KV_BF16, KV_FP16 = 0, 1
+KV_CACHE_SAME, KV_CACHE_E4M3, KV_CACHE_Q4 = 0, 1, 2
+KV_ROTARY_HALF, KV_ROTARY_INTERLEAVED = 0, 1
+KV_ROTARY_PLAIN, KV_ROTARY_LINEAR, KV_ROTARY_NTK, KV_ROTARY_YARN, KV_ROTARY_BANDS = 0, 1, 2, 3, 4
+KV_ROTATE_INVERSE = 1
+KV_STATUS_BAD_SLOT, KV_STATUS_BAD_PAGE, KV_STATUS_BAD_LENGTH = 1, 2, 4
 KVB_IPC_MAGIC = 0x4B564231
 KVB_IPC_MAGIC_SPLIT = 0x4B564253
 
@@ -57,7 +63,8 @@ EXPORTS = ("kv_pool_register", "kv_pool_register_split", "kv_pool_export", "kv_p
            "kv_ring_pop", "kv_ring_complete", "kv_ring_serve_device", "kv_ring_device_result",
            "kv_ring_device_stop", "kv_ring_ready_set", "kv_ring_ready_stream_set",
            "kv_fault_inject", "kv_l3_open", "kv_l3_close",
-           "kv_l3_put", "kv_l3_get")
+           "kv_l3_put", "kv_l3_get", "kv_cache_head_bytes", "kv_rotary_create", "kv_rotary_close",
+           "kv_rotate", "kv_append", "kv_fetch", "kv_attend", "kv_attend_workspace")
 
 
 class KvError(RuntimeError):
@@ -102,6 +109,59 @@ class kv_config(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_uint32), ("max_ctas", ctypes.c_uint32),
                 ("staging_bytes", ctypes.c_uint64), ("flags", ctypes.c_uint32),
                 ("cta_threads", ctypes.c_uint32)]
+
+
+class kv_vecs(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class kv_rotary_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_uint32), ("style", ctypes.c_uint32),
+                ("scaling", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("slow", ctypes.c_double),
+                ("fast", ctypes.c_double), ("original_len", ctypes.c_uint64),
+                ("gain", ctypes.c_double)]
+
+
+class kv_rotate_args(ctypes.Structure):
+    _fields_ = [("x", kv_vecs), ("out", kv_vecs), ("positions", ctypes.c_void_p),
+                ("rows_in", ctypes.c_void_p), ("rows_out", ctypes.c_void_p),
+                ("tokens", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class kv_append_args(ctypes.Structure):
+    _fields_ = [("k", kv_vecs), ("v", kv_vecs), ("q", kv_vecs), ("q_out", kv_vecs),
+                ("rows", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("tokens", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("format", ctypes.c_uint32), ("layer", ctypes.c_uint32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32 * 2)]
+
+
+class kv_fetch_args(ctypes.Structure):
+    _fields_ = [("k", kv_vecs), ("v", kv_vecs), ("slots", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("tokens", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("format", ctypes.c_uint32), ("layer", ctypes.c_uint32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
+class kv_attend_args(ctypes.Structure):
+    _fields_ = [("q", kv_vecs), ("out", kv_vecs), ("lse", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("status", ctypes.c_void_p), ("requests", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint32), ("max_q", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("layer", ctypes.c_uint32), ("window", ctypes.c_uint32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32 * 2)]
 
 
 def _load():
@@ -161,6 +221,14 @@ def _load():
         "kv_l3_close": (st, [vp]),
         "kv_l3_put": (st, [vp, vp, u64, vp, vp, u32]),
         "kv_l3_get": (st, [vp, vp, u64, vp, vp, u32]),
+        "kv_cache_head_bytes": (st, [u32, u32, P(u32)]),
+        "kv_rotary_create": (st, [P(kv_rotary_desc), P(vp)]),
+        "kv_rotary_close": (st, [vp]),
+        "kv_rotate": (st, [vp, P(kv_rotate_args), vp]),
+        "kv_append": (st, [vp, vp, P(kv_append_args), vp]),
+        "kv_fetch": (st, [vp, P(kv_fetch_args), vp]),
+        "kv_attend": (st, [vp, P(kv_attend_args), vp]),
+        "kv_attend_workspace": (st, [vp, P(kv_attend_args), P(u64)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -650,6 +718,107 @@ def kv_fault_inject(point: str, count: int = 1) -> None:
     """Arms a host-side fault point ("staging_alloc", "fence_reserve", "launch", "launch_nth",
     "ipc_open", "host_register"); count 0 disarms."""
     _check(_lib.kv_fault_inject(point.encode(), count))
+
+
+# ------------------------------------------- vectors of a pool's pages
+#
+# Argument blocks are built once and kept: they hold addresses, so the tensors
+# behind them have to live as long as the blocks (and captured graphs) are used.
+
+def vecs(t) -> kv_vecs:
+    """A [tokens, heads, head_dim] tensor of contiguous 16-bit vectors as a kv_vecs."""
+    if t.dim() != 3 or t.element_size() != 2:
+        raise ValueError(f"a [tokens, heads, head_dim] tensor of 16-bit values is wanted, got "
+                         f"{tuple(t.shape)} of {t.dtype}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the values of a vector must be contiguous, got strides {t.stride()}")
+    return kv_vecs(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0,
+                   t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def kv_cache_head_bytes(format: int, head_dim: int) -> int:
+    """Bytes of a head vector of `head_dim` values in a cache format (a pool layout's B)."""
+    out = ctypes.c_uint32()
+    _check(_lib.kv_cache_head_bytes(format, head_dim, ctypes.byref(out)))
+    return out.value
+
+
+def kv_rotary_create(rot_dim: int, style: int = KV_ROTARY_HALF, base: float = 10000.0,
+                     scaling: int = KV_ROTARY_PLAIN, factor: float = 1.0, original_len: int = 0,
+                     slow: float = 0.0, fast: float = 0.0, gain: float = 0.0) -> int:
+    """Rotary frequencies (kv_rotary_desc in include/kvb.h); returns their handle."""
+    d = kv_rotary_desc(rot_dim, style, scaling, 0, base, factor, slow, fast, original_len, gain)
+    out = ctypes.c_void_p()
+    _check(_lib.kv_rotary_create(ctypes.byref(d), ctypes.byref(out)))
+    return out.value
+
+
+def kv_rotary_close(rotary: int) -> None:
+    """Closes a rotary handle."""
+    _check(_lib.kv_rotary_close(rotary))
+
+
+def make_rotate_args(x: kv_vecs, out: kv_vecs, tokens: int, heads: int, head_dim: int, dtype: int,
+                     positions: int | None = None, rows_in: int | None = None,
+                     rows_out: int | None = None, inverse: bool = False) -> kv_rotate_args:
+    """The argument block of kv_rotate."""
+    return kv_rotate_args(x, out, positions, rows_in, rows_out, tokens, heads, head_dim, dtype,
+                          KV_ROTATE_INVERSE if inverse else 0, 0)
+
+
+def kv_rotate(rotary: int, args: kv_rotate_args, stream=None) -> None:
+    """Turns vectors by their positions, or by rows of cosines and sines; enqueued on `stream`."""
+    _check(_lib.kv_rotate(rotary, args, stream))
+
+
+def make_append_args(k: kv_vecs, v: kv_vecs, q: kv_vecs | None = None, q_out: kv_vecs | None = None,
+                     *, tokens: int, head_dim: int, dtype: int, format: int, layer: int, slots: int,
+                     q_heads: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                     rows: int | None = None, status: int | None = None) -> kv_append_args:
+    """The argument block of kv_append."""
+    return kv_append_args(k, v, q or kv_vecs(), q_out or kv_vecs(), rows, slots, status, tokens,
+                          q_heads, head_dim, dtype, format, layer, k_scale, v_scale)
+
+
+def kv_append(pool: int, rotary: int | None, args: kv_append_args, stream=None) -> None:
+    """Keys and values (keys turned, when `rotary` is given) to slots of one layer of the pool."""
+    _check(_lib.kv_append(pool, rotary, args, stream))
+
+
+def make_fetch_args(k: kv_vecs | None, v: kv_vecs | None, *, tokens: int, head_dim: int, dtype: int,
+                    format: int, layer: int, slots: int, k_scale: float = 1.0, v_scale: float = 1.0,
+                    status: int | None = None) -> kv_fetch_args:
+    """The argument block of kv_fetch."""
+    return kv_fetch_args(k or kv_vecs(), v or kv_vecs(), slots, status, tokens, head_dim, dtype,
+                         format, layer, k_scale, v_scale, 0)
+
+
+def kv_fetch(pool: int, args: kv_fetch_args, stream=None) -> None:
+    """Slots of one layer of the pool back to 16-bit keys and values."""
+    _check(_lib.kv_fetch(pool, args, stream))
+
+
+def make_attend_args(q: kv_vecs, out: kv_vecs, *, q_start: int, lens: int, pages: int | None,
+                     pages_stride: int, requests: int, tokens: int, max_q: int, max_len: int,
+                     q_heads: int, head_dim: int, dtype: int, layer: int, scale: float,
+                     window: int = 0, lse: int | None = None, workspace: int | None = None,
+                     workspace_bytes: int = 0, status: int | None = None) -> kv_attend_args:
+    """The argument block of kv_attend; kv_attend_workspace says how much workspace it needs."""
+    return kv_attend_args(q, out, lse, q_start, lens, pages, pages_stride, workspace,
+                          workspace_bytes, status, requests, tokens, max_q, max_len, q_heads,
+                          head_dim, dtype, layer, window, scale)
+
+
+def kv_attend_workspace(pool: int, args: kv_attend_args) -> int:
+    """Bytes of device workspace that kv_attend needs for this block (0: none)."""
+    out = ctypes.c_uint64()
+    _check(_lib.kv_attend_workspace(pool, args, ctypes.byref(out)))
+    return out.value
+
+
+def kv_attend(pool: int, args: kv_attend_args, stream=None) -> None:
+    """Attention of new tokens over one layer of a 4-bit pool."""
+    _check(_lib.kv_attend(pool, args, stream))
 
 
 def library():

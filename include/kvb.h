@@ -431,6 +431,211 @@ KVB_API kv_status kv_device_scatter(kv_pool pool, const void *buf, uint64_t buf_
 KVB_API kv_status kv_backup_staged_noalloc(kv_pool pool, kv_host host, const int32_t *src_pages,
                                            const int32_t *host_slots, uint32_t n, void *stream);
 
+/* ---------------------------------------------- vectors of a pool's pages
+ *
+ * The calls above move whole pages as opaque bytes.  The calls below write and
+ * read the head vectors inside them, as a serving loop does between a restore
+ * and a backup: turn queries and keys by their positions (kv_rotate), append
+ * keys and values of new tokens to pages (kv_append), read vectors back
+ * (kv_fetch), and attend over pages held in 4 bits (kv_attend).
+ *
+ * Common rules.  Every call is enqueued on `stream`, ordered by it alone (no
+ * fence), allocates nothing and may be captured into a CUDA graph after the
+ * first call on its device; a later replay reads the same pointers again.  All
+ * pointers in an argument block are device memory of the pool's device (of x's
+ * device for kv_rotate) unless the text says otherwise (INVALID_ARG), and stay
+ * valid until the work is done.  Blocks themselves are read before the call
+ * returns.  `reserved` members must be 0.  Counts of zero enqueue nothing.
+ * Work is counted by kv_launch_count().
+ *
+ * What only the GPU sees -- slots, page tables, lengths -- is checked there,
+ * before it is used as an address: a bad value sets bits in the 32-bit word
+ * `status` (never cleared by the library; NULL = not reported) and has the
+ * effect that its call names.
+ *
+ * Components: C = 2, keys are component 0 and values component 1 (LAYOUT
+ * otherwise).  A slot is page x T + token, as a 64-bit integer. */
+
+/* Bits of a status word. */
+#define KV_STATUS_BAD_SLOT 1u     /* slot outside [-1, P x T)                       */
+#define KV_STATUS_BAD_PAGE 2u     /* page id outside [0, P) inside a request's length */
+#define KV_STATUS_BAD_LENGTH 4u   /* length or q_start outside what the block allows */
+
+typedef enum { KV_BF16 = 0, KV_FP16 = 1 } kv_dtype;   /* type of x, q, k, v, out  */
+
+/* How a pool's head vectors hold D values.
+ *   SAME  the 16-bit values themselves:      B = 2 D, D a multiple of 8.
+ *   E4M3  value / scale in fp8 e4m3, saturating at 448 (scale: one per call and
+ *         component):                        B = D, D a multiple of 16.
+ *   Q4    4-bit codes with a scale word for each 32 values: D a multiple of 32;
+ *         D / 2 bytes of codes (value i in bits 4 (i % 8).. of 32-bit word
+ *         i / 8), D / 32 scale words, zeros up to B = 5 D / 8 rounded up to a
+ *         multiple of 16 (80 bytes for D = 128).
+ * A scale word is a float32 whose low four mantissa bits hold the zero point z:
+ * value = (code - z) x s, s = the word with those bits cleared.  For the group's
+ * values x, with lo = min(0, x...) and hi = max(0, x...): s = hi x (1/15) -
+ * lo x (1/15) in float32, each product and the difference rounded, then rounded
+ * to the nearest multiple of 16 units in the last place (half away from 0);
+ * z = round(-lo / s) and code = round(x / s) + z, both kept in 0..15, with the
+ * quotients rounded exactly, ties to even.  A group with a value that is not
+ * finite decodes to NaN; one with s < 2^-100 to zeros.  All of it is defined on
+ * float32 bits, so the bytes do not depend on the kernel that writes them. */
+typedef enum { KV_CACHE_SAME = 0, KV_CACHE_E4M3 = 1, KV_CACHE_Q4 = 2 } kv_cache_format;
+
+/* B of a format for head_dim D.  Errors: INVALID_ARG (NULL, unknown format),
+ * LAYOUT (D not a multiple the format takes, or above 256). */
+KVB_API kv_status kv_cache_head_bytes(uint32_t format, uint32_t head_dim, uint32_t *out);
+
+/* Vectors in device memory: vector (token i, head h) starts at data +
+ * i x token_stride + h x head_stride elements; its values are contiguous.
+ * data 16-B aligned, strides multiples of 8 elements (ALIGNMENT), not negative
+ * (INVALID_ARG). */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} kv_vecs;
+
+/* Rotary positions.  The first rot_dim (R) values of a vector are R/2 pairs,
+ * pair i = (x[i], x[i + R/2]) in HALF style, (x[2i], x[2i + 1]) in INTERLEAVED;
+ * at position p, (a, b) becomes (a c - b s, a s + b c) with c = gain cos(p f_i),
+ * s = gain sin(p f_i); products and sums are rounded one by one in float32.
+ * Values from R on pass through.
+ * Frequencies, with b = base and f_i = b^(-2 i / R) radians per position:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   NTK     b x factor^(R / (R - 2)) in place of b (R >= 4)
+ *   YARN    f_i / factor x r_i + f_i (1 - r_i); r_i rises from 0 at pair
+ *           floor(d(fast)) (>= 0) to 1 at pair ceil(d(slow)) (<= R - 1), where
+ *           d(t) = R ln(original_len / (2 pi t)) / (2 ln b) is the pair that
+ *           turns t times over original_len (the two pairs taken at least 0.001
+ *           apart); gain 0 means 0.1 ln(factor) + 1
+ *   BANDS   with t_i = original_len f_i / (2 pi) turns, k = (t_i - slow) /
+ *           (fast - slow) kept in [0, 1]: f_i k + f_i / factor (1 - k)
+ * gain 0 otherwise means 1. */
+typedef enum { KV_ROTARY_HALF = 0, KV_ROTARY_INTERLEAVED = 1 } kv_rotary_style;
+typedef enum { KV_ROTARY_PLAIN = 0, KV_ROTARY_LINEAR = 1, KV_ROTARY_NTK = 2, KV_ROTARY_YARN = 3,
+               KV_ROTARY_BANDS = 4 } kv_rotary_scaling;
+typedef struct {
+    uint32_t rot_dim;        /* R: even, 2..256                                   */
+    uint32_t style;          /* kv_rotary_style                                   */
+    uint32_t scaling;        /* kv_rotary_scaling                                 */
+    uint32_t reserved;
+    double base;             /* > 1                                               */
+    double factor;           /* >= 1 (LINEAR, NTK, YARN, BANDS)                   */
+    double slow, fast;       /* 0 < slow < fast (YARN, BANDS)                     */
+    uint64_t original_len;   /* >= 1 (YARN, BANDS)                                */
+    double gain;             /* >= 0                                              */
+} kv_rotary_desc;
+typedef struct kv_rotary_s *kv_rotary;
+
+/* Host state only.  Errors: INVALID_ARG, NO_MEMORY; CLOSED for a second close. */
+KVB_API kv_status kv_rotary_create(const kv_rotary_desc *desc, kv_rotary *out);
+KVB_API kv_status kv_rotary_close(kv_rotary rotary);
+
+#define KV_ROTATE_INVERSE 1u   /* turn by -p f_i: undoes a rotation of gain 1, and is
+                                  the gradient of the rotation for any gain          */
+/* out <- x turned.  The angles come from `positions` (one int64 a token, any
+ * sign) or, where that is NULL, from `rows_in`; `rows_out`, if set, receives
+ * the cosines and sines used (needs positions): rows are float32
+ * [tokens][2][R/2], the cosines of a token's pairs, then its sines, gain
+ * included, for kv_append and further kv_rotate calls of the same step (16-B
+ * aligned).  out may be x itself (same strides); otherwise they do not overlap.
+ * head_dim: a multiple of 8, R..256.  Errors: INVALID_ARG, CLOSED, ALIGNMENT,
+ * CUDA. */
+typedef struct {
+    kv_vecs x, out;
+    const int64_t *positions;
+    const float *rows_in;
+    float *rows_out;
+    uint32_t tokens, heads, head_dim, dtype;
+    uint32_t flags;          /* KV_ROTATE_*                                       */
+    uint32_t reserved;
+} kv_rotate_args;
+KVB_API kv_status kv_rotate(kv_rotary rotary, const kv_rotate_args *args, void *stream);
+
+/* Appends keys and values: for every token i and KV head, the slot slots[i] of
+ * layer `layer` receives k (turned by rows[i] when `rotary` is not NULL) and v
+ * in the pool's format; no other byte changes.  slots[i] = -1 leaves token i
+ * out; any other slot outside the pool does too and sets BAD_SLOT.  Two tokens
+ * of one call must not name the same slot (the bytes would be a mix of both).
+ * When q.data is set, q_out receives the queries turned by the same rows, for
+ * every token (needs rotary; q_out may be q itself).  layout B must be
+ * kv_cache_head_bytes(format, head_dim), head_dim <= 256.  Errors: INVALID_ARG,
+ * CLOSED, STALE, OUT_OF_RANGE (layer), LAYOUT, ALIGNMENT, CUDA. */
+typedef struct {
+    kv_vecs k, v, q, q_out;
+    const float *rows;
+    const int64_t *slots;
+    uint32_t *status;
+    uint32_t tokens, q_heads, head_dim, dtype;
+    uint32_t format;         /* kv_cache_format                                   */
+    uint32_t layer;
+    float k_scale, v_scale;  /* E4M3: finite, > 0                                 */
+    uint32_t reserved[2];
+} kv_append_args;
+KVB_API kv_status kv_append(kv_pool pool, kv_rotary rotary, const kv_append_args *args,
+                            void *stream);
+
+/* Reads keys and values back as 16-bit values, rounded once: token i of k and v
+ * (either may have data = NULL: not wanted) <- slot slots[i].  Slot -1, or one
+ * outside the pool (BAD_SLOT), gives zeros.  Errors: as kv_append. */
+typedef struct {
+    kv_vecs k, v;
+    const int64_t *slots;
+    uint32_t *status;
+    uint32_t tokens, head_dim, dtype, format, layer;
+    float k_scale, v_scale;
+    uint32_t reserved;
+} kv_fetch_args;
+KVB_API kv_status kv_fetch(kv_pool pool, const kv_fetch_args *args, void *stream);
+
+/* Attention of new tokens over one layer of a Q4 pool.  Request r has lens[r]
+ * cached tokens, token t in page pages[r x pages_stride + t / T] (the new
+ * tokens' own keys included: append first), and the query tokens q_start[r]..
+ * q_start[r + 1] - 1 of q, the last n = q_start[r + 1] - q_start[r] of its
+ * tokens.  Query i of them stands at position lens[r] - n + i and sees the
+ * cached tokens t <= that position, with window > 0 only t > position - window.
+ * q_heads is a multiple of the pool's H; query head j reads KV head
+ * j / (q_heads / H).  With x_t = scale q . k_t over the tokens it sees:
+ * out = sum exp(x_t) v_t / sum exp(x_t), lse (float32 [tokens][q_heads], NULL:
+ * not wanted) = ln sum exp(x_t).  A query that sees nothing gets out = 0 and
+ * lse = -infinity.  Scores, sums and accumulators are float32.
+ * A page id outside the pool inside a request's length sets BAD_PAGE, and the
+ * queries that see the page get NaN.  lens[r] is taken as at most max_len and
+ * at least 0, and a request whose q_start values are out of order, outside
+ * [0, tokens] or further apart than max_q is left out; both set BAD_LENGTH.
+ * A page-table row holds ceil(max_len / T) entries that may be read (only those
+ * inside lens[r] are used).  q and out hold `tokens` vectors.
+ * head_dim: 64, 96, 128, 192 or 256 (LAYOUT otherwise).  Errors: INVALID_ARG,
+ * CLOSED, STALE, OUT_OF_RANGE (layer; workspace too small), LAYOUT, ALIGNMENT
+ * (q, out, or workspace not 16-B aligned), CUDA. */
+typedef struct {
+    kv_vecs q, out;
+    float *lse;
+    const int32_t *q_start;   /* requests + 1                                     */
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;     /* entries between the rows of the page table       */
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint32_t *status;
+    uint32_t requests;        /* at most 65535                                    */
+    uint32_t tokens;          /* query tokens of all requests                     */
+    uint32_t max_q;           /* the most of one request                          */
+    uint32_t max_len;         /* the longest request, >= 0                        */
+    uint32_t q_heads, head_dim, dtype, layer;
+    uint32_t window;          /* 0: none                                          */
+    float scale;              /* finite                                           */
+    uint32_t reserved[2];
+} kv_attend_args;
+KVB_API kv_status kv_attend(kv_pool pool, const kv_attend_args *args, void *stream);
+
+/* Bytes of workspace that kv_attend needs for a block (its pointers are not
+ * looked at).  A larger one will do, and one workspace serves calls that follow
+ * one another on a stream, whatever it held before; calls that may run at the
+ * same time need one each.  0: none is needed. */
+KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, uint64_t *out);
+
 /* Host-side validation of an operation without a GPU (kind 0 = backup with
  * a = src pages, b = slots; kind 1 = restore with a = slots, b = dst pages).
  * Same checks and codes as kv_backup / kv_restore minus handle state. */
