@@ -1,13 +1,15 @@
 // kvb_attend.cu -- attention of new tokens over one layer of a 4-bit pool.
 //
 // Mathematics.  A cached value is (code - z) s with one step s and zero point z
-// for each 32 values of a vector (a group).  With codes re-centred to code - 8
-// (small integers, exact in fp16),
-//   q . k_t   = sum_groups s_t (q_g . (code_t - 8)_g - (z_t - 8) sum q_g)
-//   out[dim]  = sum_t p_t s_t (code_t[dim] - 8) - sum_t p_t s_t (z_t - 8)
-// so the matrix instructions multiply exact codes, steps scale float32 sums on
-// the key side and the probabilities on the value side, and zero points are one
-// float32 correction a group.  p_t = 2^(x_t - m) with a running maximum m.
+// for each 32 values of a vector (a group g):
+//   q . k_t   = sum_g s_tg (q_g . code_tg - z_tg sum q_g)
+//   out[dim]  = sum_t (p_t s_tg) code_t[dim] - sum_t (p_t s_tg) z_tg
+// The matrix instructions multiply codes and zero points as they are: the
+// four bits of a code in the low bits of an fp16 are the subnormal code x 2^-24
+// (x 2^-20 four bits higher), exact, and the powers of two go into the queries
+// and the last scaling.  Unpacking is one AND a pair of values and one shift for
+// two.  Steps scale float32 sums on the key side and the probabilities on
+// the value side.  p_t = 2^(x_t - m) with a running maximum m.
 #include "kvb_vec.h"
 #include "kvb_vec_internal.h"
 
@@ -44,6 +46,14 @@ __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, ui
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c = a b over 8 values of k, from nothing
+__device__ __forceinline__ void mma8(float *c, uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+                 "{%7,%7,%7,%7};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -55,26 +65,50 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Four pairs of codes (nibbles i of both 16-bit halves) as fp16 pairs code - 8.
-// 0x6400 | n is 1024 + n in fp16, and 0x6400 | n << 4 is 1024 + 16 n.
+// Four pairs of codes (nibbles i of both 16-bit halves) as fp16 subnormals:
+// code x 2^-24 for i = 0 and 2, code x 2^-20 for 1 and 3.
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t *p) {
-    const __half2 k1032 = __half2half2(__ushort_as_half(0x6408));   // 1032
-    const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
-    const __half2 k72 = __half2half2(__ushort_as_half(0xd480));     // -72
     const uint32_t v = w >> 8;
-    uint32_t t[4] = {(w & 0x000f000fu) | 0x64006400u, (w & 0x00f000f0u) | 0x64006400u,
-                     (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        __half2 h = *reinterpret_cast<__half2 *>(&t[i]);
-        h = i & 1 ? __hfma2(h, k16, k72) : __hsub2(h, k1032);
-        p[i] = *reinterpret_cast<uint32_t *>(&h);
-    }
+    p[0] = w & 0x000f000fu;
+    p[1] = w & 0x00f000f0u;
+    p[2] = v & 0x000f000fu;
+    p[3] = v & 0x00f000f0u;
 }
 
-// z - 8 of a scale word (0x4b000000 | z is 2^23 + z).
-__device__ __forceinline__ float zero8(uint32_t word) {
-    return __uint_as_float((word & 15u) | 0x4b000000u) - 8388616.0f;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four 8 x 8 blocks of 16-bit values, row i of block b at the address of lane
+// 8 b + i: lane (g, c) gets values 2 c and 2 c + 1 of row g, or with kTrans of
+// column g the rows 2 c and 2 c + 1.
+template <bool kTrans>
+__device__ __forceinline__ void blocks4(uint32_t addr, uint32_t *r) {
+    if (kTrans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t word_at(uint32_t addr) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+    return w;
+}
+
+__device__ __forceinline__ uint4 words_at(uint32_t addr) {
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(addr) : "memory");
+    return w;
+}
+
+__device__ __forceinline__ uint32_t pick(const uint4 &u, int i) {
+    return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
 }
 
 __device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
@@ -100,8 +134,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // Scores come out with a token a row; movmatrix turns the probabilities of an
 // 8 x 8 block for the second product.
 //
-// Bound: issue slots.  About 380 instructions a warp per 16 tokens of 128
-// values (2,560 B): unpacking is 10 instructions for 8 values.
+// Zero points ride on the matrix instructions too.  Keys: three more values of k
+// hold z, against -sum q_g split into three fp16 parts (33 bits).  Values: one
+// more 16-row tile holds z of group g in row g, so that its product with the
+// rounded probabilities is subtracted at the end and the rounding error of a
+// probability acts on (code - z) only.
 template <int D, int NT, bool kHalf, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     kv_attend_rows_kernel(const __grid_constant__ AttendArgs a) {
@@ -138,8 +175,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     const int64_t head_off = (int64_t)head * a.pool.s_head;
 
-    uint32_t bad_page[kStages];
-    auto load = [&](int stage, int t0) {
+    // starts the copy of a tile; returns which of its tokens are in pages outside the pool
+    auto load = [&](int stage, int t0) -> uint32_t {
         const int t = t0 + lane;
         bool ok = t < c1;
         int64_t off = 0;
@@ -148,7 +185,6 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             off = token_offset(a.pool, table, (uint32_t)t, &wrong) + head_off;
             ok = !wrong;
         }
-        bad_page[stage] = __ballot_sync(0xffffffffu, wrong);
         const uint32_t at = ring + stage * (2 * kTile * SV);
         if (!ok) off = -1;
 #pragma unroll
@@ -162,21 +198,23 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             copy16(to + kTile * SV, a.pool.base[1] + from, on);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        return __ballot_sync(0xffffffffu, wrong);
+    };
+    auto load_or_not = [&](int stage, int t0) -> uint32_t {
+        if (t0 < c1) return load(stage, t0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return 0;
     };
 
     int t0 = c0 + warp * kTile;
-#pragma unroll
-    for (int st = 0; st < kStages; ++st) {
-        bad_page[st] = 0;
-        if (t0 + st * kWarps * kTile < c1) load(st, t0 + st * kWarps * kTile);
-        else asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+    uint32_t bad_now = load_or_not(0, t0), bad_next = load_or_not(1, t0 + kWarps * kTile);
 
     // Query rows as B fragments.  Each row is scaled by a power of two that
-    // brings its largest value near 2^8, so that bf16 queries are exact in fp16
-    // (but for values 2^-30 of the row's largest); the scores undo it.
-    uint32_t qf[NT][NG][4];
-    float qsum[NT][NG][2], qs[NT][2];
+    // brings its largest value to 2^9..2^10, so that bf16 queries are exact in
+    // fp16 (but for values 2^-22 of the row's largest, where 2^-24 is lost); the
+    // scores undo it.  Values that meet odd codes are divided by 16.
+    uint32_t qf[NT][NG][4], qz[NT][NG];
+    float qs[NT][2];
     int lim[NT][2], low[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -207,29 +245,31 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(8 - exponent of top), and its inverse; 1 for zeros and infinities
+        // 2^(9 - exponent of top), and its inverse; 1 for zeros and infinities
         const uint32_t ex = __float_as_uint(top) >> 23;
         const bool scaled = ex >= 10 && ex < 255;
-        const float up = scaled ? __uint_as_float((262u - ex) << 23) : 1.0f;
-        const float back = scaled ? __uint_as_float((ex - 8u) << 23) : 1.0f;
+        const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f;
+        const float back = scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
             float y[8], sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                y[e] = __half2float(__float2half_rn(x[gr][e] * up));
-                sum += y[e];
+                const float k = e & 1 ? 0.0625f : 1.0f;
+                y[e] = __half2float(__float2half_rn(x[gr][e] * up * k));
+                sum += e & 1 ? 16.0f * y[e] : y[e];
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) qf[nt][gr][e] = half2_bits(y[e], y[e + 4]);
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            qsum[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-            qsum[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+            const float h0 = __half2float(__float2half_rn(-sum));
+            const float h1 = __half2float(__float2half_rn(-sum - h0));
+            qz[nt][gr] = c == 0 ? half2_bits(h0, h1) : c == 1 ? half2_bits(-sum - h0 - h1, 0.0f) : 0u;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            qs[nt][e] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) * a.scale_log2;
+            qs[nt][e] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) * a.scale_log2 * 16777216.0f;
             const int col = 8 * nt + 2 * c + e;
             const int pos = s.len - s.n + (row0 + col) / (int)a.group;
             lim[nt][e] = min(pos, s.len - 1);
@@ -240,19 +280,25 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const int safe_hi = min(c1, s.len - s.n + row0 / (int)a.group + 1);
     const int safe_lo = a.window ? s.len - s.n + (row0 + rows - 1) / (int)a.group - (int)a.window + 1 : 0;
 
-    float o[NG][2][NT][4], corr[NT][NG][2], f[NG], m[NT][2], l[NT][2];
+    // lane constants of the fragments' addresses and of the zero points' places
+    const uint32_t at_row = ((lane & 15) * SV) + (lane >> 4) * 16;    // rows 0..15, then the next group
+    const uint32_t z_mul = c == 0 ? 0x00010001u : c == 1 ? 1u : 0u;
+    const uint32_t z_group = (g < NG ? g : 0) * 4;
+
+    float o[NG][2][NT][4], oz[NT][4], f[NG], m[NT][2], l[NT][2];
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
         f[gr] = __uint_as_float(227u << 23);   // 2^100: set by the first step that is not 0
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            corr[nt][gr][0] = corr[nt][gr][1] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[gr][0][nt][e] = o[gr][1][nt][e] = 0.0f;
         }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oz[nt][e] = 0.0f;
         m[nt][0] = m[nt][1] = kNoMax;
         l[nt][0] = l[nt][1] = 0.0f;
     }
@@ -260,55 +306,53 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     for (int stage = 0; t0 < c1; t0 += kWarps * kTile, stage ^= 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
-        const unsigned char *ks = smem + warp * WB + stage * (2 * kTile * SV);
-        const unsigned char *vs = ks + kTile * SV;
+        const uint32_t ks = ring + stage * (2 * kTile * SV), vs = ks + kTile * SV;
 
         // scores: x[sub][nt][e] for token 16 sub + g (+ 8 for e >= 2), row 8 nt + 2 c + (e & 1)
         float x[2][NT][4];
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[sub][nt][e] = 0.0f;
-#pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-            const unsigned char *k0 = ks + (16 * sub + g) * SV, *k1 = k0 + 8 * SV;
+            const uint32_t k0 = ks + (16 * sub + g) * SV + D / 2;
             uint4 w0, w1;
+            uint32_t kw[4];
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
                 if (gr % 4 == 0) {
-                    w0 = *reinterpret_cast<const uint4 *>(k0 + D / 2 + gr * 4);
-                    w1 = *reinterpret_cast<const uint4 *>(k1 + D / 2 + gr * 4);
+                    w0 = words_at(k0 + gr * 4);
+                    w1 = words_at(k0 + 8 * SV + gr * 4);
                 }
-                const uint32_t s0 = gr % 4 == 0 ? w0.x : gr % 4 == 1 ? w0.y : gr % 4 == 2 ? w0.z : w0.w;
-                const uint32_t s1 = gr % 4 == 0 ? w1.x : gr % 4 == 1 ? w1.y : gr % 4 == 2 ? w1.z : w1.w;
+                if (gr % 2 == 0) blocks4<false>(ks + 16 * sub * SV + gr * 16 + at_row, kw);
+                const uint32_t s0 = pick(w0, gr % 4), s1 = pick(w1, gr % 4);
                 uint32_t p0[4], p1[4];
-                codes4(*reinterpret_cast<const uint32_t *>(k0 + gr * 16 + c * 4), p0);
-                codes4(*reinterpret_cast<const uint32_t *>(k1 + gr * 16 + c * 4), p1);
+                codes4(kw[gr % 2 * 2], p0);
+                codes4(kw[gr % 2 * 2 + 1], p1);
                 const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]};
                 const uint32_t a1[4] = {p0[2], p1[2], p0[3], p1[3]};
-                const float d0 = q4_step(s0), d1 = q4_step(s1), z0 = zero8(s0), z1 = zero8(s1);
+                const float d0 = q4_step(s0), d1 = q4_step(s1);
+                const uint32_t z0 = (s0 & 15u) * z_mul, z1 = (s1 & 15u) * z_mul;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float acc[4];
+                    mma8(acc, z0, z1, qz[nt][gr]);
                     mma(acc, a0, qf[nt][gr][0], qf[nt][gr][1]);
                     mma(acc, a1, qf[nt][gr][2], qf[nt][gr][3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[sub][nt][e] += (e < 2 ? d0 : d1) *
-                                         (acc[e] - (e < 2 ? z0 : z1) * qsum[nt][gr][e & 1]);
+                        x[sub][nt][e] = gr == 0 ? (e < 2 ? d0 : d1) * acc[e]
+                                                : x[sub][nt][e] + (e < 2 ? d0 : d1) * acc[e];
                 }
             }
         }
-        // x in units of log2, masked
+        // in units of log2, from the maximum; masked
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[sub][nt][e] *= qs[nt][e & 1];
-        if (t0 < safe_lo || t0 + kTile > safe_hi || bad_page[stage] != 0) {
+                for (int e = 0; e < 4; ++e)
+                    x[sub][nt][e] = x[sub][nt][e] * qs[nt][e & 1] -
+                                    (m[nt][e & 1] == kNoMax ? 0.0f : m[nt][e & 1]);
+        if (t0 < safe_lo || t0 + kTile > safe_hi || bad_now != 0) {
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
@@ -316,23 +360,25 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int in = 16 * sub + g + (e >= 2 ? 8 : 0), t = t0 + in;
-                        if (bad_page[stage] >> in & 1) x[sub][nt][e] = __uint_as_float(kNanWord);
+                        if (bad_now >> in & 1) x[sub][nt][e] = __uint_as_float(kNanWord);
                         if (t >= c1 || t > lim[nt][e & 1] || t < low[nt][e & 1])
                             x[sub][nt][e] = -INFINITY;
                     }
-            if (bad_page[stage] != 0 && a.status != nullptr && lane == 0)
+            if (bad_now != 0 && a.status != nullptr && lane == 0)
                 atomicOr(a.status, KV_STATUS_BAD_PAGE);
         }
         // The maximum moves only when a score passes it by more than 2^8: until
         // then probabilities reach up to 2^8, which costs no precision.
-        float over = kNoMax;
+        bool move = false;
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) over = fmaxf(over, x[sub][nt][e] - m[nt][e & 1]);
-        if (__any_sync(0xffffffffu, over > 8.0f)) {
+            for (int e = 0; e < 2; ++e) {
+                const float over = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]),
+                                         fmaxf(x[1][nt][e], x[1][nt][e + 2]));
+                move |= over > 8.0f || m[nt][e] == kNoMax;
+            }
+        if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -342,13 +388,24 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    t = fmaxf(t, m[nt][e]);
-                    const float k = exp2f(m[nt][e] - t);
-                    m[nt][e] = t;
+                    float k = 1.0f;
+                    if (m[nt][e] == kNoMax) {            // nothing seen so far: take it as it is
+                        if (t == -INFINITY) continue;
+                        m[nt][e] = t;
+                    } else {
+                        t = fmaxf(t, 0.0f);              // by how much the maximum rises
+                        k = exp2_fast(-t);
+                        m[nt][e] += t;
+                    }
                     l[nt][e] *= k;
+                    oz[nt][e] *= k;
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub) {
+                        x[sub][nt][e] -= t;
+                        x[sub][nt][e + 2] -= t;
+                    }
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
-                        corr[nt][gr][e] *= k;
                         o[gr][0][nt][e] *= k;
                         o[gr][0][nt][e + 2] *= k;
                         o[gr][1][nt][e] *= k;
@@ -362,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[sub][nt][e] = exp2f(x[sub][nt][e] - m[nt][e & 1]);
+                    x[sub][nt][e] = exp2_fast(x[sub][nt][e]);
                     l[nt][e & 1] += x[sub][nt][e];
                 }
 
@@ -375,17 +432,13 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
             for (int q = 0; q < (NG + 3) / 4; ++q) {
-                vw[sub][0][q] = *reinterpret_cast<const uint4 *>(vs + (16 * sub + g) * SV + D / 2 + q * 16);
-                vw[sub][1][q] = *reinterpret_cast<const uint4 *>(vs + (16 * sub + g + 8) * SV + D / 2 + q * 16);
+                vw[sub][0][q] = words_at(vs + (16 * sub + g) * SV + D / 2 + q * 16);
+                vw[sub][1][q] = words_at(vs + (16 * sub + g + 8) * SV + D / 2 + q * 16);
             }
-        auto word = [&](int sub, int k, int gr) {
-            const uint4 &u = vw[sub][k][gr / 4];
-            return gr % 4 == 0 ? u.x : gr % 4 == 1 ? u.y : gr % 4 == 2 ? u.z : u.w;
-        };
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-            most[gr] = fmaxf(fmaxf(__uint_as_float(word(0, 0, gr)), __uint_as_float(word(0, 1, gr))),
-                             fmaxf(__uint_as_float(word(1, 0, gr)), __uint_as_float(word(1, 1, gr))));
+            auto w = [&](int sub, int k) { return __uint_as_float(pick(vw[sub][k][gr / 4], gr % 4)); };
+            most[gr] = fmaxf(fmaxf(w(0, 0), w(0, 1)), fmaxf(w(1, 0), w(1, 1)));
             raise |= most[gr] * f[gr] > 64.0f;
         }
         if (__any_sync(0xffffffffu, raise)) {
@@ -400,8 +453,10 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     f[gr] = to;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        corr[nt][gr][0] *= k;
-                        corr[nt][gr][1] *= k;
+                        if (g == gr) {
+                            oz[nt][0] *= k;
+                            oz[nt][1] *= k;
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             o[gr][0][nt][e] *= k;
@@ -413,12 +468,16 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-            const unsigned char *v0 = vs + (16 * sub + 2 * c) * SV + 2 * g;
+            // zero points of group g: tokens 2 c, 2 c + 1 and the same + 8
+            const uint32_t z = vs + (16 * sub + 2 * c) * SV + D / 2 + z_group;
+            const uint32_t za = __byte_perm(word_at(z), word_at(z + SV), 0x5410) & 0x000f000fu;
+            const uint32_t zb = __byte_perm(word_at(z + 8 * SV), word_at(z + 9 * SV), 0x5410) & 0x000f000fu;
+            uint32_t vc[4];
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                const uint32_t s0 = word(sub, 0, gr), s1 = word(sub, 1, gr);
-                const float d0 = q4_step(s0) * f[gr], d1 = q4_step(s1) * f[gr];
-                const float z0 = zero8(s0), z1 = zero8(s1);
+                if (gr % 2 == 0) blocks4<true>(vs + 16 * sub * SV + gr * 16 + at_row, vc);
+                const float d0 = q4_step(pick(vw[sub][0][gr / 4], gr % 4)) * f[gr];
+                const float d1 = q4_step(pick(vw[sub][1][gr / 4], gr % 4)) * f[gr];
                 uint32_t b[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -429,32 +488,26 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                         // a token that a row does not see may hold NaN for another
                         if (kMany && x[sub][nt][e] == 0.0f) p[e] = 0.0f;
                     }
-                    corr[nt][gr][0] += p[0] * z0 + p[2] * z1;
-                    corr[nt][gr][1] += p[1] * z0 + p[3] * z1;
                     b[nt][0] = transpose8x8(half2_bits(p[0], p[1]));
                     b[nt][1] = transpose8x8(half2_bits(p[2], p[3]));
                 }
-                const unsigned char *v = v0 + gr * 16;
-                const uint32_t t0w = *reinterpret_cast<const unsigned short *>(v);
-                const uint32_t t1w = *reinterpret_cast<const unsigned short *>(v + SV);
-                const uint32_t t2w = *reinterpret_cast<const unsigned short *>(v + 8 * SV);
-                const uint32_t t3w = *reinterpret_cast<const unsigned short *>(v + 9 * SV);
                 uint32_t p0[4], p1[4];
-                codes4(__byte_perm(t0w, t1w, 0x5410), p0);
-                codes4(__byte_perm(t2w, t3w, 0x5410), p1);
+                codes4(vc[gr % 2 * 2], p0);
+                codes4(vc[gr % 2 * 2 + 1], p1);
                 const uint32_t a0[4] = {p0[0], p0[1], p1[0], p1[1]};
                 const uint32_t a1[4] = {p0[2], p0[3], p1[2], p1[3]};
+                const uint32_t az[4] = {g == gr ? za : 0u, 0u, g == gr ? zb : 0u, 0u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma(o[gr][0][nt], a0, b[nt][0], b[nt][1]);
                     mma(o[gr][1][nt], a1, b[nt][0], b[nt][1]);
+                    mma(oz[nt], az, b[nt][0], b[nt][1]);
                 }
             }
         }
         __syncwarp();
-        const int next = t0 + kStages * kWarps * kTile;
-        if (next < c1) load(stage, next);
-        else asm volatile("cp.async.commit_group;" ::: "memory");
+        bad_now = bad_next;
+        bad_next = load_or_not(stage, t0 + kStages * kWarps * kTile);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -475,13 +528,16 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                float k = corr[nt][gr][e];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) k += __shfl_xor_sync(0xffffffffu, k, d);
+                // undo f and the subnormals' 2^-24 (2^-20 for odd codes); f is a power of two
+                const float k = __shfl_sync(0xffffffffu, oz[nt][e], 4 * gr + c);
                 const float back = 1.0f / f[gr];
-                *reinterpret_cast<float4 *>(mine + row * (D + 4) + gr * 32 + 4 * g) =
-                    make_float4((o[gr][0][nt][e] - k) * back, (o[gr][0][nt][e + 2] - k) * back,
-                                (o[gr][1][nt][e] - k) * back, (o[gr][1][nt][e + 2] - k) * back);
+                float4 v = make_float4(o[gr][0][nt][e] - k, o[gr][0][nt][e + 2] * 0.0625f - k,
+                                       o[gr][1][nt][e] - k, o[gr][1][nt][e + 2] * 0.0625f - k);
+                v.x = v.x * 16777216.0f * back;
+                v.y = v.y * 16777216.0f * back;
+                v.z = v.z * 16777216.0f * back;
+                v.w = v.w * 16777216.0f * back;
+                *reinterpret_cast<float4 *>(mine + row * (D + 4) + gr * 32 + 4 * g) = v;
             }
         }
     __syncthreads();
@@ -497,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         for (int w = 0; w < kWarps; ++w) {
             const float lw = join_l[w][row];
             if (lw == 0.0f) continue;          // this warp saw nothing of the row
-            const float k = exp2f(join_m[w][row] - top);
+            const float k = exp2_fast(join_m[w][row] - top);
             const float4 v = *reinterpret_cast<const float4 *>(
                 reinterpret_cast<const float *>(smem + w * WB) + row * (D + 4) + d4 * 4);
             sum += lw * k;
