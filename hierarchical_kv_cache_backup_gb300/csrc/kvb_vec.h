@@ -126,26 +126,31 @@ KVB_HD uint32_t q4_step_bits(float lo, float hi) {
     return f_bits(b) < f_bits(0x0d800000u) ? 0u : b;   // under 2^-100: zeros
 }
 
-// round(x / s), ties to even, exactly.  x * inv (inv = 1/s) is within a few
-// units in the last place of the quotient, so its rounding r is right or one
-// off next to a half-way point; there the sign of x - (r +- 1/2) s decides, and
-// an fma's rounding never changes the sign of its exact result.  s has 20
-// significant bits and |x / s| <= 16, so nothing underflows for s >= 2^-100.
+// round(x / s), ties to even, exactly, for |x / s| < 17.  x * inv (inv = 1/s) is
+// within a few units in the last place of the quotient, so its rounding r (by
+// adding and taking off 1.5 x 2^23) is right or, next to a half-way point, one
+// off.  e = x - r s is exact in one fma: it is at most about s/2, and r s and x
+// are multiples of 2^-23 s or r is 0.  Where |e| passes s/2, or meets it with r
+// odd, r moves by one towards x.
 KVB_HD float q4_round(float x, float s, float inv) {
-    const float r = rintf(f_mul(x, inv));
-    const float up = f_fma(-(r + 0.5f), s, x), down = f_fma(-(r - 0.5f), s, x);
-    const bool odd = ((int)r & 1) != 0;
-    if (up > 0.0f || (up == 0.0f && odd)) return r + 1.0f;
-    if (down < 0.0f || (down == 0.0f && odd)) return r - 1.0f;
-    return r;
+    const float t = f_fma(x, inv, 12582912.0f);
+    const float r = f_sub(t, 12582912.0f), h = 0.5f * s;
+    const float e = f_fma(-r, s, x), a = fabsf(e);
+    const bool odd = (u_bits(t) & 1u) != 0;
+    return a > h || (a == h && odd) ? f_add(r, copysignf(1.0f, e)) : r;
 }
 
-KVB_HD float q4_zero(float lo, float s, float inv) {
-    return fminf(fmaxf(q4_round(-lo, s, inv), 0.0f), 15.0f);
+KVB_HD float q4_zero(float lo, float s, float inv) { return fminf(q4_round(-lo, s, inv), 15.0f); }
+
+// A code as a float.  x >= lo, so that round(x / s) >= -round(-lo / s): never below 0.
+KVB_HD float q4_code(float x, float s, float inv, float z) {
+    return fminf(f_add(q4_round(x, s, inv), z), 15.0f);
 }
 
-KVB_HD uint32_t q4_code(float x, float s, float inv, float z) {
-    return (uint32_t)fminf(fmaxf(q4_round(x, s, inv) + z, 0.0f), 15.0f);
+// Four codes as 16 bits: their sum below 2^16 is exact.
+KVB_HD uint32_t q4_pack(const float *c) {
+    return u_bits(f_add(f_fma(f_fma(f_fma(c[3], 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]), 8388608.0f)) &
+           0xffffu;
 }
 
 KVB_HD float q4_step(uint32_t word) { return f_bits(word & ~15u); }

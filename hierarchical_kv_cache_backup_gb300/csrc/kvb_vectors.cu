@@ -57,11 +57,9 @@ __device__ __forceinline__ float one(uint64_t p) {
 // 32 values are neighbours in the warp (every lane of the warp takes part in
 // the exchange; `on` says whether this one stores).
 template <int kFormat, bool kHalf>
-__device__ __forceinline__ void store8(uint64_t vec, int chunk, const float *y, uint32_t D, uint32_t B,
-                                       float inv_scale, bool on) {
-    if (kFormat == 0) {
-        if (on) *reinterpret_cast<uint4 *>(vec + chunk * 16) = pack8<kHalf>(y);
-    } else if (kFormat == 1) {
+__device__ __forceinline__ void store8(uint64_t vec, uint32_t chunk, const float *y, uint32_t D,
+                                       uint32_t B, float inv_scale, bool on) {
+    if (kFormat == 1) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -85,17 +83,15 @@ __device__ __forceinline__ void store8(uint64_t vec, int chunk, const float *y, 
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, s));
             bad += __shfl_xor_sync(0xffffffffu, bad, s);
         }
-        const bool fine = bad == 0.0f;
-        uint32_t word = kNanWord, codes = 0;
-        if (fine) {
-            word = q4_step_bits(lo, hi);
-            if (word != 0) {
-                const float s = __uint_as_float(word), inv = __frcp_rn(s);
-                const float z = q4_zero(lo, s, inv);
+        uint32_t word = bad == 0.0f ? q4_step_bits(lo, hi) : kNanWord, codes = 0;
+        if (bad == 0.0f && word != 0) {
+            const float s = __uint_as_float(word), inv = __frcp_rn(s);
+            const float z = q4_zero(lo, s, inv);
+            float c[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) codes |= q4_code(y[i], s, inv, z) << (4 * i);
-                word |= (uint32_t)z;
-            }
+            for (int i = 0; i < 8; ++i) c[i] = q4_code(y[i], s, inv, z);
+            codes = q4_pack(c) | q4_pack(c + 4) << 16;
+            word |= (uint32_t)z;
         }
         if (on) {
             *reinterpret_cast<uint32_t *>(vec + chunk * 4) = codes;
@@ -110,25 +106,41 @@ __device__ __forceinline__ void store8(uint64_t vec, int chunk, const float *y, 
 // ------------------------------------------------------- rotate and append
 //
 // One block takes one token and `per_block` of its vectors (queries, keys and
-// values in that order).  A lane owns 8 neighbouring values (16 bytes) of a
-// vector at the same place in every vector it meets, so the token's cosines and
-// sines go to registers once and serve all heads; a HALF-style lane also loads
-// the 8 partners (its neighbour's line, so from L1) and computes its own half
-// only, which keeps the 32 values of a 4-bit group in four adjacent lanes.
-// Vectors never straddle warps, and a warp loads before it stores, so a
-// vector may be turned in place.  kFormat: -1 rotate only, else kv_cache_format.
-template <int kFormat, bool kHalf>
+// values in that order).  A lane owns the same values of every vector that it
+// meets, so the token's cosines and sines go to registers once and serve all
+// heads.  Vectors never straddle warps, and a warp loads before it stores, so
+// a vector may be turned in place.
+//
+// kPair: a lane owns two runs of 8 values (16 bytes each): in HALF style a run of
+// first members and the run of their partners, so that each line is loaded and
+// unpacked once; in INTERLEAVED style and past the rotated part, two runs that
+// are as far apart.  Four neighbouring lanes still hold the 32 values of a
+// 4-bit group when rotated and other part are multiples of 64 values.  Where
+// they are not (or not of 16 for the other formats), a lane owns one run and
+// reads its partners itself (!kPair).  8,192 tokens of 40 vectors of 128: 52 us
+// with one run a lane, bound by instructions.
+// kFormat: -1 rotate only, else kv_cache_format.
+template <int kFormat, bool kHalf, bool kPair>
 __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_constant__ VectorArgs a,
                                                               const __grid_constant__ RotaryK r) {
+    constexpr int kRuns = kPair ? 2 : 1;
     __shared__ __align__(16) float rows[2][kMaxPairs];
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t token = blockIdx.x;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t per_vec = a.D / 8, per_warp = 32 / per_vec;
-    const uint32_t sub = lane / per_vec, chunk = lane - sub * per_vec;
+    const uint32_t per_vec = a.D / (8 * kRuns), per_warp = 32 / per_vec;
+    const uint32_t sub = lane / per_vec, place = lane - sub * per_vec;
     const uint32_t half = a.half, total = a.q_heads + 2 * a.kv_heads;
+    // this lane's runs, in units of 8 values
+    const uint32_t turned_places = 2 * half / (8 * kRuns);
+    const bool turned = kPair ? place < turned_places : place * 8 < 2 * half;
+    uint32_t run[kRuns];
+    run[0] = kPair && !turned ? 2 * turned_places + (place - turned_places) : place;
+    if (kPair) run[kRuns - 1] = run[0] + (turned ? turned_places : per_vec - turned_places);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    int64_t off = -1, slot = -1;
+    if (kFormat >= 0) slot = a.slots[token];
     for (uint32_t i = threadIdx.x; i < half; i += kThreads) {
         float c, s;
         if (kFormat == -1 && a.positions != nullptr) {
@@ -151,30 +163,37 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
         rows[0][i] = c;
         rows[1][i] = kFormat == -1 ? s * a.sin_sign : s;
     }
-    int64_t off = -1;
     if (kFormat >= 0) {
-        const int64_t slot = a.slots[token];
         off = slot_offset(a.pool, slot);
         if (off < 0 && slot != -1 && a.status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
             atomicOr(a.status, KV_STATUS_BAD_SLOT);
     }
     __syncthreads();
 
-    // this lane's cosine and signed sine for each of its 8 values: y = x c + partner s
-    float cs[8], sn[8];
-    const bool turned = half != 0 && chunk * 8 < 2 * half;
+    // cosines and sines of this lane's values: kPair HALF 8 pairs; kPair
+    // INTERLEAVED 4 pairs of each run; else one for each value, signed
     const bool aligned = a.style == 1 || (half & 7) == 0;
+    float cs[8], sn[8];
     if (turned) {
+        if (kPair) {
+            const uint32_t i0 = a.style == 1 ? run[0] * 4 : place * 8;
+            const uint32_t i1 = a.style == 1 ? run[kRuns - 1] * 4 : place * 8 + 4;
+            *reinterpret_cast<float4 *>(cs) = *reinterpret_cast<const float4 *>(&rows[0][i0]);
+            *reinterpret_cast<float4 *>(cs + 4) = *reinterpret_cast<const float4 *>(&rows[0][i1]);
+            *reinterpret_cast<float4 *>(sn) = *reinterpret_cast<const float4 *>(&rows[1][i0]);
+            *reinterpret_cast<float4 *>(sn + 4) = *reinterpret_cast<const float4 *>(&rows[1][i1]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t d = chunk * 8 + e;
-            cs[e] = 1.0f;
-            sn[e] = 0.0f;
-            if (d < 2 * half) {
-                const bool second = a.style == 1 ? (d & 1) : d >= half;
-                const uint32_t i = a.style == 1 ? d >> 1 : second ? d - half : d;
-                cs[e] = rows[0][i];
-                sn[e] = second ? rows[1][i] : -rows[1][i];
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t d = place * 8 + e;
+                cs[e] = 1.0f;
+                sn[e] = 0.0f;
+                if (d < 2 * half) {
+                    const bool second = a.style == 1 ? (d & 1) : d >= half;
+                    const uint32_t i = a.style == 1 ? d >> 1 : second ? d - half : d;
+                    cs[e] = rows[0][i];
+                    sn[e] = second ? rows[1][i] : -rows[1][i];
+                }
             }
         }
     }
@@ -183,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
     constexpr int kBatch = 2;   // vectors in flight per lane
     for (uint32_t v0 = blockIdx.y * a.per_block + warp * per_warp; v0 < end;
          v0 += kBatch * per_warp * (kThreads / 32)) {
-        uint4 own[kBatch], other[kBatch];
+        uint4 own[kBatch][2];   // this lane's runs; !kPair: its run and the partners
         uint64_t src[kBatch];
         bool live[kBatch], turn[kBatch];
 #pragma unroll
@@ -195,61 +214,98 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
             const Vecs &x = is_q ? a.q : is_k ? a.k : a.v;
             const uint32_t h = is_q ? v : is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
             src[b] = x.data + (int64_t)token * x.s_tok + (int64_t)h * x.s_head;
-            own[b] = other[b] = make_uint4(0, 0, 0, 0);
-            if (live[b]) own[b] = *reinterpret_cast<const uint4 *>(src[b] + chunk * 16);
-            if (turn[b] && a.style == 0 && aligned)
-                other[b] = *reinterpret_cast<const uint4 *>(
-                    src[b] + (chunk * 8 < half ? chunk * 8 + half : chunk * 8 - half) * 2);
+            own[b][0] = own[b][1] = make_uint4(0, 0, 0, 0);
+            if (live[b]) {
+                own[b][0] = *reinterpret_cast<const uint4 *>(src[b] + run[0] * 16);
+                if (kPair) own[b][1] = *reinterpret_cast<const uint4 *>(src[b] + run[kRuns - 1] * 16);
+            }
+            if (!kPair && turn[b] && a.style == 0 && aligned)
+                own[b][1] = *reinterpret_cast<const uint4 *>(
+                    src[b] + (place * 8 < half ? place * 8 + half : place * 8 - half) * 2);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const uint32_t v = v0 + b * per_warp * (kThreads / 32) + sub;
             const bool is_q = v < a.q_heads;
-            float y[8];
-            unpack8<kHalf>(own[b], y);
-            if (turn[b]) {
-                float x[8], z[8];
+            float y[kRuns][8];
+            const bool need = turn[b] || (kFormat > 0 && live[b] && !is_q);
+            if (need) {
+                float x[2][8];
+                unpack8<kHalf>(own[b][0], x[0]);
+                unpack8<kHalf>(own[b][1], x[1]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = y[e];
-                if (a.style == 1) {
+                for (int e = 0; e < 8; ++e) {
+                    y[0][e] = x[0][e];
+                    if (kPair) y[kRuns - 1][e] = x[1][e];
+                }
+                if (turn[b]) {
+                    if (kPair && a.style == 0) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = x[e ^ 1];
-                } else if (aligned) {
-                    unpack8<kHalf>(other[b], z);
-                } else {
+                        for (int e = 0; e < 8; ++e) {
+                            y[0][e] = __fsub_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]));
+                            y[kRuns - 1][e] = __fadd_rn(__fmul_rn(x[0][e], sn[e]),
+                                                        __fmul_rn(x[1][e], cs[e]));
+                        }
+                    } else if (kPair) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t d = chunk * 8 + e;
-                        z[e] = d < 2 * half ? one<kHalf>(src[b] + (d < half ? d + half : d - half) * 2)
-                                            : 0.0f;
+                        for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float u = x[k][2 * e], w = x[k][2 * e + 1];
+                                const float c = cs[4 * k + e], s = sn[4 * k + e];
+                                y[k][2 * e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
+                                y[k][2 * e + 1] = __fadd_rn(__fmul_rn(u, s), __fmul_rn(w, c));
+                            }
+                    } else {
+                        if (a.style == 1) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[1][e] = x[0][e ^ 1];
+                        } else if (!aligned) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t d = place * 8 + e;
+                                x[1][e] = d < 2 * half
+                                              ? one<kHalf>(src[b] + (d < half ? d + half : d - half) * 2)
+                                              : 0.0f;
+                            }
+                        }
+                        // values past the rotated part keep their bits
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (place * 8 + e < 2 * half)
+                                y[0][e] = __fadd_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]));
                     }
                 }
-                // values past the rotated part keep their bits (1 x + 0 would turn -0 and NaN)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (chunk * 8 + e < 2 * half)
-                        y[e] = __fadd_rn(__fmul_rn(x[e], cs[e]), __fmul_rn(z[e], sn[e]));
             }
             __syncwarp();
-            if (is_q && live[b]) {
-                const uint64_t dst = a.q_out.data + (int64_t)token * a.q_out.s_tok +
-                                     (int64_t)v * a.q_out.s_head;
-                *reinterpret_cast<uint4 *>(dst + chunk * 16) =
-                    turn[b] ? pack8<kHalf>(y) : own[b];
+            const bool is_k = !is_q && v < a.q_heads + a.kv_heads;
+            if (live[b] && (is_q || kFormat == 0)) {
+                uint64_t dst;
+                if (is_q) {
+                    dst = a.q_out.data + (int64_t)token * a.q_out.s_tok + (int64_t)v * a.q_out.s_head;
+                } else {
+                    const uint32_t h = is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
+                    dst = a.pool.base[is_k ? 0 : 1] + (uint64_t)off + (uint64_t)h * a.pool.s_head;
+                }
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k)
+                    *reinterpret_cast<uint4 *>(dst + run[k] * 16) = turn[b] ? pack8<kHalf>(y[k])
+                                                                            : own[b][k];
             }
-            if (kFormat >= 0) {
-                const bool is_k = v < a.q_heads + a.kv_heads;
+            // a warp of queries only has nothing to hold
+            if (kFormat > 0 && __any_sync(0xffffffffu, live[b] && !is_q)) {
                 const uint32_t h = is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
                 const uint64_t vec = a.pool.base[is_k ? 0 : 1] + (uint64_t)off +
                                      (uint64_t)h * a.pool.s_head;
-                if (kFormat == 0) {
-                    if (live[b] && !is_q)
-                        *reinterpret_cast<uint4 *>(vec + chunk * 16) =
-                            turn[b] ? pack8<kHalf>(y) : own[b];
-                } else {
-                    store8<kFormat, kHalf>(vec, chunk, y, a.D, a.pool.B, is_k ? a.k_inv : a.v_inv,
+                if (!need)
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[k][e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kRuns; ++k)
+                    store8<kFormat, kHalf>(vec, run[k], y[k], a.D, a.pool.B, is_k ? a.k_inv : a.v_inv,
                                            live[b] && !is_q);
-                }
             }
         }
     }
@@ -329,22 +385,21 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, cudaStream_t stream, bool
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-typedef void (*VectorsFn)(VectorArgs, RotaryK);
+typedef void (*VectorsFn)(VectorArgs, RotaryK);   // [format + 1][pair][fp16]
 typedef void (*FetchFn)(VectorArgs);
-const VectorsFn kVectors[4][2] = {
-    {kv_vectors_kernel<-1, false>, kv_vectors_kernel<-1, true>},
-    {kv_vectors_kernel<0, false>, kv_vectors_kernel<0, true>},
-    {kv_vectors_kernel<1, false>, kv_vectors_kernel<1, true>},
-    {kv_vectors_kernel<2, false>, kv_vectors_kernel<2, true>}};
+#define KVB_VECTORS(F)                                                        \
+    {{kv_vectors_kernel<F, false, false>, kv_vectors_kernel<F, true, false>}, \
+     {kv_vectors_kernel<F, false, true>, kv_vectors_kernel<F, true, true>}}
+const VectorsFn kVectors[4][2][2] = {KVB_VECTORS(-1), KVB_VECTORS(0), KVB_VECTORS(1), KVB_VECTORS(2)};
 const FetchFn kFetch[3][2] = {{kv_fetch_kernel<0, false>, kv_fetch_kernel<0, true>},
                               {kv_fetch_kernel<1, false>, kv_fetch_kernel<1, true>},
                               {kv_fetch_kernel<2, false>, kv_fetch_kernel<2, true>}};
 
 // Vectors a block takes: all of a token's when there are tokens enough to fill
 // the GPU, else so few that the blocks do (a block's 4 warps take
-// 4 x per_warp at a time).
-uint32_t per_block_of(uint32_t tokens, uint32_t vectors, uint32_t D) {
-    const uint32_t at_once = (32 / (D / 8)) * (kThreads / 32);
+// 4 x per_warp at a time; lanes is what a vector takes of a warp).
+uint32_t per_block_of(uint32_t tokens, uint32_t vectors, uint32_t lanes) {
+    const uint32_t at_once = (32 / lanes) * (kThreads / 32);
     uint32_t steps = (vectors + at_once - 1) / at_once;
     if (steps < 1) steps = 1;   // rows of angles alone
     const uint64_t blocks = (uint64_t)tokens * steps;
@@ -360,26 +415,31 @@ cudaError_t launch_vectors(VectorArgs a, const RotaryK &r, int format, bool fp16
                            cudaStream_t stream) {
     (void)cudaGetLastError();
     const uint32_t vectors = a.q_heads + 2 * a.kv_heads;
-    a.per_block = per_block_of(a.tokens, vectors, a.D);
+    // two runs a lane where rotated and other part divide into pairs of runs, and, for
+    // 4-bit groups, four lanes at a time
+    const uint32_t unit = format == KV_CACHE_Q4 ? 64 : 16;
+    const bool pair = 2 * a.half % unit == 0 && (a.D - 2 * a.half) % unit == 0;
+    a.per_block = per_block_of(a.tokens, vectors, a.D / (pair ? 16 : 8));
     const uint32_t blocks = (vectors + a.per_block - 1) / a.per_block;
     const dim3 grid(a.tokens, blocks != 0 ? blocks : 1);   // no vectors: the rows alone
-    return launch(kVectors[format + 1][fp16], grid, stream, pdl, a, r);
+    return launch(kVectors[format + 1][pair][fp16], grid, stream, pdl, a, r);
 }
 
 cudaError_t launch_fetch(VectorArgs a, int format, bool fp16, bool pdl, cudaStream_t stream) {
     (void)cudaGetLastError();
-    a.per_block = per_block_of(a.tokens, 2 * a.kv_heads, a.D);
+    a.per_block = per_block_of(a.tokens, 2 * a.kv_heads, a.D / 8);
     const dim3 grid(a.tokens, (2 * a.kv_heads + a.per_block - 1) / a.per_block);
     return launch(kFetch[format][fp16], grid, stream, pdl, a);
 }
 
 cudaError_t preload_vector_kernels() {
     cudaFuncAttributes at;
-    for (auto &row : kVectors)
-        for (auto f : row) {
-            const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)f);
-            if (e != cudaSuccess) return e;
-        }
+    for (auto &format : kVectors)
+        for (auto &row : format)
+            for (auto f : row) {
+                const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)f);
+                if (e != cudaSuccess) return e;
+            }
     for (auto &row : kFetch)
         for (auto f : row) {
             const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)f);

@@ -47,7 +47,9 @@ void h_encode(const float *x, uint32_t *word, uint32_t *code) {   // 32 finite v
     for (int i = 0; i < 32; ++i) code[i] = 0;
     if (*word == 0) return;
     const float s = f_bits(*word), inv = 1.0f / s, z = q4_zero(lo, s, inv);
-    for (int i = 0; i < 32; ++i) code[i] = q4_code(x[i], s, inv, z);
+    float c[32];
+    for (int i = 0; i < 32; ++i) c[i] = q4_code(x[i], s, inv, z);
+    for (int i = 0; i < 32; ++i) code[i] = q4_pack(c + i / 4 * 4) >> (4 * (i % 4)) & 15u;
     *word |= (uint32_t)z;
 }
 }
