@@ -24,7 +24,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libkvb.so")
 
 SOURCES = ["kvb_api.cpp", "kvb_kernels.cu", "kvb_noalloc.cu", "kvb_ring.cpp", "kvb_ring_kernels.cu",
-           "kvb_l3.cpp", "kvb_vec.cpp", "kvb_vectors.cu", "kvb_attend.cu"]
+           "kvb_l3.cpp", "kvb_vec.cpp", "kvb_vectors.cu", "kvb_attend.cu",
+           "kvb_attend_tc.cu"]
 HEADERS = [os.path.join(CSRC, "kvb_internal.h"), os.path.join(CSRC, "kvb_ring_internal.h"),
            os.path.join(CSRC, "kvb_vec.h"), os.path.join(CSRC, "kvb_vec_internal.h"),
            os.path.join(INCLUDE, "kvb.h")]

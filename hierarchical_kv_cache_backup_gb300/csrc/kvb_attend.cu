@@ -702,22 +702,42 @@ const Variant kVariants[] = {KVB_VARIANTS(64, 1),  KVB_VARIANTS(64, 2),  KVB_VAR
                              KVB_VARIANTS(96, 2),  KVB_VARIANTS(128, 1), KVB_VARIANTS(128, 2),
                              KVB_VARIANTS(192, 1), KVB_VARIANTS(256, 1)};
 
+struct JoinVariant {
+    uint32_t D;
+    bool fp16;
+    AttendFn *fn;
+};
+const JoinVariant kJoins[] = {
+    {64, false, kv_attend_join_kernel<64, 256, false>},   {64, true, kv_attend_join_kernel<64, 256, true>},
+    {96, false, kv_attend_join_kernel<96, 256, false>},   {96, true, kv_attend_join_kernel<96, 256, true>},
+    {128, false, kv_attend_join_kernel<128, 256, false>}, {128, true, kv_attend_join_kernel<128, 256, true>}};
+
 }  // namespace
+
+// Query rows of a request from which the tcgen05 kernel (256 rows a block) is taken.
+constexpr uint64_t kManyRows = 64;
 
 AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
                        uint32_t window, uint32_t q_heads, uint32_t kv_heads, uint32_t D, int sms) {
     AttendPlan p{};
     const uint64_t rows = (uint64_t)max_q * (q_heads / kv_heads);
-    p.rows = rows > 8 && D <= 128 ? 16 : 8;
+    p.many = D <= 128 && rows >= kManyRows;
+    p.rows = p.many ? 256 : rows > 8 && D <= 128 ? 16 : 8;
     p.row_tiles = (uint32_t)((rows + p.rows - 1) / p.rows);
     // the most cached tokens a row tile sees: its queries' windows overlap
     uint64_t span = max_len;
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + p.rows);
-    // about four blocks an SM, in chunks of at least a tile for each warp
     const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
-    const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
+    uint64_t want, unit;
+    if (p.many) {        // one block an SM at most, in chunks of 512 tokens at least
+        want = std::max<uint64_t>(1, (uint64_t)sms / units);
+        unit = 512;
+    } else {             // about four blocks an SM, in chunks of at least a tile for each warp
+        want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
+        unit = kWarps * kTile;
+    }
     uint64_t chunk = (span + want - 1) / want;
-    chunk = std::max<uint64_t>(kWarps * kTile, (chunk + kWarps * kTile - 1) / (kWarps * kTile) * (kWarps * kTile));
+    chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);
     p.chunk = (uint32_t)chunk;
     p.chunks = (uint32_t)std::max<uint64_t>(1, (span + chunk - 1) / chunk);
     if (p.chunks > 1) p.bytes = (uint64_t)p.chunks * tokens * q_heads * (D + 2) * sizeof(float);
@@ -727,6 +747,19 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
 cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
                           cudaStream_t stream, int *launches) {
     (void)cudaGetLastError();
+    const dim3 join_grid(a.q_heads, a.max_q, a.requests);
+    if (p.many) {
+        cudaError_t e = launch_attend_tc(a, p, D, fp16, pdl, stream);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        if (p.chunks > 1)
+            for (const JoinVariant &v : kJoins)
+                if (v.D == D && v.fp16 == fp16) {
+                    e = launch(v.fn, join_grid, 128, 0, stream, pdl, a);
+                    if (e == cudaSuccess) ++*launches;
+                }
+        return e;
+    }
     const bool many = a.max_q > 1;
     for (const Variant &v : kVariants) {
         if (v.D != D || v.rows != p.rows || v.fp16 != fp16 || v.many != many) continue;
@@ -735,7 +768,7 @@ cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, 
         if (e != cudaSuccess) return e;
         ++*launches;
         if (p.chunks > 1) {
-            e = launch(v.join_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
+            e = launch(v.join_fn, join_grid, 128, 0, stream, pdl, a);
             if (e == cudaSuccess) ++*launches;
         }
         return e;
@@ -753,7 +786,11 @@ cudaError_t preload_attend_kernels() {
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
+    for (const JoinVariant &v : kJoins) {
+        const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e != cudaSuccess) return e;
+    }
+    return preload_attend_tc_kernels();
 }
 
 }  // namespace kvb

@@ -1,0 +1,655 @@
+// kvb_attend_tc.cu -- attention of many new tokens (a prompt chunk) over one
+// layer of a 4-bit pool, on the fifth-generation tensor cores.
+//
+// A block takes 256 query rows (new tokens x the group of one KV head) as two
+// tiles of 128, and walks the cached tokens 128 at a time.  Warps have roles:
+//   4 warps  unpack keys and values to fp16 in shared memory (swizzled tiles)
+//   1 warp   issues tcgen05.mma: scores S = Q K^T and sums O += P V
+//   4 + 4    softmax of the two tiles, one row a thread: scores come from tensor
+//            memory, probabilities go back there as fp16, the A operand of P V
+// While one tile's softmax runs, the other's products do.  Tensor memory holds
+// S0, S1 (128 columns each; P overwrites S) and O0, O1 (D columns each).
+//
+// Range.  fp16 operands stay in range for any input by exact powers of two: steps
+// of the keys and values of each group of 32 are scaled by the largest step
+// of the request (a pass over the scale words finds it), queries take the key
+// groups' powers in exchange, and each query row is brought near 2^9.  What is
+// rounded: a key or value once (2^-12), a probability once.
+#include "kvb_vec.h"
+#include "kvb_vec_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace kvb {
+
+namespace {
+
+constexpr int kTileQ = 128, kTileK = 128;
+constexpr int kRowsTc = 2 * kTileQ;
+constexpr int kSoftWarps = 8, kUnpackWarps = 4;
+constexpr int kThreadsTc = 32 * (kSoftWarps + kUnpackWarps + 1);
+constexpr float kNoMaxTc = -3.0e38f;
+constexpr uint32_t kBlockBytes = 128 * 128;   // 128 rows of 64 fp16, 128-byte swizzle
+
+__host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
+// Q0, Q1, K x 2, V x 2, and 1 KiB to align
+__host__ __device__ constexpr int smem_tc(int D) { return 6 * blocks_of(D) * (int)kBlockBytes + 1024; }
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits until the phase of this parity is complete.  Every wait ends: after
+// about two seconds, or once another warp gave up, it returns false.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+    uint32_t done = 0;
+    long long start = 0;
+    for (uint32_t n = 0;; ++n) {
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+        if ((n & 255u) == 255u) {
+            const long long now = clock64();
+            if (start == 0) start = now;
+            if (*gave_up != 0) return false;
+            if (now - start > 4000000000ll) {
+                *gave_up = 1;
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.  Rows of
+// a K-major operand repeat every 8 rows (`stride`); of a MN-major operand
+// every 8 values of k (`stride`) and every 64 values of the other dimension (`lead`).
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+
+// Instruction descriptor: fp16 operands, float32 sums, M = 128.
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn_major) {
+    return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 | (uint32_t)(128 / 16) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t h2_bits(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// Place of 16 bytes (8 values from dim 8 chunk) of `row` in a swizzled tile.
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, uint32_t row, uint32_t chunk) {
+    return tile + (chunk >> 3) * kBlockBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+// The exponent of a largest step as a power of two (and its inverse); 1 for none.
+__device__ __forceinline__ float pow2_of(uint32_t most) {
+    return most == 0 ? 1.0f : __uint_as_float(most & 0x7f800000u);
+}
+
+struct SharedTc {
+    unsigned long long bars[16];
+    uint32_t tmem;
+    int gave_up, value_nan;
+    uint32_t most[2][4];     // largest steps of keys and values, a group each (as bits)
+};
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int NG = D / 32, NB = blocks_of(D);
+    constexpr uint32_t kTileBytes = NB * kBlockBytes;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ SharedTc sh;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q_tile[2] = {base, base + kTileBytes};
+    const uint32_t k_tile = base + 2 * kTileBytes, v_tile = base + 4 * kTileBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t bars = smem_u32(sh.bars);
+    const uint32_t k_full = bars, k_free = bars + 16, v_full = bars + 32, v_free = bars + 48,
+                   s_full = bars + 64, p_full = bars + 80, o_full = bars + 96;
+
+    const int H = (int)a.pool.H, group = (int)a.group;
+    int bx = blockIdx.x;
+    const int head = bx % H;
+    bx /= H;
+    // tiles of the last rows see most: they go first
+    const int rt = (int)a.row_tiles - 1 - bx % (int)a.row_tiles;
+    const int ci = bx / (int)a.row_tiles;
+    const int r = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    bool bad;
+    const Span s = row_span(a.q_start[r], a.q_start[r + 1], a.lens[r], (int)a.tokens, (int)a.max_q,
+                            (int)a.max_len, group, (int)a.window, rt, kRowsTc, &bad);
+    if (bad && a.status != nullptr && tid == 0 && blockIdx.x == 0) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+    const int row0 = rt * kRowsTc, rows = min(kRowsTc, s.n * group - row0);
+    if (rows <= 0) return;
+    const int c0 = s.lo + ci * (int)a.chunk, c1 = min(s.hi, c0 + (int)a.chunk);
+    if (c0 >= c1 && ci > 0) return;
+    const bool whole = s.hi - s.lo <= (int)a.chunk;
+    const int tiles = c1 > c0 ? (c1 - c0 + kTileK - 1) / kTileK : 0;
+    const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
+    const int64_t head_off = (int64_t)head * a.pool.s_head;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(k_full + 8 * i, 32 * kUnpackWarps);
+            bar_init(v_full + 8 * i, 32 * kUnpackWarps);
+            bar_init(k_free + 8 * i, 1);
+            bar_init(v_free + 8 * i, 1);
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_full + 8 * i, kTileQ);
+        }
+        bar_init(o_full, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.gave_up = 0;
+        sh.value_nan = 0;
+        for (int i = 0; i < 8; ++i) sh.most[i / 4][i % 4] = 0;
+    }
+    if (warp == kSoftWarps + kUnpackWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    // The largest step of each group among the tokens this block reads.
+    {
+        uint32_t most[2][NG];
+#pragma unroll
+        for (int i = 0; i < 2 * NG; ++i) most[i / NG][i % NG] = 0;
+#pragma unroll 4
+        for (int t = c0 + tid; t < c1; t += kThreadsTc) {
+            bool wrong;
+            const int64_t off = token_offset(a.pool, table, (uint32_t)t, &wrong);
+            if (wrong) continue;
+#pragma unroll
+            for (int comp = 0; comp < 2; ++comp) {
+                const uint64_t at = a.pool.base[comp] + off + head_off + D / 2;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(at + gr * 4) & ~15u;
+                    if (w < 0x7f800000u) most[comp][gr] = max(most[comp][gr], w);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * NG; ++i) {
+            const uint32_t w = __reduce_max_sync(0xffffffffu, most[i / NG][i % NG]);
+            if (lane == 0 && w != 0) atomicMax(&sh.most[i / NG][i % NG], w);
+        }
+    }
+    __syncthreads();
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------------------ softmax
+        const int q = warp >> 2, row = (warp & 3) * 32 + lane;      // tile and row of it
+        const int at = row0 + q * kTileQ + row;                     // row of the request
+        const bool on = q * kTileQ + row < rows;
+        const int i = on ? at / group : 0, j = on ? at - i * group : 0;
+        const int64_t tok = s.q0 + i;
+        const int qh = head * group + j;
+        const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+        float kf[NG];
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) kf[gr] = pow2_of(sh.most[0][gr]) * sign;
+        // this thread's query row, scaled, to shared memory
+        float sc;
+        {
+            const uint64_t src = a.q.data + tok * a.q.s_tok + (int64_t)qh * a.q.s_head;
+            float top = 0.0f;
+            auto value = [&](uint32_t w, int hi) {
+                if (kHalf) return __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xffffu)));
+                return __uint_as_float(hi ? w & 0xffff0000u : w << 16);
+            };
+            for (int ch = 0; ch < D / 8; ++ch) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (on) u = *reinterpret_cast<const uint4 *>(src + ch * 16);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                const float k = fabsf(kf[0]);
+                float f = k;
+#pragma unroll
+                for (int gr = 1; gr < NG; ++gr) f = ch / 4 == gr ? fabsf(kf[gr]) : f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(w[e / 2], e & 1)) * f);
+            }
+            const uint32_t ex = __float_as_uint(top) >> 23;
+            const bool scaled = ex >= 10 && ex < 255;
+            const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f;
+            sc = (scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f) * fabsf(a.scale_log2);
+            for (int ch = 0; ch < D / 8; ++ch) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (on) u = *reinterpret_cast<const uint4 *>(src + ch * 16);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                float f = kf[0];
+#pragma unroll
+                for (int gr = 1; gr < NG; ++gr) f = ch / 4 == gr ? kf[gr] : f;
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = h2_bits(value(w[e], 0) * f * up, value(w[e], 1) * f * up);
+                sts16(tile_at(q_tile[q], row, ch), make_uint4(h[0], h[1], h[2], h[3]));
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bar_arrive(p_full + 8 * q);          // phase 0 of p_full: the queries are there
+
+        const int pos = s.len - s.n + i;
+        const int lim = on ? min(pos, c1 - 1) : -1;                 // sees tokens low..lim
+        const int low = a.window ? max(0, pos - (int)a.window + 1) : 0;
+        const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+        const uint32_t sp = mine + q * 128, o = mine + 256 + q * D;
+        float m = kNoMaxTc, l = 0.0f;
+        bool alive = true;
+        for (int t = 0; t < tiles && alive; ++t) {
+            alive = bar_wait(s_full + 8 * q, t & 1, &sh.gave_up);
+            alive = __all_sync(0xffffffffu, alive);
+            if (!alive) break;
+            fence_after();
+            const int t0 = c0 + t * kTileK;
+            const bool inside = __all_sync(0xffffffffu, t0 >= low && t0 + kTileK - 1 <= lim);
+            float top = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t x[32];
+                tmem_ld32(sp + ch * 32, x);
+                tmem_ld_wait();
+                if (inside) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int tk = t0 + ch * 32 + e;
+                        if (tk >= low && tk <= lim) top = fmaxf(top, __uint_as_float(x[e]));
+                    }
+                }
+            }
+            __syncwarp();
+            top *= sc;
+            // the maximum moves when it is passed by more than 2^8; then the sums
+            // so far, O in tensor memory among them, are scaled down
+            float k = 1.0f;
+            if (m == kNoMaxTc) {
+                if (top > -INFINITY) m = top;
+            } else if (top > m + 8.0f) {
+                k = ex2(m - top);
+                m = top;
+                l *= k;
+            }
+            if (t > 0 && __any_sync(0xffffffffu, k != 1.0f)) {
+#pragma unroll 1
+                for (int ch = 0; ch < NG; ++ch) {
+                    uint32_t x[32];
+                    tmem_ld32(o + ch * 32, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
+                    tmem_st16(o + ch * 32, x);
+                    tmem_st16(o + ch * 32 + 16, x + 16);
+                }
+                tmem_st_wait();
+            }
+            __syncwarp();
+            const float less = m == kNoMaxTc ? 0.0f : -m;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t x[32], p[16];
+                tmem_ld32(sp + ch * 32, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float u = __uint_as_float(x[e]) * sc + less, v = __uint_as_float(x[e + 1]) * sc + less;
+                    if (!inside) {
+                        const int tk = t0 + ch * 32 + e;
+                        if (tk < low || tk > lim) u = -INFINITY;
+                        if (tk + 1 < low || tk + 1 > lim) v = -INFINITY;
+                    }
+                    u = ex2(u);
+                    v = ex2(v);
+                    l += u + v;
+                    p[e / 2] = h2_bits(u, v);
+                }
+                tmem_st16(sp + ch * 16, p);
+            }
+            tmem_st_wait();
+            fence_before();
+            bar_arrive(p_full + 8 * q);
+        }
+        if (tiles > 0) alive = __all_sync(0xffffffffu, alive && bar_wait(o_full, 0, &sh.gave_up));
+        fence_after();
+        // a value that is not finite: groups of the row's tokens that hold one
+        uint32_t nan_groups = alive ? 0u : 0xffu;
+        if (alive && sh.value_nan != 0)
+            for (int t = max(c0, low); t <= lim; ++t) {
+                bool wrong;
+                const int64_t off = token_offset(a.pool, table, (uint32_t)t, &wrong);
+                if (wrong) continue;
+                for (int gr = 0; gr < NG; ++gr)
+                    if (*reinterpret_cast<const uint32_t *>(a.pool.base[1] + off + head_off + D / 2 + gr * 4) >=
+                        0x7f800000u)
+                        nan_groups |= 1u << gr;
+            }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const int64_t part = ((int64_t)ci * a.tokens + tok) * a.q_heads + qh;
+#pragma unroll 1
+        for (int ch = 0; ch < NG; ++ch) {
+            uint32_t x[32];
+            if (tiles > 0 && alive) {
+                tmem_ld32(o + ch * 32, x);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = 0;
+            }
+            if (on) {
+                const float f = pow2_of(sh.most[1][ch]);
+                if (nan_groups >> ch & 1)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = kNanWord;
+                if (l == 0.0f && alive)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0;
+                if (whole) {
+                    const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head + ch * 64;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float u = __uint_as_float(x[e + 2 * b]) * f * inv;
+                            const float v = __uint_as_float(x[e + 2 * b + 1]) * f * inv;
+                            if (kHalf) {
+                                h[b] = h2_bits(u, v);
+                            } else {
+                                __nv_bfloat162 w = __floats2bfloat162_rn(u, v);
+                                h[b] = *reinterpret_cast<uint32_t *>(&w);
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(dst + e * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                } else {
+                    float *dst = a.part_o + part * D + ch * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(dst + e) =
+                            make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f,
+                                        __uint_as_float(x[e + 2]) * f, __uint_as_float(x[e + 3]) * f);
+                }
+            }
+            __syncwarp();
+        }
+        if (on && whole && a.lse != nullptr)
+            a.lse[tok * a.q_heads + qh] =
+                !alive ? __uint_as_float(kNanWord)
+                       : l != 0.0f ? ((m == kNoMaxTc ? 0.0f : m) + log2f(l)) * 0.693147180559945f : -INFINITY;
+        if (on && !whole)
+            *reinterpret_cast<float2 *>(a.part_ml + part * 2) =
+                make_float2(m == kNoMaxTc ? 0.0f : m, alive ? l : __uint_as_float(kNanWord));
+        fence_before();
+    } else if (warp < kSoftWarps + kUnpackWarps) {
+        // ------------------------------------------------- unpack to fp16 tiles
+        // A thread takes NG groups of 32 values of a tile; loads run half a tile ahead.
+        const int d = tid - 32 * kSoftWarps;
+        float f[2][NG];                       // 1 / the powers of this thread's groups
+#pragma unroll
+        for (int it = 0; it < NG; ++it) {
+            const int gr = (d + 128 * it) % NG;
+            f[0][it] = 1.0f / pow2_of(sh.most[0][gr]);
+            f[1][it] = 1.0f / pow2_of(sh.most[1][gr]);
+        }
+        int64_t off[NG];
+        uint4 code[2][NG];
+        uint32_t word[2][NG];
+        bool outside = false;
+        auto find = [&](int t) {
+#pragma unroll
+            for (int it = 0; it < NG; ++it) {
+                const int idx = d + 128 * it, tk = c0 + t * kTileK + idx / NG;
+                bool wrong = false;
+                off[it] = -1;                 // past the end: zeros
+                if (t < tiles && tk < c1) {
+                    off[it] = token_offset(a.pool, table, (uint32_t)tk, &wrong);
+                    if (wrong) off[it] = -2;  // keys NaN
+                    outside |= wrong;
+                }
+            }
+        };
+        auto fetch = [&](int comp) {
+#pragma unroll
+            for (int it = 0; it < NG; ++it) {
+                const int gr = (d + 128 * it) % NG;
+                code[comp][it] = make_uint4(0, 0, 0, 0);
+                word[comp][it] = off[it] == -2 && comp == 0 ? kNanWord : 0u;
+                if (off[it] >= 0) {
+                    const uint64_t at = a.pool.base[comp] + off[it] + head_off;
+                    code[comp][it] = *reinterpret_cast<const uint4 *>(at + gr * 16);
+                    word[comp][it] = *reinterpret_cast<const uint32_t *>(at + D / 2 + gr * 4);
+                }
+            }
+        };
+        auto put = [&](int comp, uint32_t tile) {
+            const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
+#pragma unroll
+            for (int it = 0; it < NG; ++it) {
+                const int idx = d + 128 * it, tk = idx / NG, gr = idx % NG;
+                uint32_t w = word[comp][it];
+                if (comp == 1 && w >= 0x7f800000u) {
+                    w = 0;                    // kept out of the products; the softmax warps see to it
+                    sh.value_nan = 1;
+                }
+                const float step = q4_step(w) * f[comp][it];
+                const float hi = __half2float(__float2half_rn(step));
+                const __half2 s1 = __float2half2_rn(hi), s0 = __float2half2_rn(step - hi);
+                // 1024 + z and 64 + z as fp16 pairs
+                const uint32_t zz = (w & 15u) * 0x00010001u;
+                uint32_t za = zz | 0x64006400u, zb = (zz << 4) | 0x54005400u;
+                const __half2 z1 = *reinterpret_cast<__half2 *>(&za), z16 = *reinterpret_cast<__half2 *>(&zb);
+                // lanes of groups 2 and 3 go through their words two apart from those of 0 and
+                // 1, so that 8 lanes' stores meet 8 different places of 16 bytes
+                const bool apart = (gr >> 1 & 1) != 0;
+                const uint4 u = code[comp][it];
+                const uint32_t cw[4] = {apart ? u.z : u.x, apart ? u.w : u.y, apart ? u.x : u.z,
+                                        apart ? u.y : u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // nibbles e and e + 4 meet in a pair: values are put in order by a byte pick
+                    const uint32_t v = cw[i] >> 8;
+                    uint32_t t[4] = {(cw[i] & 0x000f000fu) | 0x64006400u, (cw[i] & 0x00f000f0u) | 0x64006400u,
+                                     (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        __half2 x = *reinterpret_cast<__half2 *>(&t[e]);
+                        x = e & 1 ? __hfma2(x, k16, __hneg2(z16)) : __hsub2(x, z1);    // code - z, exact
+                        x = __hfma2(x, s1, __hmul2(x, s0));
+                        y[e] = *reinterpret_cast<uint32_t *>(&x);
+                    }
+                    const uint4 out = make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                                                 __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
+                    sts16(tile_at(tile, tk, gr * 4 + (i ^ (apart ? 2 : 0))), out);
+                }
+            }
+        };
+        bool alive = true;
+        find(0);
+        fetch(0);
+        for (int t = 0; t < tiles; ++t) {
+            const uint32_t st = t & 1, free_parity = ((t >> 1) & 1) ^ 1;
+            fetch(1);
+            if (!(alive = bar_wait(k_free + 8 * st, free_parity, &sh.gave_up))) break;
+            put(0, k_tile + st * kTileBytes);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            bar_arrive(k_full + 8 * st);
+            find(t + 1);
+            fetch(0);
+            if (!(alive = bar_wait(v_free + 8 * st, free_parity, &sh.gave_up))) break;
+            put(1, v_tile + st * kTileBytes);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            bar_arrive(v_full + 8 * st);
+        }
+        if (outside && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+    } else if (lane == 0) {
+        // ------------------------------------------------------------ products
+        constexpr uint32_t kScores = idesc(kTileK, false), kSums = idesc(D, true);
+        bool alive = true;
+        auto scores = [&](int q, int t) {
+            const uint32_t kt = k_tile + (t & 1) * kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t in = (ks >> 2) * kBlockBytes + (ks & 3) * 32;
+                mma_ss(tmem + q * 128, desc(q_tile[q] + in, 16, 1024), desc(kt + in, 16, 1024), kScores, ks != 0);
+            }
+            commit(s_full + 8 * q);
+        };
+        auto sums = [&](int q, int t) {
+            const uint32_t vt = v_tile + (t & 1) * kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < kTileK / 16; ++ks)
+                mma_ts(tmem + 256 + q * D, tmem + q * 128 + ks * 8, desc(vt + ks * 2048, kBlockBytes, 1024), kSums,
+                       t != 0 || ks != 0);
+        };
+        if (tiles > 0) {
+            alive = bar_wait(k_full, 0, &sh.gave_up);
+            for (int q = 0; q < 2 && alive; ++q) {
+                alive = bar_wait(p_full + 8 * q, 0, &sh.gave_up);   // queries in place
+                fence_after();
+                if (alive) scores(q, 0);
+            }
+            if (alive) commit(k_free);
+            for (int t = 0; t < tiles && alive; ++t) {
+                if (t + 1 < tiles)
+                    alive = bar_wait(k_full + 8 * ((t + 1) & 1), ((t + 1) >> 1) & 1, &sh.gave_up);
+                alive = alive && bar_wait(v_full + 8 * (t & 1), (t >> 1) & 1, &sh.gave_up);
+                for (int q = 0; q < 2 && alive; ++q) {
+                    alive = bar_wait(p_full + 8 * q, (t + 1) & 1, &sh.gave_up);
+                    if (!alive) break;
+                    fence_after();
+                    sums(q, t);
+                    if (t + 1 < tiles) scores(q, t + 1);
+                }
+                if (!alive) break;
+                commit(v_free + 8 * (t & 1));
+                if (t + 1 < tiles) commit(k_free + 8 * ((t + 1) & 1));
+            }
+            // all products done: the end of the work, or of what was begun when a wait gave up
+            commit(o_full);
+            int never = 0;
+            bar_wait(o_full, 0, &never);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (sh.gave_up != 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_GAVE_UP);
+    if (warp == kSoftWarps + kUnpackWarps)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+typedef void(AttendTcFn)(AttendArgs);
+struct VariantTc {
+    uint32_t D;
+    bool fp16;
+    AttendTcFn *fn;
+    int smem;
+};
+template <int D, bool kHalf>
+constexpr VariantTc variant_tc() {
+    return VariantTc{(uint32_t)D, kHalf, kv_attend_tc_kernel<D, kHalf>, smem_tc(D)};
+}
+const VariantTc kVariantsTc[] = {variant_tc<64, false>(),  variant_tc<64, true>(),  variant_tc<96, false>(),
+                                 variant_tc<96, true>(),   variant_tc<128, false>(), variant_tc<128, true>()};
+
+}  // namespace
+
+cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
+                             cudaStream_t stream) {
+    for (const VariantTc &v : kVariantsTc) {
+        if (v.D != D || v.fp16 != fp16) continue;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.pool.H * p.row_tiles * p.chunks, a.requests);
+        cfg.blockDim = dim3(kThreadsTc);
+        cfg.dynamicSmemBytes = (size_t)v.smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, v.fn, a);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t preload_attend_tc_kernels() {
+    cudaFuncAttributes at;
+    for (const VariantTc &v : kVariantsTc) {
+        cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute((const void *)v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvb

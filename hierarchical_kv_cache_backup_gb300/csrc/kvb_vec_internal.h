@@ -17,6 +17,7 @@ cudaError_t preload_vector_kernels();
 // along the tokens of one request, query rows a block takes, and workspace.
 struct AttendPlan {
     uint32_t rows, row_tiles, chunk, chunks;
+    bool many;             // the kernel for many query rows (kvb_attend_tc.cu)
     uint64_t bytes;
 };
 AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
@@ -24,6 +25,9 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
 cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
                           cudaStream_t stream, int *launches);
 cudaError_t preload_attend_kernels();
+cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
+                             cudaStream_t stream);
+cudaError_t preload_attend_tc_kernels();
 
 // Handle checks of one operator call on a pool (CLOSED / STALE), its device
 // made ready, and the end of a run of overlapped restores on `stream`.

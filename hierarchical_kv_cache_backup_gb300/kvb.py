@@ -47,7 +47,7 @@ KV_CACHE_SAME, KV_CACHE_E4M3, KV_CACHE_Q4 = 0, 1, 2
 KV_ROTARY_HALF, KV_ROTARY_INTERLEAVED = 0, 1
 KV_ROTARY_PLAIN, KV_ROTARY_LINEAR, KV_ROTARY_NTK, KV_ROTARY_YARN, KV_ROTARY_BANDS = 0, 1, 2, 3, 4
 KV_ROTATE_INVERSE = 1
-KV_STATUS_BAD_SLOT, KV_STATUS_BAD_PAGE, KV_STATUS_BAD_LENGTH = 1, 2, 4
+KV_STATUS_BAD_SLOT, KV_STATUS_BAD_PAGE, KV_STATUS_BAD_LENGTH, KV_STATUS_GAVE_UP = 1, 2, 4, 8
 KVB_IPC_MAGIC = 0x4B564231
 KVB_IPC_MAGIC_SPLIT = 0x4B564253
 

@@ -460,6 +460,7 @@ KVB_API kv_status kv_backup_staged_noalloc(kv_pool pool, kv_host host, const int
 #define KV_STATUS_BAD_SLOT 1u     /* slot outside [-1, P x T)                       */
 #define KV_STATUS_BAD_PAGE 2u     /* page id outside [0, P) inside a request's length */
 #define KV_STATUS_BAD_LENGTH 4u   /* length or q_start outside what the block allows */
+#define KV_STATUS_GAVE_UP 8u      /* a wait inside a kernel ran out (2 s): outputs are NaN */
 
 typedef enum { KV_BF16 = 0, KV_FP16 = 1 } kv_dtype;   /* type of x, q, k, v, out  */
 

@@ -475,7 +475,9 @@ class Batch:
         of absolute products leaves room for truncating adders), the argument and the result of
         exp2 2^-22 of |x| and of 1; so a weight is off by dx and out by 2 dx max|v|.  Weights times
         steps rounded to fp16: 2^-11 of each |p step (code - 8)|, and 2^-24 of the largest step a
-        token for those below fp16's normal range.  Then one rounding to the output's type."""
+        token for those below fp16's normal range.  Then one rounding to the output's type.
+        With many query rows a request the tensor-core kernel runs, which also rounds every key
+        and value to fp16 (2^-11 each), and a query to 2^-22 of the row's largest |q| x step."""
         q = (self.q if q is None else q).double().cpu().numpy()
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
         at = 0
@@ -498,6 +500,11 @@ class Batch:
                     tol = half_step(self.dt) * np.abs(want[:, j]) * (1 + 2 ** -7)
                     tol = tol + 2.0 ** -11 * (w[j] @ (s[:, h] * np.abs(c[:, h] - 8)))
                     tol = tol + 2.0 ** -24 * 8 * self.lens[i] * s[:, h].max(0)[None] / np.maximum(1, 1)
+                    if self.dim <= 128 and max(self.n_q) * self.group >= 64:
+                        both = np.abs(qi[:, j])[:, None] * np.abs(k[None, :, h])
+                        dx = dx + self.scale * 2.0 ** -11 * both.sum(2).max(1)
+                        dx = dx + self.scale * 2.0 ** -22 * 16 * self.dim * (np.abs(qi[:, j])[:, None] * ks[None, :, h]).max((1, 2))
+                        tol = tol + 2.0 ** -11 * (w[j] @ np.abs(v[:, h]))
                     tol = tol + 2 * dx[:, None] * vmax[None] + (2.0 ** -24 if self.dt == torch.float16 else 0)
                     err = np.abs(out[at:at + n, j] - want[:, j])
                     ok = ~seen | (err <= tol).all(1)
@@ -593,6 +600,114 @@ def test_attend_step_sizes_that_rise_late():
         b.pool.alloc.copy_(torch.from_numpy(raw))
         out, lse, _ = b.run()
         b.check(out, lse)
+
+
+# The kernel for many query rows: 256 rows a block, 128 cached tokens at a time.
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,H,group,n_q,lens", [
+    (128, 1, 4, [64], [64]), (128, 2, 1, [128, 65, 0], [128, 129, 5]), (64, 3, 8, [33, 8], [500, 8]),
+    (96, 1, 5, [40, 13], [257, 13]), (128, 1, 16, [8, 8, 8], [300, 127, 4]), (64, 1, 2, [300], [1100]),
+    (128, 1, 3, [43], [129])])
+@pytest.mark.parametrize("page", [dict(T=16, page_first=False, hnd=False), dict(T=17, page_first=True, hnd=True, offset=48),
+                                  dict(T=64, page_first=False, hnd=True, split=True)])
+def test_attend_many_rows(dtype, dim, H, group, n_q, lens, page):
+    with Batch(lens, n_q, H, group, dim, dtype=dtype, **page) as b:
+        out, lse, status = b.run()
+        b.check(out, lse)
+        assert status == 0
+
+
+@pytest.mark.parametrize("window", [1, 5, 100, 129])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_many_rows_window(window, dim):
+    with Batch([400, 70, 0], [90, 70, 20], 1, 4, dim, 16, "bf16", window) as b:
+        out, lse, status = b.run()
+        b.check(out, lse)
+        assert status == 0
+
+
+def test_attend_many_rows_cut_and_joined():
+    with Batch([6000, 100, 5500], [20, 3, 20], 1, 4, 128, 32, "bf16") as b:
+        assert b.args().workspace_bytes > 0
+        out, lse, status = b.run()
+        b.check(out, lse)
+        first = out.clone()
+        out, _, _ = b.run()
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("k_mul,v_mul", [(40.0, None), (1e-6, None), (1.0, [1e-20, 1.0, 1e20, 1e4]),
+                                         (1.0, [1e-25, 1e-25, 3e-20, 1e30])])
+def test_attend_many_rows_ranges(k_mul, v_mul):
+    with Batch([257, 70], [30, 20], 1, 4, 128, 16, "bf16", k_mul=k_mul, v_mul=v_mul) as b:
+        out, lse, status = b.run()
+        b.check(out, lse)
+
+
+@pytest.mark.parametrize("sign", [-1.0, 0.0])
+@pytest.mark.parametrize("n_q", [2, 40])
+def test_attend_scale_signs(sign, n_q):
+    with Batch([257], [n_q], 1, 4, 128, 16, "bf16") as b:
+        b.scale *= sign
+        out, lse, _ = b.run()
+        b.scale = abs(b.scale)             # the tolerances go by its size; 0 is a plain mean
+        if sign:
+            q = -b.q
+            want, _, _ = b.run(q=q)
+            assert torch.equal(out, want)
+        else:
+            v = vec_ref.q4_decode(b.kv[0][1], 128)
+            pos = 257 - n_q + np.arange(n_q)
+            want = np.stack([v[:p + 1, 0].mean(0) for p in pos])[:, None]
+            # rounding: 2^-8 of the result, 2^-10 of the mean size of a value
+            assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * np.abs(v).mean())
+
+
+@pytest.mark.parametrize("comp,groups", [(0, [0]), (1, [0]), (1, [1, 3]), (1, [0, 1, 2, 3])])
+def test_attend_many_rows_nan_behind_the_mask(comp, groups):
+    """A NaN among the keys makes every value NaN of the queries that see it; a NaN group among
+    the values, those of that group."""
+    with Batch([60, 60], [40, 40], 1, 2, 128, 16, "bf16", window=30) as b:
+        x = np.zeros((1, 128), np.float32)
+        for g in groups:
+            x[:, 32 * g:32 * g + 32] = np.nan
+        poke(b, 0, 57, comp, vec_ref.q4_encode(x))     # new token 37: seen by 37, 38, 39
+        poke(b, 1, 5, comp, vec_ref.q4_encode(x))      # seen up to position 34: new tokens 0..14
+        out, _, _ = b.run()
+        out = out.clone()
+        nan = torch.isnan(out.float())
+        seen = torch.zeros(80, dtype=torch.bool, device="cuda")
+        seen[37:40], seen[40:55] = True, True
+        want_nan = torch.zeros_like(nan)
+        cols = range(128) if comp == 0 else [32 * g + e for g in groups for e in range(32)]
+        want_nan[:, :, list(cols)] = seen[:, None, None]
+        assert torch.equal(nan, want_nan)
+        want, _, _ = b_without(b)
+        assert torch.equal(out[~seen], want[~seen])
+
+
+def test_attend_many_rows_query_nan_stays_in_its_row():
+    with Batch([300], [70], 1, 2, 128, 16, "bf16") as b:
+        out, _, _ = b.run()
+        want = out.clone()
+        q = b.q.clone()
+        q[1, 1, 5], q[69, 0, 9] = float("nan"), float("inf")
+        out, _, _ = b.run(q=q)
+        bad = torch.isnan(out.float()).all(-1)
+        assert bad.nonzero().tolist() == [[1, 1], [69, 0]]
+        assert torch.equal(out[~bad], want[~bad])
+
+
+def test_attend_many_rows_bad_pages():
+    with Batch([200, 200, 50], [40, 40, 10], 1, 2, 64, 16, "bf16", window=60) as b:
+        b.table[0, 1] = b.pool.P            # tokens 16..31: outside every window
+        b.table[1, 9] = -1                  # tokens 144..159: positions 144..218, all but none of 160..199
+        b.table[2, 9] = 2 ** 31 - 1         # past its length
+        out, lse, status = b.run()
+        assert status == kvb.KV_STATUS_BAD_PAGE
+        assert torch.isnan(out[40:80].float()).all() and torch.isnan(lse[40:80]).all()
+        b.check(out, lse, requests=(0, 2))
 
 
 def poke(b, i, token, comp, raw_vec):
