@@ -128,12 +128,36 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// two float32 at a time
+__device__ __forceinline__ unsigned long long pair(uint32_t lo, uint32_t hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
 
-// Place of 16 bytes (8 values from dim 8 chunk) of `row` in a swizzled tile.
+// Place of 16 bytes (8 values from dim 8 chunk) of `row` in a swizzled tile.  The
+// values of a chunk stand in the order 0 4 1 5 2 6 3 7 in every tile, as the
+// codes unpack: keys and queries agree, and the sums' columns are put right when
+// they are read.
 __device__ __forceinline__ uint32_t tile_at(uint32_t tile, uint32_t row, uint32_t chunk) {
     return tile + (chunk >> 3) * kBlockBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
@@ -286,7 +310,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 for (int gr = 1; gr < NG; ++gr) f = ch / 4 == gr ? kf[gr] : f;
                 uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = h2_bits(value(w[e], 0) * f * up, value(w[e], 1) * f * up);
+                for (int e = 0; e < 4; ++e)
+                    h[e] = h2_bits(value(w[e / 2], e & 1) * f * up, value(w[2 + e / 2], e & 1) * f * up);
                 sts16(tile_at(q_tile[q], row, ch), make_uint4(h[0], h[1], h[2], h[3]));
             }
         }
@@ -307,22 +332,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             fence_after();
             const int t0 = c0 + t * kTileK;
             const bool inside = __all_sync(0xffffffffu, t0 >= low && t0 + kTileK - 1 <= lim);
+            // Each load from tensor memory runs while the one before is worked on.
+            uint32_t x[2][32];
             float top = -INFINITY;
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t x[32];
-                tmem_ld32(sp + ch * 32, x);
-                tmem_ld_wait();
+            auto most_of = [&](const uint32_t *y, int ch) {
+                float u = -INFINITY, v = -INFINITY;
                 if (inside) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                    for (int e = 0; e < 32; e += 4) {
+                        u = fmaxf(fmaxf(u, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
+                        v = fmaxf(fmaxf(v, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int tk = t0 + ch * 32 + e;
-                        if (tk >= low && tk <= lim) top = fmaxf(top, __uint_as_float(x[e]));
+                        if (tk >= low && tk <= lim) u = fmaxf(u, __uint_as_float(y[e]));
                     }
                 }
+                top = fmaxf(top, fmaxf(u, v));
+            };
+            tmem_ld32(sp, x[0]);
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ch += 2) {
+                tmem_ld_wait();
+                tmem_ld32(sp + ch * 32 + 32, x[1]);
+                most_of(x[0], ch);
+                tmem_ld_wait();
+                tmem_ld32(sp + (ch * 32 + 64 & 127), x[0]);     // in the end: the first again
+                most_of(x[1], ch + 1);
             }
             __syncwarp();
             top *= sc;
@@ -339,38 +377,47 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             if (t > 0 && __any_sync(0xffffffffu, k != 1.0f)) {
 #pragma unroll 1
                 for (int ch = 0; ch < NG; ++ch) {
-                    uint32_t x[32];
-                    tmem_ld32(o + ch * 32, x);
+                    tmem_ld32(o + ch * 32, x[1]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * k);
-                    tmem_st16(o + ch * 32, x);
-                    tmem_st16(o + ch * 32 + 16, x + 16);
+                    for (int e = 0; e < 32; ++e) x[1][e] = __float_as_uint(__uint_as_float(x[1][e]) * k);
+                    tmem_st16(o + ch * 32, x[1]);
+                    tmem_st16(o + ch * 32 + 16, x[1] + 16);
                 }
                 tmem_st_wait();
             }
             __syncwarp();
             const float less = m == kNoMaxTc ? 0.0f : -m;
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t x[32], p[16];
-                tmem_ld32(sp + ch * 32, x);
-                tmem_ld_wait();
+            const unsigned long long sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
+            const unsigned long long less2 = pair(__float_as_uint(less), __float_as_uint(less));
+            unsigned long long sum = 0;
+            auto weights_of = [&](const uint32_t *y, int ch) {
+                uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float u = __uint_as_float(x[e]) * sc + less, v = __uint_as_float(x[e + 1]) * sc + less;
+                    float2 u = unpair(fma2(pair(y[e], y[e + 1]), sc2, less2));
                     if (!inside) {
                         const int tk = t0 + ch * 32 + e;
-                        if (tk < low || tk > lim) u = -INFINITY;
-                        if (tk + 1 < low || tk + 1 > lim) v = -INFINITY;
+                        if (tk < low || tk > lim) u.x = -INFINITY;
+                        if (tk + 1 < low || tk + 1 > lim) u.y = -INFINITY;
                     }
-                    u = ex2(u);
-                    v = ex2(v);
-                    l += u + v;
-                    p[e / 2] = h2_bits(u, v);
+                    u.x = ex2(u.x);
+                    u.y = ex2(u.y);
+                    sum = add2(sum, pair(__float_as_uint(u.x), __float_as_uint(u.y)));
+                    p[e / 2] = h2_bits(u.x, u.y);
                 }
-                tmem_st16(sp + ch * 16, p);
+                tmem_st16(sp + ch * 16, p);     // over scores that have been read twice
+            };
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ch += 2) {
+                tmem_ld_wait();
+                tmem_ld32(sp + ch * 32 + 32, x[1]);
+                weights_of(x[0], ch);
+                tmem_ld_wait();
+                if (ch == 0) tmem_ld32(sp + 64, x[0]);
+                weights_of(x[1], ch + 1);
             }
+            l += unpair(sum).x + unpair(sum).y;
             tmem_st_wait();
             fence_before();
             bar_arrive(p_full + 8 * q);
@@ -416,8 +463,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                         uint32_t h[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const float u = __uint_as_float(x[e + 2 * b]) * f * inv;
-                            const float v = __uint_as_float(x[e + 2 * b + 1]) * f * inv;
+                            // dims 2 b and 2 b + 1 of the eight
+                            const float u = __uint_as_float(x[e + (b < 2 ? 4 * b : 4 * b - 7)]) * f * inv;
+                            const float v = __uint_as_float(x[e + (b < 2 ? 4 * b + 2 : 4 * b - 5)]) * f * inv;
                             if (kHalf) {
                                 h[b] = h2_bits(u, v);
                             } else {
@@ -431,9 +479,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                     float *dst = a.part_o + part * D + ch * 32;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
+                    {
+                        const int k = e / 8 * 8 + (e & 4 ? 1 : 0);
                         *reinterpret_cast<float4 *>(dst + e) =
-                            make_float4(__uint_as_float(x[e]) * f, __uint_as_float(x[e + 1]) * f,
-                                        __uint_as_float(x[e + 2]) * f, __uint_as_float(x[e + 3]) * f);
+                            make_float4(__uint_as_float(x[k]) * f, __uint_as_float(x[k + 2]) * f,
+                                        __uint_as_float(x[k + 4]) * f, __uint_as_float(x[k + 6]) * f);
+                    }
                 }
             }
             __syncwarp();
@@ -448,104 +499,98 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         fence_before();
     } else if (warp < kSoftWarps + kUnpackWarps) {
         // ------------------------------------------------- unpack to fp16 tiles
-        // A thread takes NG groups of 32 values of a tile; loads run half a tile ahead.
+        // A thread takes one group of every 128 / NP-th token of a tile: NP groups of
+        // 32 values.  Keys and values alternate through the same code; the loads of
+        // the next half tile are under way while this one is unpacked.
+        constexpr int NP = NG == 3 ? 4 : NG;
         const int d = tid - 32 * kSoftWarps;
-        float f[2][NG];                       // 1 / the powers of this thread's groups
+        const int gr = d % NP, tk0 = d / NP;                 // group; tokens tk0 + it * 128 / NP
+        const bool idle = gr >= NG;
+        const float f[2] = {1.0f / pow2_of(sh.most[0][idle ? 0 : gr]),
+                            1.0f / pow2_of(sh.most[1][idle ? 0 : gr])};
+        // Lanes of groups 2 and 3 go through their words two apart from those of 0 and
+        // 1, so that 8 lanes' stores meet 8 different places of 16 bytes.
+        const bool apart = (gr >> 1 & 1) != 0;
+        uint32_t to[4];
 #pragma unroll
-        for (int it = 0; it < NG; ++it) {
-            const int gr = (d + 128 * it) % NG;
-            f[0][it] = 1.0f / pow2_of(sh.most[0][gr]);
-            f[1][it] = 1.0f / pow2_of(sh.most[1][gr]);
+        for (int i = 0; i < 4; ++i) to[i] = tile_at(0, tk0, gr * 4 + (i ^ (apart ? 2 : 0)));
+        int64_t off[NP];
+        uint4 code[NP];
+        uint32_t word[NP];
+        bool outside = false, alive = true;
+        auto find = [&](int it, int t) {
+            const int tk = c0 + t * kTileK + tk0 + it * (128 / NP);
+            bool wrong = false;
+            off[it] = -1;                 // past the end: zeros
+            if (t < tiles && tk < c1 && !idle) {
+                off[it] = token_offset(a.pool, table, (uint32_t)tk, &wrong) + head_off;
+                if (wrong) off[it] = -2;  // keys NaN
+                outside |= wrong;
+            }
+        };
+        auto fetch = [&](int it, int comp) {
+            code[it] = make_uint4(0, 0, 0, 0);
+            word[it] = off[it] == -2 && comp == 0 ? kNanWord : 0u;
+            if (off[it] >= 0) {
+                const uint64_t at = a.pool.base[comp] + off[it];
+                code[it] = *reinterpret_cast<const uint4 *>(at + gr * 16);
+                word[it] = *reinterpret_cast<const uint32_t *>(at + D / 2 + gr * 4);
+            }
+        };
+#pragma unroll
+        for (int it = 0; it < NP; ++it) {
+            find(it, 0);
+            fetch(it, 0);
         }
-        int64_t off[NG];
-        uint4 code[2][NG];
-        uint32_t word[2][NG];
-        bool outside = false;
-        auto find = [&](int t) {
+        const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
+#pragma unroll 1
+        for (int half = 0; half < 2 * tiles; ++half) {
+            const int t = half >> 1, comp = half & 1;
+            const uint32_t st = t & 1;
+            alive = bar_wait((comp ? v_free : k_free) + 8 * st, ((t >> 1) & 1) ^ 1, &sh.gave_up);
+            if (!alive) break;
+            const uint32_t tile = (comp ? v_tile : k_tile) + st * kTileBytes;
 #pragma unroll
-            for (int it = 0; it < NG; ++it) {
-                const int idx = d + 128 * it, tk = c0 + t * kTileK + idx / NG;
-                bool wrong = false;
-                off[it] = -1;                 // past the end: zeros
-                if (t < tiles && tk < c1) {
-                    off[it] = token_offset(a.pool, table, (uint32_t)tk, &wrong);
-                    if (wrong) off[it] = -2;  // keys NaN
-                    outside |= wrong;
+            for (int it = 0; it < NP; ++it) {
+                uint32_t w = word[it];
+                const uint4 u = code[it];
+                if (comp == 0) {
+                    fetch(it, 1);
+                } else {
+                    find(it, t + 1);
+                    fetch(it, 0);
+                    if (w >= 0x7f800000u) {
+                        w = 0;            // kept out of the products; the softmax warps see to it
+                        sh.value_nan = 1;
+                    }
                 }
-            }
-        };
-        auto fetch = [&](int comp) {
-#pragma unroll
-            for (int it = 0; it < NG; ++it) {
-                const int gr = (d + 128 * it) % NG;
-                code[comp][it] = make_uint4(0, 0, 0, 0);
-                word[comp][it] = off[it] == -2 && comp == 0 ? kNanWord : 0u;
-                if (off[it] >= 0) {
-                    const uint64_t at = a.pool.base[comp] + off[it] + head_off;
-                    code[comp][it] = *reinterpret_cast<const uint4 *>(at + gr * 16);
-                    word[comp][it] = *reinterpret_cast<const uint32_t *>(at + D / 2 + gr * 4);
-                }
-            }
-        };
-        auto put = [&](int comp, uint32_t tile) {
-            const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
-#pragma unroll
-            for (int it = 0; it < NG; ++it) {
-                const int idx = d + 128 * it, tk = idx / NG, gr = idx % NG;
-                uint32_t w = word[comp][it];
-                if (comp == 1 && w >= 0x7f800000u) {
-                    w = 0;                    // kept out of the products; the softmax warps see to it
-                    sh.value_nan = 1;
-                }
-                const float step = q4_step(w) * f[comp][it];
+                // the step as two fp16 parts: a product is rounded once, by the sum with the first
+                const float step = q4_step(w) * (comp ? f[1] : f[0]);
                 const float hi = __half2float(__float2half_rn(step));
                 const __half2 s1 = __float2half2_rn(hi), s0 = __float2half2_rn(step - hi);
-                // 1024 + z and 64 + z as fp16 pairs
                 const uint32_t zz = (w & 15u) * 0x00010001u;
-                uint32_t za = zz | 0x64006400u, zb = (zz << 4) | 0x54005400u;
+                uint32_t za = zz | 0x64006400u, zb = (zz << 4) | 0xd400d400u;    // 1024 + z, -(64 + z)
                 const __half2 z1 = *reinterpret_cast<__half2 *>(&za), z16 = *reinterpret_cast<__half2 *>(&zb);
-                // lanes of groups 2 and 3 go through their words two apart from those of 0 and
-                // 1, so that 8 lanes' stores meet 8 different places of 16 bytes
-                const bool apart = (gr >> 1 & 1) != 0;
-                const uint4 u = code[comp][it];
                 const uint32_t cw[4] = {apart ? u.z : u.x, apart ? u.w : u.y, apart ? u.x : u.z,
                                         apart ? u.y : u.w};
+                if (!idle)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // nibbles e and e + 4 meet in a pair: values are put in order by a byte pick
-                    const uint32_t v = cw[i] >> 8;
-                    uint32_t t[4] = {(cw[i] & 0x000f000fu) | 0x64006400u, (cw[i] & 0x00f000f0u) | 0x64006400u,
-                                     (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
-                    uint32_t y[4];
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t v = cw[i] >> 8;
+                        uint32_t y[4] = {(cw[i] & 0x000f000fu) | 0x64006400u, (cw[i] & 0x00f000f0u) | 0x64006400u,
+                                         (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        __half2 x = *reinterpret_cast<__half2 *>(&t[e]);
-                        x = e & 1 ? __hfma2(x, k16, __hneg2(z16)) : __hsub2(x, z1);    // code - z, exact
-                        x = __hfma2(x, s1, __hmul2(x, s0));
-                        y[e] = *reinterpret_cast<uint32_t *>(&x);
+                        for (int e = 0; e < 4; ++e) {
+                            __half2 x = *reinterpret_cast<__half2 *>(&y[e]);
+                            x = e & 1 ? __hfma2(x, k16, z16) : __hsub2(x, z1);    // code - z, exact
+                            x = __hfma2(x, s1, __hmul2(x, s0));
+                            y[e] = *reinterpret_cast<uint32_t *>(&x);
+                        }
+                        sts16(tile + to[i] + it * (128 / NP) * 128, make_uint4(y[0], y[1], y[2], y[3]));
                     }
-                    const uint4 out = make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
-                                                 __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632));
-                    sts16(tile_at(tile, tk, gr * 4 + (i ^ (apart ? 2 : 0))), out);
-                }
             }
-        };
-        bool alive = true;
-        find(0);
-        fetch(0);
-        for (int t = 0; t < tiles; ++t) {
-            const uint32_t st = t & 1, free_parity = ((t >> 1) & 1) ^ 1;
-            fetch(1);
-            if (!(alive = bar_wait(k_free + 8 * st, free_parity, &sh.gave_up))) break;
-            put(0, k_tile + st * kTileBytes);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive(k_full + 8 * st);
-            find(t + 1);
-            fetch(0);
-            if (!(alive = bar_wait(v_free + 8 * st, free_parity, &sh.gave_up))) break;
-            put(1, v_tile + st * kTileBytes);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive(v_full + 8 * st);
+            bar_arrive((comp ? v_full : k_full) + 8 * st);
         }
         if (outside && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
     } else if (lane == 0) {
