@@ -2,13 +2,16 @@
 // layer of a 4-bit pool, on the fifth-generation tensor cores.
 //
 // A block takes 256 query rows (new tokens x the group of one KV head) as two
-// tiles of 128, and walks the cached tokens 128 at a time.  Warps have roles:
+// tiles of 128, and walks the cached tokens 64 at a time.  Warps have roles:
 //   4 warps  unpack keys and values to fp16 in shared memory (swizzled tiles)
 //   1 warp   issues tcgen05.mma: scores S = Q K^T and sums O += P V
 //   4 + 4    softmax of the two tiles, one row a thread: scores come from tensor
 //            memory, probabilities go back there as fp16, the A operand of P V
-// While one tile's softmax runs, the other's products do.  Tensor memory holds
-// S0, S1 (128 columns each; P overwrites S) and O0, O1 (D columns each).
+// Tensor memory holds two buffers of 64 scores a row for each tile (P overwrites
+// S) and O0, O1 (D columns each).  With two buffers the scores of the next
+// cached tokens are there when a softmax warp is done with the ones before: with one
+// buffer of 128, each softmax waited for its own products, 370 us for 2 x 1,000
+// new tokens over 8,192 cached ones.
 //
 // Range.  fp16 operands stay in range for any input by exact powers of two: steps
 // of the keys and values of each group of 32 are scaled by the largest step
@@ -25,16 +28,19 @@ namespace kvb {
 
 namespace {
 
-constexpr int kTileQ = 128, kTileK = 128;
+constexpr int kTileQ = 128, kTileK = 64, kStagesTc = 4;
 constexpr int kRowsTc = 2 * kTileQ;
 constexpr int kSoftWarps = 8, kUnpackWarps = 4;
 constexpr int kThreadsTc = 32 * (kSoftWarps + kUnpackWarps + 1);
 constexpr float kNoMaxTc = -3.0e38f;
-constexpr uint32_t kBlockBytes = 128 * 128;   // 128 rows of 64 fp16, 128-byte swizzle
+// 64 fp16 (128 bytes, swizzled) of every row of a tile
+constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
-// Q0, Q1, K x 2, V x 2, and 1 KiB to align
-__host__ __device__ constexpr int smem_tc(int D) { return 6 * blocks_of(D) * (int)kBlockBytes + 1024; }
+// Q0, Q1, K x 4, V x 4, and 1 KiB to align
+__host__ __device__ constexpr int smem_tc(int D) {
+    return blocks_of(D) * (int)(2 * kBlockQ + 2 * kStagesTc * kBlockK) + 1024;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -81,6 +87,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
           "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
     asm volatile(
@@ -104,19 +117,28 @@ __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn_major) {
     return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(N / 8) << 17 | (uint32_t)(128 / 16) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+// The product warp runs as a whole, so that descriptors and addresses stay in
+// uniform registers, and one lane (`one`) issues.  Run by a single lane in a
+// branch of its own, each product waited about 70 cycles for its operands.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"((uint32_t)add) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add, uint32_t one) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(id), "r"((uint32_t)add), "r"(one) : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add, uint32_t one) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(id), "r"((uint32_t)add), "r"(one) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t one) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(bar), "r"(one) : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
@@ -158,8 +180,8 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
 // values of a chunk stand in the order 0 4 1 5 2 6 3 7 in every tile, as the
 // codes unpack: keys and queries agree, and the sums' columns are put right when
 // they are read.
-__device__ __forceinline__ uint32_t tile_at(uint32_t tile, uint32_t row, uint32_t chunk) {
-    return tile + (chunk >> 3) * kBlockBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, uint32_t block, uint32_t row, uint32_t chunk) {
+    return tile + (chunk >> 3) * block + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
 // The exponent of a largest step as a power of two (and its inverse); 1 for none.
@@ -168,7 +190,7 @@ __device__ __forceinline__ float pow2_of(uint32_t most) {
 }
 
 struct SharedTc {
-    unsigned long long bars[16];
+    unsigned long long bars[32];
     uint32_t tmem;
     int gave_up, value_nan;
     uint32_t most[2][4];     // largest steps of keys and values, a group each (as bits)
@@ -177,17 +199,17 @@ struct SharedTc {
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int NG = D / 32, NB = blocks_of(D);
-    constexpr uint32_t kTileBytes = NB * kBlockBytes;
+    constexpr uint32_t kBytesQ = NB * kBlockQ, kBytesK = NB * kBlockK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SharedTc sh;
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t q_tile[2] = {base, base + kTileBytes};
-    const uint32_t k_tile = base + 2 * kTileBytes, v_tile = base + 4 * kTileBytes;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + kStagesTc * kBytesK;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = smem_u32(sh.bars);
-    const uint32_t k_full = bars, k_free = bars + 16, v_full = bars + 32, v_free = bars + 48,
-                   s_full = bars + 64, p_full = bars + 80, o_full = bars + 96;
+    const uint32_t k_full = bars, k_free = bars + 32, v_full = bars + 64, v_free = bars + 96,
+                   s_full = bars + 128, p_full = bars + 160,      // [tile][buffer]
+                   o_done = bars + 192, q_full = bars + 208, o_full = bars + 216;
 
     const int H = (int)a.pool.H, group = (int)a.group;
     int bx = blockIdx.x;
@@ -208,12 +230,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
     const int c0 = s.lo + ci * (int)a.chunk, c1 = min(s.hi, c0 + (int)a.chunk);
     if (c0 >= c1 && ci > 0) return;
     const bool whole = s.hi - s.lo <= (int)a.chunk;
+    const int q_tiles = rows > kTileQ ? 2 : 1;
     const int tiles = c1 > c0 ? (c1 - c0 + kTileK - 1) / kTileK : 0;
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     const int64_t head_off = (int64_t)head * a.pool.s_head;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             bar_init(k_full + 8 * i, 32 * kUnpackWarps);
             bar_init(v_full + 8 * i, 32 * kUnpackWarps);
             bar_init(k_free + 8 * i, 1);
@@ -221,6 +244,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             bar_init(s_full + 8 * i, 1);
             bar_init(p_full + 8 * i, kTileQ);
         }
+        bar_init(o_done, 1);
+        bar_init(o_done + 8, 1);
+        bar_init(q_full, 2 * kTileQ);
         bar_init(o_full, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.gave_up = 0;
@@ -249,10 +275,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             if (wrong) continue;
 #pragma unroll
             for (int comp = 0; comp < 2; ++comp) {
-                const uint64_t at = a.pool.base[comp] + off + head_off + D / 2;
+                // four scale words, or fewer and the zeros behind them
+                const uint4 u = *reinterpret_cast<const uint4 *>(a.pool.base[comp] + off + head_off + D / 2);
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(at + gr * 4) & ~15u;
+                    const uint32_t w = v[gr] & ~15u;
                     if (w < 0x7f800000u) most[comp][gr] = max(most[comp][gr], w);
                 }
             }
@@ -273,7 +301,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const int i = on ? at / group : 0, j = on ? at - i * group : 0;
         const int64_t tok = s.q0 + i;
         const int qh = head * group + j;
-        const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+        // the scale's sign goes into the queries (0 for a scale of 0)
+        const float sign = a.scale_log2 < 0.0f ? -1.0f : a.scale_log2 == 0.0f ? 0.0f : 1.0f;
         float kf[NG];
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) kf[gr] = pow2_of(sh.most[0][gr]) * sign;
@@ -300,7 +329,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             const uint32_t ex = __float_as_uint(top) >> 23;
             const bool scaled = ex >= 10 && ex < 255;
             const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f;
-            sc = (scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f) * fabsf(a.scale_log2);
+            // never 0, so that a masked score of -infinity stays one
+            sc = fmaxf((scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f) * fabsf(a.scale_log2), 1.2e-38f);
             for (int ch = 0; ch < D / 8; ++ch) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (on) u = *reinterpret_cast<const uint4 *>(src + ch * 16);
@@ -312,77 +342,69 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     h[e] = h2_bits(value(w[e / 2], e & 1) * f * up, value(w[2 + e / 2], e & 1) * f * up);
-                sts16(tile_at(q_tile[q], row, ch), make_uint4(h[0], h[1], h[2], h[3]));
+                sts16(tile_at(base + q * kBytesQ, kBlockQ, row, ch), make_uint4(h[0], h[1], h[2], h[3]));
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(p_full + 8 * q);          // phase 0 of p_full: the queries are there
+        bar_arrive(q_full);
 
         const int pos = s.len - s.n + i;
         const int lim = on ? min(pos, c1 - 1) : -1;                 // sees tokens low..lim
         const int low = a.window ? max(0, pos - (int)a.window + 1) : 0;
         const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-        const uint32_t sp = mine + q * 128, o = mine + 256 + q * D;
+        const uint32_t o = mine + 256 + q * D;
         float m = kNoMaxTc, l = 0.0f;
         bool alive = true;
-        for (int t = 0; t < tiles && alive; ++t) {
-            alive = bar_wait(s_full + 8 * q, t & 1, &sh.gave_up);
-            alive = __all_sync(0xffffffffu, alive);
+        const int my_tiles = q < q_tiles ? tiles : 0;
+        for (int t = 0; t < my_tiles; ++t) {
+            const uint32_t buf = t & 1, sp = mine + q * 128 + buf * 64;
+            const uint32_t half_bar = 16 * q + 8 * buf;
+            alive = __all_sync(0xffffffffu, bar_wait(s_full + half_bar, (t >> 1) & 1, &sh.gave_up));
             if (!alive) break;
             fence_after();
+            uint32_t x[64];
+            tmem_ld32(sp, x);
+            tmem_ld32(sp + 32, x + 32);
             const int t0 = c0 + t * kTileK;
             const bool inside = __all_sync(0xffffffffu, t0 >= low && t0 + kTileK - 1 <= lim);
-            // Each load from tensor memory runs while the one before is worked on.
-            uint32_t x[2][32];
-            float top = -INFINITY;
-            auto most_of = [&](const uint32_t *y, int ch) {
-                float u = -INFINITY, v = -INFINITY;
-                if (inside) {
+            tmem_ld_wait();
+            if (!inside) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        u = fmaxf(fmaxf(u, __uint_as_float(y[e])), __uint_as_float(y[e + 1]));
-                        v = fmaxf(fmaxf(v, __uint_as_float(y[e + 2])), __uint_as_float(y[e + 3]));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int tk = t0 + ch * 32 + e;
-                        if (tk >= low && tk <= lim) u = fmaxf(u, __uint_as_float(y[e]));
-                    }
-                }
-                top = fmaxf(top, fmaxf(u, v));
-            };
-            tmem_ld32(sp, x[0]);
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ch += 2) {
-                tmem_ld_wait();
-                tmem_ld32(sp + ch * 32 + 32, x[1]);
-                most_of(x[0], ch);
-                tmem_ld_wait();
-                tmem_ld32(sp + (ch * 32 + 64 & 127), x[0]);     // in the end: the first again
-                most_of(x[1], ch + 1);
+                for (int e = 0; e < 64; ++e)
+                    if (t0 + e < low || t0 + e > lim) x[e] = 0xff800000u;      // -infinity
             }
-            __syncwarp();
-            top *= sc;
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    top[b] = fmaxf(fmaxf(top[b], __uint_as_float(x[e + 2 * b])), __uint_as_float(x[e + 2 * b + 1]));
+            float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            most = most == -INFINITY ? most : most * sc;
             // the maximum moves when it is passed by more than 2^8; then the sums
             // so far, O in tensor memory among them, are scaled down
             float k = 1.0f;
             if (m == kNoMaxTc) {
-                if (top > -INFINITY) m = top;
-            } else if (top > m + 8.0f) {
-                k = ex2(m - top);
-                m = top;
+                if (most > -INFINITY) m = most;
+            } else if (most > m + 8.0f) {
+                k = ex2(m - most);
+                m = most;
                 l *= k;
             }
+            __syncwarp();
             if (t > 0 && __any_sync(0xffffffffu, k != 1.0f)) {
+                // the products before have to be done
+                alive = __all_sync(0xffffffffu, bar_wait(o_done + 8 * q, (t - 1) & 1, &sh.gave_up));
+                if (!alive) break;
+                fence_after();
 #pragma unroll 1
-                for (int ch = 0; ch < NG; ++ch) {
-                    tmem_ld32(o + ch * 32, x[1]);
+                for (int ch = 0; ch < D / 16; ++ch) {
+                    uint32_t y[16];
+                    tmem_ld16(o + ch * 16, y);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[1][e] = __float_as_uint(__uint_as_float(x[1][e]) * k);
-                    tmem_st16(o + ch * 32, x[1]);
-                    tmem_st16(o + ch * 32 + 16, x[1] + 16);
+                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * k);
+                    tmem_st16(o + ch * 16, y);
                 }
                 tmem_st_wait();
             }
@@ -390,37 +412,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             const float less = m == kNoMaxTc ? 0.0f : -m;
             const unsigned long long sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
             const unsigned long long less2 = pair(__float_as_uint(less), __float_as_uint(less));
-            unsigned long long sum = 0;
-            auto weights_of = [&](const uint32_t *y, int ch) {
+            unsigned long long sum[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float2 u = unpair(fma2(pair(y[e], y[e + 1]), sc2, less2));
-                    if (!inside) {
-                        const int tk = t0 + ch * 32 + e;
-                        if (tk < low || tk > lim) u.x = -INFINITY;
-                        if (tk + 1 < low || tk + 1 > lim) u.y = -INFINITY;
-                    }
+                    float2 u = unpair(fma2(pair(x[32 * h + e], x[32 * h + e + 1]), sc2, less2));
                     u.x = ex2(u.x);
                     u.y = ex2(u.y);
-                    sum = add2(sum, pair(__float_as_uint(u.x), __float_as_uint(u.y)));
+                    sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair(__float_as_uint(u.x), __float_as_uint(u.y)));
                     p[e / 2] = h2_bits(u.x, u.y);
                 }
-                tmem_st16(sp + ch * 16, p);     // over scores that have been read twice
-            };
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ch += 2) {
-                tmem_ld_wait();
-                tmem_ld32(sp + ch * 32 + 32, x[1]);
-                weights_of(x[0], ch);
-                tmem_ld_wait();
-                if (ch == 0) tmem_ld32(sp + 64, x[0]);
-                weights_of(x[1], ch + 1);
+                tmem_st16(sp + h * 16, p);      // over the scores
             }
-            l += unpair(sum).x + unpair(sum).y;
+            const float2 both = unpair(add2(sum[0], sum[1]));
+            l += both.x + both.y;
             tmem_st_wait();
             fence_before();
-            bar_arrive(p_full + 8 * q);
+            bar_arrive(p_full + half_bar);
         }
         if (tiles > 0) alive = __all_sync(0xffffffffu, alive && bar_wait(o_full, 0, &sh.gave_up));
         fence_after();
@@ -499,10 +509,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         fence_before();
     } else if (warp < kSoftWarps + kUnpackWarps) {
         // ------------------------------------------------- unpack to fp16 tiles
-        // A thread takes one group of every 128 / NP-th token of a tile: NP groups of
-        // 32 values.  Keys and values alternate through the same code; the loads of
-        // the next half tile are under way while this one is unpacked.
-        constexpr int NP = NG == 3 ? 4 : NG;
+        // A thread takes one group of 32 values of every 128 / NP-th token of a tile.  As
+        // soon as a group is unpacked, the load of its successor in the next tile
+        // starts.
+        constexpr int NP = NG == 3 ? 4 : NG, NI = NP * kTileK / 128;
         const int d = tid - 32 * kSoftWarps;
         const int gr = d % NP, tk0 = d / NP;                 // group; tokens tk0 + it * 128 / NP
         const bool idle = gr >= NG;
@@ -513,11 +523,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const bool apart = (gr >> 1 & 1) != 0;
         uint32_t to[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = tile_at(0, tk0, gr * 4 + (i ^ (apart ? 2 : 0)));
-        int64_t off[NP];
-        uint4 code[NP];
-        uint32_t word[NP];
+        for (int i = 0; i < 4; ++i) to[i] = tile_at(0, kBlockK, tk0, gr * 4 + (i ^ (apart ? 2 : 0)));
+        int64_t off[NI];
+        uint4 code[2][NI];
+        uint32_t word[2][NI];
         bool outside = false, alive = true;
+        // Places are found a tile before the loads that use them, so that no load
+        // waits for the page table.
         auto find = [&](int it, int t) {
             const int tk = c0 + t * kTileK + tk0 + it * (128 / NP);
             bool wrong = false;
@@ -529,40 +541,39 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             }
         };
         auto fetch = [&](int it, int comp) {
-            code[it] = make_uint4(0, 0, 0, 0);
-            word[it] = off[it] == -2 && comp == 0 ? kNanWord : 0u;
+            code[comp][it] = make_uint4(0, 0, 0, 0);
+            word[comp][it] = off[it] == -2 && comp == 0 ? kNanWord : 0u;
             if (off[it] >= 0) {
                 const uint64_t at = a.pool.base[comp] + off[it];
-                code[it] = *reinterpret_cast<const uint4 *>(at + gr * 16);
-                word[it] = *reinterpret_cast<const uint32_t *>(at + D / 2 + gr * 4);
+                code[comp][it] = *reinterpret_cast<const uint4 *>(at + gr * 16);
+                word[comp][it] = *reinterpret_cast<const uint32_t *>(at + D / 2 + gr * 4);
             }
         };
 #pragma unroll
-        for (int it = 0; it < NP; ++it) {
+        for (int it = 0; it < NI; ++it) {
             find(it, 0);
             fetch(it, 0);
+            fetch(it, 1);
+            find(it, 1);
         }
         const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
 #pragma unroll 1
-        for (int half = 0; half < 2 * tiles; ++half) {
-            const int t = half >> 1, comp = half & 1;
-            const uint32_t st = t & 1;
-            alive = bar_wait((comp ? v_free : k_free) + 8 * st, ((t >> 1) & 1) ^ 1, &sh.gave_up);
-            if (!alive) break;
-            const uint32_t tile = (comp ? v_tile : k_tile) + st * kTileBytes;
+        for (int t = 0; t < tiles && alive; ++t) {
+            const uint32_t st = t % kStagesTc, parity = ((t / kStagesTc) & 1) ^ 1;
 #pragma unroll
-            for (int it = 0; it < NP; ++it) {
-                uint32_t w = word[it];
-                const uint4 u = code[it];
-                if (comp == 0) {
-                    fetch(it, 1);
-                } else {
-                    find(it, t + 1);
-                    fetch(it, 0);
-                    if (w >= 0x7f800000u) {
-                        w = 0;            // kept out of the products; the softmax warps see to it
-                        sh.value_nan = 1;
-                    }
+            for (int comp = 0; comp < 2; ++comp) {
+            alive = alive && bar_wait((comp ? v_free : k_free) + 8 * st, parity, &sh.gave_up);
+            if (!alive) break;
+            const uint32_t tile = (comp ? v_tile : k_tile) + st * kBytesK;
+#pragma unroll
+            for (int it = 0; it < NI; ++it) {
+                uint32_t w = word[comp][it];
+                const uint4 u = code[comp][it];
+                fetch(it, comp);          // of tile t + 1
+                if (comp == 1) find(it, t + 2);
+                if (comp == 1 && w >= 0x7f800000u) {
+                    w = 0;                // kept out of the products; the softmax warps see to it
+                    sh.value_nan = 1;
                 }
                 // the step as two fp16 parts: a product is rounded once, by the sum with the first
                 const float step = q4_step(w) * (comp ? f[1] : f[0]);
@@ -591,53 +602,65 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             bar_arrive((comp ? v_full : k_full) + 8 * st);
+            }
         }
         if (outside && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ products
         constexpr uint32_t kScores = idesc(kTileK, false), kSums = idesc(D, true);
+        const uint32_t one = elected();
         bool alive = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, bar_wait(bar, parity, &sh.gave_up)) != 0;
+        };
         auto scores = [&](int q, int t) {
-            const uint32_t kt = k_tile + (t & 1) * kTileBytes;
+            const uint32_t kt = k_tile + (t % kStagesTc) * kBytesK, qt = base + q * kBytesQ;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t in = (ks >> 2) * kBlockBytes + (ks & 3) * 32;
-                mma_ss(tmem + q * 128, desc(q_tile[q] + in, 16, 1024), desc(kt + in, 16, 1024), kScores, ks != 0);
-            }
-            commit(s_full + 8 * q);
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss(tmem + q * 128 + (t & 1) * 64, desc(qt + (ks >> 2) * kBlockQ + (ks & 3) * 32, 16, 1024),
+                       desc(kt + (ks >> 2) * kBlockK + (ks & 3) * 32, 16, 1024), kScores, ks != 0, one);
+            commit(s_full + 16 * q + 8 * (t & 1), one);
         };
         auto sums = [&](int q, int t) {
-            const uint32_t vt = v_tile + (t & 1) * kTileBytes;
+            const uint32_t vt = v_tile + (t % kStagesTc) * kBytesK;
 #pragma unroll
             for (int ks = 0; ks < kTileK / 16; ++ks)
-                mma_ts(tmem + 256 + q * D, tmem + q * 128 + ks * 8, desc(vt + ks * 2048, kBlockBytes, 1024), kSums,
-                       t != 0 || ks != 0);
+                mma_ts(tmem + 256 + q * D, tmem + q * 128 + (t & 1) * 64 + ks * 8,
+                       desc(vt + ks * 2048, kBlockK, 1024), kSums, t != 0 || ks != 0, one);
+            commit(o_done + 8 * q, one);
+        };
+        auto keys = [&](int t) {
+            return wait(k_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
         };
         if (tiles > 0) {
-            alive = bar_wait(k_full, 0, &sh.gave_up);
-            for (int q = 0; q < 2 && alive; ++q) {
-                alive = bar_wait(p_full + 8 * q, 0, &sh.gave_up);   // queries in place
+            alive = wait(q_full, 0);
+            for (int t = 0; t < 2 && t < tiles && alive; ++t) {      // both buffers of scores
+                alive = keys(t);
+                if (!alive) break;
                 fence_after();
-                if (alive) scores(q, 0);
+                for (int q = 0; q < q_tiles; ++q) scores(q, t);
+                commit(k_free + 8 * t, one);
             }
-            if (alive) commit(k_free);
             for (int t = 0; t < tiles && alive; ++t) {
-                if (t + 1 < tiles)
-                    alive = bar_wait(k_full + 8 * ((t + 1) & 1), ((t + 1) >> 1) & 1, &sh.gave_up);
-                alive = alive && bar_wait(v_full + 8 * (t & 1), (t >> 1) & 1, &sh.gave_up);
-                for (int q = 0; q < 2 && alive; ++q) {
-                    alive = bar_wait(p_full + 8 * q, (t + 1) & 1, &sh.gave_up);
+                alive = wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+                for (int q = 0; q < q_tiles && alive; ++q) {
+                    alive = wait(p_full + 16 * q + 8 * (t & 1), (t >> 1) & 1);
                     if (!alive) break;
                     fence_after();
                     sums(q, t);
-                    if (t + 1 < tiles) scores(q, t + 1);
+                    if (t + 2 < tiles) {
+                        if (q == 0) alive = keys(t + 2);
+                        if (!alive) break;
+                        fence_after();
+                        scores(q, t + 2);       // after the sums that read this buffer
+                    }
                 }
                 if (!alive) break;
-                commit(v_free + 8 * (t & 1));
-                if (t + 1 < tiles) commit(k_free + 8 * ((t + 1) & 1));
+                commit(v_free + 8 * (t % kStagesTc), one);
+                if (t + 2 < tiles) commit(k_free + 8 * ((t + 2) % kStagesTc), one);
             }
             // all products done: the end of the work, or of what was begun when a wait gave up
-            commit(o_full);
+            commit(o_full, one);
             int never = 0;
             bar_wait(o_full, 0, &never);
         }
