@@ -3,7 +3,7 @@
 //
 // A block takes 256 query rows (new tokens x the group of one KV head) as two
 // tiles of 128, and walks the cached tokens 64 at a time.  Warps have roles:
-//   4 warps  unpack keys and values to fp16 in shared memory (swizzled tiles)
+//   8 warps  unpack keys and values to fp16 in shared memory (swizzled tiles)
 //   1 warp   issues tcgen05.mma: scores S = Q K^T and sums O += P V
 //   4 + 4    softmax of the two tiles, one row a thread: scores come from tensor
 //            memory, probabilities go back there as fp16, the A operand of P V
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kTileQ = 128, kTileK = 64, kStagesTc = 4;
 constexpr int kRowsTc = 2 * kTileQ;
-constexpr int kSoftWarps = 8, kUnpackWarps = 4;
+constexpr int kSoftWarps = 8, kUnpackWarps = 8, kUnpackThreads = 32 * kUnpackWarps;
 constexpr int kThreadsTc = 32 * (kSoftWarps + kUnpackWarps + 1);
 constexpr float kNoMaxTc = -3.0e38f;
 // 64 fp16 (128 bytes, swizzled) of every row of a tile
@@ -509,13 +509,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         fence_before();
     } else if (warp < kSoftWarps + kUnpackWarps) {
         // ------------------------------------------------- unpack to fp16 tiles
-        // A thread takes one group of 32 values of every 128 / NP-th token of a tile.  As
-        // soon as a group is unpacked, the load of its successor in the next tile
-        // starts.
-        constexpr int NP = NG == 3 ? 4 : NG, NI = NP * kTileK / 128;
+        // A thread takes one group of 32 values of every kUnpackThreads / NP-th token
+        // of a tile.  As soon as a group is unpacked, the load of its successor in
+        // the next tile starts.
+        constexpr int NP = NG == 3 ? 4 : NG, kStep = kUnpackThreads / NP;
+        constexpr int NI = kTileK > kStep ? kTileK / kStep : 1;
         const int d = tid - 32 * kSoftWarps;
-        const int gr = d % NP, tk0 = d / NP;                 // group; tokens tk0 + it * 128 / NP
-        const bool idle = gr >= NG;
+        const int gr = d % NP, tk0 = d / NP;                 // group; tokens tk0 + it * kStep
+        const bool idle = gr >= NG || tk0 >= kTileK;
         const float f[2] = {1.0f / pow2_of(sh.most[0][idle ? 0 : gr]),
                             1.0f / pow2_of(sh.most[1][idle ? 0 : gr])};
         // Lanes of groups 2 and 3 go through their words two apart from those of 0 and
@@ -528,14 +529,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         uint4 code[2][NI];
         uint32_t word[2][NI];
         bool outside = false, alive = true;
-        // Places are found a tile before the loads that use them, so that no load
-        // waits for the page table.
+        // A place is looked up in two steps, the page one tile before the offset and
+        // that one tile before the loads that use it, so that nothing waits for the
+        // page table.
+        int32_t page[NI];
+        auto token = [&](int it, int t) { return c0 + t * kTileK + tk0 + it * kStep; };
+        auto look_up = [&](int it, int t) {
+            const int tk = token(it, t);
+            page[it] = !idle && tk < c1 ? table[div_T(a.pool, (uint32_t)tk)] : 0;
+        };
         auto find = [&](int it, int t) {
-            const int tk = c0 + t * kTileK + tk0 + it * (128 / NP);
-            bool wrong = false;
+            const int tk = token(it, t);
             off[it] = -1;                 // past the end: zeros
-            if (t < tiles && tk < c1 && !idle) {
-                off[it] = token_offset(a.pool, table, (uint32_t)tk, &wrong) + head_off;
+            if (!idle && tk < c1) {
+                bool wrong;
+                off[it] = page_offset(a.pool, (uint32_t)page[it], (uint32_t)tk, &wrong) + head_off;
                 if (wrong) off[it] = -2;  // keys NaN
                 outside |= wrong;
             }
@@ -551,10 +559,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         };
 #pragma unroll
         for (int it = 0; it < NI; ++it) {
+            look_up(it, 0);
             find(it, 0);
             fetch(it, 0);
             fetch(it, 1);
+            look_up(it, 1);
             find(it, 1);
+            look_up(it, 2);
         }
         const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
 #pragma unroll 1
@@ -570,7 +581,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 uint32_t w = word[comp][it];
                 const uint4 u = code[comp][it];
                 fetch(it, comp);          // of tile t + 1
-                if (comp == 1) find(it, t + 2);
+                if (comp == 1) {
+                    find(it, t + 2);
+                    look_up(it, t + 3);
+                }
                 if (comp == 1 && w >= 0x7f800000u) {
                     w = 0;                // kept out of the products; the softmax warps see to it
                     sh.value_nan = 1;
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                             x = __hfma2(x, s1, __hmul2(x, s0));
                             y[e] = *reinterpret_cast<uint32_t *>(&x);
                         }
-                        sts16(tile + to[i] + it * (128 / NP) * 128, make_uint4(y[0], y[1], y[2], y[3]));
+                        sts16(tile + to[i] + it * kStep * 128, make_uint4(y[0], y[1], y[2], y[3]));
                     }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -56,14 +56,17 @@ KVB_HD int64_t slot_offset(const PoolLayer &p, int64_t slot) {
     return (int64_t)(page * p.s_page + t * p.s_tok);
 }
 
-// Offset of cached token t of the request whose page-table row is `table`, or
-// -1 (and *wrong) when the table names a page outside the pool.
-KVB_HD int64_t token_offset(const PoolLayer &p, const int32_t *table, uint32_t t, bool *wrong) {
-    const uint32_t i = div_T(p, t);
-    const uint32_t page = (uint32_t)table[i];
+// Offset of a request's token t, in page `page` of the pool; -1 (and *wrong) when
+// there is no such page.
+KVB_HD int64_t page_offset(const PoolLayer &p, uint32_t page, uint32_t t, bool *wrong) {
     *wrong = page >= p.P;
     if (*wrong) return -1;
-    return (int64_t)(page * p.s_page + (uint64_t)(t - i * p.T) * p.s_tok);
+    return (int64_t)(page * p.s_page + (uint64_t)(t - div_T(p, t) * p.T) * p.s_tok);
+}
+
+// The same from the request's row of the page table.
+KVB_HD int64_t token_offset(const PoolLayer &p, const int32_t *table, uint32_t t, bool *wrong) {
+    return page_offset(p, (uint32_t)table[div_T(p, t)], t, wrong);
 }
 
 // What a tile of query rows sees.  Row x of a request is query head x % group
