@@ -207,9 +207,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
     const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + kStagesTc * kBytesK;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = smem_u32(sh.bars);
-    const uint32_t k_full = bars, k_free = bars + 32, v_full = bars + 64, v_free = bars + 96,
-                   s_full = bars + 128, p_full = bars + 160,      // [tile][buffer]
-                   o_done = bars + 192, q_full = bars + 208, o_full = bars + 216;
+    // a stage holds the keys and the values of one tile of cached tokens
+    const uint32_t k_full = bars, v_full = bars + 32, stage_free = bars + 64,
+                   s_full = bars + 96, p_full = bars + 128,      // [tile of rows][buffer]
+                   o_last = bars + 160, q_full = bars + 176, o_full = bars + 184;
 
     const int H = (int)a.pool.H, group = (int)a.group;
     int bx = blockIdx.x;
@@ -239,13 +240,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         for (int i = 0; i < 4; ++i) {
             bar_init(k_full + 8 * i, 32 * kUnpackWarps);
             bar_init(v_full + 8 * i, 32 * kUnpackWarps);
-            bar_init(k_free + 8 * i, 1);
-            bar_init(v_free + 8 * i, 1);
+            bar_init(stage_free + 8 * i, 1);
             bar_init(s_full + 8 * i, 1);
             bar_init(p_full + 8 * i, kTileQ);
         }
-        bar_init(o_done, 1);
-        bar_init(o_done + 8, 1);
+        bar_init(o_last, 1);
+        bar_init(o_last + 8, 1);
         bar_init(q_full, 2 * kTileQ);
         bar_init(o_full, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -393,8 +393,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             }
             __syncwarp();
             if (t > 0 && __any_sync(0xffffffffu, k != 1.0f)) {
-                // the products before have to be done
-                alive = __all_sync(0xffffffffu, bar_wait(o_done + 8 * q, (t - 1) & 1, &sh.gave_up));
+                // The sums of the tile before have to be done: the next scores were begun
+                // after them, and at the end there is a barrier for them.
+                const bool last = t + 1 == my_tiles;
+                alive = __all_sync(0xffffffffu, bar_wait(last ? o_last + 8 * q : s_full + 16 * q + 8 * (buf ^ 1),
+                                                         last ? 0 : (t + 1) >> 1 & 1, &sh.gave_up));
                 if (!alive) break;
                 fence_after();
 #pragma unroll 1
@@ -571,10 +574,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
 #pragma unroll 1
         for (int t = 0; t < tiles && alive; ++t) {
             const uint32_t st = t % kStagesTc, parity = ((t / kStagesTc) & 1) ^ 1;
+            alive = bar_wait(stage_free + 8 * st, parity, &sh.gave_up);
+            if (!alive) break;
 #pragma unroll
             for (int comp = 0; comp < 2; ++comp) {
-            alive = alive && bar_wait((comp ? v_free : k_free) + 8 * st, parity, &sh.gave_up);
-            if (!alive) break;
             const uint32_t tile = (comp ? v_tile : k_tile) + st * kBytesK;
 #pragma unroll
             for (int it = 0; it < NI; ++it) {
@@ -641,7 +644,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             for (int ks = 0; ks < kTileK / 16; ++ks)
                 mma_ts(tmem + 256 + q * D, tmem + q * 128 + (t & 1) * 64 + ks * 8,
                        desc(vt + ks * 2048, kBlockK, 1024), kSums, t != 0 || ks != 0, one);
-            commit(o_done + 8 * q, one);
         };
         auto keys = [&](int t) {
             return wait(k_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
@@ -653,25 +655,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 if (!alive) break;
                 fence_after();
                 for (int q = 0; q < q_tiles; ++q) scores(q, t);
-                commit(k_free + 8 * t, one);
             }
             for (int t = 0; t < tiles && alive; ++t) {
-                alive = wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+                // The unpacking warps give the values of a tile before the keys of the next, so
+                // keys that have come vouch for them; the last tile has no next.
+                if (t + 1 == tiles) alive = wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
                 for (int q = 0; q < q_tiles && alive; ++q) {
                     alive = wait(p_full + 16 * q + 8 * (t & 1), (t >> 1) & 1);
                     if (!alive) break;
                     fence_after();
                     sums(q, t);
                     if (t + 2 < tiles) {
-                        if (q == 0) alive = keys(t + 2);
-                        if (!alive) break;
-                        fence_after();
+                        if (q == 0) {
+                            alive = keys(t + 2);
+                            if (!alive) break;
+                            fence_after();
+                        }
                         scores(q, t + 2);       // after the sums that read this buffer
+                    } else if (t + 2 == tiles) {
+                        commit(o_last + 8 * q, one);
                     }
                 }
-                if (!alive) break;
-                commit(v_free + 8 * (t % kStagesTc), one);
-                if (t + 2 < tiles) commit(k_free + 8 * ((t + 2) % kStagesTc), one);
+                if (alive) commit(stage_free + 8 * (t % kStagesTc), one);
             }
             // all products done: the end of the work, or of what was begun when a wait gave up
             commit(o_full, one);
