@@ -50,25 +50,24 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Waits until the phase of this parity is complete.  Every wait ends: after
-// about two seconds, or once another warp gave up, it returns false.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    uint32_t done = 0;
+// Waits until the phase of this parity is complete.  Every wait ends: after about
+// two seconds, or once another warp gave up.  The work then runs on to its end
+// over whatever is there, every access in bounds, and the block reports it: no
+// warp's control flow depends on it, which keeps the product warp uniform.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
     long long start = 0;
     for (uint32_t n = 0;; ++n) {
+        uint32_t done;
         asm volatile("{\n\t.reg .pred p;\n\t"
                      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return true;
-        if ((n & 255u) == 255u) {
+        if (done) return;
+        if ((n & 63u) == 63u) {
             const long long now = clock64();
             if (start == 0) start = now;
-            if (*gave_up != 0) return false;
-            if (now - start > 4000000000ll) {
-                *gave_up = 1;
-                return false;
-            }
+            if (now - start > 4000000000ll) *gave_up = 1;
+            if (*gave_up != 0) return;
         }
     }
 }
@@ -354,13 +353,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const uint32_t o = mine + 256 + q * D;
         float m = kNoMaxTc, l = 0.0f;
-        bool alive = true;
         const int my_tiles = q < q_tiles ? tiles : 0;
         for (int t = 0; t < my_tiles; ++t) {
             const uint32_t buf = t & 1, sp = mine + q * 128 + buf * 64;
             const uint32_t half_bar = 16 * q + 8 * buf;
-            alive = __all_sync(0xffffffffu, bar_wait(s_full + half_bar, (t >> 1) & 1, &sh.gave_up));
-            if (!alive) break;
+            bar_wait(s_full + half_bar, (t >> 1) & 1, &sh.gave_up);
+            __syncwarp();
             fence_after();
             uint32_t x[64];
             tmem_ld32(sp, x);
@@ -396,9 +394,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 // The sums of the tile before have to be done: the next scores were begun
                 // after them, and at the end there is a barrier for them.
                 const bool last = t + 1 == my_tiles;
-                alive = __all_sync(0xffffffffu, bar_wait(last ? o_last + 8 * q : s_full + 16 * q + 8 * (buf ^ 1),
-                                                         last ? 0 : (t + 1) >> 1 & 1, &sh.gave_up));
-                if (!alive) break;
+                bar_wait(last ? o_last + 8 * q : s_full + 16 * q + 8 * (buf ^ 1), last ? 0 : (t + 1) >> 1 & 1,
+                         &sh.gave_up);
+                __syncwarp();
                 fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < D / 16; ++ch) {
@@ -435,8 +433,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             fence_before();
             bar_arrive(p_full + half_bar);
         }
-        if (tiles > 0) alive = __all_sync(0xffffffffu, alive && bar_wait(o_full, 0, &sh.gave_up));
+        if (tiles > 0) bar_wait(o_full, 0, &sh.gave_up);
+        __syncwarp();
         fence_after();
+        const bool alive = sh.gave_up == 0;
         // a value that is not finite: groups of the row's tokens that hold one
         uint32_t nan_groups = alive ? 0u : 0xffu;
         if (alive && sh.value_nan != 0)
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
 #pragma unroll 1
         for (int ch = 0; ch < NG; ++ch) {
             uint32_t x[32];
-            if (tiles > 0 && alive) {
+            if (tiles > 0) {
                 tmem_ld32(o + ch * 32, x);
                 tmem_ld_wait();
             } else {
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         int64_t off[NI];
         uint4 code[2][NI];
         uint32_t word[2][NI];
-        bool outside = false, alive = true;
+        bool outside = false;
         // A place is looked up in two steps, the page one tile before the offset and
         // that one tile before the loads that use it, so that nothing waits for the
         // page table.
@@ -572,10 +572,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         }
         const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
 #pragma unroll 1
-        for (int t = 0; t < tiles && alive; ++t) {
+        for (int t = 0; t < tiles; ++t) {
             const uint32_t st = t % kStagesTc, parity = ((t / kStagesTc) & 1) ^ 1;
-            alive = bar_wait(stage_free + 8 * st, parity, &sh.gave_up);
-            if (!alive) break;
+            bar_wait(stage_free + 8 * st, parity, &sh.gave_up);
 #pragma unroll
             for (int comp = 0; comp < 2; ++comp) {
             const uint32_t tile = (comp ? v_tile : k_tile) + st * kBytesK;
@@ -626,62 +625,60 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         // ------------------------------------------------------------ products
         constexpr uint32_t kScores = idesc(kTileK, false), kSums = idesc(D, true);
         const uint32_t one = elected();
-        bool alive = true;
+        const int n = __shfl_sync(0xffffffffu, tiles, 0), nq = __shfl_sync(0xffffffffu, q_tiles, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, bar_wait(bar, parity, &sh.gave_up)) != 0;
+            bar_wait(bar, parity, &sh.gave_up);
+            __syncwarp();
         };
         auto scores = [&](int q, int t) {
-            const uint32_t kt = k_tile + (t % kStagesTc) * kBytesK, qt = base + q * kBytesQ;
+            const uint64_t qd = desc(base + q * kBytesQ, 16, 1024), kd = desc(k_tile + (t % kStagesTc) * kBytesK, 16, 1024);
+            const uint32_t to = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss(tmem + q * 128 + (t & 1) * 64, desc(qt + (ks >> 2) * kBlockQ + (ks & 3) * 32, 16, 1024),
-                       desc(kt + (ks >> 2) * kBlockK + (ks & 3) * 32, 16, 1024), kScores, ks != 0, one);
+                mma_ss(to, qd + ((ks >> 2) * kBlockQ + (ks & 3) * 32) / 16, kd + ((ks >> 2) * kBlockK + (ks & 3) * 32) / 16,
+                       kScores, ks != 0, one);
             commit(s_full + 16 * q + 8 * (t & 1), one);
         };
         auto sums = [&](int q, int t) {
-            const uint32_t vt = v_tile + (t % kStagesTc) * kBytesK;
+            const uint64_t vd = desc(v_tile + (t % kStagesTc) * kBytesK, kBlockK, 1024);
+            const uint32_t to = tm + 256 + q * D, from = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < kTileK / 16; ++ks)
-                mma_ts(tmem + 256 + q * D, tmem + q * 128 + (t & 1) * 64 + ks * 8,
-                       desc(vt + ks * 2048, kBlockK, 1024), kSums, t != 0 || ks != 0, one);
+                mma_ts(to, from + ks * 8, vd + ks * 2048 / 16, kSums, t != 0 || ks != 0, one);
         };
         auto keys = [&](int t) {
-            return wait(k_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+            wait(k_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+            fence_after();
         };
-        if (tiles > 0) {
-            alive = wait(q_full, 0);
-            for (int t = 0; t < 2 && t < tiles && alive; ++t) {      // both buffers of scores
-                alive = keys(t);
-                if (!alive) break;
-                fence_after();
-                for (int q = 0; q < q_tiles; ++q) scores(q, t);
+        if (n > 0) {
+            wait(q_full, 0);
+            for (int t = 0; t < 2 && t < n; ++t) {      // both buffers of scores
+                keys(t);
+                for (int q = 0; q < nq; ++q) scores(q, t);
             }
-            for (int t = 0; t < tiles && alive; ++t) {
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
                 // The unpacking warps give the values of a tile before the keys of the next, so
                 // keys that have come vouch for them; the last tile has no next.
-                if (t + 1 == tiles) alive = wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
-                for (int q = 0; q < q_tiles && alive; ++q) {
-                    alive = wait(p_full + 16 * q + 8 * (t & 1), (t >> 1) & 1);
-                    if (!alive) break;
+                if (t + 1 == n) wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+#pragma unroll 1
+                for (int q = 0; q < nq; ++q) {
+                    wait(p_full + 16 * q + 8 * (t & 1), (t >> 1) & 1);
                     fence_after();
                     sums(q, t);
-                    if (t + 2 < tiles) {
-                        if (q == 0) {
-                            alive = keys(t + 2);
-                            if (!alive) break;
-                            fence_after();
-                        }
+                    if (t + 2 < n) {
+                        if (q == 0) keys(t + 2);
                         scores(q, t + 2);       // after the sums that read this buffer
-                    } else if (t + 2 == tiles) {
+                    } else if (t + 2 == n) {
                         commit(o_last + 8 * q, one);
                     }
                 }
-                if (alive) commit(stage_free + 8 * (t % kStagesTc), one);
+                commit(stage_free + 8 * (t % kStagesTc), one);
             }
-            // all products done: the end of the work, or of what was begun when a wait gave up
             commit(o_full, one);
             int never = 0;
-            bar_wait(o_full, 0, &never);
+            bar_wait(o_full, 0, &never);        // nothing in flight when tensor memory is given back
         }
     }
     __syncwarp();
