@@ -702,16 +702,6 @@ const Variant kVariants[] = {KVB_VARIANTS(64, 1),  KVB_VARIANTS(64, 2),  KVB_VAR
                              KVB_VARIANTS(96, 2),  KVB_VARIANTS(128, 1), KVB_VARIANTS(128, 2),
                              KVB_VARIANTS(192, 1), KVB_VARIANTS(256, 1)};
 
-struct JoinVariant {
-    uint32_t D;
-    bool fp16;
-    AttendFn *fn;
-};
-const JoinVariant kJoins[] = {
-    {64, false, kv_attend_join_kernel<64, 256, false>},   {64, true, kv_attend_join_kernel<64, 256, true>},
-    {96, false, kv_attend_join_kernel<96, 256, false>},   {96, true, kv_attend_join_kernel<96, 256, true>},
-    {128, false, kv_attend_join_kernel<128, 256, false>}, {128, true, kv_attend_join_kernel<128, 256, true>}};
-
 }  // namespace
 
 // Query rows of a request from which the tcgen05 kernel (256 rows a block) is taken.
@@ -727,38 +717,28 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     // the most cached tokens a row tile sees: its queries' windows overlap
     uint64_t span = max_len;
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + p.rows);
-    const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
-    uint64_t want, unit;
-    if (p.many) {        // one block an SM at most, in chunks of 512 tokens at least
-        want = std::max<uint64_t>(1, (uint64_t)sms / units);
-        unit = 512;
+    if (p.many) {
+        plan_attend_tc(&p, span, requests, kv_heads, sms);
+        p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
     } else {             // about four blocks an SM, in chunks of at least a tile for each warp
-        want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
-        unit = kWarps * kTile;
+        const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
+        const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
+        const uint64_t unit = kWarps * kTile;
+        uint64_t chunk = (span + want - 1) / want;
+        chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);
+        p.chunk = (uint32_t)chunk;
+        p.chunks = (uint32_t)std::max<uint64_t>(1, (span + chunk - 1) / chunk);
     }
-    uint64_t chunk = (span + want - 1) / want;
-    chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);
-    p.chunk = (uint32_t)chunk;
-    p.chunks = (uint32_t)std::max<uint64_t>(1, (span + chunk - 1) / chunk);
-    if (p.chunks > 1) p.bytes = (uint64_t)p.chunks * tokens * q_heads * (D + 2) * sizeof(float);
+    p.bytes = p.step_bytes;
+    if (p.chunks > 1) p.bytes += (uint64_t)p.chunks * tokens * q_heads * (D + 2) * sizeof(float);
     return p;
 }
 
 cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
                           cudaStream_t stream, int *launches) {
     (void)cudaGetLastError();
-    const dim3 join_grid(a.q_heads, a.max_q, a.requests);
     if (p.many) {
-        cudaError_t e = launch_attend_tc(a, p, D, fp16, pdl, stream);
-        if (e != cudaSuccess) return e;
-        ++*launches;
-        if (p.chunks > 1)
-            for (const JoinVariant &v : kJoins)
-                if (v.D == D && v.fp16 == fp16) {
-                    e = launch(v.fn, join_grid, 128, 0, stream, pdl, a);
-                    if (e == cudaSuccess) ++*launches;
-                }
-        return e;
+        return launch_attend_tc(a, D, fp16, pdl, stream, launches);
     }
     const bool many = a.max_q > 1;
     for (const Variant &v : kVariants) {
@@ -768,7 +748,7 @@ cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, 
         if (e != cudaSuccess) return e;
         ++*launches;
         if (p.chunks > 1) {
-            e = launch(v.join_fn, join_grid, 128, 0, stream, pdl, a);
+            e = launch(v.join_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
             if (e == cudaSuccess) ++*launches;
         }
         return e;
@@ -784,10 +764,6 @@ cudaError_t preload_attend_kernels() {
             e = cudaFuncSetAttribute((const void *)v.rows_fn,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
-        if (e != cudaSuccess) return e;
-    }
-    for (const JoinVariant &v : kJoins) {
-        const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
         if (e != cudaSuccess) return e;
     }
     return preload_attend_tc_kernels();

@@ -451,7 +451,8 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
                     "workspace 16-byte aligned");
     const AttendPlan plan = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, a->window,
                                         a->q_heads, k.pool.H, a->head_dim, p.sms);
-    if ((uint64_t)plan.row_tiles * plan.chunks * k.pool.H > 0x7fffffffull)
+    if ((uint64_t)plan.row_tiles * plan.chunks * k.pool.H * (plan.many ? a->requests : 1) > 0x7fffffffull ||
+        plan.step_parts > 65535)
         return fail(KV_ERR_INVALID_ARG, "max_q %u and max_len %u make too many blocks", a->max_q,
                     a->max_len);
     if (plan.bytes != 0 && a->workspace == nullptr)
@@ -489,8 +490,11 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     k.row_tiles = plan.row_tiles;
     k.window = a->window;
     k.scale_log2 = a->scale * 1.44269504088896340736f;
+    k.whole_units = (uint32_t)plan.whole_units;
+    k.steps = (uint32_t *)a->workspace;
+    k.step_parts = plan.step_parts;
     if (plan.bytes != 0) {
-        k.part_o = (float *)a->workspace;
+        k.part_o = (float *)((char *)a->workspace + plan.step_bytes);
         k.part_ml = k.part_o + (uint64_t)plan.chunks * a->tokens * a->q_heads * a->head_dim;
     }
     int launches = 0;

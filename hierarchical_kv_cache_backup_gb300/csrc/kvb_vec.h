@@ -203,6 +203,9 @@ struct AttendArgs {
     uint32_t requests, tokens, max_q, max_len, q_heads, group;
     uint32_t chunk, chunks;   // cached tokens a block handles; the most of one request
     uint32_t row_tiles;
+    uint32_t whole_units;     // many rows: units (row tile, head, request) that are not cut
+    uint32_t *steps;          // many rows: [requests][step_parts][H][2][4] largest steps
+    uint32_t step_parts;
     uint32_t window;
     float scale_log2;         // scale * log2(e)
 };

@@ -18,15 +18,19 @@ cudaError_t preload_vector_kernels();
 struct AttendPlan {
     uint32_t rows, row_tiles, chunk, chunks;
     bool many;             // the kernel for many query rows (kvb_attend_tc.cu)
-    uint64_t bytes;
+    uint64_t whole_units;  // many: units that are not cut
+    uint32_t step_parts;   // many: parts of a request whose largest steps are found apart
+    uint64_t step_bytes;   // workspace of those, at its start
+    uint64_t bytes;        // workspace in all
 };
 AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
                        uint32_t window, uint32_t q_heads, uint32_t kv_heads, uint32_t D, int sms);
 cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
                           cudaStream_t stream, int *launches);
 cudaError_t preload_attend_kernels();
-cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
-                             cudaStream_t stream);
+void plan_attend_tc(AttendPlan *p, uint64_t span, uint32_t requests, uint32_t kv_heads, int sms);
+cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream,
+                             int *launches);
 cudaError_t preload_attend_tc_kernels();
 
 // Handle checks of one operator call on a pool (CLOSED / STALE), its device
