@@ -173,41 +173,50 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * WB;
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
-    const int64_t head_off = (int64_t)head * a.pool.s_head;
-
+    // Tiles are copied 16 bytes a lane, a vector's PV pieces by neighbouring lanes.
+    // Lane i knows the place of token i, as a count of vectors, and hands it
+    // round.  Page ids are read a tile before they are used.
+    constexpr int kAtOnce = 32 / PV;
+    const int lane_tok = lane / PV, piece = lane - lane_tok * PV;
+    const uint64_t from_k = a.pool.base[0] + (uint64_t)head * a.pool.s_head + piece * 16;
+    const uint64_t from_v = a.pool.base[1] + (uint64_t)head * a.pool.s_head + piece * 16;
+    const uint32_t to = ring + lane_tok * SV + piece * 16;
+    int32_t page = 0;
+    auto look_up = [&](int t0) {
+        const int t = t0 + lane;
+        page = t < c1 ? table[div_T(a.pool, (uint32_t)t)] : 0;
+    };
     // starts the copy of a tile; returns which of its tokens are in pages outside the pool
     auto load = [&](int stage, int t0) -> uint32_t {
-        const int t = t0 + lane;
-        bool ok = t < c1;
-        int64_t off = 0;
-        bool wrong = false;
-        if (ok) {
-            off = token_offset(a.pool, table, (uint32_t)t, &wrong) + head_off;
-            ok = !wrong;
-        }
-        const uint32_t at = ring + stage * (2 * kTile * SV);
-        if (!ok) off = -1;
+        uint32_t wrong = 0;
+        if (t0 < c1) {
+            const int t = t0 + lane;
+            const bool in = t < c1, bad = in && (uint32_t)page >= a.pool.P, ok = in && !bad;
+            const uint32_t at = ok ? vector_index(a.pool, (uint32_t)page, (uint32_t)t) : 0;
+            const uint32_t good = __ballot_sync(0xffffffffu, ok);
+            wrong = __ballot_sync(0xffffffffu, bad);
+            const uint32_t dst = to + stage * (2 * kTile * SV);
 #pragma unroll
-        for (int k = 0; k < PV; ++k) {
-            const int idx = lane + 32 * k, tok = idx / PV, piece = idx - tok * PV;
-            const int64_t o = __shfl_sync(0xffffffffu, off, tok);
-            const bool on = o >= 0;
-            const uint64_t from = (on ? (uint64_t)o : 0) + piece * 16;
-            const uint32_t to = at + tok * SV + piece * 16;
-            copy16(to, a.pool.base[0] + from, on);
-            copy16(to + kTile * SV, a.pool.base[1] + from, on);
+            for (int k = 0; k < (kTile + kAtOnce - 1) / kAtOnce; ++k) {
+                const int tok = k * kAtOnce + lane_tok;
+                const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, at, tok & 31) * (uint32_t)vec_bytes(D);
+                if (lane_tok < kAtOnce && (kTile % kAtOnce == 0 || tok < kTile)) {
+                    copy16(dst + k * kAtOnce * SV, from_k + off, good >> (tok & 31) & 1);
+                    copy16(dst + k * kAtOnce * SV + kTile * SV, from_v + off, good >> (tok & 31) & 1);
+                }
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        return __ballot_sync(0xffffffffu, wrong);
-    };
-    auto load_or_not = [&](int stage, int t0) -> uint32_t {
-        if (t0 < c1) return load(stage, t0);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        return 0;
+        return wrong;
     };
 
     int t0 = c0 + warp * kTile;
-    uint32_t bad_now = load_or_not(0, t0), bad_next = load_or_not(1, t0 + kWarps * kTile);
+    constexpr int kTurn = kWarps * kTile;      // from a warp's tile to its next
+    look_up(t0);
+    uint32_t bad_now = load(0, t0);
+    look_up(t0 + kTurn);
+    uint32_t bad_next = load(1, t0 + kTurn);
+    look_up(t0 + 2 * kTurn);
 
     // Query rows as B fragments.  Each row is scaled by a power of two that
     // brings its largest value to 2^9..2^10, so that bf16 queries are exact in
@@ -303,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    for (int stage = 0; t0 < c1; t0 += kWarps * kTile, stage ^= 1) {
+    for (int stage = 0; t0 < c1; t0 += kTurn, stage ^= 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
         const uint32_t ks = ring + stage * (2 * kTile * SV), vs = ks + kTile * SV;
@@ -507,7 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         }
         __syncwarp();
         bad_now = bad_next;
-        bad_next = load_or_not(stage, t0 + kStages * kWarps * kTile);
+        bad_next = load(stage, t0 + kStages * kTurn);
+        look_up(t0 + (kStages + 1) * kTurn);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -720,9 +730,9 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     if (p.many) {
         plan_attend_tc(&p, span, requests, kv_heads, sms);
         p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
-    } else {             // about four blocks an SM, in chunks of at least a tile for each warp
+    } else {             // two blocks an SM (all that fit at once), in chunks of at least a tile for each warp
         const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
-        const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 4 + units - 1) / units);
+        const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 2 + units - 1) / units);
         const uint64_t unit = kWarps * kTile;
         uint64_t chunk = (span + want - 1) / want;
         chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);

@@ -121,6 +121,8 @@ kv_status pool_layer(const VecPool &p, uint32_t format, uint32_t head_dim, PoolL
     r.H = l.num_heads;
     r.B = B;
     r.P = l.num_pages;
+    r.v_page = (uint32_t)(r.s_page / B);
+    r.v_tok = r.s_tok / B;
     const FastDiv d = make_fastdiv(l.page_tokens);
     r.t_mul = d.m;
     r.t_shift = d.s;
@@ -154,6 +156,8 @@ kv_status check_attend(const kv_attend_args *a, const VecPool &p, PoolLayer *lay
         a->head_dim != 256)
         return fail(KV_ERR_LAYOUT, "head_dim %u: attention takes 64, 96, 128, 192 and 256", a->head_dim);
     TRY(pool_layer(p, KV_CACHE_Q4, a->head_dim, layer));
+    if (!vector_index_fits(*layer))
+        return fail(KV_ERR_LAYOUT, "the pool's pages span 2^32 head vectors or more");
     if (a->q_heads == 0 || a->q_heads % layer->H != 0)
         return fail(KV_ERR_INVALID_ARG, "%u query heads are not a multiple of the pool's %u", a->q_heads,
                     layer->H);

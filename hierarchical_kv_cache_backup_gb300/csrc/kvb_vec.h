@@ -26,6 +26,7 @@ struct PoolLayer {
     uint32_t s_tok;      // bytes between tokens of a page (a page is < 32 GiB / 16)
     uint32_t s_head;     // bytes between heads
     uint32_t T, H, B, P;
+    uint32_t v_page, v_tok;    // s_page and s_tok in vectors
     uint32_t t_mul, t_shift;   // division by T (FastDiv's m and s)
 };
 
@@ -67,6 +68,16 @@ KVB_HD int64_t page_offset(const PoolLayer &p, uint32_t page, uint32_t t, bool *
 // The same from the request's row of the page table.
 KVB_HD int64_t token_offset(const PoolLayer &p, const int32_t *table, uint32_t t, bool *wrong) {
     return page_offset(p, (uint32_t)table[div_T(p, t)], t, wrong);
+}
+
+// The same as a count of vectors, for a page inside the pool.  Every offset is a
+// whole number of vectors, and vector_index_fits says that all of them are below 2^32.
+KVB_HD uint32_t vector_index(const PoolLayer &p, uint32_t page, uint32_t t) {
+    return page * p.v_page + (t - div_T(p, t) * p.T) * p.v_tok;
+}
+
+KVB_HD bool vector_index_fits(const PoolLayer &p) {
+    return (uint64_t)p.P * (p.s_page / p.B) < (1ull << 32);
 }
 
 // What a tile of query rows sees.  Row x of a request is query head x % group

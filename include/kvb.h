@@ -607,7 +607,9 @@ KVB_API kv_status kv_fetch(kv_pool pool, const kv_fetch_args *args, void *stream
  * [0, tokens] or further apart than max_q is left out; both set BAD_LENGTH.
  * A page-table row holds ceil(max_len / T) entries that may be read (only those
  * inside lens[r] are used).  q and out hold `tokens` vectors.
- * head_dim: 64, 96, 128, 192 or 256 (LAYOUT otherwise).  Errors: INVALID_ARG,
+ * head_dim: 64, 96, 128, 192 or 256, and fewer than 2^32 head vectors between
+ * the layer's first and the pool's last (206 GB of D = 64, 343 GB of D = 128;
+ * LAYOUT otherwise).  Errors: INVALID_ARG,
  * CLOSED, STALE, OUT_OF_RANGE (layer; workspace too small), LAYOUT, ALIGNMENT
  * (q, out, or workspace not 16-B aligned), CUDA. */
 typedef struct {

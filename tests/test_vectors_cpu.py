@@ -38,6 +38,12 @@ void h_span(const int *in, int *out) {
     const Span s = row_span(in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], in[9], &bad);
     out[0] = s.n; out[1] = s.len; out[2] = s.q0; out[3] = s.lo; out[4] = s.hi; out[5] = bad;
 }
+int h_vector(const uint64_t *g, uint32_t B, uint32_t page, uint32_t t, uint32_t *out) {
+    PoolLayer p = layer(g);
+    p.B = B; p.v_page = (uint32_t)(p.s_page / B); p.v_tok = p.s_tok / B;
+    *out = vector_index(p, page, t);
+    return vector_index_fits(p);
+}
 float h_round(float x, float s) { return q4_round(x, s, 1.0f / s); }
 uint32_t h_step(float lo, float hi) { return q4_step_bits(lo, hi); }
 void h_encode(const float *x, uint32_t *word, uint32_t *code) {   // 32 finite values
@@ -74,6 +80,7 @@ def host(tmp_path_factory):
     lib.h_round.argtypes = [ctypes.c_float, ctypes.c_float]
     lib.h_step.restype = ctypes.c_uint32
     lib.h_step.argtypes = [ctypes.c_float, ctypes.c_float]
+    lib.h_vector.argtypes = [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint32, ctypes.c_uint32, ctypes.c_void_p]
     lib.h_span.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     lib.h_encode.argtypes = [ctypes.c_void_p] * 3
     return lib
@@ -112,6 +119,18 @@ def test_token_addresses_and_bad_pages(host):
             assert (off, wrong.value) == (page * s_page + (t % T) * s_tok, 0)
         else:
             assert (off, wrong.value) == (-1, 1)
+
+
+@pytest.mark.parametrize("T,s_page,P,fits", [(17, 70000 * 80, 60000, True), (16, 8 * 16 * 80, 2 ** 25 - 1, True),
+                                             (16, 8 * 16 * 80, 2 ** 25, False), (1, 80, 2 ** 31 - 1, True)])
+def test_vector_indexes(host, T, s_page, P, fits):
+    """Counts of vectors stay below 2^32, or the host refuses the pool."""
+    g, out = geom(s_page, 80, T, P), ctypes.c_uint32()
+    for page in (0, 1, P // 2, P - 1):
+        for t in (0, T - 1, 5 * T + T // 2):
+            assert host.h_vector(g.ctypes.data, 80, page, t, ctypes.byref(out)) == fits
+            if fits:
+                assert out.value * 80 == page * s_page + (t % T) * 80
 
 
 @pytest.mark.parametrize("group,rows", [(1, 8), (4, 8), (5, 8), (8, 8), (12, 16), (3, 16), (4, 128)])
