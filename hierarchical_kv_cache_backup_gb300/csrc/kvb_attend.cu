@@ -153,17 +153,28 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int H = (int)a.pool.H;
-    int bx = blockIdx.x;
-    const int head = bx % H;
-    bx /= H;
-    const int rt = bx % (int)a.row_tiles;
-    const int ci = bx / (int)a.row_tiles;
+    // every request's first chunk, which is the fullest, before any second one
+    const int head = blockIdx.x % H, rt = blockIdx.x / H, ci = blockIdx.z;
     const int r = blockIdx.y;
+    const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
+    constexpr int kTurn = kWarps * kTile;      // from a warp's tile to its next
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // Without a window the first tiles' places in the page table are known before the
+    // request's length is: their pages are read along with it (a row holds the pages
+    // of max_len tokens).  Lane i looks after token i of a tile.
+    int32_t page = 0, page1 = 0;
+    auto look_up = [&](int t, int end) {
+        return t < end ? table[div_T(a.pool, (uint32_t)t)] : 0;
+    };
+    if (!a.window) {
+        const int64_t t = (int64_t)ci * a.chunk + warp * kTile + lane;
+        if (t < (int64_t)a.max_len) page = look_up((int)t, (int)a.max_len);
+        if (t + kTurn < (int64_t)a.max_len) page1 = look_up((int)t + kTurn, (int)a.max_len);
+    }
     bool bad;
     const Span s = span_of<kRows>(a, r, rt, &bad);
-    if (bad && a.status != nullptr && threadIdx.x == 0 && blockIdx.x == 0)
+    if (bad && a.status != nullptr && threadIdx.x == 0 && blockIdx.x + blockIdx.z == 0)
         atomicOr(a.status, KV_STATUS_BAD_LENGTH);
     const int row0 = rt * kRows, rows = min(kRows, s.n * (int)a.group - row0);
     if (rows <= 0) return;
@@ -172,7 +183,26 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const bool whole = s.hi - s.lo <= (int)a.chunk;   // this block sees all the rows see
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * WB;
-    const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
+    const int group = (int)a.group;
+    // Row `row` of the tile as a new token and a head of the group; one new token needs
+    // no division.
+    auto new_token = [&](int row) { return kMany ? (row0 + row) / group : 0; };
+
+    // the query rows, read while the pages are
+    uint4 raw[NT][NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + g;
+        const bool on = row < rows;
+        const int i = on ? new_token(row) : 0, j = on ? row0 + row - i * group : 0;
+        const uint64_t src = a.q.data + (int64_t)(s.q0 + i) * a.q.s_tok + (int64_t)(head * group + j) * a.q.s_head;
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            raw[nt][gr] = make_uint4(0, 0, 0, 0);
+            if (on) raw[nt][gr] = *reinterpret_cast<const uint4 *>(src + (gr * 32 + c * 8) * 2);
+        }
+    }
+
     // Tiles are copied 16 bytes a lane, a vector's PV pieces by neighbouring lanes.
     // Lane i knows the place of token i, as a count of vectors, and hands it
     // round.  Page ids are read a tile before they are used.
@@ -181,13 +211,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const uint64_t from_k = a.pool.base[0] + (uint64_t)head * a.pool.s_head + piece * 16;
     const uint64_t from_v = a.pool.base[1] + (uint64_t)head * a.pool.s_head + piece * 16;
     const uint32_t to = ring + lane_tok * SV + piece * 16;
-    int32_t page = 0;
-    auto look_up = [&](int t0) {
-        const int t = t0 + lane;
-        page = t < c1 ? table[div_T(a.pool, (uint32_t)t)] : 0;
-    };
     // starts the copy of a tile; returns which of its tokens are in pages outside the pool
-    auto load = [&](int stage, int t0) -> uint32_t {
+    auto load = [&](int stage, int t0, int32_t page) -> uint32_t {
         uint32_t wrong = 0;
         if (t0 < c1) {
             const int t = t0 + lane;
@@ -211,12 +236,13 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     };
 
     int t0 = c0 + warp * kTile;
-    constexpr int kTurn = kWarps * kTile;      // from a warp's tile to its next
-    look_up(t0);
-    uint32_t bad_now = load(0, t0);
-    look_up(t0 + kTurn);
-    uint32_t bad_next = load(1, t0 + kTurn);
-    look_up(t0 + 2 * kTurn);
+    if (a.window) {
+        page = look_up(t0 + lane, c1);
+        page1 = look_up(t0 + kTurn + lane, c1);
+    }
+    uint32_t bad_now = load(0, t0, page);
+    uint32_t bad_next = load(1, t0 + kTurn, page1);
+    page = look_up(t0 + 2 * kTurn + lane, c1);
 
     // Query rows as B fragments.  Each row is scaled by a power of two that
     // brings its largest value to 2^9..2^10, so that bf16 queries are exact in
@@ -227,17 +253,10 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     int lim[NT][2], low[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int row = 8 * nt + g;
-        const bool on = row < rows;
-        const int i = on ? (row0 + row) / (int)a.group : 0;
-        const int j = on ? (row0 + row) - i * (int)a.group : 0;
-        const uint64_t src = a.q.data + (int64_t)(s.q0 + i) * a.q.s_tok +
-                             (int64_t)(head * (int)a.group + j) * a.q.s_head;
         float x[NG][8], top = 0.0f;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (on) u = *reinterpret_cast<const uint4 *>(src + (gr * 32 + c * 8) * 2);
+            const uint4 u = raw[nt][gr];
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -280,14 +299,14 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         for (int e = 0; e < 2; ++e) {
             qs[nt][e] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * e) * a.scale_log2 * 16777216.0f;
             const int col = 8 * nt + 2 * c + e;
-            const int pos = s.len - s.n + (row0 + col) / (int)a.group;
+            const int pos = s.len - s.n + new_token(col);
             lim[nt][e] = min(pos, s.len - 1);
             low[nt][e] = a.window ? pos - (int)a.window + 1 : 0;
         }
     }
     // a tile wholly inside [safe_lo, safe_hi) is seen by every row of the block
-    const int safe_hi = min(c1, s.len - s.n + row0 / (int)a.group + 1);
-    const int safe_lo = a.window ? s.len - s.n + (row0 + rows - 1) / (int)a.group - (int)a.window + 1 : 0;
+    const int safe_hi = kMany ? min(c1, s.len - s.n + new_token(0) + 1) : c1;
+    const int safe_lo = kMany && a.window ? s.len - s.n + new_token(rows - 1) - (int)a.window + 1 : 0;
 
     // lane constants of the fragments' addresses and of the zero points' places
     const uint32_t at_row = ((lane & 15) * SV) + (lane >> 4) * 16;    // rows 0..15, then the next group
@@ -370,7 +389,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     for (int e = 0; e < 4; ++e) {
                         const int in = 16 * sub + g + (e >= 2 ? 8 : 0), t = t0 + in;
                         if (bad_now >> in & 1) x[sub][nt][e] = __uint_as_float(kNanWord);
-                        if (t >= c1 || t > lim[nt][e & 1] || t < low[nt][e & 1])
+                        if (t >= c1 || (kMany && (t > lim[nt][e & 1] || t < low[nt][e & 1])))
                             x[sub][nt][e] = -INFINITY;
                     }
             if (bad_now != 0 && a.status != nullptr && lane == 0)
@@ -516,8 +535,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         }
         __syncwarp();
         bad_now = bad_next;
-        bad_next = load(stage, t0 + kStages * kTurn);
-        look_up(t0 + (kStages + 1) * kTurn);
+        bad_next = load(stage, t0 + kStages * kTurn, page);
+        page = look_up(t0 + (kStages + 1) * kTurn + lane, c1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             acc.z += v.z * k;
             acc.w += v.w * k;
         }
-        const int i = (row0 + row) / (int)a.group, j = (row0 + row) - i * (int)a.group;
+        const int i = new_token(row), j = row0 + row - i * group;
         const int64_t tok = s.q0 + i;
         const int qh = head * (int)a.group + j;
         if (whole) {
@@ -732,7 +751,7 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
         p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
     } else {             // two blocks an SM (all that fit at once), in chunks of at least a tile for each warp
         const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
-        const uint64_t want = std::max<uint64_t>(1, ((uint64_t)sms * 2 + units - 1) / units);
+        const uint64_t want = std::max<uint64_t>(1, (uint64_t)sms * 2 / units);
         const uint64_t unit = kWarps * kTile;
         uint64_t chunk = (span + want - 1) / want;
         chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);
@@ -753,7 +772,7 @@ cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, 
     const bool many = a.max_q > 1;
     for (const Variant &v : kVariants) {
         if (v.D != D || v.rows != p.rows || v.fp16 != fp16 || v.many != many) continue;
-        const dim3 grid(a.pool.H * p.row_tiles * p.chunks, a.requests);
+        const dim3 grid(a.pool.H * p.row_tiles, a.requests, p.chunks);
         cudaError_t e = launch(v.rows_fn, grid, kWarps * 32, v.smem, stream, pdl, a);
         if (e != cudaSuccess) return e;
         ++*launches;

@@ -456,7 +456,7 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     const AttendPlan plan = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, a->window,
                                         a->q_heads, k.pool.H, a->head_dim, p.sms);
     if ((uint64_t)plan.row_tiles * plan.chunks * k.pool.H * (plan.many ? a->requests : 1) > 0x7fffffffull ||
-        plan.step_parts > 65535)
+        plan.step_parts > 65535 || plan.chunks > 65535)
         return fail(KV_ERR_INVALID_ARG, "max_q %u and max_len %u make too many blocks", a->max_q,
                     a->max_len);
     if (plan.bytes != 0 && a->workspace == nullptr)
