@@ -276,24 +276,23 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         // 2^(9 - exponent of top), and its inverse; 1 for zeros and infinities
         const uint32_t ex = __float_as_uint(top) >> 23;
         const bool scaled = ex >= 10 && ex < 255;
-        const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f;
+        const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f, up16 = 0.0625f * up;
         const float back = scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f;
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-            float y[8], sum = 0.0f;
+            float part[2] = {0.0f, 0.0f};     // those that meet even and odd codes
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float k = e & 1 ? 0.0625f : 1.0f;
-                y[e] = __half2float(__float2half_rn(x[gr][e] * up * k));
-                sum += e & 1 ? 16.0f * y[e] : y[e];
+            for (int e = 0; e < 4; ++e) {
+                const float y0 = x[gr][e] * (e & 1 ? up16 : up), y1 = x[gr][e + 4] * (e & 1 ? up16 : up);
+                qf[nt][gr][e] = half2_bits(y0, y1);
+                part[e & 1] += y0 + y1;
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) qf[nt][gr][e] = half2_bits(y[e], y[e + 4]);
+            float sum = -16.0f * part[1] - part[0];
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const float h0 = __half2float(__float2half_rn(-sum));
-            const float h1 = __half2float(__float2half_rn(-sum - h0));
-            qz[nt][gr] = c == 0 ? half2_bits(h0, h1) : c == 1 ? half2_bits(-sum - h0 - h1, 0.0f) : 0u;
+            const float h0 = __half2float(__float2half_rn(sum));
+            const float h1 = __half2float(__float2half_rn(sum - h0));
+            qz[nt][gr] = c == 0 ? half2_bits(h0, h1) : c == 1 ? half2_bits(sum - h0 - h1, 0.0f) : 0u;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -557,15 +556,15 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                // undo f and the subnormals' 2^-24 (2^-20 for odd codes); f is a power of two
-                const float k = __shfl_sync(0xffffffffu, oz[nt][e], 4 * gr + c);
-                const float back = 1.0f / f[gr];
-                float4 v = make_float4(o[gr][0][nt][e] - k, o[gr][0][nt][e + 2] * 0.0625f - k,
-                                       o[gr][1][nt][e] - k, o[gr][1][nt][e + 2] * 0.0625f - k);
-                v.x = v.x * 16777216.0f * back;
-                v.y = v.y * 16777216.0f * back;
-                v.z = v.z * 16777216.0f * back;
-                v.w = v.w * 16777216.0f * back;
+                // undo f, a power of two, and the subnormals' 2^-24 (2^-20 for odd codes)
+                const float k = __shfl_sync(0xffffffffu, oz[nt][e], 4 * gr + c) * -16777216.0f;
+                const float back = __uint_as_float((254u << 23) - __float_as_uint(f[gr]));
+                float4 v = make_float4(o[gr][0][nt][e] * 16777216.0f + k, o[gr][0][nt][e + 2] * 1048576.0f + k,
+                                       o[gr][1][nt][e] * 16777216.0f + k, o[gr][1][nt][e + 2] * 1048576.0f + k);
+                v.x *= back;
+                v.y *= back;
+                v.z *= back;
+                v.w *= back;
                 *reinterpret_cast<float4 *>(mine + row * (D + 4) + gr * 32 + 4 * g) = v;
             }
         }
@@ -617,79 +616,70 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     }
 }
 
-// Joins the chunks of a row: one block a query head and token, 4 warps over the
-// chunks, a lane 4 values (twice for D > 128).
-template <int D, int kRows, bool kHalf>
+// Joins the chunks of a row (a query head and token): kW warps a row, each over
+// every kW-th chunk, a lane D / 32 values.  Rows of few chunks take one warp, four rows a
+// block; with many the parts are too long a chain for one.
+template <int D, int kRows, bool kHalf, int kW>
 __global__ void __launch_bounds__(128) kv_attend_join_kernel(const __grid_constant__ AttendArgs a) {
-    constexpr int kW = 4, NV = (D + 127) / 128;
-    __shared__ __align__(16) float acc_s[kW][D];
-    __shared__ float m_s[kW], l_s[kW];
+    constexpr int NV = D / 32;
+    __shared__ float acc_s[kW][D], m_s[kW], l_s[kW];
     asm volatile("griddepcontrol.launch_dependents;");
-    const int qh = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int qh = kW == 1 ? blockIdx.x * 4 + warp : blockIdx.x, part = kW == 1 ? 0 : warp;
     const int i = blockIdx.y, r = blockIdx.z;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (qh >= (int)a.q_heads) return;
     bool bad;
     const int j = qh % (int)a.group;
     const Span s = span_of<kRows>(a, r, (i * (int)a.group + j) / kRows, &bad);
     const int n = (s.hi - s.lo + (int)a.chunk - 1) / (int)a.chunk;
     if (i >= s.n || n <= 1) return;
     const int64_t tok = s.q0 + i;
-    float top = kNoMax, sum = 0.0f;
-    float4 acc[NV];
+    float top = kNoMax, sum = 0.0f, acc[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0, 0, 0, 0);
+    for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
 #pragma unroll 4
-    for (int k = warp; k < n; k += kW) {
+    for (int k = part; k < n; k += kW) {
         const int64_t at = ((int64_t)k * a.tokens + tok) * a.q_heads + qh;
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-        float4 x[NV];
+        float x[NV];
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (v * 128 + lane * 4 < D)
-                x[v] = *reinterpret_cast<const float4 *>(a.part_o + at * D + v * 128 + lane * 4);
+        for (int v = 0; v < NV; ++v) x[v] = a.part_o[at * D + v * 32 + lane];
         if (ml.y == 0.0f) continue;
-        const float t = fmaxf(top, ml.x), u = exp2f(top - t), w = exp2f(ml.x - t);
+        const float t = fmaxf(top, ml.x), u = exp2_fast(top - t), w = exp2_fast(ml.x - t);
         top = t;
         sum = sum * u + ml.y * w;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            acc[v].x = acc[v].x * u + x[v].x * w;
-            acc[v].y = acc[v].y * u + x[v].y * w;
-            acc[v].z = acc[v].z * u + x[v].z * w;
-            acc[v].w = acc[v].w * u + x[v].w * w;
+        for (int v = 0; v < NV; ++v) acc[v] = acc[v] * u + x[v] * w;
+    }
+    if (kW > 1) {
+        if (lane == 0) {
+            m_s[warp] = top;
+            l_s[warp] = sum;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc_s[warp][v * 32 + lane] = acc[v];
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < kW; ++w) {
+            if (l_s[w] == 0.0f) continue;
+            const float t = fmaxf(top, m_s[w]), u = exp2_fast(top - t), k = exp2_fast(m_s[w] - t);
+            top = t;
+            sum = sum * u + l_s[w] * k;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] = acc[v] * u + acc_s[w][v * 32 + lane] * k;
         }
     }
-    if (lane == 0) {
-        m_s[warp] = top;
-        l_s[warp] = sum;
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-        if (v * 128 + lane * 4 < D)
-            *reinterpret_cast<float4 *>(&acc_s[warp][v * 128 + lane * 4]) = acc[v];
-    __syncthreads();
-    float most = kNoMax, all = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) most = fmaxf(most, l_s[w] != 0.0f ? m_s[w] : kNoMax);
-    float k[kW];
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-        k[w] = l_s[w] != 0.0f ? exp2f(m_s[w] - most) : 0.0f;
-        all += l_s[w] * k[w];
-    }
-    const float inv = all != 0.0f ? 1.0f / all : 0.0f;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head;
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) y += acc_s[w][d] * k[w];
-        y *= inv;
-        if (kHalf) *reinterpret_cast<__half *>(dst + 2 * d) = __float2half_rn(y);
-        else *reinterpret_cast<__nv_bfloat16 *>(dst + 2 * d) = __float2bfloat16_rn(y);
+    for (int v = 0; v < NV; ++v) {
+        const uint64_t to = dst + 2 * (v * 32 + lane);
+        if (kHalf) *reinterpret_cast<__half *>(to) = __float2half_rn(acc[v] * inv);
+        else *reinterpret_cast<__nv_bfloat16 *>(to) = __float2bfloat16_rn(acc[v] * inv);
     }
-    if (threadIdx.x == 0 && a.lse != nullptr)
-        a.lse[tok * a.q_heads + qh] =
-            all != 0.0f ? (most + log2f(all)) * 0.693147180559945f : -INFINITY;
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
 }
 
 // ------------------------------------------------------------------ launches
@@ -714,14 +704,15 @@ typedef void(AttendFn)(AttendArgs);
 struct Variant {
     uint32_t D, rows;
     bool fp16, many;
-    AttendFn *rows_fn, *join_fn;
+    AttendFn *rows_fn, *join_fn, *join4_fn;
     int smem;
 };
 
 template <int D, int NT, bool kHalf, bool kMany>
 constexpr Variant variant() {
     return Variant{(uint32_t)D, 8u * NT, kHalf, kMany, kv_attend_rows_kernel<D, NT, kHalf, kMany>,
-                   kv_attend_join_kernel<D, 8 * NT, kHalf>, kWarps * warp_bytes(D, NT)};
+                   kv_attend_join_kernel<D, 8 * NT, kHalf, 1>,
+                   kv_attend_join_kernel<D, 8 * NT, kHalf, 4>, kWarps * warp_bytes(D, NT)};
 }
 
 #define KVB_VARIANTS(D, NT)                                                                       \
@@ -749,14 +740,31 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     if (p.many) {
         plan_attend_tc(&p, span, requests, kv_heads, sms);
         p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
-    } else {             // two blocks an SM (all that fit at once), in chunks of at least a tile for each warp
+    } else {
+        // Cut along the cached tokens into the number of chunks that ends soonest, by a
+        // model in tokens of one block: what all blocks read spread over the blocks
+        // that fit at once (requests of a batch taken as three quarters of the longest),
+        // half a chunk lost at the end when there is more than one wave, never less
+        // than a chunk; a block begins and ends in the time of 350 tokens, and parts
+        // are joined in that of 500.  64 requests of up to 8,192 tokens and 8 heads, 1 /
+        // 2 / 3 chunks: 144 / 142 / 141 us; 32 of them 88 / 82 / 79; 64 of up to 2,048
+        // 49 / 56 / 58; 24 of 2,016 of 4 heads of 64, 2 / 3 / 4 chunks: 21.5 / 18.8 / 22.5.
+        const uint64_t slots = (uint64_t)sms * (D * (p.rows / 8) <= 128 ? 2 : 1), unit = kWarps * kTile;
         const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
-        const uint64_t want = std::max<uint64_t>(1, (uint64_t)sms * 2 / units);
-        const uint64_t unit = kWarps * kTile;
-        uint64_t chunk = (span + want - 1) / want;
-        chunk = std::max<uint64_t>(unit, (chunk + unit - 1) / unit * unit);
-        p.chunk = (uint32_t)chunk;
-        p.chunks = (uint32_t)std::max<uint64_t>(1, (span + chunk - 1) / chunk);
+        const double spread = (requests > 1 ? 0.75 : 1.0) * (double)units * (double)span / (double)slots;
+        double best = 1e300;
+        for (uint64_t c : {(uint64_t)1, (uint64_t)2, (uint64_t)3, (uint64_t)4, (uint64_t)6, slots / units}) {
+            if (c == 0 || (c > 1 && span <= (c - 1) * unit)) continue;
+            const uint64_t chunk = std::max<uint64_t>(unit, ((span + c - 1) / c + unit - 1) / unit * unit);
+            const uint64_t waves = (units * c + slots - 1) / slots;
+            const double cost = std::max(spread + (waves > 1 ? 0.5 * chunk : 0.0), (double)chunk) + 350.0 * waves +
+                                (c > 1 ? 500.0 : 0.0);
+            if (cost < best) {
+                best = cost;
+                p.chunk = (uint32_t)chunk;
+            }
+        }
+        p.chunks = (uint32_t)std::max<uint64_t>(1, (span + p.chunk - 1) / p.chunk);
     }
     p.bytes = p.step_bytes;
     if (p.chunks > 1) p.bytes += (uint64_t)p.chunks * tokens * q_heads * (D + 2) * sizeof(float);
@@ -777,7 +785,10 @@ cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, 
         if (e != cudaSuccess) return e;
         ++*launches;
         if (p.chunks > 1) {
-            e = launch(v.join_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
+            if (p.chunks <= 6)
+                e = launch(v.join_fn, dim3((a.q_heads + 3) / 4, a.max_q, a.requests), 128, 0, stream, pdl, a);
+            else
+                e = launch(v.join4_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
             if (e == cudaSuccess) ++*launches;
         }
         return e;
@@ -793,6 +804,7 @@ cudaError_t preload_attend_kernels() {
             e = cudaFuncSetAttribute((const void *)v.rows_fn,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
         if (e != cudaSuccess) return e;
     }
     return preload_attend_tc_kernels();
