@@ -198,6 +198,7 @@ struct VectorArgs {
     uint32_t tokens, q_heads, kv_heads, D;
     uint32_t half, style;     // half = 0: no rotation
     uint32_t per_block;       // vectors a block handles per token
+    uint32_t token_a_warp;    // a warp handles a token by itself
     float k_inv, v_inv;       // E4M3: 1 / scale (append), scale (fetch)
     float sin_sign;
 };

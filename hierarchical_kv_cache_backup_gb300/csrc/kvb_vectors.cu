@@ -13,6 +13,7 @@ namespace kvb {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr uint32_t kTokenAWarp = 4096;   // tokens from which a warp takes one by itself
 
 template <bool kHalf>
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
@@ -105,8 +106,10 @@ __device__ __forceinline__ void store8(uint64_t vec, uint32_t chunk, const float
 
 // ------------------------------------------------------- rotate and append
 //
-// One block takes one token and `per_block` of its vectors (queries, keys and
-// values in that order).  A lane owns the same values of every vector that it
+// With many tokens a warp takes one token and all its vectors (what a token costs
+// once -- its slot, cosines and sines -- is then paid once); with few, a block takes
+// one token and `per_block` of its vectors.  Queries come first, then keys, then
+// values.  A lane owns the same values of every vector that it
 // meets, so the token's cosines and sines go to registers once and serve all
 // heads.  Vectors never straddle warps, and a warp loads before it stores, so
 // a vector may be turned in place.
@@ -124,10 +127,14 @@ template <int kFormat, bool kHalf, bool kPair>
 __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_constant__ VectorArgs a,
                                                               const __grid_constant__ RotaryK r) {
     constexpr int kRuns = kPair ? 2 : 1;
-    __shared__ __align__(16) float rows[2][kMaxPairs];
+    __shared__ __align__(16) float all_rows[kThreads / 32][2][kMaxPairs];
     asm volatile("griddepcontrol.launch_dependents;");
-    const uint32_t token = blockIdx.x;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool alone = a.token_a_warp != 0;           // this warp has a token to itself
+    const uint32_t token = alone ? blockIdx.x * (kThreads / 32) + warp : blockIdx.x;
+    if (token >= a.tokens) return;
+    float(*rows)[kMaxPairs] = all_rows[alone ? warp : 0];
+    const uint32_t first = alone ? lane : threadIdx.x, stride = alone ? 32 : kThreads;
     const uint32_t per_vec = a.D / (8 * kRuns), per_warp = 32 / per_vec;
     const uint32_t sub = lane / per_vec, place = lane - sub * per_vec;
     const uint32_t half = a.half, total = a.q_heads + 2 * a.kv_heads;
@@ -141,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
 
     int64_t off = -1, slot = -1;
     if (kFormat >= 0) slot = a.slots[token];
-    for (uint32_t i = threadIdx.x; i < half; i += kThreads) {
+    for (uint32_t i = first; i < half; i += stride) {
         float c, s;
         if (kFormat == -1 && a.positions != nullptr) {
             // the phase as a signed 64-bit fraction of a turn, then in half turns
@@ -165,10 +172,13 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
     }
     if (kFormat >= 0) {
         off = slot_offset(a.pool, slot);
-        if (off < 0 && slot != -1 && a.status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
+        if (off < 0 && slot != -1 && a.status != nullptr && first == 0 && blockIdx.y == 0)
             atomicOr(a.status, KV_STATUS_BAD_SLOT);
     }
-    __syncthreads();
+    if (alone)
+        __syncwarp();
+    else
+        __syncthreads();
 
     // cosines and sines of this lane's values: kPair HALF 8 pairs; kPair
     // INTERLEAVED 4 pairs of each run; else one for each value, signed
@@ -198,114 +208,130 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
         }
     }
 
-    const uint32_t end = min(total, (blockIdx.y + 1) * a.per_block);
-    constexpr int kBatch = 2;   // vectors in flight per lane
-    for (uint32_t v0 = blockIdx.y * a.per_block + warp * per_warp; v0 < end;
-         v0 += kBatch * per_warp * (kThreads / 32)) {
-        uint4 own[kBatch][2];   // this lane's runs; !kPair: its run and the partners
-        uint64_t src[kBatch];
-        bool live[kBatch], turn[kBatch];
+    // y <- this lane's values of a vector, turned
+    auto turn = [&](const uint4 *own, uint64_t src, float(*y)[8]) {
+        float x[2][8];
+        unpack8<kHalf>(own[0], x[0]);
+        unpack8<kHalf>(own[1], x[1]);
+        if (kPair && a.style == 0) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const uint32_t v = v0 + b * per_warp * (kThreads / 32) + sub;
-            const bool is_q = v < a.q_heads, is_k = !is_q && v < a.q_heads + a.kv_heads;
-            live[b] = sub < per_warp && v < end && (is_q || off >= 0);
-            turn[b] = live[b] && turned && (is_q || is_k);
-            const Vecs &x = is_q ? a.q : is_k ? a.k : a.v;
-            const uint32_t h = is_q ? v : is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
-            src[b] = x.data + (int64_t)token * x.s_tok + (int64_t)h * x.s_head;
-            own[b][0] = own[b][1] = make_uint4(0, 0, 0, 0);
-            if (live[b]) {
-                own[b][0] = *reinterpret_cast<const uint4 *>(src[b] + run[0] * 16);
-                if (kPair) own[b][1] = *reinterpret_cast<const uint4 *>(src[b] + run[kRuns - 1] * 16);
+            for (int e = 0; e < 8; ++e) {
+                y[0][e] = __fsub_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]));
+                y[kRuns - 1][e] = __fadd_rn(__fmul_rn(x[0][e], sn[e]), __fmul_rn(x[1][e], cs[e]));
             }
-            if (!kPair && turn[b] && a.style == 0 && aligned)
-                own[b][1] = *reinterpret_cast<const uint4 *>(
-                    src[b] + (place * 8 < half ? place * 8 + half : place * 8 - half) * 2);
-        }
+        } else if (kPair) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const uint32_t v = v0 + b * per_warp * (kThreads / 32) + sub;
-            const bool is_q = v < a.q_heads;
-            float y[kRuns][8];
-            const bool need = turn[b] || (kFormat > 0 && live[b] && !is_q);
-            if (need) {
-                float x[2][8];
-                unpack8<kHalf>(own[b][0], x[0]);
-                unpack8<kHalf>(own[b][1], x[1]);
+            for (int k = 0; k < kRuns; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[k][2 * e], w = x[k][2 * e + 1];
+                    const float c = cs[4 * k + e], s = sn[4 * k + e];
+                    y[k][2 * e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
+                    y[k][2 * e + 1] = __fadd_rn(__fmul_rn(u, s), __fmul_rn(w, c));
+                }
+        } else {
+            if (a.style == 1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[1][e] = x[0][e ^ 1];
+            } else if (!aligned) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    y[0][e] = x[0][e];
-                    if (kPair) y[kRuns - 1][e] = x[1][e];
+                    const uint32_t d = place * 8 + e;
+                    x[1][e] = d < 2 * half ? one<kHalf>(src + (d < half ? d + half : d - half) * 2) : 0.0f;
                 }
-                if (turn[b]) {
-                    if (kPair && a.style == 0) {
+            }
+            // values past the rotated part keep their bits
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            y[0][e] = __fsub_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]));
-                            y[kRuns - 1][e] = __fadd_rn(__fmul_rn(x[0][e], sn[e]),
-                                                        __fmul_rn(x[1][e], cs[e]));
-                        }
-                    } else if (kPair) {
+            for (int e = 0; e < 8; ++e)
+                y[0][e] = place * 8 + e < 2 * half
+                              ? __fadd_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]))
+                              : x[0][e];
+        }
+    };
+    auto read = [&](uint4 *own, uint64_t src, bool partners) {
+        own[0] = *reinterpret_cast<const uint4 *>(src + run[0] * 16);
+        if (kPair)
+            own[1] = *reinterpret_cast<const uint4 *>(src + run[kRuns - 1] * 16);
+        else if (partners && a.style == 0 && aligned)
+            own[1] = *reinterpret_cast<const uint4 *>(
+                src + (place * 8 < half ? place * 8 + half : place * 8 - half) * 2);
+    };
+
+    // the vectors of this block, or of the token; this warp's first and its step
+    const uint32_t lo = alone ? 0 : blockIdx.y * a.per_block;
+    const uint32_t hi = alone ? total : min(total, (blockIdx.y + 1) * a.per_block);
+    const uint32_t at = alone ? 0 : warp * per_warp, step = alone ? per_warp : per_warp * (kThreads / 32);
+    constexpr int kBatch = 2;   // vectors in flight per lane
+
+    const uint32_t q_end = min(hi, a.q_heads);
+    if (lo + at < q_end) {
+        uint64_t src = a.q.data + (int64_t)token * a.q.s_tok + (int64_t)(lo + at + sub) * a.q.s_head;
+        uint64_t dst = a.q_out.data + (int64_t)token * a.q_out.s_tok + (int64_t)(lo + at + sub) * a.q_out.s_head;
+        const int64_t src_step = (int64_t)step * a.q.s_head, dst_step = (int64_t)step * a.q_out.s_head;
+        for (uint32_t v0 = lo + at; v0 < q_end; v0 += kBatch * step) {
+            uint4 own[kBatch][2];
+            bool live[kBatch];
 #pragma unroll
-                        for (int k = 0; k < kRuns; ++k)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float u = x[k][2 * e], w = x[k][2 * e + 1];
-                                const float c = cs[4 * k + e], s = sn[4 * k + e];
-                                y[k][2 * e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
-                                y[k][2 * e + 1] = __fadd_rn(__fmul_rn(u, s), __fmul_rn(w, c));
-                            }
-                    } else {
-                        if (a.style == 1) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[1][e] = x[0][e ^ 1];
-                        } else if (!aligned) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t d = place * 8 + e;
-                                x[1][e] = d < 2 * half
-                                              ? one<kHalf>(src[b] + (d < half ? d + half : d - half) * 2)
-                                              : 0.0f;
-                            }
-                        }
-                        // values past the rotated part keep their bits
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (place * 8 + e < 2 * half)
-                                y[0][e] = __fadd_rn(__fmul_rn(x[0][e], cs[e]), __fmul_rn(x[1][e], sn[e]));
-                    }
-                }
+            for (int b = 0; b < kBatch; ++b) {
+                live[b] = sub < per_warp && v0 + b * step + sub < q_end;
+                own[b][0] = own[b][1] = make_uint4(0, 0, 0, 0);
+                if (live[b]) read(own[b], src + b * src_step, turned);
             }
             __syncwarp();
-            const bool is_k = !is_q && v < a.q_heads + a.kv_heads;
-            if (live[b] && (is_q || kFormat == 0)) {
-                uint64_t dst;
-                if (is_q) {
-                    dst = a.q_out.data + (int64_t)token * a.q_out.s_tok + (int64_t)v * a.q_out.s_head;
-                } else {
-                    const uint32_t h = is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
-                    dst = a.pool.base[is_k ? 0 : 1] + (uint64_t)off + (uint64_t)h * a.pool.s_head;
-                }
 #pragma unroll
-                for (int k = 0; k < kRuns; ++k)
-                    *reinterpret_cast<uint4 *>(dst + run[k] * 16) = turn[b] ? pack8<kHalf>(y[k])
-                                                                            : own[b][k];
-            }
-            // a warp of queries only has nothing to hold
-            if (kFormat > 0 && __any_sync(0xffffffffu, live[b] && !is_q)) {
-                const uint32_t h = is_k ? v - a.q_heads : v - a.q_heads - a.kv_heads;
-                const uint64_t vec = a.pool.base[is_k ? 0 : 1] + (uint64_t)off +
-                                     (uint64_t)h * a.pool.s_head;
-                if (!need)
+            for (int b = 0; b < kBatch; ++b) {
+                float y[kRuns][8];
+                if (turned && live[b]) turn(own[b], src + b * src_step, y);
+                __syncwarp();      // unaligned partners are read by turn()
+                if (live[b])
 #pragma unroll
                     for (int k = 0; k < kRuns; ++k)
+                        *reinterpret_cast<uint4 *>(dst + b * dst_step + run[k] * 16) =
+                            turned ? pack8<kHalf>(y[k]) : own[b][k];
+            }
+            src += kBatch * src_step;
+            dst += kBatch * dst_step;
+        }
+    }
+    if (kFormat >= 0 && off >= 0) {
+        for (uint32_t v0 = max(lo, a.q_heads) + at; v0 < hi; v0 += kBatch * step) {
+            uint4 own[kBatch][2];
+            uint64_t src[kBatch], vec[kBatch];
+            bool live[kBatch], is_k[kBatch];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[k][e] = 0.0f;
+            for (int b = 0; b < kBatch; ++b) {
+                const uint32_t u = v0 + b * step + sub - a.q_heads;
+                is_k[b] = u < a.kv_heads;
+                live[b] = sub < per_warp && v0 + b * step + sub < hi;
+                const uint32_t h = is_k[b] ? u : u - a.kv_heads;
+                src[b] = is_k[b] ? a.k.data + (int64_t)token * a.k.s_tok + (int64_t)h * a.k.s_head
+                                 : a.v.data + (int64_t)token * a.v.s_tok + (int64_t)h * a.v.s_head;
+                vec[b] = (is_k[b] ? a.pool.base[0] : a.pool.base[1]) + (uint64_t)off +
+                         (uint64_t)h * a.pool.s_head;
+                own[b][0] = own[b][1] = make_uint4(0, 0, 0, 0);
+                if (live[b]) read(own[b], src[b], turned && is_k[b]);
+            }
 #pragma unroll
-                for (int k = 0; k < kRuns; ++k)
-                    store8<kFormat, kHalf>(vec, run[k], y[k], a.D, a.pool.B, is_k ? a.k_inv : a.v_inv,
-                                           live[b] && !is_q);
+            for (int b = 0; b < kBatch; ++b) {
+                if (v0 + b * step >= hi) break;        // the whole warp
+                const bool to_turn = turned && is_k[b];
+                float y[kRuns][8];
+                unpack8<kHalf>(own[b][0], y[0]);
+                if (kPair) unpack8<kHalf>(own[b][1], y[kRuns - 1]);
+                if (to_turn && live[b]) turn(own[b], src[b], y);
+                if (kFormat == 0) {
+                    if (live[b])
+#pragma unroll
+                        for (int k = 0; k < kRuns; ++k)
+                            *reinterpret_cast<uint4 *>(vec[b] + run[k] * 16) =
+                                to_turn ? pack8<kHalf>(y[k]) : own[b][k];
+                } else {
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kRuns; ++k)
+                        store8<kFormat, kHalf>(vec[b], run[k], y[k], a.D, a.pool.B,
+                                               is_k[b] ? a.k_inv : a.v_inv, live[b]);
+                }
             }
         }
     }
@@ -313,24 +339,27 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
 
 // -------------------------------------------------------------------- fetch
 //
-// The same mapping: one block takes one token, a lane 8 values of a vector.
+// The same mapping, a lane 8 values of a vector.
 template <int kFormat, bool kHalf>
 __global__ void __launch_bounds__(kThreads) kv_fetch_kernel(const __grid_constant__ VectorArgs a) {
     asm volatile("griddepcontrol.launch_dependents;");
-    const uint32_t token = blockIdx.x;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool alone = a.token_a_warp != 0;
+    const uint32_t token = alone ? blockIdx.x * (kThreads / 32) + warp : blockIdx.x;
+    if (token >= a.tokens) return;
     const uint32_t per_vec = a.D / 8, per_warp = 32 / per_vec;
     const uint32_t sub = lane / per_vec, chunk = lane - sub * per_vec;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t slot = a.slots[token];
     const int64_t off = slot_offset(a.pool, slot);
-    if (off < 0 && slot != -1 && a.status != nullptr && threadIdx.x == 0 && blockIdx.y == 0)
+    if (off < 0 && slot != -1 && a.status != nullptr && (alone ? lane : threadIdx.x) == 0 && blockIdx.y == 0)
         atomicOr(a.status, KV_STATUS_BAD_SLOT);
     if (sub >= per_warp) return;
-    const uint32_t end = min(2 * a.kv_heads, (blockIdx.y + 1) * a.per_block);
-#pragma unroll 2
-    for (uint32_t v = blockIdx.y * a.per_block + warp * per_warp + sub; v < end;
-         v += per_warp * (kThreads / 32)) {
+    const uint32_t lo = alone ? 0 : blockIdx.y * a.per_block + warp * per_warp;
+    const uint32_t end = alone ? 2 * a.kv_heads : min(2 * a.kv_heads, (blockIdx.y + 1) * a.per_block);
+    const uint32_t step = alone ? per_warp : per_warp * (kThreads / 32);
+#pragma unroll 4
+    for (uint32_t v = lo + sub; v < end; v += step) {
         const bool is_k = v < a.kv_heads;
         const uint32_t h = is_k ? v : v - a.kv_heads;
         const Vecs &x = is_k ? a.k : a.v;
@@ -358,10 +387,24 @@ __global__ void __launch_bounds__(kThreads) kv_fetch_kernel(const __grid_constan
                     const uint32_t w = *reinterpret_cast<const uint32_t *>(vec + chunk * 4);
                     const uint32_t word =
                         *reinterpret_cast<const uint32_t *>(vec + a.D / 2 + (chunk & ~3u));
-                    const float s = q4_step(word), z = (float)(word & 15u);
+                    // code x 2^-24 as fp16 subnormals; (code - z) s has at most 24 bits, and so
+                    // have code x s and z x s: one fma gives it exactly
+                    const float s = q4_step(word), less = -(float)(word & 15u) * s;
+                    const float s24 = s * 16777216.0f, s20 = s * 1048576.0f;
+                    const uint32_t u = w >> 8;
+                    const uint32_t p[4] = {w & 0x000f000fu, w & 0x00f000f0u, u & 0x000f000fu, u & 0x00f000f0u};
+                    if (s < 1e30f) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = __fmul_rn((float)((w >> (4 * i)) & 15u) - z, s);
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&p[i]));
+                            y[i] = __fmaf_rn(c.x, i & 1 ? s20 : s24, less);
+                            y[i + 4] = __fmaf_rn(c.y, i & 1 ? s20 : s24, less);
+                        }
+                    } else {        // s x 2^24 would pass float32, or s is NaN
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = __fmul_rn((float)((w >> (4 * i)) & 15u) - (float)(word & 15u), s);
+                    }
                 }
                 out = pack8<kHalf>(y);
             }
@@ -395,18 +438,23 @@ const FetchFn kFetch[3][2] = {{kv_fetch_kernel<0, false>, kv_fetch_kernel<0, tru
                               {kv_fetch_kernel<1, false>, kv_fetch_kernel<1, true>},
                               {kv_fetch_kernel<2, false>, kv_fetch_kernel<2, true>}};
 
-// Vectors a block takes: all of a token's when there are tokens enough to fill
-// the GPU, else so few that the blocks do (a block's 4 warps take
-// 4 x per_warp at a time; lanes is what a vector takes of a warp).
-uint32_t per_block_of(uint32_t tokens, uint32_t vectors, uint32_t lanes) {
+// With tokens enough a warp takes a token (append and fetch of 8,192 tokens 61 ->
+// 54 us, of 5,000 28.5 -> 25.9, but of 2,000 19 -> 24); with fewer, a block takes so few of a token's vectors that the blocks fill the
+// GPU (its 4 warps take 4 x per_warp at a time; lanes is what a vector takes of a
+// warp).  Returns the grid.
+dim3 grid_of(VectorArgs *a, uint32_t vectors, uint32_t lanes) {
     const uint32_t at_once = (32 / lanes) * (kThreads / 32);
     uint32_t steps = (vectors + at_once - 1) / at_once;
     if (steps < 1) steps = 1;   // rows of angles alone
-    const uint64_t blocks = (uint64_t)tokens * steps;
+    a->token_a_warp = a->tokens >= kTokenAWarp;
+    if (a->token_a_warp) return dim3((a->tokens + kThreads / 32 - 1) / (kThreads / 32));
+    const uint64_t blocks = (uint64_t)a->tokens * steps;
     uint64_t each = blocks / (152 * 8);
     if (each < 1) each = 1;
     if (each > steps) each = steps;
-    return (uint32_t)each * at_once;
+    a->per_block = (uint32_t)each * at_once;
+    const uint32_t y = (vectors + a->per_block - 1) / a->per_block;
+    return dim3(a->tokens, y != 0 ? y : 1);
 }
 
 }  // namespace
@@ -419,16 +467,13 @@ cudaError_t launch_vectors(VectorArgs a, const RotaryK &r, int format, bool fp16
     // 4-bit groups, four lanes at a time
     const uint32_t unit = format == KV_CACHE_Q4 ? 64 : 16;
     const bool pair = 2 * a.half % unit == 0 && (a.D - 2 * a.half) % unit == 0;
-    a.per_block = per_block_of(a.tokens, vectors, a.D / (pair ? 16 : 8));
-    const uint32_t blocks = (vectors + a.per_block - 1) / a.per_block;
-    const dim3 grid(a.tokens, blocks != 0 ? blocks : 1);   // no vectors: the rows alone
+    const dim3 grid = grid_of(&a, vectors, a.D / (pair ? 16 : 8));
     return launch(kVectors[format + 1][pair][fp16], grid, stream, pdl, a, r);
 }
 
 cudaError_t launch_fetch(VectorArgs a, int format, bool fp16, bool pdl, cudaStream_t stream) {
     (void)cudaGetLastError();
-    a.per_block = per_block_of(a.tokens, 2 * a.kv_heads, a.D / 8);
-    const dim3 grid(a.tokens, (2 * a.kv_heads + a.per_block - 1) / a.per_block);
+    const dim3 grid = grid_of(&a, 2 * a.kv_heads, a.D / 8);
     return launch(kFetch[format][fp16], grid, stream, pdl, a);
 }
 
