@@ -17,7 +17,12 @@
 // of the keys and values of each group of 32 are scaled by the largest step
 // of the request (a kernel that reads the scale words finds it), queries take the key
 // groups' powers in exchange, and each query row is brought near 2^9.  What is
-// rounded: a key or value once (2^-12), a probability once.
+// rounded: a value once (2^-12), a probability once.  Keys are two fp16 parts each,
+// which their products with the queries take in turn, where the caller wants the
+// logarithms of the sums: with one part (2^-12) a logarithm of few terms is off by
+// 1e-5 of itself, which float32 has to show and 16-bit outputs do not.  Without
+// them one part is taken: 2 x 1,000 new tokens over 8,192 cached ones, 330 us
+// with two parts, bound by the reads of shared memory (272 KB a tile of 64 tokens).
 #include "kvb_vec.h"
 #include "kvb_vec_internal.h"
 
@@ -28,7 +33,7 @@ namespace kvb {
 
 namespace {
 
-constexpr int kTileQ = 128, kTileK = 64, kStagesTc = 4;
+constexpr int kTileQ = 128, kTileK = 64, kStagesK = 3, kStagesV = 4;
 constexpr int kRowsTc = 2 * kTileQ;
 constexpr int kSoftWarps = 8, kUnpackWarps = 8, kUnpackThreads = 32 * kUnpackWarps;
 constexpr int kThreadsTc = 32 * (kSoftWarps + kUnpackWarps + 1);
@@ -37,9 +42,9 @@ constexpr float kNoMaxTc = -3.0e38f;
 constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
-// Q0, Q1, K x 4, V x 4, and 1 KiB to align
+// Q0, Q1, three stages of K (two parts), four of V, and 1 KiB to align
 __host__ __device__ constexpr int smem_tc(int D) {
-    return blocks_of(D) * (int)(2 * kBlockQ + 2 * kStagesTc * kBlockK) + 1024;
+    return blocks_of(D) * (int)(2 * kBlockQ + (2 * kStagesK + kStagesV) * kBlockK) + 1024;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -251,13 +256,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
     __shared__ SharedTc sh;
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + kStagesTc * kBytesK;
+    const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + 2 * kStagesK * kBytesK;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = smem_u32(sh.bars);
-    // a stage holds the keys and the values of one tile of cached tokens
-    const uint32_t k_full = bars, v_full = bars + 32, stage_free = bars + 64,
-                   s_full = bars + 96, p_full = bars + 128,      // [tile of rows][buffer]
-                   o_last = bars + 160, q_full = bars + 176, o_full = bars + 184;
+    const uint32_t k_full = bars, v_full = bars + 32, k_free = bars + 64, v_free = bars + 96,
+                   s_full = bars + 128, p_full = bars + 160,      // [tile of rows][buffer]
+                   o_last = bars + 192, q_full = bars + 208, o_full = bars + 216;
 
     const int H = (int)a.pool.H, group = (int)a.group;
     // Blocks of whole units first, then those of the units that are cut.
@@ -289,7 +293,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         for (int i = 0; i < 4; ++i) {
             bar_init(k_full + 8 * i, 32 * kUnpackWarps);
             bar_init(v_full + 8 * i, 32 * kUnpackWarps);
-            bar_init(stage_free + 8 * i, 1);
+            bar_init(k_free + 8 * i, 1);
+            bar_init(v_free + 8 * i, 1);
             bar_init(s_full + 8 * i, 1);
             bar_init(p_full + 8 * i, kTileQ);
         }
@@ -607,13 +612,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             look_up(it, 2);
         }
         const __half2 k16 = __half2half2(__ushort_as_half(0x2c00));     // 1/16
+        uint32_t ks = 0, kp = 1;              // stage of the keys, and its parity
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
-            const uint32_t st = t % kStagesTc, parity = ((t / kStagesTc) & 1) ^ 1;
-            bar_wait(stage_free + 8 * st, parity, &sh.gave_up);
 #pragma unroll
             for (int comp = 0; comp < 2; ++comp) {
-            const uint32_t tile = (comp ? v_tile : k_tile) + st * kBytesK;
+            const uint32_t vs = t % kStagesV;
+            bar_wait(comp ? v_free + 8 * vs : k_free + 8 * ks, comp ? ((t / kStagesV) & 1) ^ 1 : kp, &sh.gave_up);
+            const uint32_t tile = comp ? v_tile + vs * kBytesK : k_tile + ks * (2 * kBytesK);
 #pragma unroll
             for (int it = 0; it < NI; ++it) {
                 uint32_t w = word[comp][it];
@@ -627,9 +633,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                     w = 0;                // kept out of the products; the softmax warps see to it
                     sh.value_nan = 1;
                 }
-                // the step as two fp16 parts: a product is rounded once, by the sum with the first
+                // The step as two fp16 parts; a product is rounded once, by the sum with the
+                // first part's.  Keys in two parts: the first has 7 bits, so that its products
+                // with code - z are exact, and the second's products go to a tile of their
+                // own; scores then err by 2^-19 of a product.
                 const float step = q4_step(w) * (comp ? f[1] : f[0]);
-                const float hi = __half2float(__float2half_rn(step));
+                const bool split = comp == 0 && a.lse != nullptr;
+                const float hi = split ? __uint_as_float((__float_as_uint(step) + 0x10000u) & 0xfffe0000u)
+                                       : __half2float(__float2half_rn(step));
                 const __half2 s1 = __float2half2_rn(hi), s0 = __float2half2_rn(step - hi);
                 const uint32_t zz = (w & 15u) * 0x00010001u;
                 uint32_t za = zz | 0x64006400u, zb = (zz << 4) | 0xd400d400u;    // 1024 + z, -(64 + z)
@@ -642,18 +653,26 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                         const uint32_t v = cw[i] >> 8;
                         uint32_t y[4] = {(cw[i] & 0x000f000fu) | 0x64006400u, (cw[i] & 0x00f000f0u) | 0x64006400u,
                                          (v & 0x000f000fu) | 0x64006400u, (v & 0x00f000f0u) | 0x64006400u};
+                        uint32_t y0[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             __half2 x = *reinterpret_cast<__half2 *>(&y[e]);
                             x = e & 1 ? __hfma2(x, k16, z16) : __hsub2(x, z1);    // code - z, exact
-                            x = __hfma2(x, s1, __hmul2(x, s0));
-                            y[e] = *reinterpret_cast<uint32_t *>(&x);
+                            __half2 low = __hmul2(x, s0), high = split ? __hmul2(x, s1) : __hfma2(x, s1, low);
+                            y[e] = *reinterpret_cast<uint32_t *>(&high);
+                            y0[e] = *reinterpret_cast<uint32_t *>(&low);
                         }
                         sts16(tile + to[i] + it * kStep * 128, make_uint4(y[0], y[1], y[2], y[3]));
+                        if (split)
+                            sts16(tile + kBytesK + to[i] + it * kStep * 128, make_uint4(y0[0], y0[1], y0[2], y0[3]));
                     }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive((comp ? v_full : k_full) + 8 * st);
+            bar_arrive(comp ? v_full + 8 * vs : k_full + 8 * ks);
+            }
+            if (++ks == kStagesK) {
+                ks = 0;
+                kp ^= 1;
             }
         }
         if (outside && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
@@ -663,35 +682,50 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const uint32_t one = elected();
         const int n = __shfl_sync(0xffffffffu, tiles, 0), nq = __shfl_sync(0xffffffffu, q_tiles, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int parts = a.lse != nullptr ? 2 : 1;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             bar_wait(bar, parity, &sh.gave_up);
             __syncwarp();
         };
-        auto scores = [&](int q, int t) {
-            const uint64_t qd = desc(base + q * kBytesQ, 16, 1024), kd = desc(k_tile + (t % kStagesTc) * kBytesK, 16, 1024);
+        auto scores = [&](int q, int t, uint32_t stage) {
+            const uint64_t qd = desc(base + q * kBytesQ, 16, 1024), kd = desc(k_tile + stage * (2 * kBytesK), 16, 1024);
             const uint32_t to = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss(to, qd + ((ks >> 2) * kBlockQ + (ks & 3) * 32) / 16, kd + ((ks >> 2) * kBlockK + (ks & 3) * 32) / 16,
-                       kScores, ks != 0, one);
+            for (int part = 0; part < 2; ++part) {     // of the keys' steps
+                if (part >= parts) break;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_ss(to, qd + ((ks >> 2) * kBlockQ + (ks & 3) * 32) / 16,
+                           kd + (part * kBytesK + (ks >> 2) * kBlockK + (ks & 3) * 32) / 16, kScores,
+                           part + ks != 0, one);
+            }
             commit(s_full + 16 * q + 8 * (t & 1), one);
         };
-        auto sums = [&](int q, int t) {
-            const uint64_t vd = desc(v_tile + (t % kStagesTc) * kBytesK, kBlockK, 1024);
+        auto sums = [&](int q, int t, uint32_t stage) {
+            const uint64_t vd = desc(v_tile + stage * kBytesK, kBlockK, 1024);
             const uint32_t to = tm + 256 + q * D, from = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
             for (int ks = 0; ks < kTileK / 16; ++ks)
                 mma_ts(to, from + ks * 8, vd + ks * 2048 / 16, kSums, t != 0 || ks != 0, one);
         };
-        auto keys = [&](int t) {
-            wait(k_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+        uint32_t ks = 0, kp = 0;        // stage of the keys asked for next, and its parity
+        auto keys = [&]() {
+            wait(k_full + 8 * ks, kp);
             fence_after();
+        };
+        auto next_keys = [&]() {
+            commit(k_free + 8 * ks, one);
+            if (++ks == kStagesK) {
+                ks = 0;
+                kp ^= 1;
+            }
         };
         if (n > 0) {
             wait(q_full, 0);
             for (int t = 0; t < 2 && t < n; ++t) {      // both buffers of scores
-                keys(t);
-                for (int q = 0; q < nq; ++q) scores(q, t);
+                keys();
+                for (int q = 0; q < nq; ++q) scores(q, t, ks);
+                next_keys();
             }
             // Straight code: a jump back costs this warp an instruction fetch of some 350
             // cycles, since the other warps' code goes through the same caches; four tiles
@@ -700,21 +734,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             for (int t = 0; t < n; ++t) {
                 // The unpacking warps give the values of a tile before the keys of the next, so
                 // keys that have come vouch for them; the last tile has no next.
-                if (t + 1 == n) wait(v_full + 8 * (t % kStagesTc), (t / kStagesTc) & 1);
+                const uint32_t vs = t % kStagesV;
+                if (t + 1 == n) wait(v_full + 8 * vs, (t / kStagesV) & 1);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     if (q >= nq) break;
                     wait(p_full + 16 * q + 8 * (t & 1), (t >> 1) & 1);
                     fence_after();
-                    sums(q, t);
+                    sums(q, t, vs);
                     if (t + 2 < n) {
-                        if (q == 0) keys(t + 2);
-                        scores(q, t + 2);       // after the sums that read this buffer
+                        if (q == 0) keys();
+                        scores(q, t + 2, ks);       // after the sums that read this buffer
                     } else if (t + 2 == n) {
                         commit(o_last + 8 * q, one);
                     }
                 }
-                commit(stage_free + 8 * (t % kStagesTc), one);
+                if (t + 2 < n) next_keys();
+                commit(v_free + 8 * vs, one);
             }
             commit(o_full, one);
             int never = 0;

@@ -627,6 +627,32 @@ def test_attend_many_rows_window(window, dim):
         assert status == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_q,lens", [([64, 65], [64, 300]), ([20, 3, 20], [6000, 100, 5500])])
+def test_attend_many_rows_without_lse(dtype, n_q, lens):
+    """Where no logarithms are wanted the keys are rounded to fp16 (as `check` allows)."""
+    with Batch(lens, n_q, 1, 4, 128, 16, dtype) as b:
+        out, lse, status = b.run()
+        exact = lse.clone()
+        out, lse, status = b.run(lse=None)
+        assert (lse == 7).all() and status == 0
+        b.check(out, exact)
+
+
+def test_attend_many_rows_lse_of_few_terms():
+    """Sums of few terms: 2^-18 of the sizes of the products, with keys in two parts."""
+    with Batch([8, 3], [8, 3], 1, 16, 64, 16, "fp16", k_mul=3.0) as b:
+        _, lse, _ = b.run()
+        at = 0
+        for i, n in enumerate(b.n_q):
+            k, v = (vec_ref.q4_decode(x, 64) for x in b.kv[i])
+            q = b.q[at:at + n].double().cpu().numpy()
+            _, want, _ = vec_ref.attend(q, k, v, b.scale)
+            size = b.scale * np.abs(q).max() * np.abs(k).max() * 64
+            assert np.abs(lse[at:at + n].double().cpu().numpy() - want).max() <= 2.0 ** -18 * size
+            at += n
+
+
 def test_attend_many_rows_cut_and_joined():
     with Batch([6000, 100, 5500], [20, 3, 20], 1, 4, 128, 32, "bf16") as b:
         assert b.args().workspace_bytes > 0
