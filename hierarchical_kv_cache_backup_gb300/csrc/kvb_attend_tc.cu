@@ -33,7 +33,7 @@ namespace kvb {
 
 namespace {
 
-constexpr int kTileQ = 128, kTileK = 64, kStagesK = 3, kStagesV = 4;
+constexpr int kTileQ = 128, kTileK = 64;
 constexpr int kRowsTc = 2 * kTileQ;
 constexpr int kSoftWarps = 8, kUnpackWarps = 8, kUnpackThreads = 32 * kUnpackWarps;
 constexpr int kThreadsTc = 32 * (kSoftWarps + kUnpackWarps + 1);
@@ -42,9 +42,12 @@ constexpr float kNoMaxTc = -3.0e38f;
 constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
-// Q0, Q1, three stages of K (two parts), four of V, and 1 KiB to align
-__host__ __device__ constexpr int smem_tc(int D) {
-    return blocks_of(D) * (int)(2 * kBlockQ + (2 * kStagesK + kStagesV) * kBlockK) + 1024;
+// Stages of K (one part or two) and V: what fits beside Q0 and Q1.
+__host__ __device__ constexpr int stages_k(int parts) { return parts == 1 ? 4 : 3; }
+constexpr int kStagesV = 4;
+// Q0, Q1, the stages, and 1 KiB to align
+__host__ __device__ constexpr int smem_tc(int D, int parts) {
+    return blocks_of(D) * (int)(2 * kBlockQ + (parts * stages_k(parts) + kStagesV) * kBlockK) + 1024;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -248,15 +251,16 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
     if (tid < 8) a.steps[(((int64_t)r * a.step_parts + part) * a.pool.H + head) * 8 + tid] = all[tid];
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, int kParts>
 __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int NG = D / 32, NB = blocks_of(D);
+    constexpr int kStagesK = stages_k(kParts);
     constexpr uint32_t kBytesQ = NB * kBlockQ, kBytesK = NB * kBlockK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SharedTc sh;
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + 2 * kStagesK * kBytesK;
+    const uint32_t k_tile = base + 2 * kBytesQ, v_tile = k_tile + kParts * kStagesK * kBytesK;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t bars = smem_u32(sh.bars);
     const uint32_t k_full = bars, v_full = bars + 32, k_free = bars + 64, v_free = bars + 96,
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             for (int comp = 0; comp < 2; ++comp) {
             const uint32_t vs = t % kStagesV;
             bar_wait(comp ? v_free + 8 * vs : k_free + 8 * ks, comp ? ((t / kStagesV) & 1) ^ 1 : kp, &sh.gave_up);
-            const uint32_t tile = comp ? v_tile + vs * kBytesK : k_tile + ks * (2 * kBytesK);
+            const uint32_t tile = comp ? v_tile + vs * kBytesK : k_tile + ks * (kParts * kBytesK);
 #pragma unroll
             for (int it = 0; it < NI; ++it) {
                 uint32_t w = word[comp][it];
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 // with code - z are exact, and the second's products go to a tile of their
                 // own; scores then err by 2^-19 of a product.
                 const float step = q4_step(w) * (comp ? f[1] : f[0]);
-                const bool split = comp == 0 && a.lse != nullptr;
+                const bool split = comp == 0 && kParts == 2;
                 const float hi = split ? __uint_as_float((__float_as_uint(step) + 0x10000u) & 0xfffe0000u)
                                        : __half2float(__float2half_rn(step));
                 const __half2 s1 = __float2half2_rn(hi), s0 = __float2half2_rn(step - hi);
@@ -682,23 +686,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const uint32_t one = elected();
         const int n = __shfl_sync(0xffffffffu, tiles, 0), nq = __shfl_sync(0xffffffffu, q_tiles, 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const int parts = a.lse != nullptr ? 2 : 1;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             bar_wait(bar, parity, &sh.gave_up);
             __syncwarp();
         };
         auto scores = [&](int q, int t, uint32_t stage) {
-            const uint64_t qd = desc(base + q * kBytesQ, 16, 1024), kd = desc(k_tile + stage * (2 * kBytesK), 16, 1024);
+            const uint64_t qd = desc(base + q * kBytesQ, 16, 1024), kd = desc(k_tile + stage * (kParts * kBytesK), 16, 1024);
             const uint32_t to = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {     // of the keys' steps
-                if (part >= parts) break;
+            for (int part = 0; part < kParts; ++part)     // of the keys' steps
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_ss(to, qd + ((ks >> 2) * kBlockQ + (ks & 3) * 32) / 16,
                            kd + (part * kBytesK + (ks >> 2) * kBlockK + (ks & 3) * 32) / 16, kScores,
                            part + ks != 0, one);
-            }
             commit(s_full + 16 * q + 8 * (t & 1), one);
         };
         auto sums = [&](int q, int t, uint32_t stage) {
@@ -818,16 +819,18 @@ typedef void(AttendTcFn)(AttendArgs);
 struct VariantTc {
     uint32_t D;
     bool fp16;
+    int parts;
     AttendTcFn *fn, *steps_fn, *join_fn;
     int smem;
 };
-template <int D, bool kHalf>
+template <int D, bool kHalf, int kParts>
 constexpr VariantTc variant_tc() {
-    return VariantTc{(uint32_t)D, kHalf, kv_attend_tc_kernel<D, kHalf>, kv_attend_steps_kernel<D>,
-                     kv_attend_join_tc_kernel<D, kHalf>, smem_tc(D)};
+    return VariantTc{(uint32_t)D, kHalf, kParts, kv_attend_tc_kernel<D, kHalf, kParts>, kv_attend_steps_kernel<D>,
+                     kv_attend_join_tc_kernel<D, kHalf>, smem_tc(D, kParts)};
 }
-const VariantTc kVariantsTc[] = {variant_tc<64, false>(),  variant_tc<64, true>(),  variant_tc<96, false>(),
-                                 variant_tc<96, true>(),   variant_tc<128, false>(), variant_tc<128, true>()};
+#define KVB_VARIANTS_TC(D) \
+    variant_tc<D, false, 1>(), variant_tc<D, true, 1>(), variant_tc<D, false, 2>(), variant_tc<D, true, 2>()
+const VariantTc kVariantsTc[] = {KVB_VARIANTS_TC(64), KVB_VARIANTS_TC(96), KVB_VARIANTS_TC(128)};
 
 }  // namespace
 
@@ -866,7 +869,7 @@ void plan_attend_tc(AttendPlan *p, uint64_t span, uint32_t requests, uint32_t kv
 cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream,
                              int *launches) {
     for (const VariantTc &v : kVariantsTc) {
-        if (v.D != D || v.fp16 != fp16) continue;
+        if (v.D != D || v.fp16 != fp16 || v.parts != (a.lse != nullptr ? 2 : 1)) continue;
         cudaLaunchConfig_t cfg = {};
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
