@@ -21,8 +21,14 @@
 // which their products with the queries take in turn, where the caller wants the
 // logarithms of the sums: with one part (2^-12) a logarithm of few terms is off by
 // 1e-5 of itself, which float32 has to show and 16-bit outputs do not.  Without
-// them one part is taken: 2 x 1,000 new tokens over 8,192 cached ones, 330 us
-// with two parts, bound by the reads of shared memory (272 KB a tile of 64 tokens).
+// them one part is taken: 2 x 1,000 new tokens over 8,192 cached ones, 295 us with
+// two parts and 235 with one.
+//
+// Bound: the products.  A tcgen05.mma of 128 x 64 x 16 with both operands in
+// shared memory takes 48 cycles and more where its arithmetic takes 32, since it
+// reads 6 KB; a tile of 64 cached tokens has 32 of them and 8 of 128 x 128 x 16 for
+// the sums (64 cycles), about 2,050 cycles; traces of one block show 2,400-2,900 a
+// tile, the product warp never waiting for the softmax warps.
 #include "kvb_vec.h"
 #include "kvb_vec_internal.h"
 
@@ -42,12 +48,14 @@ constexpr float kNoMaxTc = -3.0e38f;
 constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
-// Stages of K (one part or two) and V: what fits beside Q0 and Q1.
-__host__ __device__ constexpr int stages_k(int parts) { return parts == 1 ? 4 : 3; }
-constexpr int kStagesV = 4;
+// Stages of K (of one part or two) and of V.  Two of K: with three the unpacking
+// warps run further ahead and the products more slowly (two parts 327 -> 295 us, one part
+// 242 -> 235); V needs three.
+constexpr int kStagesK = 2, kStagesV = 4;
+static_assert(kStagesK <= 4 && kStagesV <= 4, "four barriers of each kind");
 // Q0, Q1, the stages, and 1 KiB to align
 __host__ __device__ constexpr int smem_tc(int D, int parts) {
-    return blocks_of(D) * (int)(2 * kBlockQ + (parts * stages_k(parts) + kStagesV) * kBlockK) + 1024;
+    return blocks_of(D) * (int)(2 * kBlockQ + (parts * kStagesK + kStagesV) * kBlockK) + 1024;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -254,7 +262,6 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
 template <int D, bool kHalf, int kParts>
 __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int NG = D / 32, NB = blocks_of(D);
-    constexpr int kStagesK = stages_k(kParts);
     constexpr uint32_t kBytesQ = NB * kBlockQ, kBytesK = NB * kBlockK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SharedTc sh;
