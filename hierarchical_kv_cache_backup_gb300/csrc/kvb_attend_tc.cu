@@ -17,7 +17,7 @@
 // of the keys and values of each group of 32 are scaled by the largest step
 // of the request (a kernel that reads the scale words finds it), queries take the key
 // groups' powers in exchange, and each query row is brought near 2^9.  What is
-// rounded: a value once (2^-12), a probability once.  Keys are two fp16 parts each,
+// rounded: a value once (2^-12; not for fp16 outputs), a probability once.  Keys are two fp16 parts each,
 // which their products with the queries take in turn, where the caller wants the
 // logarithms of the sums: with one part (2^-12) a logarithm of few terms is off by
 // 1e-5 of itself, which float32 has to show and 16-bit outputs do not.  Without
@@ -51,11 +51,15 @@ __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
 // Stages of K (of one part or two) and of V.  Two of K: with three the unpacking
 // warps run further ahead and the products more slowly (two parts 327 -> 295 us, one part
 // 242 -> 235); V needs three.
-constexpr int kStagesK = 2, kStagesV = 4;
+constexpr int kStagesK = 2, kStagesV = 3;
 static_assert(kStagesK <= 4 && kStagesV <= 4, "four barriers of each kind");
+// fp16 parts of a value: two where the output is fp16, so that only the
+// probabilities are rounded before it (error against 64 bits 1.4 times that of a float32
+// result rounded once, 1.6 with one part; a bf16 output does not show it).
+__host__ __device__ constexpr int value_parts(bool half) { return half ? 2 : 1; }
 // Q0, Q1, the stages, and 1 KiB to align
-__host__ __device__ constexpr int smem_tc(int D, int parts) {
-    return blocks_of(D) * (int)(2 * kBlockQ + (parts * kStagesK + kStagesV) * kBlockK) + 1024;
+__host__ __device__ constexpr int smem_tc(int D, bool half, int parts) {
+    return blocks_of(D) * (int)(2 * kBlockQ + (parts * kStagesK + value_parts(half) * kStagesV) * kBlockK) + 1024;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -262,6 +266,7 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
 template <int D, bool kHalf, int kParts>
 __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int NG = D / 32, NB = blocks_of(D);
+    constexpr int kPartsV = value_parts(kHalf);
     constexpr uint32_t kBytesQ = NB * kBlockQ, kBytesK = NB * kBlockK;
     extern __shared__ unsigned char smem_raw[];
     __shared__ SharedTc sh;
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             for (int comp = 0; comp < 2; ++comp) {
             const uint32_t vs = t % kStagesV;
             bar_wait(comp ? v_free + 8 * vs : k_free + 8 * ks, comp ? ((t / kStagesV) & 1) ^ 1 : kp, &sh.gave_up);
-            const uint32_t tile = comp ? v_tile + vs * kBytesK : k_tile + ks * (kParts * kBytesK);
+            const uint32_t tile = comp ? v_tile + vs * (kPartsV * kBytesK) : k_tile + ks * (kParts * kBytesK);
 #pragma unroll
             for (int it = 0; it < NI; ++it) {
                 uint32_t w = word[comp][it];
@@ -645,11 +650,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                     sh.value_nan = 1;
                 }
                 // The step as two fp16 parts; a product is rounded once, by the sum with the
-                // first part's.  Keys in two parts: the first has 7 bits, so that its products
+                // first part's.  Tiles in two parts: the first has 7 bits, so that its products
                 // with code - z are exact, and the second's products go to a tile of their
-                // own; scores then err by 2^-19 of a product.
+                // own; products with either err by 2^-19.
                 const float step = q4_step(w) * (comp ? f[1] : f[0]);
-                const bool split = comp == 0 && kParts == 2;
+                const bool split = (comp ? kPartsV : kParts) == 2;
                 const float hi = split ? __uint_as_float((__float_as_uint(step) + 0x10000u) & 0xfffe0000u)
                                        : __half2float(__float2half_rn(step));
                 const __half2 s1 = __float2half2_rn(hi), s0 = __float2half2_rn(step - hi);
@@ -710,11 +715,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             commit(s_full + 16 * q + 8 * (t & 1), one);
         };
         auto sums = [&](int q, int t, uint32_t stage) {
-            const uint64_t vd = desc(v_tile + stage * kBytesK, kBlockK, 1024);
+            const uint64_t vd = desc(v_tile + stage * (kPartsV * kBytesK), kBlockK, 1024);
             const uint32_t to = tm + 256 + q * D, from = tm + q * 128 + (t & 1) * 64;
 #pragma unroll
-            for (int ks = 0; ks < kTileK / 16; ++ks)
-                mma_ts(to, from + ks * 8, vd + ks * 2048 / 16, kSums, t != 0 || ks != 0, one);
+            for (int part = 0; part < kPartsV; ++part)
+#pragma unroll
+                for (int ks = 0; ks < kTileK / 16; ++ks)
+                    mma_ts(to, from + ks * 8, vd + (part * kBytesK + ks * 2048) / 16, kSums,
+                           t != 0 || part + ks != 0, one);
         };
         uint32_t ks = 0, kp = 0;        // stage of the keys asked for next, and its parity
         auto keys = [&]() {
@@ -833,7 +841,7 @@ struct VariantTc {
 template <int D, bool kHalf, int kParts>
 constexpr VariantTc variant_tc() {
     return VariantTc{(uint32_t)D, kHalf, kParts, kv_attend_tc_kernel<D, kHalf, kParts>, kv_attend_steps_kernel<D>,
-                     kv_attend_join_tc_kernel<D, kHalf>, smem_tc(D, kParts)};
+                     kv_attend_join_tc_kernel<D, kHalf>, smem_tc(D, kHalf, kParts)};
 }
 #define KVB_VARIANTS_TC(D) \
     variant_tc<D, false, 1>(), variant_tc<D, true, 1>(), variant_tc<D, false, 2>(), variant_tc<D, true, 2>()
