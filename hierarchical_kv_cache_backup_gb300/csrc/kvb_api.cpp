@@ -1626,7 +1626,12 @@ int vec_enter_device(int device, void *stream, bool *pdl) {
     return KV_OK;
 }
 
-int vec_enter_pool(const void *pool_handle, uint32_t layer, void *stream, bool launch, VecPool *out) {
+void vec_begin(int device, void *stream) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    forget_stream(g_dev[device], stream);
+}
+
+int vec_enter_pool(const void *pool_handle, uint32_t layer, VecPool *out) {
     std::lock_guard<std::mutex> lk(g_mu);
     if (pool_handle == nullptr) return fail(KV_ERR_INVALID_ARG, "pool handle is NULL");
     PoolObj *pool = find_pool((kv_pool)pool_handle);
@@ -1639,10 +1644,8 @@ int vec_enter_pool(const void *pool_handle, uint32_t layer, void *stream, bool l
     if (layer >= g.L)
         return fail(KV_ERR_OUT_OF_RANGE, "layer %u is outside [0, %llu)", layer, (unsigned long long)g.L);
     const int d = pool->device;
-    DeviceGuard guard(d);
-    const kv_status st = init_device(d);
+    const kv_status st = init_device(d);       // makes d current for what it does
     if (st != KV_OK) return st;
-    if (launch) forget_stream(g_dev[d], stream);
     const Side s = pool_side(*pool);
     out->layout = pool->layout;
     out->s_page = s.s_id;

@@ -312,7 +312,7 @@ kv_status kv_rotate(kv_rotary rotary, const kv_rotate_args *a, void *stream) {
 kv_status kv_append(kv_pool pool, kv_rotary rotary, const kv_append_args *a, void *stream) {
     if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
     VecPool p;
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, false, &p));
+    TRY((kv_status)vec_enter_pool(pool, a->layer, &p));
     RotaryK r{};
     if (rotary != nullptr && !find_rotary(rotary, &r))
         return fail(KV_ERR_CLOSED, "rotary handle is closed or unknown");
@@ -354,7 +354,7 @@ kv_status kv_append(kv_pool pool, kv_rotary rotary, const kv_append_args *a, voi
         TRY(on_device(a->q_out.data, "q_out", p.device));
     }
     Guard guard(p.device);
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, true, &p));
+    vec_begin(p.device, stream);
     k.k = vecs(a->k);
     k.v = vecs(a->v);
     if (with_q) {
@@ -383,7 +383,7 @@ kv_status kv_append(kv_pool pool, kv_rotary rotary, const kv_append_args *a, voi
 kv_status kv_fetch(kv_pool pool, const kv_fetch_args *a, void *stream) {
     if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
     VecPool p;
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, false, &p));
+    TRY((kv_status)vec_enter_pool(pool, a->layer, &p));
     if (a->reserved != 0) return fail(KV_ERR_INVALID_ARG, "reserved members must be 0");
     TRY(check_dim(a->head_dim, a->dtype));
     VectorArgs k{};
@@ -402,7 +402,7 @@ kv_status kv_fetch(kv_pool pool, const kv_fetch_args *a, void *stream) {
     TRY(on_device(a->slots, "slots", p.device));
     if (a->status != nullptr) TRY(on_device(a->status, "status", p.device));
     Guard guard(p.device);
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, true, &p));
+    vec_begin(p.device, stream);
     k.k = vecs(a->k);
     k.v = vecs(a->v);
     k.slots = a->slots;
@@ -423,7 +423,7 @@ kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *a, uint64_t *o
     if (a == nullptr || out == nullptr)
         return fail(KV_ERR_INVALID_ARG, "argument block or output pointer is NULL");
     VecPool p;
-    TRY((kv_status)vec_enter_pool(pool, a->layer, nullptr, false, &p));
+    TRY((kv_status)vec_enter_pool(pool, a->layer, &p));
     PoolLayer layer;
     TRY(check_attend(a, p, &layer));
     *out = 0;
@@ -436,7 +436,7 @@ kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *a, uint64_t *o
 kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
     VecPool p;
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, false, &p));
+    TRY((kv_status)vec_enter_pool(pool, a->layer, &p));
     AttendArgs k{};
     TRY(check_attend(a, p, &k.pool));
     if (a->requests == 0 || a->tokens == 0 || a->max_q == 0) return KV_OK;
@@ -474,7 +474,7 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     if (a->status != nullptr) TRY(on_device(a->status, "status", p.device));
     if (plan.bytes != 0) TRY(on_device(a->workspace, "workspace", p.device));
     Guard guard(p.device);
-    TRY((kv_status)vec_enter_pool(pool, a->layer, stream, true, &p));
+    vec_begin(p.device, stream);
     k.q = vecs(a->q);
     k.out = vecs(a->out);
     k.lse = a->lse;

@@ -33,8 +33,8 @@ cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pd
                              int *launches);
 cudaError_t preload_attend_tc_kernels();
 
-// Handle checks of one operator call on a pool (CLOSED / STALE), its device
-// made ready, and the end of a run of overlapped restores on `stream`.
+// Handle checks of one operator call on a pool (CLOSED / STALE) and its device
+// made ready; vec_begin ends a run of overlapped restores on `stream`.
 struct VecPool {
     kv_layout layout;
     uint64_t base[2];      // component bases of the layer
@@ -42,7 +42,8 @@ struct VecPool {
     int device, sms;
     bool pdl;
 };
-int vec_enter_pool(const void *pool_handle, uint32_t layer, void *stream, bool launch, VecPool *out);
+int vec_enter_pool(const void *pool_handle, uint32_t layer, VecPool *out);
+void vec_begin(int device, void *stream);
 int vec_enter_device(int device, void *stream, bool *pdl);
 int vec_cuda_error(cudaError_t e, const char *what);
 void vec_count(int launches);
