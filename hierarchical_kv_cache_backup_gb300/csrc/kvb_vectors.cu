@@ -120,11 +120,13 @@ __device__ __forceinline__ void store8(uint64_t vec, uint32_t chunk, const float
 // are as far apart.  Four neighbouring lanes still hold the 32 values of a
 // 4-bit group when rotated and other part are multiples of 64 values.  Where
 // they are not (or not of 16 for the other formats), a lane owns one run and
-// reads its partners itself (!kPair).  8,192 tokens of 40 vectors of 128: 52 us
-// with one run a lane, bound by instructions.
-// kFormat: -1 rotate only, else kv_cache_format.
+// reads its partners itself (!kPair).  8,192 tokens of 40 vectors of 128: 30 us
+// (5.8 TB/s, bound by memory), 52 with one run a lane, bound by instructions.
+// kFormat: -1 rotate only, else kv_cache_format.  Quantising takes 87 registers where
+// it may; seven blocks an SM (72 registers) hide more: append and fetch of 8,192
+// tokens 53.7 -> 50.3 us (the append 38, at 3.9 TB/s and 46% of the ALU pipe).
 template <int kFormat, bool kHalf, bool kPair>
-__global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_constant__ VectorArgs a,
+__global__ void __launch_bounds__(kThreads, kFormat == 2 ? 7 : 1) kv_vectors_kernel(const __grid_constant__ VectorArgs a,
                                                               const __grid_constant__ RotaryK r) {
     constexpr int kRuns = kPair ? 2 : 1;
     __shared__ __align__(16) float all_rows[kThreads / 32][2][kMaxPairs];
@@ -339,7 +341,9 @@ __global__ void __launch_bounds__(kThreads) kv_vectors_kernel(const __grid_const
 
 // -------------------------------------------------------------------- fetch
 //
-// The same mapping, a lane 8 values of a vector.
+// The same mapping, a lane 8 values of a vector.  Bound by the latency of a token's
+// two dependent reads (slot, then vectors): 8,192 tokens of 16 vectors of 128 in 4 bits,
+// 12 us.
 template <int kFormat, bool kHalf>
 __global__ void __launch_bounds__(kThreads) kv_fetch_kernel(const __grid_constant__ VectorArgs a) {
     asm volatile("griddepcontrol.launch_dependents;");
