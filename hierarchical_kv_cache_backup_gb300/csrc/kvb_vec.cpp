@@ -147,6 +147,9 @@ kv_status scales(uint32_t format, float k, float v) {
     return KV_OK;
 }
 
+// A window longer than any request hides nothing.
+uint32_t window_of(const kv_attend_args *a) { return std::min(a->window, 1u << 30); }
+
 // What plan_attend and the kernels need of a block, without its pointers.
 kv_status check_attend(const kv_attend_args *a, const VecPool &p, PoolLayer *layer) {
     TRY(check_dim(a->head_dim, a->dtype));
@@ -164,9 +167,11 @@ kv_status check_attend(const kv_attend_args *a, const VecPool &p, PoolLayer *lay
     if (a->q_heads > 65535 || a->requests > 65535 || a->max_q > 65535)
         return fail(KV_ERR_INVALID_ARG, "requests %u, max_q %u and q_heads %u: 65535 at most each",
                     a->requests, a->max_q, a->q_heads);
-    if (a->tokens > 0x7fffffffu || a->max_len > 0x7fff0000u || a->window > 0x7fff0000u)
-        return fail(KV_ERR_INVALID_ARG, "tokens %u, max_len %u or window %u too large", a->tokens,
-                    a->max_len, a->window);
+    // the kernels count rows, tokens and places in 32 bits with room to add
+    if (a->tokens > 0x7fffffffu || a->max_len > (1u << 30) ||
+        (uint64_t)a->max_q * (a->q_heads / layer->H) > (1u << 30))
+        return fail(KV_ERR_INVALID_ARG, "tokens %u, max_len %u or max_q %u (of %u heads a KV head) too large",
+                    a->tokens, a->max_len, a->max_q, a->q_heads / layer->H);
     if (a->max_q > a->tokens)
         return fail(KV_ERR_INVALID_ARG, "max_q %u is more than all %u query tokens", a->max_q, a->tokens);
     if (!std::isfinite(a->scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
@@ -428,7 +433,7 @@ kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *a, uint64_t *o
     TRY(check_attend(a, p, &layer));
     *out = 0;
     if (a->requests != 0 && a->tokens != 0 && a->max_q != 0)
-        *out = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, a->window, a->q_heads, layer.H,
+        *out = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, window_of(a), a->q_heads, layer.H,
                            a->head_dim, p.sms).bytes;
     return KV_OK;
 }
@@ -453,7 +458,7 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
         (uintptr_t)a->lse % 4 != 0 || (uintptr_t)a->status % 4 != 0 || (uintptr_t)a->workspace % 16 != 0)
         return fail(KV_ERR_ALIGNMENT, "q_start, lens, pages, lse and status must be 4-byte and the "
                     "workspace 16-byte aligned");
-    const AttendPlan plan = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, a->window,
+    const AttendPlan plan = plan_attend(a->requests, a->tokens, a->max_q, a->max_len, window_of(a),
                                         a->q_heads, k.pool.H, a->head_dim, p.sms);
     if ((uint64_t)plan.row_tiles * plan.chunks * k.pool.H * (plan.many ? a->requests : 1) > 0x7fffffffull ||
         plan.step_parts > 65535 || plan.chunks > 65535)
@@ -492,7 +497,7 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     k.chunk = plan.chunk;
     k.chunks = plan.chunks;
     k.row_tiles = plan.row_tiles;
-    k.window = a->window;
+    k.window = window_of(a);
     k.scale_log2 = a->scale * 1.44269504088896340736f;
     k.whole_units = (uint32_t)plan.whole_units;
     k.steps = (uint32_t *)a->workspace;

@@ -625,7 +625,7 @@ typedef struct {
     uint32_t requests;        /* at most 65535                                    */
     uint32_t tokens;          /* query tokens of all requests                     */
     uint32_t max_q;           /* the most of one request                          */
-    uint32_t max_len;         /* the longest request, >= 0                        */
+    uint32_t max_len;         /* the longest request, 0..2^30                     */
     uint32_t q_heads, head_dim, dtype, layer;
     uint32_t window;          /* 0: none                                          */
     float scale;              /* finite                                           */

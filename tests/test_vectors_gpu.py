@@ -890,6 +890,7 @@ def test_attend_refusals():
         refused(INV, max_q=9)
         refused(INV, scale=float("nan"))
         refused(INV, scale=float("inf"))
+        refused(INV, max_len=2 ** 30 + 1, pages_stride=2 ** 31)
         refused(INV, lens=None)
         refused(INV, q_start=None)
         refused(INV, pages=None)
@@ -917,6 +918,42 @@ def test_attend_refusals():
         with pytest.raises(kvb.KvError) as e:
             kvb.kv_attend(b.pool.pool, a)
         assert e.value.status == kvb.KV_ERR_INVALID_ARG
+
+
+def test_attend_of_empty_requests_and_wide_windows():
+    """No cached token anywhere (no page table either); a window past every length."""
+    with Batch([0, 0], [2, 1], 1, 2, 64, 16, "bf16") as b:
+        a = b.args(max_len=0, pages=None)
+        kvb.kv_attend(b.pool.pool, a)
+        torch.cuda.synchronize()
+        assert not b.out.any() and torch.isneginf(b.lse).all() and int(b.status) == 0
+    with Batch([0], [40], 1, 2, 128, 16, "bf16") as b:          # the kernel for many rows
+        kvb.kv_attend(b.pool.pool, b.args(max_len=0, pages=None))
+        torch.cuda.synchronize()
+        assert not b.out.any() and torch.isneginf(b.lse).all()
+    for n_q in ([3], [60]):
+        with Batch([300], n_q, 1, 2, 128, 16, "bf16") as b:
+            out, lse, _ = b.run()
+            want = out.clone()
+            out, _, _ = b.run(window=2 ** 32 - 1)
+            assert torch.equal(out, want)
+
+
+def test_e4m3_saturates():
+    x = torch.tensor([1e6, -1e6, float("inf"), -float("inf"), float("nan"), 448.0, 0.001, 0.0] * 6, device="cuda")
+    x = x.view(1, 1, 48).to(torch.bfloat16)
+    with Pool(48, "e4m3", T=2, H=1, P=2) as p:
+        slots = torch.tensor([3], device="cuda")
+        args = dict(tokens=1, head_dim=48, dtype=0, format=FMT["e4m3"], layer=1, slots=slots.data_ptr(), k_scale=1.0, v_scale=2.0)
+        kvb.kv_append(p.pool, None, kvb.make_append_args(kvb.vecs(x), kvb.vecs(x), **args))
+        k, v = torch.empty_like(x), torch.empty_like(x)
+        kvb.kv_fetch(p.pool, kvb.make_fetch_args(kvb.vecs(k), kvb.vecs(v), **args))
+        torch.cuda.synchronize()
+        for got, top in ((k, 448.0), (v, 896.0)):
+            got = got.float().view(6, 8)
+            assert (got[:, 0] == top).all() and (got[:, 1] == -top).all() and (got[:, 2] == top).all()
+            assert (got[:, 3] == -top).all() and torch.isnan(got[:, 4]).all() and (got[:, 7] == 0).all()
+            assert (got[:, 5] == 448.0).all()
 
 
 def test_nothing_to_do():
