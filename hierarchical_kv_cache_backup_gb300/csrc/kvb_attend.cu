@@ -139,6 +139,14 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // more 16-row tile holds z of group g in row g, so that its product with the
 // rounded probabilities is subtracted at the end and the rounding error of a
 // probability acts on (code - z) only.
+//
+// Bound: instructions.  16 tokens of 128 values (2,560 bytes) take 334 a warp
+// through both products for 8 query rows, a warp begins and ends with about 1,200; the ALU
+// pipe is 57% busy at 2.3 instructions a cycle and SM, 16 warps of 128 registers.  Of
+// one request of 131,072 tokens (8 heads, 48 us) the part that grows with the tokens
+// runs at 5.1 TB/s of 6.75.  Measured and dropped: query fragments in shared memory
+// (2% slower), four-warp blocks with 96 registers (5-30% slower), several heads a block for
+// NHD pages (20% slower), both halves' exponentials at once for four rows (no change).
 template <int D, int NT, bool kHalf, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     kv_attend_rows_kernel(const __grid_constant__ AttendArgs a) {
