@@ -513,7 +513,12 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 if (gr % 2 == 0) blocks4<true>(vs + 16 * sub * SV + gr * 16 + at_row, vc);
                 const float d0 = q4_step(pick(vw[sub][0][gr / 4], gr % 4)) * f[gr];
                 const float d1 = q4_step(pick(vw[sub][1][gr / 4], gr % 4)) * f[gr];
-                uint32_t b[NT][2];
+                // fp16 outputs: weights in two fp16 parts, so that only the output is rounded
+                // (17 requests of up to 8,906 tokens, 5 heads over 1 of 96: error against 64
+                // bits 2.2e-4, 3.2e-4 with one part, 2.1e-4 for a float32 plain form; 24
+                // requests of 2,000 tokens: heads of 64 18.7 -> 20.5 us, of 256 56 -> 63).
+                // A bf16 output does not show it.
+                uint32_t b[NT][2], rest[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float p[4];
@@ -523,8 +528,15 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                         // a token that a row does not see may hold NaN for another
                         if (kMany && x[sub][nt][e] == 0.0f) p[e] = 0.0f;
                     }
-                    b[nt][0] = transpose8x8(half2_bits(p[0], p[1]));
-                    b[nt][1] = transpose8x8(half2_bits(p[2], p[3]));
+                    uint32_t h[2] = {half2_bits(p[0], p[1]), half2_bits(p[2], p[3])};
+                    b[nt][0] = transpose8x8(h[0]);
+                    b[nt][1] = transpose8x8(h[1]);
+                    if (kHalf) {
+                        const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h[0]));
+                        const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h[1]));
+                        rest[nt][0] = transpose8x8(half2_bits(p[0] - f0.x, p[1] - f0.y));
+                        rest[nt][1] = transpose8x8(half2_bits(p[2] - f1.x, p[3] - f1.y));
+                    }
                 }
                 uint32_t p0[4], p1[4];
                 codes4(vc[gr % 2 * 2], p0);
@@ -537,6 +549,11 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     mma(o[gr][0][nt], a0, b[nt][0], b[nt][1]);
                     mma(o[gr][1][nt], a1, b[nt][0], b[nt][1]);
                     mma(oz[nt], az, b[nt][0], b[nt][1]);
+                    if (kHalf) {
+                        mma(o[gr][0][nt], a0, rest[nt][0], rest[nt][1]);
+                        mma(o[gr][1][nt], a1, rest[nt][0], rest[nt][1]);
+                        mma(oz[nt], az, rest[nt][0], rest[nt][1]);
+                    }
                 }
             }
         }
@@ -759,7 +776,8 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
         // than a chunk; a block begins and ends in the time of 350 tokens, and parts
         // are joined in that of 500.  64 requests of up to 8,192 tokens and 8 heads, 1 /
         // 2 / 3 chunks: 144 / 142 / 141 us; 32 of them 88 / 82 / 79; 64 of up to 2,048
-        // 49 / 56 / 58; 24 of 2,016 of 4 heads of 64, 2 / 3 / 4 chunks: 21.5 / 18.8 / 22.5.
+        // 49 / 56 / 58; 24 of 2,016 of 4 heads of 64, 2 / 3 / 4 chunks: 21.5 / 18.8 / 22.5
+        // (weights in one part).
         const uint64_t slots = (uint64_t)sms * (D * (p.rows / 8) <= 128 ? 2 : 1), unit = kWarps * kTile;
         const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
         const double spread = (requests > 1 ? 0.75 : 1.0) * (double)units * (double)span / (double)slots;
