@@ -767,6 +767,7 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     if (window) span = std::min<uint64_t>(span, (uint64_t)window + p.rows);
     if (p.many) {
         plan_attend_tc(&p, span, requests, kv_heads, sms);
+        p.step_parts = step_parts_of(max_len, window, max_q);
         p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
     } else {
         // Cut along the cached tokens into the number of chunks that ends soonest, by a

@@ -216,8 +216,8 @@ struct SharedTc {
 };
 
 // The largest steps (as float bits) of the keys and values that kStepTokens tokens
-// of a request hold for one head: [request][part][head][2][4].
-constexpr int kStepTokens = 1024;
+// of a request hold for one head: [request][part][head][2][4].  Together the parts
+// cover what all rows of the request see.
 
 template <int D>
 __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_constant__ AttendArgs a) {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
                             (int)a.max_len, (int)a.group, (int)a.window, 0, (int)(a.max_q * a.group), &bad);
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     const int64_t head_off = (int64_t)head * a.pool.s_head;
-    const int t0 = s.lo + part * kStepTokens, t1 = min(s.hi, t0 + kStepTokens);
+    const int t0 = s.lo + part * (int)kStepTokens, t1 = min(s.hi, t0 + (int)kStepTokens);
     uint32_t most[2][NG];
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i) most[i / NG][i % NG] = 0;
@@ -877,8 +877,6 @@ void plan_attend_tc(AttendPlan *p, uint64_t span, uint32_t requests, uint32_t kv
         p->whole_units = units;
         p->chunk = 0x7fffffffu;
     }
-    p->step_parts = (uint32_t)((span + kStepTokens - 1) / kStepTokens);
-    if (p->step_parts == 0) p->step_parts = 1;
 }
 
 cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream,

@@ -110,6 +110,17 @@ KVB_HD Span row_span(int q0, int q1, int len, int tokens, int max_q, int max_len
     return s;
 }
 
+// The largest steps of a request are found kStepTokens tokens at a time, over all that its
+// rows together see (a window and its new tokens, not only what one tile of rows sees).
+constexpr uint32_t kStepTokens = 1024;
+
+KVB_HD uint32_t step_parts_of(uint32_t max_len, uint32_t window, uint32_t max_q) {
+    uint64_t span = max_len;
+    if (window && (uint64_t)window + max_q - 1 < span) span = (uint64_t)window + max_q - 1;
+    const uint32_t parts = (uint32_t)((span + kStepTokens - 1) / kStepTokens);
+    return parts != 0 ? parts : 1;
+}
+
 // ------------------------------------------------------------ 4-bit format
 
 constexpr uint32_t kGroup = 32;           // values of one scale word
