@@ -111,6 +111,13 @@ __device__ __forceinline__ uint32_t pick(const uint4 &u, int i) {
     return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
 }
 
+__device__ __forceinline__ void clear(uint4 &u, int i) {
+    if (i == 0) u.x = 0;
+    else if (i == 1) u.y = 0;
+    else if (i == 2) u.z = 0;
+    else u.w = 0;
+}
+
 __device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem),
                  "r"(on ? 16 : 0)
@@ -139,6 +146,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // more 16-row tile holds z of group g in row g, so that its product with the
 // rounded probabilities is subtracted at the end and the rounding error of a
 // probability acts on (code - z) only.
+//
+// A group of a value that is not finite makes that group of the outputs NaN, for the rows
+// that see the token, and nothing else: its step is taken as 0 in the products (0 x NaN would
+// reach every group through the zero points' tile and rows whose weight is 0), and the rows
+// that see it are marked.
 //
 // Bound: instructions.  16 tokens of 128 values (2,560 bytes) take 334 a warp
 // through both products for 8 query rows, a warp begins and ends with about 1,200; the ALU
@@ -321,6 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     const uint32_t z_group = (g < NG ? g : 0) * 4;
 
     float o[NG][2][NT][4], oz[NT][4], f[NG], m[NT][2], l[NT][2];
+    uint32_t nan_groups = 0;      // bit 8 (2 nt + e) + gr: that row's group gr is NaN
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
         f[gr] = __uint_as_float(227u << 23);   // 2^100: set by the first step that is not 0
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         // keeps p x step inside fp16 (p <= 2^8, step x f <= 2^6).
         uint4 vw[2][2][(NG + 3) / 4];
         float most[NG];
-        bool raise = false;
+        bool raise = false, not_finite = false;
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
@@ -472,9 +485,33 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-            auto w = [&](int sub, int k) { return __uint_as_float(pick(vw[sub][k][gr / 4], gr % 4)); };
-            most[gr] = fmaxf(fmaxf(w(0, 0), w(0, 1)), fmaxf(w(1, 0), w(1, 1)));
+            auto w = [&](int sub, int k) { return pick(vw[sub][k][gr / 4], gr % 4); };
+            const uint32_t top = max(max(w(0, 0), w(0, 1)), max(w(1, 0), w(1, 1)));
+            not_finite |= top >= 0x7f800000u;
+            most[gr] = __uint_as_float(top);
             raise |= most[gr] * f[gr] > 64.0f;
+        }
+        if (__any_sync(0xffffffffu, not_finite)) {
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                most[gr] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint4 &u = vw[k / 2][k % 2][gr / 4];
+                    if (pick(u, gr % 4) >= 0x7f800000u) {
+                        clear(u, gr % 4);
+                        const int t = t0 + 8 * k + g;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (t < c1 && (!kMany || (t <= lim[nt][e] && t >= low[nt][e])))
+                                    nan_groups |= 1u << (8 * (2 * nt + e) + gr);
+                    }
+                    most[gr] = fmaxf(most[gr], __uint_as_float(pick(u, gr % 4)));
+                }
+                raise |= most[gr] * f[gr] > 64.0f;
+            }
         }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -523,11 +560,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 for (int nt = 0; nt < NT; ++nt) {
                     float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = x[sub][nt][e] * (e < 2 ? d0 : d1);
-                        // a token that a row does not see may hold NaN for another
-                        if (kMany && x[sub][nt][e] == 0.0f) p[e] = 0.0f;
-                    }
+                    for (int e = 0; e < 4; ++e) p[e] = x[sub][nt][e] * (e < 2 ? d0 : d1);
                     uint32_t h[2] = {half2_bits(p[0], p[1]), half2_bits(p[2], p[3])};
                     b[nt][0] = transpose8x8(h[0]);
                     b[nt][1] = transpose8x8(h[1]);
@@ -567,6 +600,10 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
 
     // Join the warps.  A warp's accumulators go to its own ring as [row][D + 4].
     float *mine = reinterpret_cast<float *>(smem + warp * WB);
+    if (__any_sync(0xffffffffu, nan_groups != 0)) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) nan_groups |= __shfl_xor_sync(0xffffffffu, nan_groups, d);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -590,6 +627,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 v.y *= back;
                 v.z *= back;
                 v.w *= back;
+                if (nan_groups >> (8 * (2 * nt + e) + gr) & 1)
+                    v.x = v.y = v.z = v.w = __uint_as_float(kNanWord);
                 *reinterpret_cast<float4 *>(mine + row * (D + 4) + gr * 32 + 4 * g) = v;
             }
         }

@@ -1,5 +1,5 @@
 """kv_attend where a window's prompt chunk spans more tokens than one tile of queries sees, and
-other ranges of steps and values."""
+where a group of a value is not finite."""
 import numpy as np
 import pytest
 
@@ -11,7 +11,7 @@ if not torch.cuda.is_available():
 
 import vec_check  # noqa: E402
 import vec_ref  # noqa: E402
-from test_vectors_gpu import Batch  # noqa: E402
+from test_vectors_gpu import Batch, b_without, poke  # noqa: E402
 
 
 def put(b, i, comp, tokens, x):
@@ -73,3 +73,55 @@ def test_window_prompt_with_zeros_first(dtype, comp):
         out, lse, status = b.run()
         assert status == 0
         vec_check.check(b, out, lse)
+
+
+# -------------------------------------------------- a group that is not finite
+
+def not_finite(dim, groups):
+    x = np.zeros((1, dim), np.float32)
+    for g in groups:
+        x[:, 32 * g:32 * g + 32] = np.nan
+    return vec_ref.q4_encode(x)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(128, 4, 1), (128, 2, 6), (128, 4, 19), (64, 4, 1), (64, 4, 19), (96, 3, 1),
+                                           (96, 2, 6), (256, 2, 1), (256, 2, 40), (192, 1, 6)])
+@pytest.mark.parametrize("groups", [[0], [1], [0, 1]])
+def test_few_rows_a_value_group_that_is_not_finite(dtype, dim, group, n_q, groups):
+    """Only that group's dims are NaN, and only for the queries that see the token."""
+    with Batch([90, 90], [n_q, n_q], 1, group, dim, 16, dtype, window=60) as b:
+        late = 90 - 1 - n_q // 3                        # seen from its own position on
+        early = 90 - n_q - 60 + 1 + n_q // 3            # seen as long as the window holds it
+        poke(b, 0, late, 1, not_finite(dim, groups))
+        poke(b, 1, early, 1, not_finite(dim, groups))
+        out, lse, _ = b.run()
+        out, lse = out.clone(), lse.clone()
+        pos = 90 - n_q + np.arange(n_q)
+        sees = np.concatenate(((pos >= late) & (pos - 60 < late), (pos >= early) & (pos - 60 < early)))
+        want_nan = torch.zeros(out.shape, dtype=torch.bool)
+        cols = [32 * g + e for g in groups for e in range(32)]
+        want_nan[torch.from_numpy(sees)] = torch.isin(torch.arange(dim), torch.tensor(cols))
+        nan = torch.isnan(out.float()).cpu()
+        assert torch.equal(nan, want_nan)
+        want, _, _ = b_without(b)
+        assert torch.equal(out[torch.from_numpy(~sees).cuda()], want[torch.from_numpy(~sees).cuda()])
+        # the other dims of the queries that see it: as if that token's values were zeros there
+        for i, t in ((0, late), (1, early)):
+            put(b, i, 1, t, 0.0)
+        out = torch.where(want_nan.cuda(), 0.0, out.float())
+        zeroed, lse0, _ = b.run()
+        assert torch.equal(out, torch.where(want_nan.cuda(), 0.0, zeroed.float())) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_few_rows_a_group_that_is_not_finite_joined_over_chunks(dtype, n_q):
+    with Batch([9000, 5000], [n_q, n_q], 1, 4, 128, 32, dtype) as b:
+        assert b.args().workspace_bytes > 0
+        poke(b, 0, 4321, 1, not_finite(128, [2]))
+        out, _, _ = b.run()
+        nan = torch.isnan(out.float())
+        want_nan = torch.zeros_like(nan)
+        want_nan[:n_q, :, 64:96] = True
+        assert torch.equal(nan, want_nan)
