@@ -7,8 +7,13 @@
 // The matrix instructions multiply codes and zero points as they are: the
 // four bits of a code in the low bits of an fp16 are the subnormal code x 2^-24
 // (x 2^-20 four bits higher), exact, and the powers of two go into the queries
-// and the last scaling.  Unpacking is one AND a pair of values and one shift for
-// two.  Steps scale float32 sums on the key side and the probabilities on
+// and the last scaling.  Unpacking is one AND a pair of values, and one shift for
+// four pairs of keys, three for four of values: the products of an instruction
+// are lined up by the exponents of their operands, 2^-14 for all subnormals, and
+// what is far below that is lost.  Products with keys share a token and its step;
+// those with values do not, and a token whose weight x step is 2^20 times its
+// neighbours' would leave them nothing at 2^-24 (64 requests of up to 8,192
+// tokens: 3 us of 148).  Steps scale float32 sums on the key side and the probabilities on
 // the value side.  p_t = 2^(x_t - m) with a running maximum m.
 #include "kvb_vec.h"
 #include "kvb_vec_internal.h"
@@ -26,6 +31,8 @@ constexpr int kWarps = 8;
 constexpr int kTile = 32;        // cached tokens a warp takes at a time
 constexpr int kStages = 2;       // tiles in shared memory per warp
 constexpr float kNoMax = -3.0e38f;
+constexpr int kScaleMost = 100;               // exponents of f: at most this
+constexpr float kWeightMost = 32768.0f;       // 2^15: what a weight is kept to, below fp16's 65,504
 
 __host__ __device__ constexpr int vec_bytes(int D) { return (D / 2 + D / 8 + 15) / 16 * 16; }
 // Bytes between vectors in shared memory: an odd multiple of 16, so that the 8
@@ -65,13 +72,14 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Four pairs of codes (nibbles i of both 16-bit halves) as fp16 subnormals:
-// code x 2^-24 for i = 0 and 2, code x 2^-20 for 1 and 3.
+// Four pairs of codes (nibbles i of both 16-bit halves) as fp16 subnormals: of keys
+// code x 2^-24 for i = 0 and 2 and code x 2^-20 for 1 and 3, of values code x 2^-20.
+template <bool kValues>
 __device__ __forceinline__ void codes4(uint32_t w, uint32_t *p) {
     const uint32_t v = w >> 8;
-    p[0] = w & 0x000f000fu;
+    p[0] = kValues ? (w << 4) & 0x00f000f0u : w & 0x000f000fu;
     p[1] = w & 0x00f000f0u;
-    p[2] = v & 0x000f000fu;
+    p[2] = kValues ? (w >> 4) & 0x00f000f0u : v & 0x000f000fu;
     p[3] = v & 0x00f000f0u;
 }
 
@@ -106,6 +114,18 @@ __device__ __forceinline__ uint4 words_at(uint32_t addr) {
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(addr) : "memory");
     return w;
 }
+
+// two products at a time
+__device__ __forceinline__ float2 mul2(float a0, float a1, float b0, float b1) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+    return r;
+}
+
+// 2^e, 0 for e below -126
+__device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(e + 127) << 23); }
 
 __device__ __forceinline__ uint32_t pick(const uint4 &u, int i) {
     return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
@@ -145,7 +165,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // hold z, against -sum q_g split into three fp16 parts (33 bits).  Values: one
 // more 16-row tile holds z of group g in row g, so that its product with the
 // rounded probabilities is subtracted at the end and the rounding error of a
-// probability acts on (code - z) only.
+// probability acts on (code - z) only.  Zero points stand as z x 2^-18, the most that a
+// subnormal holds.
 //
 // A group of a value that is not finite makes that group of the outputs NaN, for the rows
 // that see the token, and nothing else: its step is taken as 0 in the products (0 x NaN would
@@ -307,7 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 qf[nt][gr][e] = half2_bits(y0, y1);
                 part[e & 1] += y0 + y1;
             }
-            float sum = -16.0f * part[1] - part[0];
+            float sum = -0.25f * part[1] - 0.015625f * part[0];      // zero points are z x 2^-18
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             const float h0 = __half2float(__float2half_rn(sum));
@@ -329,16 +350,16 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
 
     // lane constants of the fragments' addresses and of the zero points' places
     const uint32_t at_row = ((lane & 15) * SV) + (lane >> 4) * 16;    // rows 0..15, then the next group
-    const uint32_t z_mul = c == 0 ? 0x00010001u : c == 1 ? 1u : 0u;
+    const uint32_t z_mul = c == 0 ? 0x00400040u : c == 1 ? 0x40u : 0u;
     const uint32_t z_group = (g < NG ? g : 0) * 4;
 
-    float o[NG][2][NT][4], oz[NT][4], f[NG], m[NT][2], l[NT][2];
+    float o[NG][2][NT][4], oz[NT][4], f[NG][NT][2], m[NT][2], l[NT][2];
     uint32_t nan_groups = 0;      // bit 8 (2 nt + e) + gr: that row's group gr is NaN
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-        f[gr] = __uint_as_float(227u << 23);   // 2^100: set by the first step that is not 0
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            f[gr][nt][0] = f[gr][nt][1] = __uint_as_float((127u + kScaleMost) << 23);   // set by the first weight that is not 0
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[gr][0][nt][e] = o[gr][1][nt][e] = 0.0f;
         }
@@ -351,6 +372,13 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         l[nt][0] = l[nt][1] = 0.0f;
     }
 
+    auto scale_sums = [&](int gr, int nt, int e, float k) {
+        if (g == gr) oz[nt][e] *= k;
+        o[gr][0][nt][e] *= k;
+        o[gr][0][nt][e + 2] *= k;
+        o[gr][1][nt][e] *= k;
+        o[gr][1][nt][e + 2] *= k;
+    };
     for (int stage = 0; t0 < c1; t0 += kTurn, stage ^= 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
@@ -372,8 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 if (gr % 2 == 0) blocks4<false>(ks + 16 * sub * SV + gr * 16 + at_row, kw);
                 const uint32_t s0 = pick(w0, gr % 4), s1 = pick(w1, gr % 4);
                 uint32_t p0[4], p1[4];
-                codes4(kw[gr % 2 * 2], p0);
-                codes4(kw[gr % 2 * 2 + 1], p1);
+                codes4<false>(kw[gr % 2 * 2], p0);
+                codes4<false>(kw[gr % 2 * 2 + 1], p1);
                 const uint32_t a0[4] = {p0[0], p1[0], p0[1], p1[1]};
                 const uint32_t a1[4] = {p0[2], p1[2], p0[3], p1[3]};
                 const float d0 = q4_step(s0), d1 = q4_step(s1);
@@ -436,28 +464,28 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    float k = 1.0f;
+                    int rise = 0;                        // of the maximum
                     if (m[nt][e] == kNoMax) {            // nothing seen so far: take it as it is
                         if (t == -INFINITY) continue;
                         m[nt][e] = t;
                     } else {
-                        t = fmaxf(t, 0.0f);              // by how much the maximum rises
-                        k = exp2_fast(-t);
+                        t = ceilf(fmaxf(t, 0.0f));
                         m[nt][e] += t;
+                        rise = (int)fminf(t, 1000.0f);
                     }
-                    l[nt][e] *= k;
-                    oz[nt][e] *= k;
 #pragma unroll
                     for (int sub = 0; sub < 2; ++sub) {
                         x[sub][nt][e] -= t;
                         x[sub][nt][e + 2] -= t;
                     }
+                    l[nt][e] *= pow2i(-rise);
+                    // The weights' sums stay: f rises by as much as the weights fall.
 #pragma unroll
                     for (int gr = 0; gr < NG; ++gr) {
-                        o[gr][0][nt][e] *= k;
-                        o[gr][0][nt][e + 2] *= k;
-                        o[gr][1][nt][e] *= k;
-                        o[gr][1][nt][e + 2] *= k;
+                        const int most = kScaleMost + 127 - (int)(__float_as_uint(f[gr][nt][e]) >> 23);
+                        const int up = min(rise, most);
+                        f[gr][nt][e] = __uint_as_float(__float_as_uint(f[gr][nt][e]) + ((uint32_t)up << 23));
+                        if (up < rise) scale_sums(gr, nt, e, pow2i(up - rise));
                     }
                 }
         }
@@ -471,11 +499,19 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     l[nt][e & 1] += x[sub][nt][e];
                 }
 
-        // Steps of the values, in units of 1/f: f is a power of two a group that
-        // keeps p x step inside fp16 (p <= 2^8, step x f <= 2^6).
+        // Weights p x step in units of 1/f.  f belongs to one row and group and follows the
+        // largest weight that the row has met (it is brought to 2^4..2^5 and may grow to
+        // 2^15), so that neither a step that the row does not see nor one that its
+        // probability makes small takes bits from the others.
+        float most_p[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                most_p[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
         uint4 vw[2][2][(NG + 3) / 4];
-        float most[NG];
-        bool raise = false, not_finite = false;
+        float bound = 0.0f;           // on the weights of this lane's tokens
+        bool not_finite = false;
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
@@ -488,13 +524,15 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             auto w = [&](int sub, int k) { return pick(vw[sub][k][gr / 4], gr % 4); };
             const uint32_t top = max(max(w(0, 0), w(0, 1)), max(w(1, 0), w(1, 1)));
             not_finite |= top >= 0x7f800000u;
-            most[gr] = __uint_as_float(top);
-            raise |= most[gr] * f[gr] > 64.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 u = mul2(most_p[nt][0], most_p[nt][1], f[gr][nt][0], f[gr][nt][1]);
+                bound = fmaxf(bound, fmaxf(u.x, u.y) * __uint_as_float(top));
+            }
         }
         if (__any_sync(0xffffffffu, not_finite)) {
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                most[gr] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint4 &u = vw[k / 2][k % 2][gr / 4];
@@ -508,48 +546,42 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                                 if (t < c1 && (!kMany || (t <= lim[nt][e] && t >= low[nt][e])))
                                     nan_groups |= 1u << (8 * (2 * nt + e) + gr);
                     }
-                    most[gr] = fmaxf(most[gr], __uint_as_float(pick(u, gr % 4)));
                 }
-                raise |= most[gr] * f[gr] > 64.0f;
             }
         }
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, bound > kWeightMost || not_finite)) {
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                float t = most[gr];
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
-                const uint32_t ex = min(__float_as_uint(t) >> 23, 252u);
-                if (t * f[gr] > 64.0f) {
-                    const float to = __uint_as_float((254u - ex) << 23), k = to / f[gr];
-                    f[gr] = to;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (g == gr) {
-                            oz[nt][0] *= k;
-                            oz[nt][1] *= k;
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        float t = 0.0f;      // the row's largest weight in these tokens
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[gr][0][nt][e] *= k;
-                            o[gr][1][nt][e] *= k;
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            t = fmaxf(t, x[k / 2][nt][e + k % 2 * 2] * q4_step(pick(vw[k / 2][k % 2][gr / 4], gr % 4)));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+                        // no branch: one for each row and group takes longer
+                        const uint32_t at = __float_as_uint(f[gr][nt][e]) >> 23;
+                        const uint32_t to = t * f[gr][nt][e] > kWeightMost ? 258u - min(__float_as_uint(t) >> 23, 254u) : at;
+                        scale_sums(gr, nt, e, pow2i((int)to - (int)at));
+                        f[gr][nt][e] = __uint_as_float(to << 23);
                     }
-                }
             }
         }
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
             // zero points of group g: tokens 2 c, 2 c + 1 and the same + 8
             const uint32_t z = vs + (16 * sub + 2 * c) * SV + D / 2 + z_group;
-            const uint32_t za = __byte_perm(word_at(z), word_at(z + SV), 0x5410) & 0x000f000fu;
-            const uint32_t zb = __byte_perm(word_at(z + 8 * SV), word_at(z + 9 * SV), 0x5410) & 0x000f000fu;
+            const uint32_t za = (__byte_perm(word_at(z), word_at(z + SV), 0x5410) & 0x000f000fu) << 6;
+            const uint32_t zb = (__byte_perm(word_at(z + 8 * SV), word_at(z + 9 * SV), 0x5410) & 0x000f000fu) << 6;
             uint32_t vc[4];
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
                 if (gr % 2 == 0) blocks4<true>(vs + 16 * sub * SV + gr * 16 + at_row, vc);
-                const float d0 = q4_step(pick(vw[sub][0][gr / 4], gr % 4)) * f[gr];
-                const float d1 = q4_step(pick(vw[sub][1][gr / 4], gr % 4)) * f[gr];
+                const float d0 = q4_step(pick(vw[sub][0][gr / 4], gr % 4));
+                const float d1 = q4_step(pick(vw[sub][1][gr / 4], gr % 4));
                 // fp16 outputs: weights in two fp16 parts, so that only the output is rounded
                 // (17 requests of up to 8,906 tokens, 5 heads over 1 of 96: error against 64
                 // bits 2.2e-4, 3.2e-4 with one part, 2.1e-4 for a float32 plain form; 24
@@ -558,9 +590,9 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                 uint32_t b[NT][2], rest[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = x[sub][nt][e] * (e < 2 ? d0 : d1);
+                    const float2 u0 = mul2(x[sub][nt][0], x[sub][nt][1], f[gr][nt][0], f[gr][nt][1]);
+                    const float2 u1 = mul2(x[sub][nt][2], x[sub][nt][3], f[gr][nt][0], f[gr][nt][1]);
+                    const float p[4] = {u0.x * d0, u0.y * d0, u1.x * d1, u1.y * d1};
                     uint32_t h[2] = {half2_bits(p[0], p[1]), half2_bits(p[2], p[3])};
                     b[nt][0] = transpose8x8(h[0]);
                     b[nt][1] = transpose8x8(h[1]);
@@ -572,8 +604,8 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
                     }
                 }
                 uint32_t p0[4], p1[4];
-                codes4(vc[gr % 2 * 2], p0);
-                codes4(vc[gr % 2 * 2 + 1], p1);
+                codes4<true>(vc[gr % 2 * 2], p0);
+                codes4<true>(vc[gr % 2 * 2 + 1], p1);
                 const uint32_t a0[4] = {p0[0], p0[1], p1[0], p1[1]};
                 const uint32_t a1[4] = {p0[2], p0[3], p1[2], p1[3]};
                 const uint32_t az[4] = {g == gr ? za : 0u, 0u, g == gr ? zb : 0u, 0u};
@@ -618,11 +650,11 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
             }
 #pragma unroll
             for (int gr = 0; gr < NG; ++gr) {
-                // undo f, a power of two, and the subnormals' 2^-24 (2^-20 for odd codes)
-                const float k = __shfl_sync(0xffffffffu, oz[nt][e], 4 * gr + c) * -16777216.0f;
-                const float back = __uint_as_float((254u << 23) - __float_as_uint(f[gr]));
-                float4 v = make_float4(o[gr][0][nt][e] * 16777216.0f + k, o[gr][0][nt][e + 2] * 1048576.0f + k,
-                                       o[gr][1][nt][e] * 16777216.0f + k, o[gr][1][nt][e + 2] * 1048576.0f + k);
+                // undo f, a power of two, and the subnormals' 2^-20 (2^-18 for zero points)
+                const float k = __shfl_sync(0xffffffffu, oz[nt][e], 4 * gr + c) * -262144.0f;
+                const float back = __uint_as_float((254u << 23) - __float_as_uint(f[gr][nt][e]));
+                float4 v = make_float4(o[gr][0][nt][e] * 1048576.0f + k, o[gr][0][nt][e + 2] * 1048576.0f + k,
+                                       o[gr][1][nt][e] * 1048576.0f + k, o[gr][1][nt][e + 2] * 1048576.0f + k);
                 v.x *= back;
                 v.y *= back;
                 v.z *= back;

@@ -1,5 +1,6 @@
-"""kv_attend where a window's prompt chunk spans more tokens than one tile of queries sees, and
-where a group of a value is not finite."""
+"""kv_attend where a window's prompt chunk spans more tokens than one tile of queries sees,
+where a group of a value is not finite, and where steps of the 4-bit format differ widely from
+token to token: a query's result must not depend on what it does not see."""
 import numpy as np
 import pytest
 
@@ -125,3 +126,64 @@ def test_few_rows_a_group_that_is_not_finite_joined_over_chunks(dtype, n_q):
         want_nan = torch.zeros_like(nan)
         want_nan[:n_q, :, 64:96] = True
         assert torch.equal(nan, want_nan)
+
+
+# ------------------------------------------- steps that differ between tokens
+
+FEW = [(128, 2, 6), (64, 4, 19), (96, 1, 6), (128, 4, 19), (256, 2, 40), (192, 1, 6)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", FEW)
+@pytest.mark.parametrize("power,groups", [(20, None), (45, [0]), (45, [1]), (90, None)])
+def test_few_rows_do_not_feel_large_values_they_do_not_see(dtype, dim, group, n_q, power, groups):
+    """A later new token's values are 2^power times the others': the queries before it get the
+    bytes that they get without it."""
+    with Batch([150], [n_q], 1, group, dim, 16, dtype) as b:
+        want, wl, _ = b.run()
+        want, wl, t = want.clone(), wl.clone(), 150 - n_q // 3 - 1
+        grow(b, 0, 1, t, power, groups)
+        out, lse, status = b.run()
+        before = t - (150 - n_q)
+        assert before > 0 and status == 0
+        assert torch.equal(out[:before], want[:before]) and torch.equal(lse, wl)
+        if dtype == "bf16":                              # fp16 outputs overflow
+            vec_check.check(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(128, 4, 1), (64, 2, 1), (256, 2, 1), (96, 3, 1)] + FEW)
+@pytest.mark.parametrize("power,groups", [(20, None), (45, [0]), (45, [1])])
+@pytest.mark.parametrize("at", [3, 140])
+def test_few_rows_large_values_without_weight(dtype, dim, group, n_q, power, groups, at):
+    """A token with large values whose key points away from every query: weight 0 or nearly so."""
+    if at == 140 and n_q > 10:
+        at = 100
+    with Batch([150], [n_q], 1, group, dim, 16, dtype) as b:
+        away(b, 0, at)
+        grow(b, 0, 1, at, power, groups)
+        out, lse, status = b.run()
+        assert status == 0
+        vec_check.check(b, out, lse)
+
+
+def away(b, i, t, by=-12.0):
+    """All queries nearly the same, and request i's key t against them: a weight of about e^-130."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(77)
+    one = torch.randn(1, 1, b.dim, generator=g, device="cuda")
+    b.q = (one + 0.1 * torch.randn(b.q.shape, generator=g, device="cuda")).to(b.dt)
+    put(b, i, 0, t, by * one[0].cpu().numpy() * (128 / b.dim) ** 0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(128, 4, 1), (64, 4, 5)])
+def test_few_rows_maximum_that_rises_far(dtype, dim, group, n_q):
+    """Scores that rise by hundreds after tokens with large values: the large ones end with no
+    weight and must not keep the scale that they brought."""
+    with Batch([1000], [n_q], 1, group, dim, 16, dtype) as b:
+        away(b, 0, slice(0, 400), by=-14.0)
+        grow(b, 0, 1, slice(0, 400), 30)
+        out, lse, status = b.run()
+        assert status == 0
+        vec_check.check(b, out, lse)
