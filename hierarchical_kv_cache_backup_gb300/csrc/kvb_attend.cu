@@ -181,25 +181,19 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // (2% slower), four-warp blocks with 96 registers (5-30% slower), several heads a block for
 // NHD pages (20% slower), both halves' exponentials at once for four rows (no change).
 template <int D, int NT, bool kHalf, bool kMany>
-__global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
-    kv_attend_rows_kernel(const __grid_constant__ AttendArgs a) {
+__device__ __forceinline__ void attend_rows(const AttendArgs &a, int head, int rt, int r, int ci, int chunk,
+                                            bool report) {
     constexpr int NG = D / 32;                 // groups of a vector
     constexpr int SV = vec_stride(D), PV = vec_bytes(D) / 16;
     constexpr int kRows = 8 * NT;
     constexpr int WB = warp_bytes(D, NT);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float join_m[kWarps][kRows], join_l[kWarps][kRows];
-    asm volatile("griddepcontrol.launch_dependents;");
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int H = (int)a.pool.H;
-    // every request's first chunk, which is the fullest, before any second one
-    const int head = blockIdx.x % H, rt = blockIdx.x / H, ci = blockIdx.z;
-    const int r = blockIdx.y;
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     constexpr int kTurn = kWarps * kTile;      // from a warp's tile to its next
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Without a window the first tiles' places in the page table are known before the
     // request's length is: their pages are read along with it (a row holds the pages
@@ -209,19 +203,19 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
         return t < end ? table[div_T(a.pool, (uint32_t)t)] : 0;
     };
     if (!a.window) {
-        const int64_t t = (int64_t)ci * a.chunk + warp * kTile + lane;
+        const int64_t t = (int64_t)ci * chunk + warp * kTile + lane;
         if (t < (int64_t)a.max_len) page = look_up((int)t, (int)a.max_len);
         if (t + kTurn < (int64_t)a.max_len) page1 = look_up((int)t + kTurn, (int)a.max_len);
     }
     bool bad;
     const Span s = span_of<kRows>(a, r, rt, &bad);
-    if (bad && a.status != nullptr && threadIdx.x == 0 && blockIdx.x + blockIdx.z == 0)
+    if (bad && a.status != nullptr && threadIdx.x == 0 && report)
         atomicOr(a.status, KV_STATUS_BAD_LENGTH);
     const int row0 = rt * kRows, rows = min(kRows, s.n * (int)a.group - row0);
     if (rows <= 0) return;
-    const int c0 = s.lo + ci * (int)a.chunk, c1 = min(s.hi, c0 + (int)a.chunk);
+    const int c0 = s.lo + ci * chunk, c1 = min(s.hi, c0 + chunk);
     if (c0 >= c1 && ci > 0) return;
-    const bool whole = s.hi - s.lo <= (int)a.chunk;   // this block sees all the rows see
+    const bool whole = s.hi - s.lo <= chunk;          // this block sees all the rows see
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * WB;
     const int group = (int)a.group;
@@ -712,6 +706,33 @@ __global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
     }
 }
 
+template <int D, int NT, bool kHalf, bool kMany>
+__global__ void __launch_bounds__(kWarps * 32, D * NT <= 128 ? 2 : 1)
+    kv_attend_rows_kernel(const __grid_constant__ AttendArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int H = (int)a.pool.H;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // every request's first chunk, which is the fullest, before any second one
+    attend_rows<D, NT, kHalf, kMany>(a, (int)blockIdx.x % H, (int)blockIdx.x / H, (int)blockIdx.y, (int)blockIdx.z,
+                                     (int)a.chunk, blockIdx.x + blockIdx.z == 0);
+}
+
+// Requests with many rows whose steps differ too much for the kernel that holds keys
+// and values in fp16 (it says so in a.uneven): a block takes row tiles of one head
+// and request in turn, each over all its cached tokens.  Blocks of even requests end at once.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kWarps * 32, 1) kv_attend_uneven_kernel(const __grid_constant__ AttendArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int head = (int)blockIdx.x, r = (int)blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = (int)min((int64_t)a.q_start[r + 1] - a.q_start[r], (int64_t)a.max_q);
+    if (n <= 0 || a.uneven[(int64_t)r * a.pool.H + head] == 0) return;
+    for (int rt = (int)blockIdx.z; rt * 16 < n * (int)a.group; rt += (int)gridDim.z) {
+        attend_rows<D, 2, kHalf, true>(a, head, rt, r, 0, 1 << 30, false);
+        __syncthreads();      // the next tile's copies go where this one's sums stand
+    }
+}
+
 // Joins the chunks of a row (a query head and token): kW warps a row, each over
 // every kW-th chunk, a lane D / 32 values.  Rows of few chunks take one warp, four rows a
 // block; with many the parts are too long a chain for one.
@@ -818,6 +839,17 @@ const Variant kVariants[] = {KVB_VARIANTS(64, 1),  KVB_VARIANTS(64, 2),  KVB_VAR
                              KVB_VARIANTS(96, 2),  KVB_VARIANTS(128, 1), KVB_VARIANTS(128, 2),
                              KVB_VARIANTS(192, 1), KVB_VARIANTS(256, 1)};
 
+struct UnevenVariant {
+    uint32_t D;
+    bool fp16;
+    AttendFn *fn;
+    int smem;
+};
+#define KVB_UNEVEN(D)                                                            \
+    UnevenVariant{D, false, kv_attend_uneven_kernel<D, false>, kWarps * warp_bytes(D, 2)}, \
+        UnevenVariant{D, true, kv_attend_uneven_kernel<D, true>, kWarps * warp_bytes(D, 2)}
+const UnevenVariant kUnevenVariants[] = {KVB_UNEVEN(64), KVB_UNEVEN(96), KVB_UNEVEN(128)};
+
 }  // namespace
 
 // Query rows of a request from which the tcgen05 kernel (256 rows a block) is taken.
@@ -839,7 +871,10 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     if (p.many) {
         plan_attend_tc(&p, span, requests, kv_heads, sms);
         p.step_parts = step_parts_of(max_len, window, max_q);
-        p.step_bytes = ((uint64_t)requests * p.step_parts * kv_heads * 8 * sizeof(uint32_t) + 255) / 256 * 256;
+        p.step_bytes = ((uint64_t)requests * (p.step_parts * (uint64_t)kStepWords + 1) * kv_heads * sizeof(uint32_t) + 255) /
+                       256 * 256;
+        p.uneven_blocks = (uint32_t)std::min<uint64_t>(
+            (rows + 15) / 16, std::max<uint64_t>(1, 2ull * (uint64_t)sms / ((uint64_t)requests * kv_heads)));
     } else {
         // Cut along the cached tokens into the number of chunks that ends soonest, by a
         // model in tokens of one block: what all blocks read spread over the blocks
@@ -872,11 +907,22 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
     return p;
 }
 
+cudaError_t launch_attend_uneven(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
+                                 cudaStream_t stream) {
+    for (const UnevenVariant &v : kUnevenVariants)
+        if (v.D == D && v.fp16 == fp16)
+            return launch(v.fn, dim3(a.pool.H, a.requests, p.uneven_blocks), kWarps * 32, v.smem, stream, pdl, a);
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
                           cudaStream_t stream, int *launches) {
     (void)cudaGetLastError();
     if (p.many) {
-        return launch_attend_tc(a, D, fp16, pdl, stream, launches);
+        cudaError_t e = launch_attend_tc(a, D, fp16, pdl, stream, launches);
+        if (e == cudaSuccess) e = launch_attend_uneven(a, p, D, fp16, pdl, stream);
+        if (e == cudaSuccess) ++*launches;
+        return e;
     }
     const bool many = a.max_q > 1;
     for (const Variant &v : kVariants) {
@@ -906,6 +952,12 @@ cudaError_t preload_attend_kernels() {
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
+        if (e != cudaSuccess) return e;
+    }
+    for (const UnevenVariant &v : kUnevenVariants) {
+        cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute((const void *)v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e != cudaSuccess) return e;
     }
     return preload_attend_tc_kernels();

@@ -13,13 +13,18 @@
 // buffer of 128, each softmax waited for its own products, 370 us for 2 x 1,000
 // new tokens over 8,192 cached ones.
 //
-// Range.  fp16 operands stay in range for any input by exact powers of two: steps
-// of the keys and values of each group of 32 are scaled by the largest step
-// of the request (a kernel that reads the scale words finds it), queries take the key
-// groups' powers in exchange, and each query row is brought near 2^9.  What is
-// rounded: a value once (2^-12; not for fp16 outputs), a probability once.  Keys are two fp16 parts each,
+// Range.  fp16 operands stay in range by exact powers of two: steps of the keys and
+// values of each group of 32 are brought to 2^12 at most by the largest step of the
+// request (a kernel that reads the scale words finds it), queries take the key groups'
+// powers in exchange, each query row is brought to 2^14..2^15, and probabilities to
+// 2^7..2^15 at a row's largest.  That keeps every step's bits where all steps of
+// a group are within 2^16 of each other, over all that the request's rows see; a request
+// and head where they are not (its small steps would lose bits to a large one that a row may not
+// see, or gives no weight) goes to the kernel for few rows, which scales by rows.
+// What is rounded: a value once (2^-11; not for fp16 outputs), a probability once
+// (2^-11).  Keys are two fp16 parts each,
 // which their products with the queries take in turn, where the caller wants the
-// logarithms of the sums: with one part (2^-12) a logarithm of few terms is off by
+// logarithms of the sums: with one part (2^-11) a logarithm of few terms is off by
 // 1e-5 of itself, which float32 has to show and 16-bit outputs do not.  Without
 // them one part is taken: 2 x 1,000 new tokens over 8,192 cached ones, 295 us with
 // two parts and 235 with one.
@@ -208,24 +213,31 @@ __device__ __forceinline__ float pow2_of(uint32_t most) {
     return most == 0 ? 1.0f : __uint_as_float(most & 0x7f800000u);
 }
 
+// Bits that steps of a group may differ by, and the power of two that the largest is near.
+constexpr uint32_t kStepBits = 15;
+constexpr float kStepUp = 2048.0f;
+// A row's largest probability is taken as 2^7, and may pass that by 2^8 before the maximum moves.
+constexpr float kProbBits = 7.0f, kProbDown = 0.0078125f;
+
 struct SharedTc {
     unsigned long long bars[32];
     uint32_t tmem;
     int gave_up, value_nan;
     uint32_t most[2][4];     // largest steps of keys and values, a group each (as bits)
+    uint32_t least[2][4];    // and the least that are not 0
 };
 
-// The largest steps (as float bits) of the keys and values that kStepTokens tokens
-// of a request hold for one head: [request][part][head][2][4].  Together the parts
-// cover what all rows of the request see.
+// The largest and the least steps but 0 (as float bits) of the keys and values that
+// kStepTokens tokens of a request hold for one head: [request][part][head][2][4 and 4].
+// Together the parts cover what all rows of the request see.
 
 template <int D>
 __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int NG = D / 32;
-    __shared__ uint32_t all[8];
+    __shared__ uint32_t all[kStepWords];     // as in a.steps
     asm volatile("griddepcontrol.launch_dependents;");
     const int head = blockIdx.x, part = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
-    if (tid < 8) all[tid] = 0;
+    if (tid < (int)kStepWords) all[tid] = tid & 4 ? 0xffffffffu : 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __syncthreads();
     bool bad;
@@ -234,9 +246,12 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     const int64_t head_off = (int64_t)head * a.pool.s_head;
     const int t0 = s.lo + part * (int)kStepTokens, t1 = min(s.hi, t0 + (int)kStepTokens);
-    uint32_t most[2][NG];
+    uint32_t most[2][NG], least[2][NG];
 #pragma unroll
-    for (int i = 0; i < 2 * NG; ++i) most[i / NG][i % NG] = 0;
+    for (int i = 0; i < 2 * NG; ++i) {
+        most[i / NG][i % NG] = 0;
+        least[i / NG][i % NG] = 0xffffffffu;
+    }
 #pragma unroll 4
     for (int t = t0 + tid; t < t1; t += 256) {
         bool wrong;
@@ -251,16 +266,22 @@ __global__ void __launch_bounds__(256) kv_attend_steps_kernel(const __grid_const
             for (int gr = 0; gr < NG; ++gr) {
                 const uint32_t w = v[gr] & ~15u;
                 if (w < 0x7f800000u) most[comp][gr] = max(most[comp][gr], w);
+                if (w != 0) least[comp][gr] = min(least[comp][gr], w);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i) {
         const uint32_t w = __reduce_max_sync(0xffffffffu, most[i / NG][i % NG]);
-        if ((tid & 31) == 0 && w != 0) atomicMax(&all[i / NG * 4 + i % NG], w);
+        const uint32_t u = __reduce_min_sync(0xffffffffu, least[i / NG][i % NG]);
+        if ((tid & 31) == 0) {
+            atomicMax(&all[i / NG * 8 + i % NG], w);
+            atomicMin(&all[i / NG * 8 + 4 + i % NG], u);
+        }
     }
     __syncthreads();
-    if (tid < 8) a.steps[(((int64_t)r * a.step_parts + part) * a.pool.H + head) * 8 + tid] = all[tid];
+    if (tid < (int)kStepWords)
+        a.steps[(((int64_t)r * a.step_parts + part) * a.pool.H + head) * kStepWords + tid] = all[tid];
 }
 
 template <int D, bool kHalf, int kParts>
@@ -321,7 +342,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.gave_up = 0;
         sh.value_nan = 0;
-        for (int i = 0; i < 8; ++i) sh.most[i / 4][i % 4] = 0;
+        for (int i = 0; i < 8; ++i) {
+            sh.most[i / 4][i % 4] = 0;
+            sh.least[i / 4][i % 4] = 0xffffffffu;
+        }
     }
     if (warp == kSoftWarps + kUnpackWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem))
@@ -333,12 +357,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
     fence_after();
     const uint32_t tmem = sh.tmem;
 
-    // the largest step of each group of the request and head
-    for (int k = tid; k < (int)a.step_parts * 8; k += kThreadsTc) {
-        const uint32_t w = a.steps[(((int64_t)r * a.step_parts + (k >> 3)) * H + head) * 8 + (k & 7)];
-        if (w != 0) atomicMax(&sh.most[k >> 2 & 1][k & 3], w);
+    // the largest and least step of each group of the request and head
+    for (int k = tid; k < (int)(a.step_parts * kStepWords); k += kThreadsTc) {
+        const uint32_t w = a.steps[(((int64_t)r * a.step_parts + k / kStepWords) * H + head) * kStepWords + k % kStepWords];
+        if ((k & 4) == 0) atomicMax(&sh.most[k >> 3 & 1][k & 3], w);
+        else atomicMin(&sh.least[k >> 3 & 1][k & 3], w);
     }
     __syncthreads();
+    bool uneven = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = sh.most[i / 4][i % 4];
+        uneven |= w != 0 && (w >> 23) - (sh.least[i / 4][i % 4] >> 23) > kStepBits;
+    }
+    if (rt == 0 && ci == 0 && tid == 0) a.uneven[(int64_t)r * H + head] = uneven;
+    if (uneven) {
+        if (warp == kSoftWarps + kUnpackWarps)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        return;
+    }
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax
@@ -380,11 +417,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 }
             }
             if (sign == 0.0f) top = 0.0f;
-            const uint32_t ex = __float_as_uint(top) >> 23;
-            const bool scaled = ex >= 10 && ex < 255;
-            const float up = scaled ? __uint_as_float((263u - ex) << 23) : 1.0f;
+            // 2^(14 - exponent of top), and its inverse; 1 for infinities and NaN
+            const uint32_t ex = max(__float_as_uint(top) >> 23, 15u);
+            const float up = ex < 255 ? __uint_as_float((268u - ex) << 23) : 1.0f;
             // never 0, so that a masked score of -infinity stays one
-            sc = fmaxf((scaled ? __uint_as_float((ex - 9u) << 23) : 1.0f) * fabsf(a.scale_log2), 1.2e-38f);
+            sc = fmaxf((ex < 255 ? __uint_as_float((ex - 14u) << 23) : 1.0f) * (fabsf(a.scale_log2) / kStepUp), 1.2e-38f);
 #pragma unroll 2
             for (int gr = 0; gr < NG; ++gr) {
                 const float f = pow2_of(sh.most[0][gr]) * sign;
@@ -439,6 +476,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             // the maximum moves when it is passed by more than 2^8; then the sums
             // so far, O in tensor memory among them, are scaled down
             float k = 1.0f;
+            most -= kProbBits;
             if (m == kNoMaxTc) {
                 if (most > -INFINITY) m = most;
             } else if (most > m + 8.0f) {
@@ -519,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                 for (int e = 0; e < 32; ++e) x[e] = 0;
             }
             if (on) {
-                const float f = pow2_of(sh.most[1][ch]);
+                const float f = pow2_of(sh.most[1][ch]) / kStepUp;
                 if (nan_groups >> ch & 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = kNanWord;
@@ -534,8 +572,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
                             // dims 2 b and 2 b + 1 of the eight
-                            const float u = __uint_as_float(x[e + (b < 2 ? 4 * b : 4 * b - 7)]) * f * inv;
-                            const float v = __uint_as_float(x[e + (b < 2 ? 4 * b + 2 : 4 * b - 5)]) * f * inv;
+                            const float u = __uint_as_float(x[e + (b < 2 ? 4 * b : 4 * b - 7)]) * inv * f;
+                            const float v = __uint_as_float(x[e + (b < 2 ? 4 * b + 2 : 4 * b - 5)]) * inv * f;
                             if (kHalf) {
                                 h[b] = h2_bits(u, v);
                             } else {
@@ -547,13 +585,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                     }
                 } else {
                     float *dst = a.part_o + part * D + ch * 32;
+                    const float fp = f * kProbDown;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                     {
                         const int k = e / 8 * 8 + (e & 4 ? 1 : 0);
                         *reinterpret_cast<float4 *>(dst + e) =
-                            make_float4(__uint_as_float(x[k]) * f, __uint_as_float(x[k + 2]) * f,
-                                        __uint_as_float(x[k + 4]) * f, __uint_as_float(x[k + 6]) * f);
+                            make_float4(__uint_as_float(x[k]) * fp, __uint_as_float(x[k + 2]) * fp,
+                                        __uint_as_float(x[k + 4]) * fp, __uint_as_float(x[k + 6]) * fp);
                     }
                 }
             }
@@ -565,7 +604,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
                        : l != 0.0f ? ((m == kNoMaxTc ? 0.0f : m) + log2f(l)) * 0.693147180559945f : -INFINITY;
         if (on && !whole)
             *reinterpret_cast<float2 *>(a.part_ml + part * 2) =
-                make_float2(m == kNoMaxTc ? 0.0f : m, alive ? l : __uint_as_float(kNanWord));
+                make_float2(m == kNoMaxTc ? 0.0f : m + kProbBits, alive ? l * kProbDown : __uint_as_float(kNanWord));
         fence_before();
     } else if (warp < kSoftWarps + kUnpackWarps) {
         // ------------------------------------------------- unpack to fp16 tiles
@@ -577,8 +616,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
         const int d = tid - 32 * kSoftWarps;
         const int gr = d % NP, tk0 = d / NP;                 // group; tokens tk0 + it * kStep
         const bool idle = gr >= NG || tk0 >= kTileK;
-        const float f[2] = {1.0f / pow2_of(sh.most[0][idle ? 0 : gr]),
-                            1.0f / pow2_of(sh.most[1][idle ? 0 : gr])};
+        const float f[2] = {kStepUp / pow2_of(sh.most[0][idle ? 0 : gr]),
+                            kStepUp / pow2_of(sh.most[1][idle ? 0 : gr])};
         // Lanes of groups 2 and 3 go through their words two apart from those of 0 and
         // 1, so that 8 lanes' stores meet 8 different places of 16 bytes.
         const bool apart = (gr >> 1 & 1) != 0;
@@ -798,7 +837,7 @@ __global__ void __launch_bounds__(128) kv_attend_join_tc_kernel(const __grid_con
     const Span s = row_span(a.q_start[r], a.q_start[r + 1], a.lens[r], (int)a.tokens, (int)a.max_q,
                             (int)a.max_len, group, (int)a.window, rt, kRowsTc, &bad);
     const int n = (s.hi - s.lo + (int)a.chunk - 1) / (int)a.chunk;
-    if (row >= s.n * group || n <= 1) return;
+    if (row >= s.n * group || n <= 1 || a.uneven[(int64_t)r * H + head] != 0) return;
     const int64_t tok = s.q0 + row / group;
     const int qh = head * group + row % group;
     float top = kNoMaxTc, sum = 0.0f, acc[NV];

@@ -502,6 +502,7 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
     k.whole_units = (uint32_t)plan.whole_units;
     k.steps = (uint32_t *)a->workspace;
     k.step_parts = plan.step_parts;
+    k.uneven = k.steps + (uint64_t)a->requests * plan.step_parts * k.pool.H * kStepWords;
     if (plan.bytes != 0) {
         k.part_o = (float *)((char *)a->workspace + plan.step_bytes);
         k.part_ml = k.part_o + (uint64_t)plan.chunks * a->tokens * a->q_heads * a->head_dim;

@@ -110,9 +110,10 @@ KVB_HD Span row_span(int q0, int q1, int len, int tokens, int max_q, int max_len
     return s;
 }
 
-// The largest steps of a request are found kStepTokens tokens at a time, over all that its
+// The largest and least steps of a request are found kStepTokens tokens at a time, over all that its
 // rows together see (a window and its new tokens, not only what one tile of rows sees).
 constexpr uint32_t kStepTokens = 1024;
+constexpr uint32_t kStepWords = 16;       // of a part and head: keys' and values' largest and least
 
 KVB_HD uint32_t step_parts_of(uint32_t max_len, uint32_t window, uint32_t max_q) {
     uint64_t span = max_len;
@@ -227,8 +228,9 @@ struct AttendArgs {
     uint32_t chunk, chunks;   // cached tokens a block handles; the most of one request
     uint32_t row_tiles;
     uint32_t whole_units;     // many rows: units (row tile, head, request) that are not cut
-    uint32_t *steps;          // many rows: [requests][step_parts][H][2][4] largest steps
+    uint32_t *steps;          // many rows: [requests][step_parts][H][2][largest 4, least 4] steps
     uint32_t step_parts;
+    uint32_t *uneven;         // many rows: [requests][H] 1 where steps differ too much for fp16
     uint32_t window;
     float scale_log2;         // scale * log2(e)
 };

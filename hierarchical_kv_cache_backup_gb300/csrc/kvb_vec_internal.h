@@ -19,8 +19,9 @@ struct AttendPlan {
     uint32_t rows, row_tiles, chunk, chunks;
     bool many;             // the kernel for many query rows (kvb_attend_tc.cu)
     uint64_t whole_units;  // many: units that are not cut
-    uint32_t step_parts;   // many: parts of a request whose largest steps are found apart
-    uint64_t step_bytes;   // workspace of those, at its start
+    uint32_t step_parts;   // many: parts of a request whose steps are looked over apart
+    uint64_t step_bytes;   // workspace of those, and of what they find, at its start
+    uint32_t uneven_blocks;// many: blocks a head and request for those whose steps differ too much
     uint64_t bytes;        // workspace in all
 };
 AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
@@ -29,6 +30,9 @@ cudaError_t launch_attend(const AttendArgs &a, const AttendPlan &p, uint32_t D, 
                           cudaStream_t stream, int *launches);
 cudaError_t preload_attend_kernels();
 void plan_attend_tc(AttendPlan *p, uint64_t span, uint32_t requests, uint32_t kv_heads, int sms);
+// What launch_attend_tc leaves to the kernel for few rows (a.uneven).
+cudaError_t launch_attend_uneven(const AttendArgs &a, const AttendPlan &p, uint32_t D, bool fp16, bool pdl,
+                                 cudaStream_t stream);
 cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream,
                              int *launches);
 cudaError_t preload_attend_tc_kernels();

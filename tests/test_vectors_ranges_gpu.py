@@ -12,6 +12,7 @@ if not torch.cuda.is_available():
 
 import vec_check  # noqa: E402
 import vec_ref  # noqa: E402
+from hierarchical_kv_cache_backup_gb300 import kvb  # noqa: E402
 from test_vectors_gpu import Batch, b_without, poke  # noqa: E402
 
 
@@ -187,3 +188,82 @@ def test_few_rows_maximum_that_rises_far(dtype, dim, group, n_q):
         out, lse, status = b.run()
         assert status == 0
         vec_check.check(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype,dim,with_lse,comp,power", [
+    (d, n, e, c, p) for d, n, e in (("bf16", 128, True), ("bf16", 64, False), ("fp16", 128, False), ("fp16", 96, True))
+    for c in (0, 1) for p in (13, 15, 17)])
+def test_window_prompt_with_steps_far_apart(dtype, dim, with_lse, comp, power):
+    late_large_steps(dtype, dim, with_lse, comp, power)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(128, 4, 40), (64, 1, 90), (96, 8, 11), (128, 1, 300)])
+@pytest.mark.parametrize("comp,power,groups", [(1, 13, None), (1, 20, None), (1, 45, [0]), (1, 90, [1]), (0, 20, None),
+                                               (0, 45, [1])])
+def test_many_rows_do_not_feel_large_steps_they_do_not_see(dtype, dim, group, n_q, comp, power, groups):
+    """The last new token's keys or values are 2^power times the others'."""
+    with Batch([400, 350], [n_q, n_q], 2, group, dim, 16, dtype) as b:
+        want, wl, _ = b.run()
+        want, wl = want.clone(), wl.clone()
+        grow(b, 0, comp, 399, power, groups, heads=1)
+        for with_lse in (True, False):
+            out, lse, status = b.run(**({} if with_lse else dict(lse=None)))
+            assert status == 0
+            if with_lse:                                  # the other head and request: as before
+                assert torch.equal(out[:n_q, :group], want[:n_q, :group]) and torch.equal(out[n_q:], want[n_q:])
+                assert torch.equal(lse[:n_q, :group], wl[:n_q, :group]) and torch.equal(lse[n_q:], wl[n_q:])
+            o, c, l = out.clone(), b.n_q, lse.clone()
+            # the queries before the last token, as a batch of their own
+            b.n_q = [n_q - 1, 0]
+            lens, kv, b.lens = b.lens, b.kv, [399, 350]
+            b.kv = [[x[:399] for x in kv[0]], kv[1]]
+            vec_check.check(b, o, l if with_lse else None, many=True, key_parts=2 if with_lse else 1)
+            b.lens, b.kv, b.n_q = lens, kv, c
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("power,groups", [(13, None), (20, None), (45, [0])])
+@pytest.mark.parametrize("at", [3, 360])
+def test_many_rows_large_values_without_weight(dtype, power, groups, at):
+    with Batch([400], [30], 1, 4, 128, 16, dtype) as b:
+        away(b, 0, at)
+        grow(b, 0, 1, at, power, groups)
+        out, lse, status = b.run()
+        assert status == 0
+        vec_check.check(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("window", [0, 500])
+def test_many_rows_uneven_steps_cut_and_windowed(dtype, window):
+    """Requests long enough to be cut along their tokens, one of them with uneven steps."""
+    with Batch([6000, 100, 5500], [40, 3, 40], 1, 4, 128, 32, dtype, window) as b:
+        assert b.args().workspace_bytes > 0
+        want, wl, _ = b.run()
+        want, wl = want.clone(), wl.clone()
+        grow(b, 0, 1, slice(5500, 6000, 97), 18, [1])
+        grow(b, 0, 0, slice(5400, 6000, 89), -25, [0])
+        out, lse, status = b.run()
+        assert status == 0
+        assert torch.equal(out[40:], want[40:]) and torch.equal(lse[40:], wl[40:])
+        if dtype == "bf16":
+            vec_check.check(b, out, lse)
+        first = out.clone()
+        out, _, _ = b.run()
+        assert torch.equal(out, first)
+
+
+def test_many_rows_uneven_steps_with_bad_pages_and_not_finite_groups():
+    with Batch([200, 200], [40, 40], 1, 2, 64, 16, "bf16", window=60) as b:
+        for i in (0, 1):
+            grow(b, i, 1, 199, 40)
+        poke(b, 0, 170, 1, not_finite(64, [1]))      # seen by the new tokens at 170..199
+        b.table[1, 9] = -1                           # tokens 144..159: all but none of 160..199 see some
+        out, lse, status = b.run()
+        assert status == kvb.KV_STATUS_BAD_PAGE
+        assert torch.isnan(out[40:].float()).all() and torch.isnan(lse[40:]).all()
+        nan = torch.isnan(out[:40].float())
+        want_nan = torch.zeros_like(nan)
+        want_nan[10:, :, 32:] = True
+        assert torch.equal(nan, want_nan)
