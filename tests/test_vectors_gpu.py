@@ -602,7 +602,7 @@ def test_attend_step_sizes_that_rise_late():
         b.check(out, lse)
 
 
-# The kernel for many query rows: 256 rows a block, 128 cached tokens at a time.
+# The kernel for many query rows: 256 rows a block, 64 cached tokens at a time.
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("dim,H,group,n_q,lens", [

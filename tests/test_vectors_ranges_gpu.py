@@ -1,6 +1,7 @@
 """kv_attend where a window's prompt chunk spans more tokens than one tile of queries sees,
 where a group of a value is not finite, and where steps of the 4-bit format differ widely from
-token to token: a query's result must not depend on what it does not see."""
+token to token: a query's result must not depend on what it does not see.  Few-row calls of
+several tokens, cut and in windows, and long requests whose every tile shows."""
 import numpy as np
 import pytest
 
@@ -267,3 +268,46 @@ def test_many_rows_uneven_steps_with_bad_pages_and_not_finite_groups():
         want_nan = torch.zeros_like(nan)
         want_nan[10:, :, 32:] = True
         assert torch.equal(nan, want_nan)
+
+
+# ------------------------------------- branches that small cases do not reach
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,H,group,n_q", [(64, 2, 4, 2), (64, 1, 3, 5), (64, 1, 8, 9), (96, 2, 2, 8), (96, 1, 5, 3),
+                                             (128, 2, 4, 5), (128, 1, 8, 8), (128, 1, 1, 79), (64, 1, 1, 79), (96, 1, 3, 26)])
+@pytest.mark.parametrize("window", [0, 1, 37, 300])
+def test_few_rows_several_tokens(dtype, dim, H, group, n_q, window):
+    """9 to 79 query rows at heads of 128 and fewer, ragged, more new tokens than cached ones."""
+    with Batch([500, n_q, max(1, n_q - 2), 0, 33], [n_q, n_q, n_q, 2, 1], H, group, dim, 17, dtype, window, hnd=True) as b:
+        assert max(b.n_q) * group < 80
+        out, lse, status = b.run()
+        assert status == 0
+        vec_check.check(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(64, 4, 5), (96, 8, 2), (128, 8, 6), (128, 1, 40), (256, 2, 5)])
+@pytest.mark.parametrize("window", [0, 2500])
+def test_few_rows_several_tokens_joined(dtype, dim, group, n_q, window):
+    with Batch([5200, 3900, 10], [n_q, n_q, 1], 1, group, dim, 32, dtype, window) as b:
+        assert b.args().workspace_bytes > 0
+        out, lse, status = b.run()
+        assert status == 0
+        vec_check.check(b, out, lse)
+        first = out.clone()
+        out, _, _ = b.run()
+        assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim,group,n_q", [(128, 4, 1), (64, 4, 5), (256, 2, 1), (128, 4, 30)])
+def test_long_requests_lose_no_tile(dtype, dim, group, n_q):
+    """Values of every 32 tokens lie around +3 or -3: one tile left out, or taken twice, moves the
+    outputs by several times the tolerance, without any logarithm to tell."""
+    with Batch([9000], [n_q], 1, group, dim, 16, dtype) as b:
+        sign = np.random.default_rng(3).choice([-3.0, 3.0], 282).repeat(32)[:9000, None, None]
+        put(b, 0, 1, slice(None), values(b, 0, 1) * 0.1 + sign)
+        put(b, 0, 0, slice(None), values(b, 0, 0) * 0.1)
+        out, _, status = b.run(lse=None)
+        assert status == 0
+        vec_check.check(b, out, key_parts=1)

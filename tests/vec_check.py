@@ -79,7 +79,7 @@ def check(b, out, lse=None, q=None, requests=None, many=None, key_parts=2):
                 worst = max(worst, float((err / np.maximum(tol, 1e-300))[~none].max()))
                 assert ok.all(), (i, j, np.argwhere(~ok)[:4].tolist(), worst)
                 if lse is not None:
-                    el = np.abs(lse[at:at + n, j] - wl)[~none]
+                    el = np.abs(lse[at:at + n, j][~none] - wl[~none])
                     lim = ((w * dx).sum(1) + 2.0 ** -20 + 2.0 ** -21 * np.abs(np.where(none, 0, wl)))[~none]
                     assert np.all(el <= lim), (i, j, float((el / lim).max()))
         at += n
