@@ -141,9 +141,12 @@ struct Guard {
     }
 };
 
+// Below 2^-128 a scale's inverse is infinite, and zeros would be held as NaN.
 kv_status scales(uint32_t format, float k, float v) {
-    if (format == KV_CACHE_E4M3 && (!(k > 0.0f) || !std::isfinite(k) || !(v > 0.0f) || !std::isfinite(v)))
-        return fail(KV_ERR_INVALID_ARG, "k_scale %g and v_scale %g must be finite and above 0", k, v);
+    if (format != KV_CACHE_E4M3) return KV_OK;
+    for (const float s : {k, v})
+        if (!(s > 0.0f) || !std::isfinite(s) || !std::isfinite(1.0f / s))
+            return fail(KV_ERR_INVALID_ARG, "k_scale %g and v_scale %g must be above 0 and finite, and so their inverses", k, v);
     return KV_OK;
 }
 

@@ -466,8 +466,9 @@ typedef enum { KV_BF16 = 0, KV_FP16 = 1 } kv_dtype;   /* type of x, q, k, v, out
 
 /* How a pool's head vectors hold D values.
  *   SAME  the 16-bit values themselves:      B = 2 D, D a multiple of 8.
- *   E4M3  value / scale in fp8 e4m3, saturating at 448 (scale: one per call and
- *         component):                        B = D, D a multiple of 16.
+ *   E4M3  value x (1 / scale) in fp8 e4m3, inverse and product rounded in
+ *         float32, saturating at 448 (scale: one per call and component):
+ *                                            B = D, D a multiple of 16.
  *   Q4    4-bit codes with a scale word for each 32 values: D a multiple of 32;
  *         D / 2 bytes of codes (value i in bits 4 (i % 8).. of 32-bit word
  *         i / 8), D / 32 scale words, zeros up to B = 5 D / 8 rounded up to a
@@ -571,7 +572,7 @@ typedef struct {
     uint32_t tokens, q_heads, head_dim, dtype;
     uint32_t format;         /* kv_cache_format                                   */
     uint32_t layer;
-    float k_scale, v_scale;  /* E4M3: finite, > 0                                 */
+    float k_scale, v_scale;  /* E4M3: finite, > 0, with a finite inverse          */
     uint32_t reserved[2];
 } kv_append_args;
 KVB_API kv_status kv_append(kv_pool pool, kv_rotary rotary, const kv_append_args *args,
