@@ -200,8 +200,8 @@ kv_status kv_rotary_create(const kv_rotary_desc *d, kv_rotary *out) {
         return fail(KV_ERR_INVALID_ARG, "unknown style %u or scaling %u", d->style, d->scaling);
     if (!(d->base > 1.0) || !std::isfinite(d->base))
         return fail(KV_ERR_INVALID_ARG, "base %g must be finite and above 1", d->base);
-    if (!(d->gain >= 0.0) || !std::isfinite(d->gain))
-        return fail(KV_ERR_INVALID_ARG, "gain %g must be finite and not negative", d->gain);
+    if (!(d->gain >= 0.0) || !std::isfinite((float)d->gain))   // cosines and sines are float32
+        return fail(KV_ERR_INVALID_ARG, "gain %g must be a finite float32 and not negative", d->gain);
     const uint32_t sc = d->scaling;
     if (sc != KV_ROTARY_PLAIN && (!(d->factor >= 1.0) || !std::isfinite(d->factor)))
         return fail(KV_ERR_INVALID_ARG, "factor %g must be finite and at least 1", d->factor);

@@ -526,7 +526,7 @@ typedef struct {
     double factor;           /* >= 1 (LINEAR, NTK, YARN, BANDS)                   */
     double slow, fast;       /* 0 < slow < fast (YARN, BANDS)                     */
     uint64_t original_len;   /* >= 1 (YARN, BANDS)                                */
-    double gain;             /* >= 0                                              */
+    double gain;             /* >= 0, finite as a float32                         */
 } kv_rotary_desc;
 typedef struct kv_rotary_s *kv_rotary;
 
