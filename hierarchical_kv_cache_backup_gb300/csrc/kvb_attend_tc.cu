@@ -62,6 +62,10 @@ static_assert(kStagesK <= 4 && kStagesV <= 4, "four barriers of each kind");
 // probabilities are rounded before it (error against 64 bits 1.4 times that of a float32
 // result rounded once, 1.6 with one part; a bf16 output does not show it).
 __host__ __device__ constexpr int value_parts(bool half) { return half ? 2 : 1; }
+// and of a key: two where the logarithm is wanted or the output is fp16 (300 new tokens over
+// 8,192, error against 64 bits 2.4 times that of a float32 result with keys in one part; so
+// fp16 outputs are the same bits with and without logarithms).
+constexpr int key_parts(bool half, bool lse) { return half || lse ? 2 : 1; }
 // Q0, Q1, the stages, and 1 KiB to align
 __host__ __device__ constexpr int smem_tc(int D, bool half, int parts) {
     return blocks_of(D) * (int)(2 * kBlockQ + (parts * kStagesK + value_parts(half) * kStagesV) * kBlockK) + 1024;
@@ -883,7 +887,7 @@ constexpr VariantTc variant_tc() {
                      kv_attend_join_tc_kernel<D, kHalf>, smem_tc(D, kHalf, kParts)};
 }
 #define KVB_VARIANTS_TC(D) \
-    variant_tc<D, false, 1>(), variant_tc<D, true, 1>(), variant_tc<D, false, 2>(), variant_tc<D, true, 2>()
+    variant_tc<D, false, 1>(), variant_tc<D, false, 2>(), variant_tc<D, true, 2>()
 const VariantTc kVariantsTc[] = {KVB_VARIANTS_TC(64), KVB_VARIANTS_TC(96), KVB_VARIANTS_TC(128)};
 
 }  // namespace
@@ -921,7 +925,7 @@ void plan_attend_tc(AttendPlan *p, uint64_t span, uint32_t requests, uint32_t kv
 cudaError_t launch_attend_tc(const AttendArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream,
                              int *launches) {
     for (const VariantTc &v : kVariantsTc) {
-        if (v.D != D || v.fp16 != fp16 || v.parts != (a.lse != nullptr ? 2 : 1)) continue;
+        if (v.D != D || v.fp16 != fp16 || v.parts != key_parts(fp16, a.lse != nullptr)) continue;
         cudaLaunchConfig_t cfg = {};
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];

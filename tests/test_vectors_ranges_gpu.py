@@ -311,3 +311,14 @@ def test_long_requests_lose_no_tile(dtype, dim, group, n_q):
         out, _, status = b.run(lse=None)
         assert status == 0
         vec_check.check(b, out, key_parts=1)
+
+
+@pytest.mark.parametrize("dim,group,n_q,window", [(128, 4, 40, 0), (64, 1, 90, 0), (96, 8, 11, 200), (128, 1, 300, 0),
+                                                  (128, 4, 1, 0), (64, 4, 5, 0)])
+def test_logarithms_change_no_bit_of_fp16_outputs(dim, group, n_q, window):
+    with Batch([900, 350], [n_q, n_q], 2, group, dim, 16, "fp16", window) as b:
+        out, lse, _ = b.run()
+        want, wl = out.clone(), lse.clone()
+        out, lse, status = b.run(lse=None)
+        assert torch.equal(out, want) and (lse == 7).all() and status == 0
+        vec_check.check(b, out, wl)
