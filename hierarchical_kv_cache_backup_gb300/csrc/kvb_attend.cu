@@ -173,11 +173,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int r, int rt, bool
 // reach every group through the zero points' tile and rows whose weight is 0), and the rows
 // that see it are marked.
 //
-// Bound: instructions.  16 tokens of 128 values (2,560 bytes) take 334 a warp
-// through both products for 8 query rows, a warp begins and ends with about 1,200; the ALU
-// pipe is 57% busy at 2.3 instructions a cycle and SM, 16 warps of 128 registers.  Of
-// one request of 131,072 tokens (8 heads, 48 us) the part that grows with the tokens
-// runs at 5.1 TB/s of 6.75.  Measured and dropped: query fragments in shared memory
+// Bound: instructions.  16 tokens of 128 values (2,560 bytes) take 358 a warp
+// through both products for 8 query rows, a warp begins and ends with about 1,300; the ALU
+// pipe is 57% busy at 2.4 instructions a cycle and SM, 16 warps of 128 registers.  Of
+// one request of 131,072 tokens (8 heads, 49.5 us) the part that grows with the tokens
+// runs at 5.0 TB/s of 6.8.  Measured and dropped: query fragments in shared memory
 // (2% slower), four-warp blocks with 96 registers (5-30% slower), several heads a block for
 // NHD pages (20% slower), both halves' exponentials at once for four rows (no change).
 template <int D, int NT, bool kHalf, bool kMany>
@@ -578,8 +578,8 @@ __device__ __forceinline__ void attend_rows(const AttendArgs &a, int head, int r
                 const float d1 = q4_step(pick(vw[sub][1][gr / 4], gr % 4));
                 // fp16 outputs: weights in two fp16 parts, so that only the output is rounded
                 // (17 requests of up to 8,906 tokens, 5 heads over 1 of 96: error against 64
-                // bits 2.2e-4, 3.2e-4 with one part, 2.1e-4 for a float32 plain form; 24
-                // requests of 2,000 tokens: heads of 64 18.7 -> 20.5 us, of 256 56 -> 63).
+                // bits 2.05e-4 as for a float32 plain form, 2.96e-4 with one part; 24
+                // requests of 2,000 tokens: heads of 64 19.7 -> 21.5 us, of 256 58 -> 68).
                 // A bf16 output does not show it.
                 uint32_t b[NT][2], rest[NT][2];
 #pragma unroll
@@ -853,9 +853,9 @@ const UnevenVariant kUnevenVariants[] = {KVB_UNEVEN(64), KVB_UNEVEN(96), KVB_UNE
 }  // namespace
 
 // Query rows of a request from which the tcgen05 kernel (256 rows a block) is taken.
-// 2 / 16 requests of 4,000 tokens, 8 heads, groups of 4, this kernel against that one:
-// 64 rows 28.7 against 31.4 / 87.6 against 108 us, 96 rows 42.6 against 33.0 / 117
-// against 108, 256 rows 72 against 44 / 277 against 117.
+// 2 / 16 requests of 4,000 tokens, 8 heads of 128, groups of 4, this kernel against that
+// one: 64 rows 29.1 against 32.9 / 88 against 97 us, 80 rows 38.3 against 33.9 / 104
+// against 98, 256 rows 73 against 44 / 280 against 109.
 constexpr uint64_t kManyRows = 80;
 
 AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len,
@@ -882,9 +882,8 @@ AttendPlan plan_attend(uint32_t requests, uint32_t tokens, uint32_t max_q, uint3
         // half a chunk lost at the end when there is more than one wave, never less
         // than a chunk; a block begins and ends in the time of 350 tokens, and parts
         // are joined in that of 500.  64 requests of up to 8,192 tokens and 8 heads, 1 /
-        // 2 / 3 chunks: 144 / 142 / 141 us; 32 of them 88 / 82 / 79; 64 of up to 2,048
-        // 49 / 56 / 58; 24 of 2,016 of 4 heads of 64, 2 / 3 / 4 chunks: 21.5 / 18.8 / 22.5
-        // (weights in one part).
+        // 2 / 3 chunks: 148 / 148 / 147 us; 32 of them 90 / 86 / 82; 64 of up to 2,048
+        // 51 / 58 / 61; 24 of 2,016 of 4 heads of 64, 2 / 3 / 4 chunks: 23.4 / 21.5 / 25.0.
         const uint64_t slots = (uint64_t)sms * (D * (p.rows / 8) <= 128 ? 2 : 1), unit = kWarps * kTile;
         const uint64_t units = std::max<uint64_t>(1, (uint64_t)requests * kv_heads * p.row_tiles);
         const double spread = (requests > 1 ? 0.75 : 1.0) * (double)units * (double)span / (double)slots;

@@ -22,12 +22,12 @@
 // and head where they are not (its small steps would lose bits to a large one that a row may not
 // see, or gives no weight) goes to the kernel for few rows, which scales by rows.
 // What is rounded: a value once (2^-11; not for fp16 outputs), a probability once
-// (2^-11).  Keys are two fp16 parts each,
-// which their products with the queries take in turn, where the caller wants the
-// logarithms of the sums: with one part (2^-11) a logarithm of few terms is off by
-// 1e-5 of itself, which float32 has to show and 16-bit outputs do not.  Without
-// them one part is taken: 2 x 1,000 new tokens over 8,192 cached ones, 295 us with
-// two parts and 235 with one.
+// (2^-11).  Keys are two fp16 parts each, which their products with the queries take
+// in turn, for fp16 outputs and where the caller wants the logarithms of the sums:
+// with one part (2^-11) a logarithm of few terms is off by 1e-5 of itself, which
+// float32 has to show and bf16 outputs do not.  Without them bf16 outputs take one
+// part: 2 x 1,000 new tokens over 8,192 cached ones, 282 us with two parts and 229
+// with one.
 //
 // Bound: the products.  A tcgen05.mma of 128 x 64 x 16 with both operands in
 // shared memory takes 48 cycles and more where its arithmetic takes 32, since it
@@ -54,13 +54,14 @@ constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
 // Stages of K (of one part or two) and of V.  Two of K: with three the unpacking
-// warps run further ahead and the products more slowly (two parts 327 -> 295 us, one part
-// 242 -> 235); V needs three.
+// warps run further ahead and the products more slowly (two parts 287 us, 282 with two
+// stages; one part 230 and 229); V needs three.
 constexpr int kStagesK = 2, kStagesV = 3;
 static_assert(kStagesK <= 4 && kStagesV <= 4, "four barriers of each kind");
 // fp16 parts of a value: two where the output is fp16, so that only the
-// probabilities are rounded before it (error against 64 bits 1.4 times that of a float32
-// result rounded once, 1.6 with one part; a bf16 output does not show it).
+// probabilities are rounded before it (300 new tokens over 8,192: error against 64 bits 1.4
+// times that of a float32 result rounded once, 1.7 with one part; a bf16 output does not
+// show it).
 __host__ __device__ constexpr int value_parts(bool half) { return half ? 2 : 1; }
 // and of a key: two where the logarithm is wanted or the output is fp16 (300 new tokens over
 // 8,192, error against 64 bits 2.4 times that of a float32 result with keys in one part; so
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) kv_attend_tc_kernel(const __gri
             }
             // Straight code: a jump back costs this warp an instruction fetch of some 350
             // cycles, since the other warps' code goes through the same caches; four tiles
-            // at a time are slower again (242, 235 and 256 us for 1, 2 and 4).
+            // at a time gain nothing more (235, 229 and 230 us for 1, 2 and 4).
 #pragma unroll 2
             for (int t = 0; t < n; ++t) {
                 // The unpacking warps give the values of a tile before the keys of the next, so

@@ -191,8 +191,9 @@ struct Vecs {
 constexpr int kMaxPairs = 128;
 
 // Turns per position of each pair as 64-bit fractions: the phase of position p
-// is p * turns mod 2^64, exact for any p (integer arithmetic wraps at one whole
-// turn), so angles at far positions lose nothing before they become floats.
+// is p * turns mod 2^64, where integer arithmetic wraps at one whole turn without
+// error.  What is left is the fraction's own error, that of a frequency in 53 bits:
+// 2^-53 x p x frequency radians (1e-4 at p = 2^40 for a frequency of 1).
 struct RotaryK {
     unsigned long long turns[kMaxPairs];
     float gain;

@@ -120,11 +120,11 @@ __device__ __forceinline__ void store8(uint64_t vec, uint32_t chunk, const float
 // are as far apart.  Four neighbouring lanes still hold the 32 values of a
 // 4-bit group when rotated and other part are multiples of 64 values.  Where
 // they are not (or not of 16 for the other formats), a lane owns one run and
-// reads its partners itself (!kPair).  8,192 tokens of 40 vectors of 128: 30 us
-// (5.8 TB/s, bound by memory), 52 with one run a lane, bound by instructions.
+// reads its partners itself (!kPair).  8,192 tokens of 40 vectors of 128: 31.5
+// us (5.5 TB/s, bound by memory), 52 with one run a lane, bound by instructions.
 // kFormat: -1 rotate only, else kv_cache_format.  Quantising takes 87 registers where
 // it may; seven blocks an SM (72 registers) hide more: append and fetch of 8,192
-// tokens 53.7 -> 50.3 us (the append 38, at 3.9 TB/s and 46% of the ALU pipe).
+// tokens 53.7 -> 50 us (the append 38.5, 4.7 TB/s of what it reads and writes, 53% of the ALU pipe).
 template <int kFormat, bool kHalf, bool kPair>
 __global__ void __launch_bounds__(kThreads, kFormat == 2 ? 7 : 1) kv_vectors_kernel(const __grid_constant__ VectorArgs a,
                                                               const __grid_constant__ RotaryK r) {

@@ -601,7 +601,24 @@ KVB_API kv_status kv_fetch(kv_pool pool, const kv_fetch_args *args, void *stream
  * j / (q_heads / H).  With x_t = scale q . k_t over the tokens it sees:
  * out = sum exp(x_t) v_t / sum exp(x_t), lse (float32 [tokens][q_heads], NULL:
  * not wanted) = ln sum exp(x_t).  A query that sees nothing gets out = 0 and
- * lse = -infinity.  Scores, sums and accumulators are float32.
+ * lse = -infinity.
+ * Scores, softmax statistics and sums are float32.  Rounded to fewer bits are:
+ *   a query       values under 2^-22 of the vector's largest
+ *   a weight      exp(x_t - largest) (in calls with few rows times the value's
+ *                 step) to fp16, 2^-11 of itself; in calls with few rows and fp16
+ *                 outputs to two fp16 parts.  Below 2^-18 of the query's largest it
+ *                 loses bits
+ * and, in calls with many rows (max_q x q_heads / H of 80 or more, head_dim of
+ * 128 or less),
+ *   a value       to fp16, 2^-11 of itself; two parts (2^-19) for fp16 outputs
+ *   a key         to fp16 for bf16 outputs without lse, two parts otherwise: with
+ *                 lse the last bits of bf16 outputs may be other ones
+ * in requests (and KV heads) whose steps are less than 2^16 apart in every group;
+ * others take the way of few rows, about four times as long.  What a query does
+ * not see, or gives no weight, takes no bits from it: steps may differ by any
+ * factor.
+ * A group of a key that is not finite makes the outputs and lse of the queries
+ * that see it NaN; a group of a value the outputs' dims of that group.
  * A page id outside the pool inside a request's length sets BAD_PAGE, and the
  * queries that see the page get NaN.  lens[r] is taken as at most max_len and
  * at least 0, and a request whose q_start values are out of order, outside

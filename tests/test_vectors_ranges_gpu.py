@@ -322,3 +322,30 @@ def test_logarithms_change_no_bit_of_fp16_outputs(dim, group, n_q, window):
         out, lse, status = b.run(lse=None)
         assert torch.equal(out, want) and (lse == 7).all() and status == 0
         vec_check.check(b, out, wl)
+
+
+def test_many_rows_in_a_graph_that_meets_uneven_steps_later():
+    """One captured call, replayed over even and uneven steps and over other lengths."""
+    with Batch([6000, 5500], [40, 40], 1, 4, 128, 32, "bf16") as b:
+        a = b.args()
+        assert a.workspace_bytes > 0
+        kvb.kv_attend(b.pool.pool, a)
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            kvb.kv_attend(b.pool.pool, a, side.cuda_stream)
+        out, lse, lens_d, status = b.out, b.lse, b.lens_d, b.status
+        for step in range(4):
+            if step == 1:
+                grow(b, 1, 1, 5400, 20)
+            if step == 2:
+                grow(b, 1, 1, 5400, -20)
+            if step == 3:
+                b.lens = [3000, 41]
+                b.kv = [[x[:n] for x in kv] for kv, n in zip(b.kv, b.lens)]
+                lens_d.copy_(torch.tensor(b.lens, device="cuda"))
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            vec_check.check(b, out, lse)
+            assert int(status) == 0
