@@ -14,6 +14,7 @@
 #include "kvb.h"
 #include "kvb_internal.h"
 #include "kvb_ring_internal.h"
+#include "kvb_pages_internal.h"
 #include "kvb_vec_internal.h"
 
 #include <cuda.h>   // CUresult / CUdeviceptr types only; the function comes from the runtime
@@ -348,6 +349,8 @@ kv_status init_device(int d) {
     if (e0 == cudaSuccess) e0 = preload_ring_kernels();
     if (e0 == cudaSuccess) e0 = preload_vector_kernels();
     if (e0 == cudaSuccess) e0 = preload_attend_kernels();
+    if (e0 == cudaSuccess) e0 = preload_pages_kernels();
+    if (e0 == cudaSuccess) e0 = preload_select_kernels();
     if (e0 != cudaSuccess) return cuda_fail(e0, "loading the library's kernels");
     // mapped pinned table: kRing fence words, kRing status words, the error word
     const size_t table = 2 * kRing * sizeof(unsigned long long) + 64;

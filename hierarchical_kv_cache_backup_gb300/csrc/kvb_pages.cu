@@ -1,0 +1,784 @@
+// kvb_pages.cu -- attention over pages held in 16 bits or in fp8 (kv_attend_shared,
+// kv_attend_selected): the kernel for few query rows, and the kernel that joins pieces.
+//
+// Mathematics.  A piece is some cached tokens t of a unit (KV head, 16 query rows).  With a
+// running maximum m of x_t = scale log2(e) q . k_t, it keeps l = sum 2^(x_t - m) and
+// o = sum 2^(x_t - m) v_t in float32; pieces join as o = sum o_i 2^(m_i - m), l likewise,
+// and out = o / l.  Attention of a shared prefix is that: the prefix is a unit of its own,
+// read once for all requests of the group, whose pieces join with those of each request's own
+// tokens.
+#include "kvb_pages.h"
+#include "kvb_pages_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+namespace kvb {
+
+namespace {
+
+constexpr int kWarps = 4;        // of a block
+constexpr int kTile = 16;        // cached tokens a warp takes at a time
+constexpr int kRowsP = 16;       // query rows of a unit
+constexpr float kNoMax = -3.0e38f;
+
+// The 16-byte pieces of a token's values; in shared memory a token takes one more, so that
+// the 8 rows of a fragment start in different banks (an odd multiple of 16 bytes apart).
+__host__ __device__ constexpr int row_bytes(int D, bool f8) { return f8 ? D : 2 * D; }
+__host__ __device__ constexpr int smem_stride(int D, bool f8) { return row_bytes(D, f8) + 16; }
+__host__ __device__ constexpr int stage_bytes(int D, bool f8) { return 2 * kTile * smem_stride(D, f8); }
+__host__ __device__ constexpr int stages_of(int D, bool f8) { return row_bytes(D, f8) >= 256 ? 3 : 4; }
+__host__ __device__ constexpr int ring_bytes(int D, bool f8) {
+    const int ring = stages_of(D, f8) * stage_bytes(D, f8), join = kRowsP * (D + 4) * 4;
+    return ring > join ? ring : join;
+}
+__host__ __device__ constexpr int blocks_per_sm(int D, bool f8) {
+    const int by_smem = 227 * 1024 / (kWarps * ring_bytes(D, f8) + 2048), by_regs = D <= 64 ? 4 : D <= 128 ? 3 : 2;
+    return by_smem < 1 ? 1 : by_smem < by_regs ? by_smem : by_regs;
+}
+
+__device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldm(uint32_t addr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm_t(uint32_t addr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool kBf>
+__device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    if (kBf)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// two fp8 values as fp16, exact
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)w));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <bool kBf>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if (kBf) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+template <bool kBf>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (kBf) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+// which 16-bit or fp8 values of a word are not finite, as a mask of their bits
+template <bool kF8, bool kBf>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    if (kF8) return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    const uint32_t e = kBf ? 0x7f807f80u : 0x7c007c00u;
+    return __vcmpeq2(w & e, e);
+}
+
+// Threads of a team (worker) wait for one another.
+__device__ __forceinline__ void team_sync(uint32_t team, uint32_t id) {
+    if (team == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(team * 32) : "memory");
+}
+
+// Sums tiles and units of all segments over the block, writes the sums before each segment to
+// the workspace (block 0, for the join) and finds the segment of each worker's first tile.
+// `worker0`: the block's first worker.  Returns the tiles of a worker.
+template <int kThreads>
+__device__ __forceinline__ unsigned long long share_out(const PageAttendArgs &a, const PageEngine &e, uint32_t worker0,
+                                                        uint32_t workers_here, PageCursor *starts, unsigned long long *total) {
+    constexpr int kW = kThreads / 32;
+    __shared__ unsigned long long sums[2][kW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t n = seg_count(a, e);
+    unsigned long long share = 0, all_t = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        unsigned long long run_t = 0, run_u = 0;
+        for (uint32_t s0 = 0; s0 < n; s0 += kThreads) {
+            const uint32_t s = s0 + tid;
+            unsigned long long t = 0, u = 0;
+            if (s < n) {
+                const PageSeg g = seg_at(a, e, s);
+                t = seg_tiles(a, e, g);
+                u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
+                if (g.bad && pass == 0 && worker0 == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+            }
+            unsigned long long it = t, iu = u;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned long long xt = __shfl_up_sync(0xffffffffu, it, d), xu = __shfl_up_sync(0xffffffffu, iu, d);
+                if (lane >= d) {
+                    it += xt;
+                    iu += xu;
+                }
+            }
+            __syncthreads();
+            if (lane == 31) {
+                sums[0][warp] = it;
+                sums[1][warp] = iu;
+            }
+            __syncthreads();
+            unsigned long long bt = run_t, bu = run_u;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                if (w < warp) {
+                    bt += sums[0][w];
+                    bu += sums[1][w];
+                }
+                run_t += sums[0][w];
+                run_u += sums[1][w];
+            }
+            if (pass == 1 && s < n) {
+                const unsigned long long before = bt + it - t;
+                for (uint32_t k = 0; k < workers_here; ++k) {
+                    const unsigned long long x = (worker0 + k) * share;
+                    if (x >= before && x < before + t) starts[k] = PageCursor{before, bu + iu - u, s};
+                }
+                if (worker0 == 0) {
+                    e.seg_tiles[s] = before;
+                    e.seg_units[s] = bu + iu - u;
+                }
+            }
+        }
+        all_t = run_u > e.units ? 0 : run_t;
+        share = share_of(all_t, e.workers);
+        if (run_u > e.units && worker0 == 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+        if (pass == 1 && worker0 == 0 && tid == 0) {
+            e.seg_tiles[n] = run_t;
+            e.seg_units[n] = run_u;
+        }
+    }
+    __syncthreads();
+    *total = all_t;
+    return share;
+}
+
+// ------------------------------------------------------------- few query rows
+//
+// A worker is a team of 1 or 4 warps.  Warps take 16 cached tokens in turn, each with a
+// private ring of cp.async stages (no barrier in the loop); query rows are the 16 rows of
+// mma.sync m16n8k16, cached tokens the 8 columns of the first product and the 16 k of the
+// second, so that weights go from one to the other in registers.
+template <int D, bool kF8, bool kHalf>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
+    kv_pages_rows_kernel(const __grid_constant__ PageAttendArgs a) {
+    constexpr bool kBf = !kF8 && !kHalf;          // type of the products' operands
+    // Weights in two parts: bf16 (8 bits) alone errs as much as the output's rounding again, and
+    // so does fp16 for fp16 outputs; fp16 is enough for bf16 outputs.
+    constexpr bool kTwo = !kF8 || kHalf;
+    // fp16 weights stand 2^7 higher, so that those down to 2^-21 of the largest keep their bits
+    constexpr float kBits = kBf ? 0.0f : 7.0f;
+    constexpr int RB = row_bytes(D, kF8), SV = smem_stride(D, kF8), PV = RB / 16, kStages = stages_of(D, kF8);
+    constexpr int KS = D / 16;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float join_m[kWarps][kRowsP], join_l[kWarps][kRowsP];
+    __shared__ PageCursor starts[kWarps];
+    __shared__ uint32_t masks[kWarps][kStages];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const PageEngine &e = a.rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t team = e.team, team_id = warp / team, w_in = warp % team, teams = kWarps / team;
+    const uint32_t worker = blockIdx.x * teams + team_id;
+    unsigned long long total;
+    const unsigned long long share = share_out<kWarps * 32>(a, e, blockIdx.x * teams, teams, starts, &total);
+    unsigned long long x = worker * share;
+    const unsigned long long x1 = min(total, x + share);
+    if (x >= x1) return;                          // no barrier of the whole block follows
+    PageCursor at = starts[team_id];
+
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ring_bytes(D, kF8);
+    float *mine = reinterpret_cast<float *>(smem + warp * ring_bytes(D, kF8));
+    const int group = (int)a.group, H = (int)a.pool.H;
+    const bool picked = a.picks != nullptr;
+    // Tiles are copied 16 bytes a lane, a token's PV pieces by neighbouring lanes.  Lane i
+    // (and i + 16) knows the place of token i and hands it round.
+    constexpr int kAtOnce = 32 / PV;
+    const int lane_tok = lane / PV, piece16 = lane - lane_tok * PV;
+    const uint32_t to = ring + lane_tok * SV + piece16 * 16;
+
+    while (x < x1) {
+        const PagePiece piece = piece_at(a, e, &at, x, x1, worker);
+        const PageSeg &s = piece.s;
+        const int rt = piece.rt, head = piece.head, k0 = piece.k0, k1 = piece.k1;
+        x += k1 - k0;
+
+        const int end = seen_tokens(a, e, s, rt);
+        // rows of the tile: new token and head of the group
+        const int per = (group + kRowsP - 1) / kRowsP;
+        const int tok0 = picked ? rt / per : 0, row0 = picked ? rt % per * kRowsP : rt * kRowsP;
+        const int rows = min(kRowsP, (picked ? group : s.n * group) - row0);
+        auto new_token = [&](int row) { return picked ? tok0 : (row0 + row) / group; };
+        auto head_of = [&](int row) { return picked ? row0 + row : (row0 + row) % group; };
+        const int32_t *table = s.prefix ? a.prefix_pages + (int64_t)s.index * a.prefix_stride
+                                        : a.pages + (int64_t)s.index * a.pages_stride;
+        const int32_t *list = picked ? a.picks + ((int64_t)(s.q0 + tok0) * H + head) * a.budget : nullptr;
+        const int pos0 = s.len - s.n + tok0;      // picked: the query's position
+        const int pages0 = pages_seen(s.len, s.n, tok0, a.pool.T);
+        const bool alone = !s.prefix && group_of(a, s.index, s.q0, s.n) < 0;
+        const bool whole = alone && k0 == 0 && k1 == piece.n_tiles;
+
+        // Token of this lane in tile k (-1: none that is seen), and its page.
+        bool wrong_pick = false;
+        auto token_of = [&](int k) {
+            const int t = (k * (int)team + (int)w_in) * kTile + (lane & 15);
+            if (k >= k1 || t >= end) return -1;
+            if (!picked) return t;
+            const uint32_t i = div_T(a.pool, (uint32_t)t);
+            const int p = list[i];
+            if ((uint32_t)p >= (uint32_t)pages0) {
+                wrong_pick |= p != -1;
+                return -1;
+            }
+            const int real = p * (int)a.pool.T + (t - (int)i * (int)a.pool.T);
+            return real <= pos0 ? real : -1;
+        };
+        auto page_of = [&](int t) { return t >= 0 ? table[div_T(a.pool, (uint32_t)t)] : 0; };
+        const uint64_t from_k = a.pool.base[0] + (uint64_t)head * a.pool.s_head + piece16 * 16;
+        const uint64_t from_v = a.pool.base[1] + (uint64_t)head * a.pool.s_head + piece16 * 16;
+        auto load = [&](int stage, int k, int t, int32_t page) {
+            if (k < k1) {
+                const bool bad = t >= 0 && (uint32_t)page >= a.pool.P, ok = t >= 0 && !bad;
+                const uint32_t where = ok ? vector_index(a.pool, (uint32_t)page, (uint32_t)t) : 0;
+                const uint32_t good = __ballot_sync(0xffffffffu, ok), bads = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) masks[warp][stage] = (good & 0xffffu) | bads << 16;
+                const uint32_t dst = to + stage * stage_bytes(D, kF8);
+#pragma unroll
+                for (int i = 0; i < (kTile + kAtOnce - 1) / kAtOnce; ++i) {
+                    const int tok = i * kAtOnce + lane_tok;
+                    const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, where, tok & 15) * (uint32_t)RB;
+                    if (lane_tok < kAtOnce && (kTile % kAtOnce == 0 || tok < kTile)) {
+                        copy16(dst + i * kAtOnce * SV, from_k + off, good >> (tok & 15) & 1);
+                        copy16(dst + (i * kAtOnce + kTile) * SV, from_v + off, good >> (tok & 15) & 1);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int tk[kStages + 2];
+        int32_t pg[kStages + 1];
+#pragma unroll
+        for (int i = 0; i < kStages + 2; ++i) tk[i] = token_of(k0 + i);
+#pragma unroll
+        for (int i = 0; i < kStages + 1; ++i) pg[i] = page_of(tk[i]);
+
+        // Query rows as A fragments.  fp8 keys meet fp16 queries: a bf16 row is scaled by
+        // the power of two that brings its largest value to 2^14..2^15 (values under 2^-22
+        // of it lose bits), which its scores undo.
+        uint32_t qf[KS][4];
+        float sc[2];
+        int lim[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            const bool on = row < rows;
+            const int i = on ? new_token(row) : 0, j = on ? head_of(row) : 0;
+            const uint64_t src = a.q.data + (int64_t)(s.q0 + i) * a.q.s_tok + (int64_t)(head * group + j) * a.q.s_head;
+            lim[r] = s.prefix || picked || !on ? end - 1 : s.len - s.n + i;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // the lane's pairs of dims: 2 c and 2 c + 8 of a run of 16, or with fp8, whose
+                    // fragments come 4 values a lane, 4 c and 4 c + 2
+                    const int d = 16 * ks + (kF8 ? 4 * c + 2 * h : 2 * c + 8 * h);
+                    qf[ks][r + 2 * h] = on ? *reinterpret_cast<const uint32_t *>(src + d * 2) : 0u;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) load(i, k0 + i, tk[i], pg[i]);
+        int t_ahead = tk[kStages + 1];
+        int t_next = tk[kStages];
+        int32_t page_next = pg[kStages];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            sc[r] = a.scale_log2;
+            if (kF8 && !kHalf) {
+                float top = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 f = unpack2<true>(qf[ks][r + 2 * h]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t ex = max(__float_as_uint(top) >> 23, 15u);
+                const float up = ex < 255 ? __uint_as_float((268u - ex) << 23) : 1.0f;
+                sc[r] *= ex < 255 ? __uint_as_float((ex - 14u) << 23) : 1.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 f = unpack2<true>(qf[ks][r + 2 * h]);
+                        qf[ks][r + 2 * h] = pack2<false>(f.x * up, f.y * up);
+                    }
+            }
+        }
+        const int all_see = s.prefix || picked ? end : s.len - s.n + new_token(0) + 1;   // tokens that every row sees
+
+        float o[2 * KS][4], m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+
+        // lane constants of the fragments' addresses
+        const uint32_t k_at = kF8 ? ((lane >> 3 & 1) * 8 + (lane & 7)) * SV + (lane >> 4) * 16
+                                  : ((lane >> 4) * 8 + (lane & 7)) * SV + (lane >> 3 & 1) * 16;
+        const uint32_t v_at = ((lane >> 3 & 1) * 8 + (lane & 7)) * SV + (lane >> 4) * 16 + kTile * SV;
+        int stage = 0;
+        for (int k = k0; k < k1; ++k) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+            const uint32_t tile = ring + stage * stage_bytes(D, kF8);
+            const uint32_t mask = masks[warp][stage];
+            const int t0 = (k * (int)team + (int)w_in) * kTile;
+            const bool edge = !picked && min(t0 + kTile, end) > all_see;      // rows see different tokens
+            if (mask != 0) {                      // a token that some row sees
+                float y[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[n][i] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += kF8 ? 2 : 1) {
+                    uint32_t b[4];
+                    ldm(tile + k_at + ks * (kF8 ? 16 : 32), b);
+                    if (kF8) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+                                mma<false>(y[n], qf[ks + h], e4m3x2(b[2 * h + n]), e4m3x2(b[2 * h + n] >> 16));
+                    } else {
+                        mma<kBf>(y[0], qf[ks], b[0], b[1]);
+                        mma<kBf>(y[1], qf[ks], b[2], b[3]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[n][i] = y[n][i] * sc[i >> 1] - (m[i >> 1] == kNoMax ? 0.0f : m[i >> 1]);
+                if (mask != 0xffffu || edge) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int in = 8 * n + 2 * c + (i & 1);
+                            if (mask >> 16 >> in & 1) y[n][i] = __uint_as_float(kNanWord);
+                            if (!((mask | mask >> 16) >> in & 1) || (!picked && t0 + in > lim[i >> 1])) y[n][i] = -INFINITY;
+                        }
+                    if (mask >> 16 != 0 && a.status != nullptr && lane == 0) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+                    if (edge) {
+                        // A value that is not finite must not reach rows that do not see it (0 x NaN): it
+                        // makes its dim NaN in those that do, and leaves the tile.
+                        uint32_t found = 0;
+                        for (int i = lane; i < kTile * PV; i += 32) {
+                            const uint32_t p = tile + (kTile + i / PV) * SV + i % PV * 16;
+                            uint32_t w[4];
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p) : "memory");
+                            found |= not_finite<kF8, kBf>(w[0]) | not_finite<kF8, kBf>(w[1]) | not_finite<kF8, kBf>(w[2]) | not_finite<kF8, kBf>(w[3]);
+                        }
+                        if (__any_sync(0xffffffffu, found != 0)) {
+                            for (int t = 0; t < kTile; ++t)
+#pragma unroll
+                                for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int d = kF8 ? 16 * (n >> 1) + 4 * c + 2 * (i & 1) + (n & 1) : 8 * n + 2 * c + (i & 1);
+                                        const unsigned char *v = smem + (tile - (uint32_t)__cvta_generic_to_shared(smem)) + (kTile + t) * SV;
+                                        const uint32_t w = kF8 ? v[d] * 0x01010101u : reinterpret_cast<const unsigned short *>(v)[d];
+                                        if ((not_finite<kF8, kBf>(w) & (kF8 ? 0xffu : 0xffffu)) != 0 && t0 + t <= lim[i >> 1]) o[n][i] = __uint_as_float(kNanWord);
+                                    }
+                            __syncwarp();
+                            for (int i = lane; i < kTile * RB / 4; i += 32) {
+                                uint32_t *p = reinterpret_cast<uint32_t *>(smem + (tile - (uint32_t)__cvta_generic_to_shared(smem)) + (kTile + i / (RB / 4)) * SV) + i % (RB / 4);
+                                *p &= ~not_finite<kF8, kBf>(*p);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+                // The maximum moves only when a score passes it by more than 2^8.
+                const float over[2] = {fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1])),
+                                       fmaxf(fmaxf(y[0][2], y[0][3]), fmaxf(y[1][2], y[1][3]))};
+                bool move = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) move |= over[r] > kBits + 8.0f || m[r] == kNoMax;
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float t = over[r];
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                        if (t == -INFINITY) continue;
+                        float up = 0.0f;
+                        if (m[r] == kNoMax) {
+                            up = t - kBits;
+                            m[r] = up;
+                        } else if (t > kBits + 8.0f) {
+                            up = t - kBits;
+                            m[r] += up;
+                            const float f = exp2_fast(-up);
+                            l[r] *= f;
+#pragma unroll
+                            for (int n = 0; n < 2 * KS; ++n) {
+                                o[n][2 * r] *= f;
+                                o[n][2 * r + 1] *= f;
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            y[n][2 * r] -= up;
+                            y[n][2 * r + 1] -= up;
+                        }
+                    }
+                }
+                uint32_t p[4], rest[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float u = exp2_fast(y[n][2 * r]), v = exp2_fast(y[n][2 * r + 1]);
+                        l[r] += u + v;
+                        p[2 * n + r] = pack2<kBf>(u, v);
+                        if (kTwo) {
+                            const float2 f = unpack2<kBf>(p[2 * n + r]);
+                            rest[2 * n + r] = pack2<kBf>(u - f.x, v - f.y);
+                        }
+                    }
+#pragma unroll
+                for (int j = 0; j < 2 * KS; j += kF8 ? 4 : 2) {
+                    uint32_t b[4];
+                    ldm_t(tile + v_at + j * (kF8 ? 8 : 16), b);
+                    if (kF8) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // even and odd dims of 16
+                            const uint32_t e0 = e4m3x2(__byte_perm(b[2 * h], 0, 0x4420)), e1 = e4m3x2(__byte_perm(b[2 * h + 1], 0, 0x4420));
+                            const uint32_t o0 = e4m3x2(__byte_perm(b[2 * h], 0, 0x4431)), o1 = e4m3x2(__byte_perm(b[2 * h + 1], 0, 0x4431));
+                            mma<false>(o[j + 2 * h], p, e0, e1);
+                            mma<false>(o[j + 2 * h + 1], p, o0, o1);
+                            if (kTwo) {
+                                mma<false>(o[j + 2 * h], rest, e0, e1);
+                                mma<false>(o[j + 2 * h + 1], rest, o0, o1);
+                            }
+                        }
+                    } else {
+                        mma<kBf>(o[j], p, b[0], b[1]);
+                        mma<kBf>(o[j + 1], p, b[2], b[3]);
+                        if (kTwo) {
+                            mma<kBf>(o[j], rest, b[0], b[1]);
+                            mma<kBf>(o[j + 1], rest, b[2], b[3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            load(stage, k + kStages, t_next, page_next);
+            t_next = t_ahead;
+            page_next = page_of(t_next);
+            t_ahead = token_of(k + kStages + 2);
+            if (++stage == kStages) stage = 0;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        if (wrong_pick && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+
+        // Join the team's warps: accumulators go to the warp's own ring as [row][D + 4].
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float t = l[r];
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            const int row = g + 8 * r;
+            if (c == 0) {
+                join_m[warp][row] = m[r];
+                join_l[warp][row] = t;
+            }
+            float *dst = mine + row * (D + 4);
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n) {
+                if (kF8) {
+                    if ((n & 1) == 0)
+                        *reinterpret_cast<float4 *>(dst + 16 * (n >> 1) + 4 * c) =
+                            make_float4(o[n][2 * r], o[n + 1][2 * r], o[n][2 * r + 1], o[n + 1][2 * r + 1]);
+                } else {
+                    *reinterpret_cast<float2 *>(dst + 8 * n + 2 * c) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                }
+            }
+        }
+        team_sync(team, team_id);
+        constexpr int D4 = D / 4;
+        const int first = (int)(team_id * team);
+        for (int it = (int)w_in * 32 + lane; it < rows * D4; it += (int)team * 32) {
+            const int row = it / D4, d4 = it - row * D4;
+            float top = kNoMax, sum = 0.0f;
+            for (int w = first; w < first + (int)team; ++w)
+                if (join_l[w][row] != 0.0f) top = fmaxf(top, join_m[w][row]);
+            float4 acc = make_float4(0, 0, 0, 0);
+            for (int w = first; w < first + (int)team; ++w) {
+                const float lw = join_l[w][row];
+                if (lw == 0.0f) continue;         // this warp saw nothing of the row
+                const float f = exp2_fast(join_m[w][row] - top);
+                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * ring_bytes(D, kF8)) +
+                                                                   row * (D + 4) + d4 * 4);
+                sum += lw * f;
+                acc.x += v.x * f;
+                acc.y += v.y * f;
+                acc.z += v.z * f;
+                acc.w += v.w * f;
+            }
+            if (whole) {
+                const int64_t tok = s.q0 + new_token(row);
+                const int qh = head * group + head_of(row);
+                const float inv = sum != 0.0f ? a.v_scale / sum : 0.0f;
+                *reinterpret_cast<uint2 *>(a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head + d4 * 8) =
+                    make_uint2(pack2<!kHalf>(acc.x * inv, acc.y * inv), pack2<!kHalf>(acc.z * inv, acc.w * inv));
+                if (d4 == 0 && a.lse != nullptr)
+                    a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
+            } else {
+                const uint64_t to_row = piece.slot * e.slot_rows + row;
+                *reinterpret_cast<float4 *>(e.part_o + to_row * D + d4 * 4) = acc;
+                if (d4 == 0) *reinterpret_cast<float2 *>(e.part_ml + to_row * 2) = make_float2(top, sum);
+            }
+        }
+        team_sync(team, team_id);                 // rings are free again
+    }
+}
+
+// ------------------------------------------------------------------- the join
+//
+// A row (query token and head) takes the pieces of its prefix and of its own tokens, kW
+// warps a row, each every kW-th piece, a lane D / 32 values.  Rows that one worker held alone
+// were written by it.
+template <int D, bool kHalf, int kW>
+__global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constant__ PageAttendArgs a) {
+    constexpr int NV = D / 32;
+    __shared__ float acc_s[kW][D], m_s[kW], l_s[kW];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int qh = kW == 1 ? blockIdx.x * 4 + warp : blockIdx.x, part = kW == 1 ? 0 : warp;
+    const int i = blockIdx.y, r = blockIdx.z, group = (int)a.group;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (qh >= (int)a.q_heads) return;
+    const PageSeg own = own_seg(a, r);
+    if (i >= own.n) return;
+    const int64_t tok = own.q0 + i;
+    const int head = qh / group, j = qh - head * group;
+    const int in = group_of(a, r, own.q0, own.n);
+    if (a.rows.on && a.rows.seg_units[seg_count(a, a.rows)] > a.rows.units) return;
+    if (a.tc.on && a.tc.seg_units[seg_count(a, a.tc)] > a.tc.units) return;
+    float top = kNoMax, sum = 0.0f, acc[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
+    for (int side = in >= 0 ? 0 : 1; side < 2; ++side) {
+        const PageSeg s = side == 0 ? prefix_seg(a, in) : own;
+        const PageEngine &e = (side == 0 ? a.tc.prefix : a.tc.own) && a.tc.on ? a.tc : a.rows;
+        if (s.len == 0) continue;
+        const uint32_t at = side == 0 ? (uint32_t)in : (e.prefix ? a.groups : 0) + (uint32_t)r;
+        const RowPieces p = row_pieces(a, e, s, at, (int)(tok - s.q0), head, j);
+        if (!p.any) continue;
+        if (side == 1 && in < 0 && p.w0 == p.w1) return;
+#pragma unroll 4
+        for (uint64_t w = p.w0 + part; w <= p.w1; w += kW) {
+            const uint64_t from = (p.unit + w) * e.slot_rows + p.row;
+            const float2 ml = *reinterpret_cast<const float2 *>(e.part_ml + from * 2);
+            float x[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) x[v] = e.part_o[from * D + v * 32 + lane];
+            if (ml.y == 0.0f) continue;
+            const float t = fmaxf(top, ml.x), u = exp2_fast(top - t), f = exp2_fast(ml.x - t);
+            top = t;
+            sum = sum * u + ml.y * f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] = acc[v] * u + x[v] * f;
+        }
+    }
+    if (kW > 1) {
+        if (lane == 0) {
+            m_s[warp] = top;
+            l_s[warp] = sum;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc_s[warp][v * 32 + lane] = acc[v];
+        __syncthreads();
+        if (warp != 0) return;
+        float most = kNoMax;
+#pragma unroll
+        for (int w = 0; w < kW; ++w)
+            if (l_s[w] != 0.0f) most = fmaxf(most, m_s[w]);
+        sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            if (l_s[w] == 0.0f) continue;
+            const float f = exp2_fast(m_s[w] - most);
+            sum += l_s[w] * f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) acc[v] += acc_s[w][v * 32 + lane] * f;
+        }
+        top = most;
+    }
+    const float inv = sum != 0.0f ? a.v_scale / sum : 0.0f;
+    const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const uint64_t to = dst + 2 * (v * 32 + lane);
+        if (kHalf) *reinterpret_cast<__half *>(to) = __float2half_rn(acc[v] * inv);
+        else *reinterpret_cast<__nv_bfloat16 *>(to) = __float2bfloat16_rn(acc[v] * inv);
+    }
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
+}
+
+typedef void(PagesFn)(PageAttendArgs);
+struct Variant {
+    uint32_t D;
+    bool fp8, fp16;
+    PagesFn *rows_fn, *join_fn, *join4_fn;
+    int smem, blocks;
+};
+template <int D, bool kF8, bool kHalf>
+constexpr Variant variant() {
+    return Variant{(uint32_t)D, kF8, kHalf, kv_pages_rows_kernel<D, kF8, kHalf>, kv_pages_join_kernel<D, kHalf, 1>,
+                   kv_pages_join_kernel<D, kHalf, 4>, kWarps * ring_bytes(D, kF8), blocks_per_sm(D, kF8)};
+}
+#define KVB_PAGES(D) variant<D, false, false>(), variant<D, false, true>(), variant<D, true, false>(), variant<D, true, true>()
+const Variant kVariants[] = {KVB_PAGES(64), KVB_PAGES(96), KVB_PAGES(128), KVB_PAGES(192), KVB_PAGES(256)};
+
+const Variant *find_variant(uint32_t D, bool fp8, bool fp16) {
+    for (const Variant &v : kVariants)
+        if (v.D == D && v.fp8 == fp8 && v.fp16 == fp16) return &v;
+    return nullptr;
+}
+
+cudaError_t launch(PagesFn *fn, dim3 grid, int threads, int smem, cudaStream_t stream, bool pdl, const PageAttendArgs &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+// Space in the workspace, 256 bytes aligned.
+uint64_t take(uint64_t *at, uint64_t bytes) {
+    const uint64_t p = *at;
+    *at += (bytes + 255) / 256 * 256;
+    return p;
+}
+
+// The most units that an engine may meet.
+uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t groups, uint32_t max_group,
+                    uint32_t group, bool picked, uint32_t H) {
+    uint64_t u = 0;
+    auto tiles = [&](uint64_t segs, uint64_t most_tokens) {
+        const uint64_t rt = e.row_tile;
+        if (picked) return (uint64_t)tokens * ((group + rt - 1) / rt);
+        // each segment alone, or all tokens cut once and one ragged tile a segment
+        return std::min(segs * ((most_tokens * group + rt - 1) / rt), (uint64_t)tokens * group / rt + segs);
+    };
+    if (e.prefix) u += tiles(groups, max_group);
+    if (e.own) u += tiles(requests, max_q);
+    return u * H;
+}
+
+void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint32_t D) {
+    e->units = units;
+    const uint64_t rows = (units + e->workers) * e->slot_rows;
+    e->seg_tiles = (uint64_t *)take(at, (segs + 1) * 8);
+    e->seg_units = (uint64_t *)take(at, (segs + 1) * 8);
+    e->part_ml = (float *)take(at, rows * 8);
+    e->part_o = (float *)take(at, rows * D * 4);
+}
+
+}  // namespace
+
+PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len, uint32_t groups,
+                    uint32_t max_group, uint32_t max_prefix, uint32_t budget, uint32_t T, uint32_t q_heads,
+                    uint32_t kv_heads, uint32_t D, bool fp8, int sms) {
+    PagePlan p{};
+    const uint32_t group = q_heads / kv_heads;
+    const bool picked = budget != 0;
+    const uint32_t prefix_rows = (uint32_t)std::min<uint64_t>((uint64_t)max_group * group, 1u << 30);
+    const uint32_t own_rows = picked ? group : max_q * group;
+    PageEngine &e = p.rows;
+    e.on = 1;
+    e.prefix = groups != 0;
+    e.own = 1;
+    e.row_tile = kRowsP;
+    e.slot_rows = std::min<uint32_t>(kRowsP, std::max(own_rows, groups != 0 ? prefix_rows : 0));
+    const uint64_t units = most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
+    const Variant *v = find_variant(D, fp8, false);
+    const uint32_t blocks = (uint32_t)(sms * v->blocks);
+    // A warp works by itself where units are many and short; where there are few of them a
+    // block's four warps share one, so that fewer pieces have to be joined.
+    e.team = units >= 2ull * blocks ? 1 : kWarps;
+    e.kv_tile = kTile * e.team;
+    e.workers = blocks * (kWarps / e.team);
+    uint64_t at = 0;
+    place(&e, &at, units, (uint64_t)groups + requests, D);
+    p.wide_join = e.workers > 6 * units;
+    p.bytes = at;
+    return p;
+}
+
+cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D, bool fp8, bool fp16, bool pdl,
+                         cudaStream_t stream, int *launches) {
+    (void)cudaGetLastError();
+    const Variant *v = find_variant(D, fp8, fp16);
+    if (v == nullptr) return cudaErrorInvalidValue;
+    const uint32_t teams = kWarps / a.rows.team;
+    cudaError_t e = launch(v->rows_fn, dim3(a.rows.workers / teams), kWarps * 32, v->smem, stream, pdl, a);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    if (p.wide_join) e = launch(v->join4_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
+    else e = launch(v->join_fn, dim3((a.q_heads + 3) / 4, a.max_q, a.requests), 128, 0, stream, pdl, a);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+cudaError_t preload_pages_kernels() {
+    cudaFuncAttributes at;
+    for (const Variant &v : kVariants) {
+        cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.rows_fn);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute((const void *)v.rows_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvb

@@ -1,0 +1,283 @@
+// kvb_pages.h -- what the operators on 16-bit and fp8 pages share (kv_attend_shared,
+// kv_bound, kv_select, kv_attend_selected): parameter blocks, and how attention's work
+// is cut into equal shares.  The functions here also compile as host C++ for the CPU
+// tests.  Not part of the public ABI.
+#pragma once
+
+#include "kvb_vec.h"
+
+namespace kvb {
+
+// ------------------------------------------------------ attention: units of work
+//
+// A segment is a run of cached tokens with the queries that see it: the prefix of a group
+// of requests, or the own tokens of one request.  A unit is one KV head and one tile of
+// query rows of a segment; its cached tokens are counted in tiles of kv_tile.  All tiles
+// of a call, in the order segment, row tile, head, cached tokens, are cut into equal runs,
+// one a worker, so that ragged lengths leave nobody idle; what a worker holds of a unit is a
+// piece, and a kernel behind joins the pieces of each query row.  Unit u's piece at worker
+// w has slot u + w of the workspace: from one piece to the next u, w or both go up, so
+// slots are distinct.  More units than valid query ranges can have (ranges that overlap) are
+// refused on the GPU: nothing of the call is done.
+
+struct PageEngine {
+    uint32_t on;              // launched for this call
+    uint32_t prefix, own;     // which segments it takes: groups' prefixes first, then requests
+    uint32_t row_tile, kv_tile;
+    uint32_t workers;
+    uint32_t slot_rows;       // query rows of a slot
+    uint32_t team;            // warps of a worker (kernel for few rows)
+    uint64_t units;           // that the workspace has room for
+    float *part_o;            // [slot][slot_rows][D] sums
+    float *part_ml;           // [slot][slot_rows][2] maxima (base 2), sums of weights
+    uint64_t *seg_tiles;      // [segments + 1] tiles before each segment (written by worker 0)
+    uint64_t *seg_units;      // [segments + 1]
+};
+
+struct PageAttendArgs {
+    Vecs q, out;
+    float *lse;
+    const int32_t *q_start, *lens, *pages;
+    int64_t pages_stride;
+    const int32_t *group_start, *prefix_lens, *prefix_pages;
+    int64_t prefix_stride;
+    const int32_t *picks;     // [tokens][H][budget], or null: all pages
+    uint32_t budget;
+    uint32_t *status;
+    PoolLayer pool;
+    uint32_t requests, tokens, max_q, max_len, groups, max_group, max_prefix;
+    uint32_t q_heads, group;  // group: query heads of a KV head
+    float scale_log2;         // scale * log2(e), the keys' scale included
+    float v_scale;
+    PageEngine rows, tc;      // kernel for few rows, kernel on tcgen05
+};
+
+struct PageSeg {
+    int q0, n, len;           // first query token, query tokens, cached tokens
+    bool prefix, bad;
+    uint32_t index;           // of the group or request
+};
+
+// Request r's queries and cached tokens, brought into range.
+KVB_HD PageSeg own_seg(const PageAttendArgs &a, uint32_t r) {
+    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], len = a.lens[r];
+    const bool out = q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_q;
+    PageSeg s;
+    s.bad = out || len < 0 || len > (int)a.max_len;
+    s.q0 = out ? 0 : q0;
+    s.n = out ? 0 : q1 - q0;
+    s.len = len < 0 ? 0 : len > (int)a.max_len ? (int)a.max_len : len;
+    s.prefix = false;
+    s.index = r;
+    return s;
+}
+
+// Group g's: all query tokens of its requests.  A group that is out of order or holds more
+// than max_group query tokens has none.
+KVB_HD PageSeg prefix_seg(const PageAttendArgs &a, uint32_t g) {
+    const int r0 = a.group_start[g], r1 = a.group_start[g + 1], len = a.prefix_lens[g];
+    bool out = r0 < 0 || r1 < r0 || r1 > (int)a.requests;
+    int q0 = 0, q1 = 0;
+    if (!out) {
+        q0 = a.q_start[r0];
+        q1 = a.q_start[r1];
+        out = q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_group;
+    }
+    PageSeg s;
+    s.bad = out || len < 0 || len > (int)a.max_prefix;
+    s.q0 = out ? 0 : q0;
+    s.n = out ? 0 : q1 - q0;
+    s.len = len < 0 ? 0 : len > (int)a.max_prefix ? (int)a.max_prefix : len;
+    s.prefix = true;
+    s.index = g;
+    return s;
+}
+
+// The group whose prefix request r's queries q0 .. q0 + n - 1 see, or -1.  Groups are in
+// order; where they are not, whichever the search meets.
+KVB_HD int group_of(const PageAttendArgs &a, uint32_t r, int q0, int n) {
+    if (a.groups == 0) return -1;
+    uint32_t lo = 0, hi = a.groups;              // last group that starts at r or before
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (a.group_start[mid] <= (int)r) lo = mid;
+        else hi = mid;
+    }
+    // empty groups in front of the one that holds r start at the same request
+    const PageSeg s = prefix_seg(a, lo);
+    if (s.n == 0 || s.len == 0 || a.group_start[lo] > (int)r || a.group_start[lo + 1] <= (int)r) return -1;
+    if (q0 < s.q0 || q0 + n > s.q0 + s.n) return -1;
+    return (int)lo;
+}
+
+KVB_HD uint32_t seg_count(const PageAttendArgs &a, const PageEngine &e) {
+    return (e.prefix ? a.groups : 0) + (e.own ? a.requests : 0);
+}
+
+KVB_HD PageSeg seg_at(const PageAttendArgs &a, const PageEngine &e, uint32_t s) {
+    const uint32_t before = e.prefix ? a.groups : 0;
+    return s < before ? prefix_seg(a, s) : own_seg(a, s - before);
+}
+
+// Row tiles of a segment.  Rows are (query token, head of the group); where every token
+// has pages of its own, a tile holds rows of one token.
+KVB_HD int row_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s) {
+    const int rt = (int)e.row_tile, g = (int)a.group;
+    return a.picks != nullptr ? s.n * ((g + rt - 1) / rt) : (int)(((int64_t)s.n * g + rt - 1) / rt);
+}
+
+// Cached tokens that some row of a tile sees: [0, that).
+KVB_HD int seen_tokens(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
+    if (s.prefix) return s.len;
+    if (a.picks != nullptr) {
+        // whole pages of the list, as many as the request's last token may have
+        const uint32_t all = (uint32_t)(((uint64_t)s.len + a.pool.T - 1) / a.pool.T);
+        return (int)((all < a.budget ? all : a.budget) * a.pool.T);
+    }
+    int64_t last = (((int64_t)rt + 1) * e.row_tile - 1) / a.group;
+    if (last > s.n - 1) last = s.n - 1;
+    const int64_t hi = (int64_t)s.len - s.n + last + 1;
+    return hi < 0 ? 0 : (int)hi;                 // at most len
+}
+
+KVB_HD uint32_t unit_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
+    return ((uint32_t)seen_tokens(a, e, s, rt) + e.kv_tile - 1) / e.kv_tile;
+}
+
+// Tiles of the row tiles before rt, for one head.
+KVB_HD uint64_t tiles_before(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
+    if (rt == 0) return 0;
+    if (s.prefix || a.picks != nullptr) return (uint64_t)rt * unit_tiles(a, e, s, 0);
+    uint64_t sum = 0;
+    for (int i = 0; i < rt; ++i) sum += unit_tiles(a, e, s, i);
+    return sum;
+}
+
+KVB_HD uint64_t seg_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s) {
+    return s.n == 0 || s.len == 0 ? 0 : tiles_before(a, e, s, row_tiles(a, e, s)) * a.pool.H;
+}
+
+// Tiles of a worker.
+KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : (tiles + workers - 1) / workers; }
+
+// Where a worker stands: a segment, and tiles and units before it.
+struct PageCursor {
+    uint64_t tiles, units;
+    uint32_t seg;
+};
+
+// A worker's tiles [k0, k1) of the n_tiles of a unit.
+struct PagePiece {
+    PageSeg s;
+    int rt, head, k0, k1, n_tiles;
+    uint64_t slot;
+};
+
+// The piece of `worker` that begins with tile x (x < x1, its last tile), from a cursor at
+// its segment or before.
+KVB_HD PagePiece piece_at(const PageAttendArgs &a, const PageEngine &e, PageCursor *at, uint64_t x, uint64_t x1,
+                          uint32_t worker) {
+    PagePiece p;
+    p.s = seg_at(a, e, at->seg);
+    uint64_t tiles = seg_tiles(a, e, p.s);
+    while (x >= at->tiles + tiles) {
+        if (tiles != 0) at->units += (uint64_t)row_tiles(a, e, p.s) * a.pool.H;
+        at->tiles += tiles;
+        p.s = seg_at(a, e, ++at->seg);
+        tiles = seg_tiles(a, e, p.s);
+    }
+    uint64_t rel = x - at->tiles;
+    uint32_t n = unit_tiles(a, e, p.s, 0);
+    p.rt = 0;
+    if (p.s.prefix || a.picks != nullptr) {
+        p.rt = (int)(rel / ((uint64_t)n * a.pool.H));
+        rel -= (uint64_t)p.rt * n * a.pool.H;
+    } else {
+        while (rel >= (uint64_t)n * a.pool.H) {
+            rel -= (uint64_t)n * a.pool.H;
+            n = unit_tiles(a, e, p.s, ++p.rt);
+        }
+    }
+    p.n_tiles = (int)n;
+    p.head = (int)(rel / n);
+    p.k0 = (int)(rel % n);
+    const uint64_t left = p.k0 + (x1 - x);
+    p.k1 = left < n ? (int)left : (int)n;
+    p.slot = at->units + (uint64_t)p.rt * a.pool.H + p.head + worker;
+    return p;
+}
+
+// Where the pieces of a query row are: workers w0 .. w1, slots unit + w, row `row` of each.
+struct RowPieces {
+    uint64_t unit, w0, w1;
+    int row;
+    bool any;
+};
+
+// Row (query token i of segment s, head j of the KV head's group) of a segment that is number
+// `at` of the engine's.
+KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint32_t at, int i, int head, int j) {
+    RowPieces p;
+    const int rt_n = (int)e.row_tile, g = (int)a.group;
+    const int64_t row = (int64_t)i * g + j;
+    const int rt = a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + j / rt_n : (int)(row / rt_n);
+    const uint32_t n = unit_tiles(a, e, s, rt);
+    p.any = n != 0;
+    p.row = a.picks != nullptr ? j % rt_n : (int)(row % rt_n);
+    const uint64_t share = share_of(e.seg_tiles[seg_count(a, e)], e.workers);
+    const uint64_t t0 = e.seg_tiles[at] + tiles_before(a, e, s, rt) * a.pool.H + (uint64_t)head * n;
+    p.w0 = t0 / share;
+    p.w1 = (t0 + (n != 0 ? n : 1) - 1) / share;
+    p.unit = e.seg_units[at] + (uint64_t)rt * a.pool.H + head;
+    return p;
+}
+
+// ------------------------------------------------------------ bounds of pages
+
+constexpr uint32_t kTinyBits = 0x0d800000u;      // 2^-100: a group below it is zeros
+constexpr float kMostScore = 3.402823466e38f;
+
+KVB_HD uint32_t record_bytes(uint32_t D) { return (2 * D + D / 8 + 15) / 16 * 16; }
+
+// The step of a group whose largest magnitude has these bits: the least power of two s
+// with m <= 127 s; *inv = 1 / s.  0 and 0 below 2^-100, infinity and 0 for what is not finite.
+KVB_HD float bound_step(uint32_t m, float *inv) {
+    *inv = 0.0f;
+    if (m < kTinyBits) return 0.0f;
+    if (m >= 0x7f800000u) return f_bits(0x7f800000u);
+    const uint32_t e = (m + 0x1ffffu) >> 23;     // 127 / 64 = 1.984375 is mantissa 0x7e0000
+    *inv = f_bits((260u - e) << 23);
+    return f_bits((e - 6u) << 23);
+}
+
+struct BoundArgs {
+    uint8_t *bounds;          // [P][H] records
+    const int32_t *lens, *first, *pages;
+    int64_t pages_stride;
+    uint32_t *status;
+    PoolLayer pool;
+    uint32_t requests, max_len, max_new;
+    uint32_t most_pages;      // that one request's new tokens may touch
+};
+
+struct SelectArgs {
+    const uint8_t *bounds;
+    Vecs q;
+    const int32_t *q_start, *lens, *pages;
+    int64_t pages_stride;
+    int32_t *picks;           // [tokens][H][budget]
+    float *scores;            // [tokens][H][max_pages]
+    uint32_t *status;
+    uint32_t T, P, H;
+    uint32_t requests, tokens, max_q, max_len, max_pages, q_heads, group;
+    uint32_t budget, keep_first, keep_last;
+    uint32_t block_pages;     // pages a block scores
+};
+
+// Pages of a request that query i of n sees: 0 .. that - 1.
+KVB_HD int pages_seen(int len, int n, int i, uint32_t T) {
+    const int pos = len - n + i;
+    return pos < 0 ? 0 : (int)((uint32_t)pos / T) + 1;
+}
+
+}  // namespace kvb

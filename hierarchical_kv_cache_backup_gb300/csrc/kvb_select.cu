@@ -1,0 +1,509 @@
+// kvb_select.cu -- bounds of the keys of each page (kv_bound) and the pages whose bounds
+// promise a query most (kv_select).
+//
+// Mathematics.  For a page and KV head, lo_d <= k_d <= hi_d for all its keys, so q . k is
+// at most sum_d max(q_d lo_d, q_d hi_d) = sum over q_d > 0 of q_d hi_d + sum over q_d < 0 of
+// q_d lo_d.  Bounds and queries are 8-bit codes in units of a power of two for each 32 dims,
+// rounded outwards for bounds: a group's sum is then a whole number below 2^19, exact in any order of
+// additions, so that the pages selected do not depend on how the sums are taken, and a page is
+// read in half the bytes that 16-bit bounds would take.
+#include "kvb_pages.h"
+#include "kvb_pages_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+namespace kvb {
+
+namespace {
+
+template <bool kBf>
+struct Pair16;
+template <>
+struct Pair16<true> {
+    using T = __nv_bfloat162;
+    __device__ static float2 f(T x) { return __bfloat1622float2(x); }
+};
+template <>
+struct Pair16<false> {
+    using T = __half2;
+    __device__ static float2 f(T x) { return __half22float2(x); }
+};
+
+// ------------------------------------------------------------------- kv_bound
+//
+// A warp takes one page and KV head: 16 bytes of a token a lane, several tokens at once where
+// a vector is short, least and largest values two at a time in their own type (fp8 as fp16,
+// exact).  Bound: memory, keys read once.
+constexpr int kBoundWarps = 8;
+
+template <int D, bool kF8, bool kHalf>
+__global__ void __launch_bounds__(kBoundWarps * 32) kv_bound_kernel(const __grid_constant__ BoundArgs a) {
+    constexpr bool kBf = !kF8 && !kHalf;
+    using P = Pair16<kBf>;
+    using T2 = typename P::T;
+    constexpr int LT = D / (kF8 ? 16 : 8), AT = 32 / LT;     // lanes of a token, tokens at once
+    constexpr int NP = kF8 ? 8 : 4, LG = kF8 ? 2 : 4;        // pairs of a lane, lanes of a group
+    constexpr uint32_t kRec = (2 * D + D / 8 + 15) / 16 * 16;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31, H = (int)a.pool.H;
+    const int in = lane / LT, piece = lane - in * LT;
+    const uint64_t units = (uint64_t)a.requests * a.most_pages * H;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (uint64_t u = (uint64_t)blockIdx.x * kBoundWarps + (threadIdx.x >> 5); u < units; u += (uint64_t)gridDim.x * kBoundWarps) {
+        const int head = (int)(u % H);
+        const uint32_t jr = (uint32_t)(u / H % a.most_pages), r = (uint32_t)(u / H / a.most_pages);
+        const int len = a.lens[r], first = a.first != nullptr ? a.first[r] : 0;
+        if (len < 0 || len > (int)a.max_len || first < 0 || first > len || len - first > (int)a.max_new) {
+            if (jr == 0 && head == 0 && lane == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+            continue;
+        }
+        const uint32_t j = div_T(a.pool, (uint32_t)first) + jr;
+        const int64_t t0 = (int64_t)j * a.pool.T;
+        if (first == len || t0 >= len) continue;
+        const int n = (int)min((int64_t)a.pool.T, len - t0);
+        const uint32_t page = (uint32_t)a.pages[(int64_t)r * a.pages_stride + j];
+        if (page >= a.pool.P) {
+            if (head == 0 && lane == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+            continue;
+        }
+        T2 lo[NP], hi[NP];
+        const uint32_t top = kBf ? 0x7f807f80u : 0x7c007c00u, low = top | 0x80008000u;      // infinities
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            lo[i] = *reinterpret_cast<const T2 *>(&top);
+            hi[i] = *reinterpret_cast<const T2 *>(&low);
+        }
+        const uint64_t from = a.pool.base[0] + (uint64_t)page * a.pool.s_page + (uint64_t)head * a.pool.s_head + piece * 16;
+        auto take = [&](const uint4 &w) {
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (kF8) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((unsigned short)(v[i] >> (16 * h))));
+                        const T2 y = *reinterpret_cast<const T2 *>(&x);
+                        lo[2 * i + h < NP ? 2 * i + h : 0] = __hmin2_nan(lo[2 * i + h < NP ? 2 * i + h : 0], y);
+                        hi[2 * i + h < NP ? 2 * i + h : 0] = __hmax2_nan(hi[2 * i + h < NP ? 2 * i + h : 0], y);
+                    }
+                } else {
+                    const T2 y = *reinterpret_cast<const T2 *>(&v[i]);
+                    lo[i] = __hmin2_nan(lo[i], y);
+                    hi[i] = __hmax2_nan(hi[i], y);
+                }
+            }
+        };
+        if (in < AT) {
+            int t = in;
+            for (; t + 7 * AT < n; t += 8 * AT) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4 *>(from + (uint64_t)(t + i * AT) * a.pool.s_tok);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) take(w[i]);
+            }
+            for (; t < n; t += AT) take(*reinterpret_cast<const uint4 *>(from + (uint64_t)t * a.pool.s_tok));
+        }
+        // over the tokens that other lanes had
+        if (AT > 1) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                T2 l = lo[i], h = hi[i];
+#pragma unroll
+                for (int s = 1; s < AT; ++s) {
+                    const uint32_t lw = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&lo[i]), piece + s * LT);
+                    const uint32_t hw = __shfl_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&hi[i]), piece + s * LT);
+                    l = __hmin2_nan(l, *reinterpret_cast<const T2 *>(&lw));
+                    h = __hmax2_nan(h, *reinterpret_cast<const T2 *>(&hw));
+                }
+                lo[i] = l;
+                hi[i] = h;
+            }
+        }
+        float fl[2 * NP], fh[2 * NP];
+        uint32_t most = 0;                                   // of the group, as bits: NaN above infinity
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float2 l = P::f(lo[i]), h = P::f(hi[i]);
+            fl[2 * i] = l.x;
+            fl[2 * i + 1] = l.y;
+            fh[2 * i] = h.x;
+            fh[2 * i + 1] = h.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i)
+            most = max(most, max(__float_as_uint(fl[i]) & 0x7fffffffu, __float_as_uint(fh[i]) & 0x7fffffffu));
+#pragma unroll
+        for (int d = 1; d < LG; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+        float inv;
+        const float step = bound_step(most, &inv);
+        if (lane < LT) {
+            uint8_t *rec = a.bounds + ((uint64_t)page * H + head) * kRec;
+            uint32_t wl[NP / 2], wh[NP / 2];
+#pragma unroll
+            for (int i = 0; i < NP / 2; ++i) {
+                wl[i] = wh[i] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int cl = inv != 0.0f ? (int)floorf(__fmul_rn(fl[4 * i + b], inv)) : 0;
+                    const int ch = inv != 0.0f ? (int)ceilf(__fmul_rn(fh[4 * i + b], inv)) : 0;
+                    wl[i] |= (uint32_t)(cl & 255) << (8 * b);
+                    wh[i] |= (uint32_t)(ch & 255) << (8 * b);
+                }
+            }
+            if (kF8) {
+                *reinterpret_cast<uint4 *>(rec + 16 * lane) = make_uint4(wl[0], wl[1], wl[2 % (NP / 2)], wl[3 % (NP / 2)]);
+                *reinterpret_cast<uint4 *>(rec + D + 16 * lane) = make_uint4(wh[0], wh[1], wh[2 % (NP / 2)], wh[3 % (NP / 2)]);
+            } else {
+                *reinterpret_cast<uint2 *>(rec + 8 * lane) = make_uint2(wl[0], wl[1]);
+                *reinterpret_cast<uint2 *>(rec + D + 8 * lane) = make_uint2(wh[0], wh[1]);
+            }
+            if (lane % LG == 0) *reinterpret_cast<float *>(rec + 2 * D + lane / LG * 4) = step;
+            if (lane < (int)(kRec - 2 * D - D / 8) / 4) *reinterpret_cast<uint32_t *>(rec + 2 * D + D / 8 + lane * 4) = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ kv_select
+//
+// Scores: a block takes some pages of one query and KV head.  A lane holds the codes of one
+// group of 32 dims of four query heads, positive and negative ones apart, and takes that group
+// of a page's record: two 8-bit dot products of 4 a word, whose float terms the group's lanes
+// add in the order of the groups.
+constexpr int kScoreWarps = 8, kHeads = 4;
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kScoreWarps * 32) kv_score_kernel(const __grid_constant__ SelectArgs a) {
+    using P = Pair16<!kHalf>;
+    constexpr int NG = D / 32, LG = NG <= 2 ? 2 : NG <= 4 ? 4 : 8, SLOTS = 32 / LG;
+    constexpr uint32_t kRec = (2 * D + D / 8 + 15) / 16 * 16;
+    __shared__ __align__(16) int8_t code[kHeads][2][D];
+    __shared__ float unit[kHeads][NG];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunks = (int)((a.max_pages + a.block_pages - 1) / a.block_pages);
+    const int head = (int)blockIdx.x / chunks, p0 = (int)(blockIdx.x % chunks) * (int)a.block_pages;
+    const int i = blockIdx.y, r = blockIdx.z;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], len = a.lens[r];
+    if (q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_q || len < 0 || len > (int)a.max_len) return;
+    if (i >= q1 - q0) return;
+    const int seen = pages_seen(len, q1 - q0, i, a.T);
+    if (seen <= (int)a.budget || p0 >= seen) return;
+    const int64_t tok = q0 + i;
+    const int p1 = min(seen, p0 + (int)a.block_pages);
+    const int slot = lane / LG, gr = lane % LG;
+    const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
+    float *scores = a.scores + (tok * a.H + head) * (int64_t)a.max_pages;
+
+    for (int h0 = 0; h0 < (int)a.group; h0 += kHeads) {
+        const int heads = min(kHeads, (int)a.group - h0);
+        __syncthreads();
+        // codes of the query: a warp a group of 32 values, a lane a value
+        for (int k = warp; k < kHeads * NG; k += kScoreWarps) {
+            const int h = k / NG, g = k % NG;
+            float x = 0.0f;
+            if (h < heads) {
+                const uint64_t src = a.q.data + tok * a.q.s_tok + (int64_t)(head * a.group + h0 + h) * a.q.s_head + (32 * g + lane) * 2;
+                const uint32_t w = *reinterpret_cast<const unsigned short *>(src);
+                const uint32_t both = w | w << 16;
+                x = P::f(*reinterpret_cast<const typename P::T *>(&both)).x;
+            }
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
+            float inv;
+            const float step = bound_step(most, &inv);
+            const int c = inv != 0.0f ? (int)rintf(__fmul_rn(x, inv)) : 0;
+            code[h][0][32 * g + lane] = (int8_t)max(c, 0);
+            code[h][1][32 * g + lane] = (int8_t)min(c, 0);
+            if (lane == 0) unit[h][g] = step;
+        }
+        __syncthreads();
+        int pos[kHeads][8], neg[kHeads][8];
+        float t[kHeads];
+        const int gu = gr < NG ? gr : 0;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            const int4 *cp = reinterpret_cast<const int4 *>(&code[h][0][32 * gu]), *cn = reinterpret_cast<const int4 *>(&code[h][1][32 * gu]);
+            const int4 u = cp[0], v = cp[1], w = cn[0], x = cn[1];
+            pos[h][0] = u.x; pos[h][1] = u.y; pos[h][2] = u.z; pos[h][3] = u.w;
+            pos[h][4] = v.x; pos[h][5] = v.y; pos[h][6] = v.z; pos[h][7] = v.w;
+            neg[h][0] = w.x; neg[h][1] = w.y; neg[h][2] = w.z; neg[h][3] = w.w;
+            neg[h][4] = x.x; neg[h][5] = x.y; neg[h][6] = x.z; neg[h][7] = x.w;
+            t[h] = unit[h][gu];
+        }
+#pragma unroll 2
+        for (int p = p0 + warp * SLOTS; p < p1; p += kScoreWarps * SLOTS) {
+            const int mine = p + slot;
+            const bool on = mine < p1;
+            const uint32_t page = on ? (uint32_t)table[mine] : 0;
+            const bool bad = on && page >= a.P;
+            int lo[8], hi[8];
+            float step = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) lo[k] = hi[k] = 0;
+            if (on && !bad && gr < NG) {
+                const uint8_t *rec = a.bounds + ((uint64_t)page * a.H + head) * kRec + 32 * gr;
+                const int4 u = *reinterpret_cast<const int4 *>(rec), v = *reinterpret_cast<const int4 *>(rec + 16);
+                const int4 w = *reinterpret_cast<const int4 *>(rec + D), x = *reinterpret_cast<const int4 *>(rec + D + 16);
+                step = *reinterpret_cast<const float *>(rec + 2 * D - 32 * gr + 4 * gr);
+                lo[0] = u.x; lo[1] = u.y; lo[2] = u.z; lo[3] = u.w; lo[4] = v.x; lo[5] = v.y; lo[6] = v.z; lo[7] = v.w;
+                hi[0] = w.x; hi[1] = w.y; hi[2] = w.z; hi[3] = w.w; hi[4] = x.x; hi[5] = x.y; hi[6] = x.z; hi[7] = x.w;
+            }
+            float best = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                int dot = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dot = __dp4a(neg[h][k], lo[k], __dp4a(pos[h][k], hi[k], dot));
+                const float term = __fmul_rn((float)dot, __fmul_rn(step, t[h]));
+                float sum = __shfl_sync(0xffffffffu, term, slot * LG);
+#pragma unroll
+                for (int g = 1; g < NG; ++g) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, term, slot * LG + g));
+                if (!(fabsf(sum) <= kMostScore)) sum = kMostScore;
+                if (h < heads) best = fmaxf(best, sum);
+            }
+            if (on && gr == 0) {
+                if (bad) best = -kMostScore;                 // nothing to be found there
+                if (h0 != 0) best = fmaxf(best, scores[mine]);
+                scores[mine] = best;
+                if (bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+            }
+        }
+    }
+}
+
+// Picks: a block takes one query and KV head.  The least key that is selected is found by
+// histograms over the range of keys that is left, 2,048 bins at a time (the first over the keys'
+// own range, so that scores of one size spread over the bins); then every thread looks at a run
+// of pages, and a sum over the block says where its picks go, in the order of the pages.
+constexpr int kPickThreads = 1024, kBins = 2048, kHeld = 8;
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) != 0 ? 0xffffffffu : 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_constant__ SelectArgs a) {
+    __shared__ uint32_t bins[kBins];
+    __shared__ unsigned long long sums[32];
+    __shared__ uint32_t least_s[32], most_s[32], found[3];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int head = blockIdx.x, i = blockIdx.y, r = blockIdx.z;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], len = a.lens[r];
+    if (q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_q || len < 0 || len > (int)a.max_len) {
+        if (tid == 0 && head == 0 && i == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+        return;
+    }
+    if (i >= q1 - q0) return;
+    const int64_t row = (int64_t)(q0 + i) * a.H + head;
+    const int n = pages_seen(len, q1 - q0, i, a.T), budget = (int)a.budget;
+    int32_t *picks = a.picks + row * budget;
+    if (n <= budget) {
+        for (int k = tid; k < budget; k += kPickThreads) picks[k] = k < n ? k : -1;
+        return;
+    }
+    const float *scores = a.scores + row * (int64_t)a.max_pages;
+    const int c0 = (int)a.keep_first, c1 = n - (int)a.keep_last;      // candidates [c0, c1); the rest is kept
+    uint32_t k = (uint32_t)(budget - c0 - (int)a.keep_last);
+    const int per = (n + kPickThreads - 1) / kPickThreads, b0 = tid * per;
+    // this thread's run of pages, held in registers where it is short
+    uint32_t held[kHeld];
+    auto candidate = [&](int p) { return p >= c0 && p < c1; };
+    if (per <= kHeld) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) held[j] = j < per && candidate(b0 + j) ? order_key(scores[b0 + j]) : 0u;
+    }
+    auto each = [&](auto &&f) {
+        if (per <= kHeld) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (j < per && candidate(b0 + j)) f(held[j]);
+        } else {
+            for (int p = c0 + tid; p < c1; p += kPickThreads) f(order_key(scores[p]));
+        }
+    };
+    uint32_t lo = 0xffffffffu, hi = 0;
+    each([&](uint32_t u) {
+        lo = min(lo, u);
+        hi = max(hi, u);
+    });
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        least_s[warp] = lo;
+        most_s[warp] = hi;
+    }
+    __syncthreads();
+    lo = __reduce_min_sync(0xffffffffu, least_s[lane]);
+    hi = __reduce_max_sync(0xffffffffu, most_s[lane]);
+    uint32_t need = k;                                       // of the keys equal to the least one selected
+    while (k != 0 && lo != hi) {
+        const int shift = max(0, 32 - __clz(hi - lo) - 11);
+        for (int b = tid; b < kBins; b += kPickThreads) bins[b] = 0;
+        __syncthreads();
+        each([&](uint32_t u) {
+            if (u >= lo && u <= hi) atomicAdd(&bins[(u - lo) >> shift], 1u);
+        });
+        __syncthreads();
+        // keys in the bins above: thread t looks after bins 2046 - 2 t and the next
+        const uint32_t x1 = bins[kBins - 1 - 2 * tid], x0 = bins[kBins - 2 - 2 * tid];
+        uint32_t s = x0 + x1;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        if (lane == 31) least_s[warp] = s;
+        __syncthreads();
+        uint32_t before = lane < warp ? least_s[lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, before) + s - x0 - x1;
+        if (before < k && before + x1 >= k) {
+            found[0] = (uint32_t)(kBins - 1 - 2 * tid);
+            found[1] = before;
+            found[2] = x1;
+        } else if (before + x1 < k && before + x1 + x0 >= k) {
+            found[0] = (uint32_t)(kBins - 2 - 2 * tid);
+            found[1] = before + x1;
+            found[2] = x0;
+        }
+        __syncthreads();
+        const uint32_t bin = found[0], inside = found[2];
+        k -= found[1];
+        lo += bin << shift;
+        hi = min(hi, lo + ((1u << shift) - 1u));
+        need = k;
+        if (inside == k) {                                   // all of the bin
+            need = 0xffffffffu;
+            break;
+        }
+    }
+    if (k == 0) {                                            // the pages that are kept fill the budget
+        lo = 0xffffffffu;
+        need = 0;
+    }
+    // key > lo is selected, key == lo for the first `need` of them, and with need without bound all from lo on
+    auto above = [&](int p, uint32_t u) { return !candidate(p) || u > lo; };
+    unsigned long long mine = 0;                             // above, and equal in the high word
+    for (int j = 0; j < per; ++j) {
+        const int p = b0 + j;
+        if (p >= n) break;
+        const uint32_t u = candidate(p) ? order_key(scores[p]) : 0;
+        if (above(p, u)) mine += 1;
+        else if (u == lo) mine += 1ull << 32;
+    }
+    unsigned long long s = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    unsigned long long before = s - mine;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    uint32_t gt = (uint32_t)before, eq = (uint32_t)(before >> 32);
+    for (int j = 0; j < per; ++j) {
+        const int p = b0 + j;
+        if (p >= n) break;
+        const uint32_t u = candidate(p) ? order_key(scores[p]) : 0;
+        if (above(p, u)) {
+            picks[gt + min(eq, need)] = p;
+            ++gt;
+        } else if (u == lo) {
+            if (eq < need) picks[gt + eq] = p;
+            ++eq;
+        }
+    }
+}
+
+typedef void(BoundFn)(BoundArgs);
+typedef void(SelectFn)(SelectArgs);
+struct BoundVariant {
+    uint32_t D;
+    bool fp8, fp16;
+    BoundFn *fn;
+};
+struct ScoreVariant {
+    uint32_t D;
+    bool fp16;
+    SelectFn *fn;
+};
+// fp8 values are the same whatever the queries' type
+#define KVB_BOUND(D)                                                                              \
+    BoundVariant{D, false, false, kv_bound_kernel<D, false, false>},                              \
+        BoundVariant{D, false, true, kv_bound_kernel<D, false, true>}, BoundVariant{D, true, true, kv_bound_kernel<D, true, true>}
+#define KVB_SCORE(D) ScoreVariant{D, false, kv_score_kernel<D, false>}, ScoreVariant{D, true, kv_score_kernel<D, true>}
+const BoundVariant kBounds[] = {KVB_BOUND(64), KVB_BOUND(96), KVB_BOUND(128), KVB_BOUND(192), KVB_BOUND(256)};
+const ScoreVariant kScores[] = {KVB_SCORE(64), KVB_SCORE(96), KVB_SCORE(128), KVB_SCORE(192), KVB_SCORE(256)};
+
+template <class Args>
+cudaError_t launch(void (*fn)(Args), dim3 grid, int threads, cudaStream_t stream, bool pdl, const Args &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+}  // namespace
+
+cudaError_t launch_bound(const BoundArgs &a, uint32_t D, bool fp8, bool fp16, bool pdl, int sms, cudaStream_t stream) {
+    (void)cudaGetLastError();
+    for (const BoundVariant &v : kBounds) {
+        if (v.D != D || v.fp8 != fp8 || (!fp8 && v.fp16 != fp16)) continue;
+        const uint64_t blocks = ((uint64_t)a.requests * a.most_pages * a.pool.H + kBoundWarps - 1) / kBoundWarps;
+        return launch(v.fn, dim3((unsigned)std::min<uint64_t>(blocks, (uint64_t)sms * 64)), kBoundWarps * 32, stream, pdl, a);
+    }
+    return cudaErrorInvalidValue;
+}
+
+uint32_t select_block_pages(uint64_t pages, int sms) {
+    // about four blocks an SM, of 64 pages at least (a step of the block's warps at heads of 128) and 1,024 at most
+    const uint64_t want = pages / (4ull * (uint64_t)sms);
+    return (uint32_t)std::min<uint64_t>(1024, std::max<uint64_t>(64, (want + 63) / 64 * 64));
+}
+
+cudaError_t launch_select(const SelectArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream, int *launches) {
+    (void)cudaGetLastError();
+    for (const ScoreVariant &v : kScores) {
+        if (v.D != D || v.fp16 != fp16) continue;
+        if (a.max_pages > a.budget) {             // otherwise every page is picked
+            const uint32_t chunks = (a.max_pages + a.block_pages - 1) / a.block_pages;
+            const cudaError_t e = launch(v.fn, dim3(chunks * a.H, a.max_q, a.requests), kScoreWarps * 32, stream, pdl, a);
+            if (e != cudaSuccess) return e;
+            ++*launches;
+        }
+        const cudaError_t e = launch(kv_pick_kernel, dim3(a.H, a.max_q, a.requests), kPickThreads, stream, pdl, a);
+        if (e == cudaSuccess) ++*launches;
+        return e;
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t preload_select_kernels() {
+    cudaFuncAttributes at;
+    for (const BoundVariant &v : kBounds) {
+        const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e != cudaSuccess) return e;
+    }
+    for (const ScoreVariant &v : kScores) {
+        const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaFuncGetAttributes(&at, (const void *)kv_pick_kernel);
+}
+
+}  // namespace kvb

@@ -1,9 +1,11 @@
 // kvb_vec.cpp -- C ABI of the operators on single head vectors: kv_rotary_*,
-// kv_rotate, kv_append, kv_fetch, kv_attend.  Checks of arguments, frequencies,
-// and the launch of each call; the kernels are in kvb_vectors.cu and
-// kvb_attend.cu.
+// kv_rotate, kv_append, kv_fetch, kv_attend, kv_attend_shared, kv_bound, kv_select,
+// kv_attend_selected.  Checks of arguments, frequencies, and the launch of each
+// call; the kernels are in kvb_vectors.cu, kvb_attend.cu, kvb_pages.cu and
+// kvb_select.cu.
 #include "kvb.h"
 #include "kvb_internal.h"
+#include "kvb_pages_internal.h"
 #include "kvb_vec.h"
 #include "kvb_vec_internal.h"
 
@@ -178,6 +180,241 @@ kv_status check_attend(const kv_attend_args *a, const VecPool &p, PoolLayer *lay
     if (a->max_q > a->tokens)
         return fail(KV_ERR_INVALID_ARG, "max_q %u is more than all %u query tokens", a->max_q, a->tokens);
     if (!std::isfinite(a->scale)) return fail(KV_ERR_INVALID_ARG, "scale is not finite");
+    return KV_OK;
+}
+
+constexpr uint32_t kMostTokens = 1u << 29;     // of a request, or of a prefix
+
+kv_status check_wide_dim(uint32_t head_dim, const char *what) {
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 192 && head_dim != 256)
+        return fail(KV_ERR_LAYOUT, "head_dim %u: %s takes 64, 96, 128, 192 and 256", head_dim, what);
+    return KV_OK;
+}
+
+// Counts that the operators on 16-bit and fp8 pages share.
+kv_status check_counts(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len, uint32_t q_heads,
+                       uint32_t H, uint32_t T) {
+    if (T > (1u << 20)) return fail(KV_ERR_LAYOUT, "pages of %u tokens: 2^20 at most", T);
+    if (H > 65535) return fail(KV_ERR_LAYOUT, "%u KV heads: 65535 at most", H);
+    if (q_heads == 0 || q_heads % H != 0)
+        return fail(KV_ERR_INVALID_ARG, "%u query heads are not a multiple of the pool's %u", q_heads, H);
+    if (q_heads > 65535 || requests > 65535 || max_q > 65535)
+        return fail(KV_ERR_INVALID_ARG, "requests %u, max_q %u and q_heads %u: 65535 at most each", requests,
+                    max_q, q_heads);
+    if (tokens > 0x7fffffffu || max_len > kMostTokens || (uint64_t)max_q * (q_heads / H) > (1u << 30) ||
+        (uint64_t)tokens * (q_heads / H) > (1u << 30))
+        return fail(KV_ERR_INVALID_ARG, "tokens %u, max_len %u or max_q %u (of %u heads a KV head) too large",
+                    tokens, max_len, max_q, q_heads / H);
+    if (max_q > tokens)
+        return fail(KV_ERR_INVALID_ARG, "max_q %u is more than all %u query tokens", max_q, tokens);
+    return KV_OK;
+}
+
+kv_status check_table(const void *pages, int64_t stride, uint32_t rows, uint32_t max_len, uint32_t T, const char *name) {
+    if (pages == nullptr && max_len != 0) return fail(KV_ERR_INVALID_ARG, "%s is NULL", name);
+    const uint64_t entries = ((uint64_t)max_len + T - 1) / T;
+    if (stride < 0 || (rows > 1 && (uint64_t)stride < entries))
+        return fail(KV_ERR_INVALID_ARG, "the stride of %s, %lld, is less than the %llu pages of %u tokens", name,
+                    (long long)stride, (unsigned long long)entries, max_len);
+    return KV_OK;
+}
+
+kv_status check_space(const void *workspace, uint64_t have, uint64_t need) {
+    if (need != 0 && workspace == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "workspace is NULL; %llu bytes are needed", (unsigned long long)need);
+    if (have < need)
+        return fail(KV_ERR_OUT_OF_RANGE, "workspace of %llu bytes; %llu are needed", (unsigned long long)have,
+                    (unsigned long long)need);
+    if ((uintptr_t)workspace % 16 != 0) return fail(KV_ERR_ALIGNMENT, "the workspace is not 16-byte aligned");
+    return KV_OK;
+}
+
+// kv_attend_shared and kv_attend_selected as one: a selected call has no groups, a shared one no budget.
+struct PagesCall {
+    kv_attend_shared_args a;
+    const int32_t *picks;
+    uint32_t budget;
+};
+
+PagesCall shared_call(const kv_attend_shared_args *a) { return PagesCall{*a, nullptr, 0}; }
+
+PagesCall selected_call(const kv_attend_selected_args *s) {
+    PagesCall c{};
+    kv_attend_shared_args &a = c.a;
+    a.q = s->q;
+    a.out = s->out;
+    a.lse = s->lse;
+    a.q_start = s->q_start;
+    a.lens = s->lens;
+    a.pages = s->pages;
+    a.pages_stride = s->pages_stride;
+    a.workspace = s->workspace;
+    a.workspace_bytes = s->workspace_bytes;
+    a.status = s->status;
+    a.requests = s->requests;
+    a.tokens = s->tokens;
+    a.max_q = s->max_q;
+    a.max_len = s->max_len;
+    a.q_heads = s->q_heads;
+    a.head_dim = s->head_dim;
+    a.dtype = s->dtype;
+    a.format = s->format;
+    a.layer = s->layer;
+    a.scale = s->scale;
+    a.k_scale = s->k_scale;
+    a.v_scale = s->v_scale;
+    a.reserved = s->reserved;
+    c.picks = s->picks;
+    c.budget = s->budget;
+    return c;
+}
+
+bool empty_call(const kv_attend_shared_args &a) { return a.requests == 0 || a.tokens == 0 || a.max_q == 0; }
+
+// What the plan and the kernels need of a block, without its pointers.
+kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolLayer *layer, PagePlan *plan) {
+    const kv_attend_shared_args &a = c.a;
+    TRY(check_dim(a.head_dim, a.dtype));
+    if (a.reserved != 0) return fail(KV_ERR_INVALID_ARG, "reserved members must be 0");
+    TRY(check_wide_dim(a.head_dim, "attention"));
+    if (a.format != KV_CACHE_SAME && a.format != KV_CACHE_E4M3)
+        return fail(KV_ERR_INVALID_ARG, "format %u: SAME and E4M3 pages are taken (Q4 by kv_attend)", a.format);
+    TRY(pool_layer(p, a.format, a.head_dim, layer));
+    if (!vector_index_fits(*layer))
+        return fail(KV_ERR_LAYOUT, "the pool's pages span 2^32 head vectors or more");
+    TRY(check_counts(a.requests, a.tokens, a.max_q, a.max_len, a.q_heads, layer->H, layer->T));
+    if (a.groups > 65535 || a.max_prefix > kMostTokens)
+        return fail(KV_ERR_INVALID_ARG, "groups %u or max_prefix %u too large", a.groups, a.max_prefix);
+    if (selected && (c.budget == 0 || c.budget > (1u << 24)))
+        return fail(KV_ERR_INVALID_ARG, "budget %u is not in 1..2^24", c.budget);
+    TRY(scales(a.format, a.k_scale, a.v_scale));
+    const float scale = a.scale * (a.format == KV_CACHE_E4M3 ? a.k_scale : 1.0f) * 1.44269504088896340736f;
+    if (!std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale (with k_scale) is not finite");
+    *plan = PagePlan{};
+    if (!empty_call(a))
+        *plan = plan_pages(a.requests, a.tokens, a.max_q, a.max_len, a.groups, std::min(a.max_group, a.tokens), a.max_prefix, c.budget,
+                           layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms);
+    return KV_OK;
+}
+
+kv_status pages_workspace(kv_pool pool, const PagesCall &c, bool selected, uint64_t *out) {
+    VecPool p;
+    TRY((kv_status)vec_enter_pool(pool, c.a.layer, &p));
+    PoolLayer layer;
+    PagePlan plan;
+    TRY(check_pages(c, selected, p, &layer, &plan));
+    *out = plan.bytes;
+    return KV_OK;
+}
+
+void at_workspace(PageEngine *e, void *workspace) {
+    const uint64_t w = (uint64_t)(uintptr_t)workspace;
+    e->part_o = (float *)((uint64_t)(uintptr_t)e->part_o + w);
+    e->part_ml = (float *)((uint64_t)(uintptr_t)e->part_ml + w);
+    e->seg_tiles = (uint64_t *)((uint64_t)(uintptr_t)e->seg_tiles + w);
+    e->seg_units = (uint64_t *)((uint64_t)(uintptr_t)e->seg_units + w);
+}
+
+kv_status attend_pages(kv_pool pool, const PagesCall &c, bool selected, void *stream) {
+    const kv_attend_shared_args &a = c.a;
+    VecPool p;
+    TRY((kv_status)vec_enter_pool(pool, a.layer, &p));
+    PageAttendArgs k{};
+    PagePlan plan;
+    TRY(check_pages(c, selected, p, &k.pool, &plan));
+    if (empty_call(a)) return KV_OK;
+    TRY(check_vecs(a.q, "q"));
+    TRY(check_vecs(a.out, "out"));
+    if (a.q_start == nullptr || a.lens == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "q_start or lens is NULL");
+    TRY(check_table(a.pages, a.pages_stride, a.requests, a.max_len, k.pool.T, "pages"));
+    if (a.groups != 0) {
+        if (a.group_start == nullptr || a.prefix_lens == nullptr)
+            return fail(KV_ERR_INVALID_ARG, "group_start or prefix_lens is NULL");
+        TRY(check_table(a.prefix_pages, a.prefix_stride, a.groups, a.max_prefix, k.pool.T, "prefix_pages"));
+    }
+    if (selected && c.picks == nullptr) return fail(KV_ERR_INVALID_ARG, "picks is NULL");
+    const void *words[] = {a.q_start, a.lens, a.pages, a.lse, a.status, a.group_start, a.prefix_lens, a.prefix_pages, c.picks};
+    for (const void *w : words)
+        if ((uintptr_t)w % 4 != 0)
+            return fail(KV_ERR_ALIGNMENT, "arrays of 32-bit words must be 4-byte aligned (%p is not)", w);
+    TRY(check_space(a.workspace, a.workspace_bytes, plan.bytes));
+    TRY(on_device(a.q.data, "q", p.device));
+    TRY(on_device(a.out.data, "out", p.device));
+    TRY(on_device(a.q_start, "q_start", p.device));
+    TRY(on_device(a.lens, "lens", p.device));
+    if (a.pages != nullptr) TRY(on_device(a.pages, "pages", p.device));
+    if (a.lse != nullptr) TRY(on_device(a.lse, "lse", p.device));
+    if (a.status != nullptr) TRY(on_device(a.status, "status", p.device));
+    if (selected) TRY(on_device(c.picks, "picks", p.device));
+    if (a.groups != 0) {
+        TRY(on_device(a.group_start, "group_start", p.device));
+        TRY(on_device(a.prefix_lens, "prefix_lens", p.device));
+        if (a.prefix_pages != nullptr) TRY(on_device(a.prefix_pages, "prefix_pages", p.device));
+    }
+    if (plan.bytes != 0) TRY(on_device(a.workspace, "workspace", p.device));
+    Guard guard(p.device);
+    vec_begin(p.device, stream);
+    k.q = vecs(a.q);
+    k.out = vecs(a.out);
+    k.lse = a.lse;
+    k.q_start = a.q_start;
+    k.lens = a.lens;
+    k.pages = a.pages;
+    k.pages_stride = a.pages_stride;
+    k.group_start = a.group_start;
+    k.prefix_lens = a.prefix_lens;
+    k.prefix_pages = a.prefix_pages;
+    k.prefix_stride = a.prefix_stride;
+    k.picks = c.picks;
+    k.budget = c.budget;
+    k.status = a.status;
+    k.requests = a.requests;
+    k.tokens = a.tokens;
+    k.max_q = a.max_q;
+    k.max_len = a.max_len;
+    k.groups = a.groups;
+    k.max_group = std::min(a.max_group, a.tokens);
+    k.max_prefix = a.max_prefix;
+    k.q_heads = a.q_heads;
+    k.group = a.q_heads / k.pool.H;
+    const bool fp8 = a.format == KV_CACHE_E4M3;
+    k.scale_log2 = a.scale * (fp8 ? a.k_scale : 1.0f) * 1.44269504088896340736f;
+    k.v_scale = fp8 ? a.v_scale : 1.0f;
+    k.rows = plan.rows;
+    k.tc = plan.tc;
+    at_workspace(&k.rows, a.workspace);
+    at_workspace(&k.tc, a.workspace);
+    int launches = 0;
+    const cudaError_t e = launch_pages(k, plan, a.head_dim, fp8, a.dtype == KV_FP16, p.pdl, (cudaStream_t)stream,
+                                       &launches);
+    vec_count(launches);
+    if (e != cudaSuccess) return (kv_status)vec_cuda_error(e, "launch of the attention kernels");
+    return KV_OK;
+}
+
+kv_status check_select(const kv_select_args *a, const VecPool &p, SelectArgs *k, uint64_t *need) {
+    TRY(check_dim(a->head_dim, a->dtype));
+    if (a->reserved[0] != 0 || a->reserved[1] != 0)
+        return fail(KV_ERR_INVALID_ARG, "reserved members must be 0");
+    TRY(check_wide_dim(a->head_dim, "selection"));
+    const kv_layout &l = p.layout;
+    TRY(check_counts(a->requests, a->tokens, a->max_q, a->max_len, a->q_heads, l.num_heads, l.page_tokens));
+    if (a->budget == 0 || a->budget > (1u << 24))
+        return fail(KV_ERR_INVALID_ARG, "budget %u is not in 1..2^24", a->budget);
+    if (a->keep_first > a->budget || a->keep_last > a->budget - a->keep_first)
+        return fail(KV_ERR_INVALID_ARG, "keep_first %u and keep_last %u are more than the budget of %u", a->keep_first,
+                    a->keep_last, a->budget);
+    k->T = l.page_tokens;
+    k->P = l.num_pages;
+    k->H = l.num_heads;
+    k->max_pages = (a->max_len + l.page_tokens - 1) / l.page_tokens;
+    const uint64_t rows = (uint64_t)a->tokens * l.num_heads;
+    k->block_pages = select_block_pages(rows * k->max_pages, p.sms);
+    const uint64_t chunks = (k->max_pages + k->block_pages - 1) / k->block_pages;
+    if (chunks * l.num_heads > 0x7fffffffull)
+        return fail(KV_ERR_INVALID_ARG, "max_len %u makes too many blocks", a->max_len);
+    *need = k->max_pages > a->budget ? rows * k->max_pages * sizeof(float) : 0;
     return KV_OK;
 }
 
@@ -515,6 +752,141 @@ kv_status kv_attend(kv_pool pool, const kv_attend_args *a, void *stream) {
                                         (cudaStream_t)stream, &launches);
     vec_count(launches);
     if (e != cudaSuccess) return (kv_status)vec_cuda_error(e, "launch of the attention kernel");
+    return KV_OK;
+}
+
+kv_status kv_attend_shared_workspace(kv_pool pool, const kv_attend_shared_args *a, uint64_t *out) {
+    if (a == nullptr || out == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "argument block or output pointer is NULL");
+    return pages_workspace(pool, shared_call(a), false, out);
+}
+
+kv_status kv_attend_shared(kv_pool pool, const kv_attend_shared_args *a, void *stream) {
+    if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
+    return attend_pages(pool, shared_call(a), false, stream);
+}
+
+kv_status kv_attend_selected_workspace(kv_pool pool, const kv_attend_selected_args *a, uint64_t *out) {
+    if (a == nullptr || out == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "argument block or output pointer is NULL");
+    return pages_workspace(pool, selected_call(a), true, out);
+}
+
+kv_status kv_attend_selected(kv_pool pool, const kv_attend_selected_args *a, void *stream) {
+    if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
+    return attend_pages(pool, selected_call(a), true, stream);
+}
+
+kv_status kv_bound_bytes(uint32_t head_dim, uint32_t *out) {
+    if (out == nullptr) return fail(KV_ERR_INVALID_ARG, "output pointer is NULL");
+    TRY(check_wide_dim(head_dim, "kv_bound"));
+    *out = record_bytes(head_dim);
+    return KV_OK;
+}
+
+kv_status kv_bound(kv_pool pool, const kv_bound_args *a, void *stream) {
+    if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
+    VecPool p;
+    TRY((kv_status)vec_enter_pool(pool, a->layer, &p));
+    TRY(check_dim(a->head_dim, a->dtype));
+    if (a->reserved != 0) return fail(KV_ERR_INVALID_ARG, "reserved members must be 0");
+    TRY(check_wide_dim(a->head_dim, "kv_bound"));
+    if (a->format != KV_CACHE_SAME && a->format != KV_CACHE_E4M3)
+        return fail(KV_ERR_INVALID_ARG, "format %u: SAME and E4M3 pages are taken", a->format);
+    BoundArgs k{};
+    TRY(pool_layer(p, a->format, a->head_dim, &k.pool));
+    if (k.pool.T > (1u << 20)) return fail(KV_ERR_LAYOUT, "pages of %u tokens: 2^20 at most", k.pool.T);
+    if (a->requests > 65535 || a->max_len > kMostTokens || a->max_new > a->max_len)
+        return fail(KV_ERR_INVALID_ARG, "requests %u, max_len %u or max_new %u too large", a->requests, a->max_len,
+                    a->max_new);
+    if (a->requests == 0 || a->max_new == 0) return KV_OK;
+    if (a->bounds == nullptr || a->lens == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "bounds or lens is NULL");
+    TRY(check_table(a->pages, a->pages_stride, a->requests, a->max_len, k.pool.T, "pages"));
+    if ((uintptr_t)a->bounds % 16 != 0 || (uintptr_t)a->lens % 4 != 0 || (uintptr_t)a->first % 4 != 0 ||
+        (uintptr_t)a->pages % 4 != 0 || (uintptr_t)a->status % 4 != 0)
+        return fail(KV_ERR_ALIGNMENT, "bounds must be 16-byte, lens, first, pages and status 4-byte aligned");
+    TRY(on_device(a->bounds, "bounds", p.device));
+    TRY(on_device(a->lens, "lens", p.device));
+    if (a->first != nullptr) TRY(on_device(a->first, "first", p.device));
+    TRY(on_device(a->pages, "pages", p.device));
+    if (a->status != nullptr) TRY(on_device(a->status, "status", p.device));
+    Guard guard(p.device);
+    vec_begin(p.device, stream);
+    k.bounds = (uint8_t *)a->bounds;
+    k.lens = a->lens;
+    k.first = a->first;
+    k.pages = a->pages;
+    k.pages_stride = a->pages_stride;
+    k.status = a->status;
+    k.requests = a->requests;
+    k.max_len = a->max_len;
+    k.max_new = a->max_new;
+    k.most_pages = (a->max_new - 1 + k.pool.T - 1) / k.pool.T + 1;
+    const cudaError_t e = launch_bound(k, a->head_dim, a->format == KV_CACHE_E4M3, a->dtype == KV_FP16, p.pdl, p.sms,
+                                       (cudaStream_t)stream);
+    if (e != cudaSuccess) return (kv_status)vec_cuda_error(e, "launch of the bounds kernel");
+    vec_count(1);
+    return KV_OK;
+}
+
+kv_status kv_select_workspace(kv_pool pool, const kv_select_args *a, uint64_t *out) {
+    if (a == nullptr || out == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "argument block or output pointer is NULL");
+    VecPool p;
+    TRY((kv_status)vec_enter_pool(pool, 0, &p));
+    SelectArgs k{};
+    return check_select(a, p, &k, out);
+}
+
+kv_status kv_select(kv_pool pool, const kv_select_args *a, void *stream) {
+    if (a == nullptr) return fail(KV_ERR_INVALID_ARG, "argument block is NULL");
+    VecPool p;
+    TRY((kv_status)vec_enter_pool(pool, 0, &p));
+    SelectArgs k{};
+    uint64_t need = 0;
+    TRY(check_select(a, p, &k, &need));
+    if (a->requests == 0 || a->tokens == 0 || a->max_q == 0) return KV_OK;
+    TRY(check_vecs(a->q, "q"));
+    if (a->q_start == nullptr || a->lens == nullptr || a->picks == nullptr || a->bounds == nullptr)
+        return fail(KV_ERR_INVALID_ARG, "q_start, lens, picks or bounds is NULL");
+    TRY(check_table(a->pages, a->pages_stride, a->requests, a->max_len, k.T, "pages"));
+    if ((uintptr_t)a->bounds % 16 != 0 || (uintptr_t)a->q_start % 4 != 0 || (uintptr_t)a->lens % 4 != 0 ||
+        (uintptr_t)a->pages % 4 != 0 || (uintptr_t)a->picks % 4 != 0 || (uintptr_t)a->status % 4 != 0)
+        return fail(KV_ERR_ALIGNMENT, "bounds must be 16-byte, q_start, lens, pages, picks and status 4-byte aligned");
+    TRY(check_space(a->workspace, a->workspace_bytes, need));
+    TRY(on_device(a->bounds, "bounds", p.device));
+    TRY(on_device(a->q.data, "q", p.device));
+    TRY(on_device(a->q_start, "q_start", p.device));
+    TRY(on_device(a->lens, "lens", p.device));
+    if (a->pages != nullptr) TRY(on_device(a->pages, "pages", p.device));
+    TRY(on_device(a->picks, "picks", p.device));
+    if (a->status != nullptr) TRY(on_device(a->status, "status", p.device));
+    if (need != 0) TRY(on_device(a->workspace, "workspace", p.device));
+    Guard guard(p.device);
+    vec_begin(p.device, stream);
+    k.bounds = (const uint8_t *)a->bounds;
+    k.q = vecs(a->q);
+    k.q_start = a->q_start;
+    k.lens = a->lens;
+    k.pages = a->pages;
+    k.pages_stride = a->pages_stride;
+    k.picks = a->picks;
+    k.scores = (float *)a->workspace;
+    k.status = a->status;
+    k.requests = a->requests;
+    k.tokens = a->tokens;
+    k.max_q = a->max_q;
+    k.max_len = a->max_len;
+    k.q_heads = a->q_heads;
+    k.group = a->q_heads / k.H;
+    k.budget = a->budget;
+    k.keep_first = a->keep_first;
+    k.keep_last = a->keep_last;
+    int launches = 0;
+    const cudaError_t e = launch_select(k, a->head_dim, a->dtype == KV_FP16, p.pdl, (cudaStream_t)stream, &launches);
+    vec_count(launches);
+    if (e != cudaSuccess) return (kv_status)vec_cuda_error(e, "launch of the selection kernels");
     return KV_OK;
 }
 

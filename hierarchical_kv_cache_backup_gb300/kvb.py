@@ -64,7 +64,9 @@ EXPORTS = ("kv_pool_register", "kv_pool_register_split", "kv_pool_export", "kv_p
            "kv_ring_device_stop", "kv_ring_ready_set", "kv_ring_ready_stream_set",
            "kv_fault_inject", "kv_l3_open", "kv_l3_close",
            "kv_l3_put", "kv_l3_get", "kv_cache_head_bytes", "kv_rotary_create", "kv_rotary_close",
-           "kv_rotate", "kv_append", "kv_fetch", "kv_attend", "kv_attend_workspace")
+           "kv_rotate", "kv_append", "kv_fetch", "kv_attend", "kv_attend_workspace",
+           "kv_attend_shared", "kv_attend_shared_workspace", "kv_bound", "kv_bound_bytes", "kv_select",
+           "kv_select_workspace", "kv_attend_selected", "kv_attend_selected_workspace")
 
 
 class KvError(RuntimeError):
@@ -164,6 +166,61 @@ class kv_attend_args(ctypes.Structure):
                 ("reserved", ctypes.c_uint32 * 2)]
 
 
+class kv_attend_shared_args(ctypes.Structure):
+    _fields_ = [("q", kv_vecs), ("out", kv_vecs), ("lse", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("group_start", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("prefix_pages", ctypes.c_void_p), ("prefix_stride", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("status", ctypes.c_void_p), ("requests", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint32), ("max_q", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("groups", ctypes.c_uint32),
+                ("max_group", ctypes.c_uint32), ("max_prefix", ctypes.c_uint32),
+                ("q_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("dtype", ctypes.c_uint32), ("format", ctypes.c_uint32), ("layer", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
+class kv_bound_args(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("status", ctypes.c_void_p), ("requests", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("max_new", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("format", ctypes.c_uint32), ("layer", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+class kv_select_args(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("q", kv_vecs), ("q_start", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("pages_stride", ctypes.c_int64), ("picks", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("status", ctypes.c_void_p), ("requests", ctypes.c_uint32),
+                ("tokens", ctypes.c_uint32), ("max_q", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("budget", ctypes.c_uint32), ("keep_first", ctypes.c_uint32),
+                ("keep_last", ctypes.c_uint32), ("reserved", ctypes.c_uint32 * 2)]
+
+
+class kv_attend_selected_args(ctypes.Structure):
+    _fields_ = [("q", kv_vecs), ("out", kv_vecs), ("lse", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("pages_stride", ctypes.c_int64),
+                ("picks", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_uint64), ("status", ctypes.c_void_p),
+                ("requests", ctypes.c_uint32), ("tokens", ctypes.c_uint32),
+                ("max_q", ctypes.c_uint32), ("max_len", ctypes.c_uint32),
+                ("budget", ctypes.c_uint32), ("q_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32),
+                ("format", ctypes.c_uint32), ("layer", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build the CUDA library first "
@@ -229,6 +286,14 @@ def _load():
         "kv_fetch": (st, [vp, P(kv_fetch_args), vp]),
         "kv_attend": (st, [vp, P(kv_attend_args), vp]),
         "kv_attend_workspace": (st, [vp, P(kv_attend_args), P(u64)]),
+        "kv_attend_shared": (st, [vp, P(kv_attend_shared_args), vp]),
+        "kv_attend_shared_workspace": (st, [vp, P(kv_attend_shared_args), P(u64)]),
+        "kv_bound": (st, [vp, P(kv_bound_args), vp]),
+        "kv_bound_bytes": (st, [u32, P(u32)]),
+        "kv_select": (st, [vp, P(kv_select_args), vp]),
+        "kv_select_workspace": (st, [vp, P(kv_select_args), P(u64)]),
+        "kv_attend_selected": (st, [vp, P(kv_attend_selected_args), vp]),
+        "kv_attend_selected_workspace": (st, [vp, P(kv_attend_selected_args), P(u64)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -819,6 +884,107 @@ def kv_attend_workspace(pool: int, args: kv_attend_args) -> int:
 def kv_attend(pool: int, args: kv_attend_args, stream=None) -> None:
     """Attention of new tokens over one layer of a 4-bit pool."""
     _check(_lib.kv_attend(pool, args, stream))
+
+
+def make_attend_shared_args(q: kv_vecs, out: kv_vecs, *, q_start: int, lens: int, pages: int | None,
+                            pages_stride: int, requests: int, tokens: int, max_q: int, max_len: int,
+                            q_heads: int, head_dim: int, dtype: int, format: int, layer: int,
+                            scale: float, k_scale: float = 1.0, v_scale: float = 1.0,
+                            groups: int = 0, group_start: int | None = None,
+                            prefix_lens: int | None = None, prefix_pages: int | None = None,
+                            prefix_stride: int = 0, max_group: int = 0, max_prefix: int = 0,
+                            lse: int | None = None, workspace: int | None = None,
+                            workspace_bytes: int = 0,
+                            status: int | None = None) -> kv_attend_shared_args:
+    """The argument block of kv_attend_shared; kv_attend_shared_workspace says how much workspace
+    it needs."""
+    return kv_attend_shared_args(q, out, lse, q_start, lens, pages, pages_stride, group_start,
+                                 prefix_lens, prefix_pages, prefix_stride, workspace,
+                                 workspace_bytes, status, requests, tokens, max_q, max_len, groups,
+                                 max_group, max_prefix, q_heads, head_dim, dtype, format, layer,
+                                 scale, k_scale, v_scale, 0)
+
+
+def kv_attend_shared_workspace(pool: int, args: kv_attend_shared_args) -> int:
+    """Bytes of device workspace that kv_attend_shared needs for this block (0: none)."""
+    out = ctypes.c_uint64()
+    _check(_lib.kv_attend_shared_workspace(pool, args, ctypes.byref(out)))
+    return out.value
+
+
+def kv_attend_shared(pool: int, args: kv_attend_shared_args, stream=None) -> None:
+    """Attention over one layer of a 16-bit or fp8 pool, for requests whose groups share prefixes."""
+    _check(_lib.kv_attend_shared(pool, args, stream))
+
+
+def kv_bound_bytes(head_dim: int) -> int:
+    """Bytes of the bounds of one page and KV head (a buffer of kv_bound holds P x H of them)."""
+    out = ctypes.c_uint32()
+    _check(_lib.kv_bound_bytes(head_dim, ctypes.byref(out)))
+    return out.value
+
+
+def make_bound_args(bounds: int, *, lens: int, pages: int, pages_stride: int, requests: int,
+                    max_len: int, max_new: int, head_dim: int, dtype: int, format: int, layer: int,
+                    first: int | None = None, status: int | None = None) -> kv_bound_args:
+    """The argument block of kv_bound."""
+    return kv_bound_args(bounds, lens, first, pages, pages_stride, status, requests, max_len,
+                         max_new, head_dim, dtype, format, layer, 0)
+
+
+def kv_bound(pool: int, args: kv_bound_args, stream=None) -> None:
+    """Bounds of the keys of the pages that hold new tokens."""
+    _check(_lib.kv_bound(pool, args, stream))
+
+
+def make_select_args(bounds: int, q: kv_vecs, picks: int, *, q_start: int, lens: int,
+                     pages: int | None, pages_stride: int, requests: int, tokens: int, max_q: int,
+                     max_len: int, q_heads: int, head_dim: int, dtype: int, budget: int,
+                     keep_first: int = 0, keep_last: int = 0, workspace: int | None = None,
+                     workspace_bytes: int = 0, status: int | None = None) -> kv_select_args:
+    """The argument block of kv_select; kv_select_workspace says how much workspace it needs."""
+    return kv_select_args(bounds, q, q_start, lens, pages, pages_stride, picks, workspace,
+                          workspace_bytes, status, requests, tokens, max_q, max_len, q_heads,
+                          head_dim, dtype, budget, keep_first, keep_last)
+
+
+def kv_select_workspace(pool: int, args: kv_select_args) -> int:
+    """Bytes of device workspace that kv_select needs for this block (0: none)."""
+    out = ctypes.c_uint64()
+    _check(_lib.kv_select_workspace(pool, args, ctypes.byref(out)))
+    return out.value
+
+
+def kv_select(pool: int, args: kv_select_args, stream=None) -> None:
+    """The pages whose bounds promise each query most."""
+    _check(_lib.kv_select(pool, args, stream))
+
+
+def make_attend_selected_args(q: kv_vecs, out: kv_vecs, *, q_start: int, lens: int,
+                              pages: int | None, pages_stride: int, picks: int, budget: int,
+                              requests: int, tokens: int, max_q: int, max_len: int, q_heads: int,
+                              head_dim: int, dtype: int, format: int, layer: int, scale: float,
+                              k_scale: float = 1.0, v_scale: float = 1.0, lse: int | None = None,
+                              workspace: int | None = None, workspace_bytes: int = 0,
+                              status: int | None = None) -> kv_attend_selected_args:
+    """The argument block of kv_attend_selected; kv_attend_selected_workspace says how much
+    workspace it needs."""
+    return kv_attend_selected_args(q, out, lse, q_start, lens, pages, pages_stride, picks,
+                                   workspace, workspace_bytes, status, requests, tokens, max_q,
+                                   max_len, budget, q_heads, head_dim, dtype, format, layer, scale,
+                                   k_scale, v_scale, 0)
+
+
+def kv_attend_selected_workspace(pool: int, args: kv_attend_selected_args) -> int:
+    """Bytes of device workspace that kv_attend_selected needs for this block (0: none)."""
+    out = ctypes.c_uint64()
+    _check(_lib.kv_attend_selected_workspace(pool, args, ctypes.byref(out)))
+    return out.value
+
+
+def kv_attend_selected(pool: int, args: kv_attend_selected_args, stream=None) -> None:
+    """Attention of each query over the pages that were selected for it."""
+    _check(_lib.kv_attend_selected(pool, args, stream))
 
 
 def library():

@@ -437,7 +437,9 @@ KVB_API kv_status kv_backup_staged_noalloc(kv_pool pool, kv_host host, const int
  * read the head vectors inside them, as a serving loop does between a restore
  * and a backup: turn queries and keys by their positions (kv_rotate), append
  * keys and values of new tokens to pages (kv_append), read vectors back
- * (kv_fetch), and attend over pages held in 4 bits (kv_attend).
+ * (kv_fetch), attend over pages held in 4 bits (kv_attend), and over pages held in
+ * 16 bits or fp8: requests that share a long prefix (kv_attend_shared), or pages
+ * that a query selects (kv_bound, kv_select, kv_attend_selected).
  *
  * Common rules.  Every call is enqueued on `stream`, ordered by it alone (no
  * fence), allocates nothing and may be captured into a CUDA graph after the
@@ -656,6 +658,170 @@ KVB_API kv_status kv_attend(kv_pool pool, const kv_attend_args *args, void *stre
  * one another on a stream, whatever it held before; calls that may run at the
  * same time need one each.  0: none is needed. */
 KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, uint64_t *out);
+
+/* Attention over pages held in 16 bits (SAME, of the queries' dtype) or in fp8
+ * (E4M3), for requests in groups that share a prefix.  Request r has lens[r]
+ * cached tokens of its own, token t in page pages[r x pages_stride + t / T] (its
+ * new tokens' keys included: append first), and the query tokens q_start[r]..
+ * q_start[r + 1] - 1 of q, the last n = q_start[r + 1] - q_start[r] of its tokens.
+ * Group g is the requests group_start[g]..group_start[g + 1] - 1 (groups in
+ * order, a request in one at most); in front of each one's own tokens stand the
+ * prefix_lens[g] tokens of its pages prefix_pages[g x prefix_stride + t / T], which
+ * are read once for all of the group's queries.  Query i of request r sees its
+ * group's whole prefix and the own tokens t <= lens[r] - n + i.  groups = 0: no
+ * prefixes, attention of each request by itself.  q_heads is a multiple of the
+ * pool's H; query head j reads KV head j / (q_heads / H).  With x_t = scale q . k_t
+ * over the tokens it sees: out = sum exp(x_t) v_t / sum exp(x_t), lse (float32
+ * [tokens][q_heads], NULL: not wanted) = ln sum exp(x_t).  A query that sees
+ * nothing gets out = 0 and lse = -infinity.  k_scale and v_scale: of E4M3 pages.
+ * Scores, softmax statistics and sums are float32.  Rounded to fewer bits are:
+ *   a weight      exp(x_t - largest) to two parts of 8 bits (bf16 pages), to two
+ *                 parts of 11 bits (fp16 outputs), to 11 bits (fp8 pages, bf16
+ *                 outputs); in calls with many rows (more than 16 query rows, tokens x
+ *                 q_heads / H, in a prefix or request) to one part of these.
+ *                 Those under 2^-21 of the query's largest lose bits (not on bf16 pages)
+ *   a query       of bf16 against fp8 pages: values under 2^-22 of the vector's
+ *                 largest
+ * A key or value that is not finite makes outputs of the queries that see it not
+ * finite (a value: of its dim), and no others.
+ * A page id outside the pool inside a length sets BAD_PAGE, and the queries that
+ * see the page get NaN.  lens[r] and prefix_lens[g] are taken as at most max_len
+ * and max_prefix and at least 0; a request whose q_start values are out of order,
+ * outside [0, tokens] or further apart than max_q is left out; a group whose
+ * requests are out of order or outside [0, requests], or hold more than max_group
+ * query tokens, has no prefix.  All of these set BAD_LENGTH.  Requests that share query
+ * tokens may make all of the call be left out (BAD_LENGTH).
+ * A row of a page table holds ceil(max_len / T) (ceil(max_prefix / T)) entries that
+ * may be read.  q and out hold `tokens` vectors.  head_dim: 64, 96, 128, 192 or
+ * 256; fewer than 2^32 head vectors between the layer's first and the pool's
+ * last; T at most 2^20 (LAYOUT otherwise).  Errors: as kv_attend. */
+typedef struct {
+    kv_vecs q, out;
+    float *lse;
+    const int32_t *q_start;      /* requests + 1                                  */
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;        /* entries between the rows of the page table    */
+    const int32_t *group_start;  /* groups + 1                                    */
+    const int32_t *prefix_lens;
+    const int32_t *prefix_pages;
+    int64_t prefix_stride;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint32_t *status;
+    uint32_t requests;           /* at most 65535                                 */
+    uint32_t tokens;             /* query tokens of all requests                  */
+    uint32_t max_q;              /* the most of one request                       */
+    uint32_t max_len;            /* the most own tokens, 0..2^29                  */
+    uint32_t groups;             /* at most 65535                                 */
+    uint32_t max_group;          /* the most query tokens of one group            */
+    uint32_t max_prefix;         /* the longest prefix, 0..2^29                   */
+    uint32_t q_heads, head_dim, dtype, format, layer;
+    float scale;                 /* finite                                        */
+    float k_scale, v_scale;      /* E4M3: finite, > 0, with a finite inverse      */
+    uint32_t reserved;
+} kv_attend_shared_args;
+KVB_API kv_status kv_attend_shared(kv_pool pool, const kv_attend_shared_args *args, void *stream);
+/* As kv_attend_workspace. */
+KVB_API kv_status kv_attend_shared_workspace(kv_pool pool, const kv_attend_shared_args *args,
+                                             uint64_t *out);
+
+/* Bounds of the keys of pages, by which kv_select chooses.  bounds[page x H + h]
+ * is a record of kv_bound_bytes(head_dim) bytes (16-B aligned, one buffer a
+ * layer, P x H records): for each dim the least and the largest value that the
+ * page's keys of KV head h hold, in units of a step for each 32 dims.  With m the
+ * largest magnitude of the group's 64 bounds, its step s is the least power of two
+ * with m <= 127 s; a record holds head_dim codes floor(least / s) (int8), head_dim
+ * codes ceil(largest / s), head_dim / 32 steps (float32) and zeros.  m < 2^-100: s
+ * and codes 0; a value that is not finite: s = infinity, codes 0.  E4M3 keys are
+ * taken before their scale.  The call writes the records of all pages that hold one of the tokens
+ * first[r]..lens[r] - 1 of a request (first = NULL: 0), each over all of the page's tokens below
+ * lens[r]; no other byte changes.  A page that two requests name holds the same tokens for
+ * both, or its record is one of the two.
+ * A request with lens[r] outside [0, max_len], first[r] outside [0, lens[r]] or more than
+ * max_new tokens between them is left out (BAD_LENGTH); so is a page outside the pool (BAD_PAGE).
+ * head_dim: 64, 96, 128, 192 or 256.  Errors: as kv_append. */
+typedef struct {
+    void *bounds;
+    const int32_t *lens;
+    const int32_t *first;
+    const int32_t *pages;
+    int64_t pages_stride;
+    uint32_t *status;
+    uint32_t requests;           /* at most 65535                                 */
+    uint32_t max_len;            /* 0..2^29                                       */
+    uint32_t max_new;            /* the most tokens of lens[r] - first[r]         */
+    uint32_t head_dim, dtype, format, layer;
+    uint32_t reserved;
+} kv_bound_args;
+KVB_API kv_status kv_bound(kv_pool pool, const kv_bound_args *args, void *stream);
+/* Errors: INVALID_ARG (NULL), LAYOUT (head_dim). */
+KVB_API kv_status kv_bound_bytes(uint32_t head_dim, uint32_t *out);
+
+/* Selects, for each query token and KV head, the pages (as indices into the
+ * request's row of the page table, ascending) whose keys promise it most: picks
+ * [tokens][H][budget], -1 behind the last.  A query at position p = lens[r] - n + i
+ * sees the pages 0..p / T.  Up to `budget` of them are all picked; of more, the first
+ * keep_first, the last keep_last and those of the largest scores, ties to the lowest index.
+ * A page's score for a query head: the head's values are codes too, round(q / t) with
+ * t the step as above of their 32, ties to even; with b the code of the largest where the
+ * query's is positive and of the least where it is negative, a group's term is (sum of
+ * code x b) x (s x t), and the score the sum of the terms in the order of the groups,
+ * each product and sum rounded in float32; one that is not finite counts as
+ * the largest float32.  The score for a KV head is the largest of its query heads'.
+ * A page id outside the pool sets BAD_PAGE and is picked last.  Requests are checked as
+ * by kv_attend_shared (BAD_LENGTH; what is left out has its picks left as they were, and so
+ * has a request whose length is outside [0, max_len]).  The
+ * bounds of every page that is seen must be those of its keys.  Errors: as kv_attend. */
+typedef struct {
+    const void *bounds;
+    kv_vecs q;
+    const int32_t *q_start;      /* requests + 1                                  */
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;
+    int32_t *picks;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint32_t *status;
+    uint32_t requests, tokens, max_q, max_len;
+    uint32_t q_heads, head_dim, dtype;
+    uint32_t budget;             /* 1..2^24                                       */
+    uint32_t keep_first, keep_last;   /* together at most the budget              */
+    uint32_t reserved[2];
+} kv_select_args;
+KVB_API kv_status kv_select(kv_pool pool, const kv_select_args *args, void *stream);
+/* As kv_attend_workspace. */
+KVB_API kv_status kv_select_workspace(kv_pool pool, const kv_select_args *args, uint64_t *out);
+
+/* Attention over selected pages: as kv_attend_shared without groups, but query i of
+ * request r sees, for KV head h, the tokens t <= lens[r] - n + i of those pages alone whose
+ * indices stand in its picks[token][h][0..budget).  An entry of -1 is skipped; one outside
+ * [-1, pages that the query sees) is too and sets BAD_PAGE.  Of a list, as many entries
+ * are looked at as the request has pages.  An index that stands twice counts twice.
+ * Weights are rounded as in calls with few rows.  Errors: as kv_attend. */
+typedef struct {
+    kv_vecs q, out;
+    float *lse;
+    const int32_t *q_start;      /* requests + 1                                  */
+    const int32_t *lens;
+    const int32_t *pages;
+    int64_t pages_stride;
+    const int32_t *picks;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint32_t *status;
+    uint32_t requests, tokens, max_q, max_len;
+    uint32_t budget;             /* 1..2^24                                       */
+    uint32_t q_heads, head_dim, dtype, format, layer;
+    float scale, k_scale, v_scale;
+    uint32_t reserved;
+} kv_attend_selected_args;
+KVB_API kv_status kv_attend_selected(kv_pool pool, const kv_attend_selected_args *args,
+                                     void *stream);
+/* As kv_attend_workspace. */
+KVB_API kv_status kv_attend_selected_workspace(kv_pool pool, const kv_attend_selected_args *args,
+                                               uint64_t *out);
 
 /* Host-side validation of an operation without a GPU (kind 0 = backup with
  * a = src pages, b = slots; kind 1 = restore with a = slots, b = dst pages).

@@ -1,0 +1,200 @@
+"""Attention over 16-bit and fp8 pages, bounds and selection without a GPU: how a call's work is
+cut and joined, compiled for the host, and refusals that need no device."""
+import ctypes
+import random
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+from hierarchical_kv_cache_backup_gb300 import build as kbuild
+
+kbuild.build_library()
+
+HARNESS = r"""
+#include <map>
+#include <vector>
+#include "kvb_pages.h"
+using namespace kvb;
+// Cuts a call among workers and takes every row's pieces back together.  Returns 0, or the number of
+// the check that failed.  in: requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group,
+// T, budget, row_tile, kv_tile, workers, prefix, own; units: room in the workspace.
+extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const int *group_start, const int *prefix_lens,
+                     unsigned long long units, unsigned long long *total) {
+    PageAttendArgs a{};
+    a.q_start = q_start; a.lens = lens; a.group_start = group_start; a.prefix_lens = prefix_lens;
+    a.requests = in[0]; a.tokens = in[1]; a.max_q = in[2]; a.max_len = in[3]; a.groups = in[4]; a.max_group = in[5];
+    a.max_prefix = in[6]; a.pool.H = in[7]; a.group = in[8]; a.pool.T = in[9]; a.budget = in[10];
+    int picked = 0;
+    a.picks = in[10] ? &picked : nullptr;
+    PageEngine &e = a.rows;
+    e.row_tile = in[11]; e.kv_tile = in[12]; e.workers = in[13]; e.prefix = in[14]; e.own = in[15];
+    const uint32_t n = seg_count(a, e);
+    std::vector<uint64_t> st(n + 1), su(n + 1);
+    uint64_t t = 0, u = 0;
+    for (uint32_t s = 0; s < n; ++s) {
+        st[s] = t; su[s] = u;
+        const PageSeg g = seg_at(a, e, s);
+        const uint64_t x = seg_tiles(a, e, g);
+        t += x;
+        if (x) u += (uint64_t)row_tiles(a, e, g) * a.pool.H;
+    }
+    st[n] = t; su[n] = u;
+    e.seg_tiles = st.data(); e.seg_units = su.data();
+    *total = t;
+    if (u > units) return 1;
+    const uint64_t share = share_of(t, e.workers);
+    std::map<uint64_t, PagePiece> slots;
+    uint64_t done = 0;
+    for (uint32_t w = 0; w < e.workers; ++w) {
+        uint64_t x = w * share, x1 = x + share < t ? x + share : t;
+        if (x >= x1) continue;
+        PageCursor c{};
+        for (uint32_t s = 0; s < n; ++s) if (x >= st[s] && x < st[s + 1]) c = PageCursor{st[s], su[s], s};
+        while (x < x1) {
+            const PagePiece p = piece_at(a, e, &c, x, x1, w);
+            if (p.k1 <= p.k0 || p.k1 > p.n_tiles || p.head >= (int)a.pool.H || p.rt >= row_tiles(a, e, p.s)) return 2;
+            if ((uint64_t)(p.n_tiles - 1) * e.kv_tile >= (uint64_t)seen_tokens(a, e, p.s, p.rt)) return 3;
+            if (p.slot >= units + e.workers || !slots.emplace(p.slot, p).second) return 4;
+            done += p.k1 - p.k0;
+            x += p.k1 - p.k0;
+        }
+    }
+    if (done != t) return 5;
+    for (uint32_t s = 0; s < n; ++s) {
+        const PageSeg g = seg_at(a, e, s);
+        if (g.len == 0) continue;
+        for (int i = 0; i < g.n; ++i)
+            for (uint32_t h = 0; h < a.pool.H; ++h)
+                for (uint32_t j = 0; j < a.group; ++j) {
+                    const RowPieces r = row_pieces(a, e, g, s, i, h, j);
+                    int at = 0;
+                    if (r.any)
+                        for (uint64_t w = r.w0; w <= r.w1; ++w) {
+                            auto f = slots.find(r.unit + w);
+                            if (f == slots.end()) return 6;
+                            const PagePiece &p = f->second;
+                            if (p.s.prefix != g.prefix || p.s.index != g.index || p.head != (int)h || p.k0 != at) return 7;
+                            const int per = (int)((a.group + e.row_tile - 1) / e.row_tile);
+                            const int row = a.picks ? p.rt % per * (int)e.row_tile + r.row : p.rt * (int)e.row_tile + r.row;
+                            if (a.picks ? p.rt / per != i || row != (int)j : row != i * (int)a.group + (int)j) return 8;
+                            at = p.k1;
+                            if (w == r.w1 && at != p.n_tiles) return 9;
+                        }
+                    // all that the row sees is in its pieces
+                    const int sees = g.prefix ? g.len : a.picks ? 0 : g.len - g.n + i + 1;
+                    if ((int64_t)at * e.kv_tile < sees) return 10;
+                }
+    }
+    return 0;
+}
+extern "C" int h_group(const int *in, const int *q_start, const int *group_start, const int *prefix_lens, int r, int q0, int n) {
+    PageAttendArgs a{};
+    a.q_start = q_start; a.group_start = group_start; a.prefix_lens = prefix_lens;
+    a.requests = in[0]; a.tokens = in[1]; a.groups = in[2]; a.max_group = in[3]; a.max_prefix = in[4];
+    return group_of(a, r, q0, n);
+}
+extern "C" float h_step(unsigned bits, float *inv) { return bound_step(bits, inv); }
+"""
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    cc = shutil.which("g++")
+    if cc is None:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("pages")
+    (d / "h.cpp").write_text(HARNESS)
+    subprocess.run([cc, "-O1", "-std=c++17", "-shared", "-fPIC", "-I", kbuild.CSRC, str(d / "h.cpp"), "-o", str(d / "h.so")],
+                   check=True)
+    lib = ctypes.CDLL(str(d / "h.so"))
+    lib.h_step.restype = ctypes.c_float
+    lib.h_cut.argtypes = [ctypes.c_void_p] * 5 + [ctypes.c_uint64, ctypes.c_void_p]
+    return lib
+
+
+def i32(x):
+    return np.ascontiguousarray(x, dtype=np.int32)
+
+
+def most_units(segs, tokens, most, group, row_tile, picked):
+    """The room that the workspace has, as the library counts it."""
+    if picked:
+        return tokens * -(-group // row_tile)
+    return min(segs * -(-most * group // row_tile), tokens * group // row_tile + segs)
+
+
+def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, budget, row_tile, kv_tile, workers, prefix, own):
+    n_q = [rng.choice((0, 1, max_q, rng.randint(0, max_q))) for _ in range(requests)]
+    q_start = np.cumsum([0] + n_q)
+    lens = [rng.choice((0, 1, max_len, rng.randint(0, max_len))) for _ in range(requests)]
+    marks = sorted(rng.randint(0, requests) for _ in range(groups + 1))
+    prefix_lens = [rng.choice((0, 1, max_prefix, rng.randint(0, max_prefix))) for _ in range(groups)]
+    tokens = max(1, int(q_start[-1]))
+    max_group = max([int(q_start[b] - q_start[a]) for a, b in zip(marks, marks[1:])], default=0)
+    units = H * ((most_units(groups, tokens, max_group, group, row_tile, False) if prefix else 0) +
+                 (most_units(requests, tokens, max_q, group, row_tile, budget > 0) if own else 0))
+    arrays = [i32(x) for x in ([requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group, T, budget,
+                                row_tile, kv_tile, workers, prefix, own], q_start, lens, marks, prefix_lens or [0])]
+    total = ctypes.c_uint64()
+    got = host.h_cut(*(x.ctypes.data for x in arrays), units, ctypes.byref(total))
+    assert got == 0, (got, n_q, lens, marks, prefix_lens)
+    return total.value
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_pieces_cover_every_row_once(host, seed):
+    rng = random.Random(seed)
+    picked = seed % 3 == 0
+    groups = 0 if picked else rng.choice((0, 1, 5))
+    which = (0, 1) if picked or groups == 0 else rng.choice(((1, 1), (1, 0), (0, 1)))
+    cut(host, rng, rng.choice((1, 3, 40)), rng.choice((1, 5, 33)), rng.choice((1, 17, 500)), groups, rng.choice((0, 1, 900)),
+        rng.choice((1, 2, 8)), rng.choice((1, 4, 5, 16, 17, 40)), rng.choice((1, 16, 17, 64)),
+        rng.choice((1, 3, 100)) if picked else 0, rng.choice((16, 128, 256)), rng.choice((16, 64)),
+        rng.choice((1, 7, 152, 1216)), *which)
+
+
+def test_nothing_to_do_is_nothing(host):
+    rng = random.Random(0)
+    assert cut(host, rng, 3, 0, 50, 2, 0, 4, 4, 16, 0, 16, 16, 9, 1, 1) == 0
+
+
+def test_overlapping_queries_pass_the_room(host):
+    """Ranges that overlap (every other one out of order) may hold more units than the workspace has room for."""
+    requests, tokens = 64, 100
+    q_start, lens = i32([100 * (i % 2) for i in range(requests + 1)]), i32([300] * requests)
+    args = i32([requests, tokens, 100, 300, 0, 0, 0, 2, 4, 16, 0, 16, 16, 152, 0, 1])
+    none = i32([0, 0])
+    room = 2 * most_units(requests, tokens, 100, 4, 16, False)
+    got = host.h_cut(args.ctypes.data, q_start.ctypes.data, lens.ctypes.data, none.ctypes.data, none.ctypes.data, room,
+                     ctypes.byref(ctypes.c_uint64()))
+    assert got == 1
+
+
+def test_group_of_a_request(host):
+    q_start = i32([0, 2, 2, 5, 6, 9])
+    marks, lens = i32([0, 2, 2, 4, 4]), i32([7, 7, 9, 9])          # groups 0: requests 0, 1; 2: 2, 3; 4 has none
+    args = i32([5, 9, 4, 9, 100])
+    at = lambda r, m=marks, a=args, k=lens: host.h_group(  # noqa: E731
+        a.ctypes.data, q_start.ctypes.data, m.ctypes.data, k.ctypes.data, r, int(q_start[r]), int(q_start[r + 1] - q_start[r]))
+    assert [at(r) for r in range(5)] == [0, 0, 2, 2, -1]
+    assert at(0, k=i32([0, 7, 9, 9])) == -1                        # an empty prefix
+    assert at(3, a=i32([5, 9, 4, 3, 100])) == -1                   # more queries than max_group
+    assert at(0, m=i32([3, 1, 4, 9, 0])) == -1                     # out of order
+    assert at(1, m=i32([3, 1, 4, 9, 0])) == 1
+    assert at(4, m=i32([0, 2, 2, 4, 7])) == -1
+
+
+@pytest.mark.parametrize("m", [0.0, 1e-45, 2.0 ** -101, 2.0 ** -100, 0.01, 1.0, 1.984375, 1.984375 * (1 + 2 ** -23), 1.99, 127.0,
+                               127.5, 1e30, 3.4028235e38, np.inf, np.nan])
+def test_step_of_bounds(host, m):
+    inv = ctypes.c_float()
+    s = host.h_step(int(np.float32(m).view(np.uint32)), ctypes.byref(inv))
+    if not np.isfinite(m):
+        assert s == np.inf and inv.value == 0
+    elif m < 2.0 ** -100:
+        assert s == 0 and inv.value == 0
+    else:
+        assert np.frexp(s)[0] == 0.5 and s * inv.value == 1
+        assert float(np.float32(m)) <= 127 * s and float(np.float32(m)) > 63.5 * s
