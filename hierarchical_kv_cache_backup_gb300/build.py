@@ -25,10 +25,12 @@ LIB = os.path.join(LIBDIR, "libkvb.so")
 
 SOURCES = ["kvb_api.cpp", "kvb_kernels.cu", "kvb_noalloc.cu", "kvb_ring.cpp", "kvb_ring_kernels.cu",
            "kvb_l3.cpp", "kvb_vec.cpp", "kvb_vectors.cu", "kvb_attend.cu",
-           "kvb_attend_tc.cu", "kvb_pages.cu", "kvb_select.cu"]
+           "kvb_attend_tc.cu", "kvb_pages.cu", "kvb_pages_tc.cu",
+           "kvb_select.cu"]
 HEADERS = [os.path.join(CSRC, "kvb_internal.h"), os.path.join(CSRC, "kvb_ring_internal.h"),
            os.path.join(CSRC, "kvb_vec.h"), os.path.join(CSRC, "kvb_vec_internal.h"),
            os.path.join(CSRC, "kvb_pages.h"), os.path.join(CSRC, "kvb_pages_internal.h"),
+           os.path.join(CSRC, "kvb_pages_device.h"), os.path.join(CSRC, "kvb_tc.h"),
            os.path.join(INCLUDE, "kvb.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

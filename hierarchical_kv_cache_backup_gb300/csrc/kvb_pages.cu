@@ -8,6 +8,7 @@
 // read once for all requests of the group, whose pieces join with those of each request's own
 // tokens.
 #include "kvb_pages.h"
+#include "kvb_pages_device.h"
 #include "kvb_pages_internal.h"
 
 #include <cuda_bf16.h>
@@ -20,7 +21,7 @@ namespace kvb {
 namespace {
 
 constexpr int kWarps = 4;        // of a block
-constexpr int kTile = 16;        // cached tokens a warp takes at a time
+constexpr int kTile = 16;        // cached tokens a warp takes at a time (2^4)
 constexpr int kRowsP = 16;       // query rows of a unit
 constexpr float kNoMax = -3.0e38f;
 
@@ -61,115 +62,15 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two fp8 values as fp16, exact
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)w));
-    return r;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-template <bool kBf>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if (kBf) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t *>(&h);
-    }
-    __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
-template <bool kBf>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-    if (kBf) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
-// which 16-bit or fp8 values of a word are not finite, as a mask of their bits
-template <bool kF8, bool kBf>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-    if (kF8) return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-    const uint32_t e = kBf ? 0x7f807f80u : 0x7c007c00u;
-    return __vcmpeq2(w & e, e);
-}
-
 // Threads of a team (worker) wait for one another.
 __device__ __forceinline__ void team_sync(uint32_t team, uint32_t id) {
     if (team == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(team * 32) : "memory");
-}
-
-// Sums tiles and units of all segments over the block, writes the sums before each segment to
-// the workspace (block 0, for the join) and finds the segment of each worker's first tile.
-// `worker0`: the block's first worker.  Returns the tiles of a worker.
-template <int kThreads>
-__device__ __forceinline__ unsigned long long share_out(const PageAttendArgs &a, const PageEngine &e, uint32_t worker0,
-                                                        uint32_t workers_here, PageCursor *starts, unsigned long long *total) {
-    constexpr int kW = kThreads / 32;
-    __shared__ unsigned long long sums[2][kW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t n = seg_count(a, e);
-    unsigned long long share = 0, all_t = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        unsigned long long run_t = 0, run_u = 0;
-        for (uint32_t s0 = 0; s0 < n; s0 += kThreads) {
-            const uint32_t s = s0 + tid;
-            unsigned long long t = 0, u = 0;
-            if (s < n) {
-                const PageSeg g = seg_at(a, e, s);
-                t = seg_tiles(a, e, g);
-                u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
-                if (g.bad && pass == 0 && worker0 == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-            }
-            unsigned long long it = t, iu = u;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long xt = __shfl_up_sync(0xffffffffu, it, d), xu = __shfl_up_sync(0xffffffffu, iu, d);
-                if (lane >= d) {
-                    it += xt;
-                    iu += xu;
-                }
-            }
-            __syncthreads();
-            if (lane == 31) {
-                sums[0][warp] = it;
-                sums[1][warp] = iu;
-            }
-            __syncthreads();
-            unsigned long long bt = run_t, bu = run_u;
-#pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                if (w < warp) {
-                    bt += sums[0][w];
-                    bu += sums[1][w];
-                }
-                run_t += sums[0][w];
-                run_u += sums[1][w];
-            }
-            if (pass == 1 && s < n) {
-                const unsigned long long before = bt + it - t;
-                for (uint32_t k = 0; k < workers_here; ++k) {
-                    const unsigned long long x = (worker0 + k) * share;
-                    if (x >= before && x < before + t) starts[k] = PageCursor{before, bu + iu - u, s};
-                }
-                if (worker0 == 0) {
-                    e.seg_tiles[s] = before;
-                    e.seg_units[s] = bu + iu - u;
-                }
-            }
-        }
-        all_t = run_u > e.units ? 0 : run_t;
-        share = share_of(all_t, e.workers);
-        if (run_u > e.units && worker0 == 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-        if (pass == 1 && worker0 == 0 && tid == 0) {
-            e.seg_tiles[n] = run_t;
-            e.seg_units[n] = run_u;
-        }
-    }
-    __syncthreads();
-    *total = all_t;
-    return share;
 }
 
 // ------------------------------------------------------------- few query rows
@@ -193,19 +94,29 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
     __shared__ float join_m[kWarps][kRowsP], join_l[kWarps][kRowsP];
     __shared__ PageCursor starts[kWarps];
     __shared__ uint32_t masks[kWarps][kStages];
+    // Behind the kernel on tcgen05, which lets this one start once what came before it is done, the two
+    // have nothing to wait for in each other; this one ends after it, so that the join finds both done.
+    if (!a.tc.on) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const PageEngine &e = a.rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t team = e.team, team_id = warp / team, w_in = warp % team, teams = kWarps / team;
     const uint32_t worker = blockIdx.x * teams + team_id;
-    unsigned long long total;
-    const unsigned long long share = share_out<kWarps * 32>(a, e, blockIdx.x * teams, teams, starts, &total);
+    unsigned long long total, share;
+    PageCursor at{};
+    if (seg_count(a, e) <= kWarpSegs) {
+        share = warp_share(a, e, worker, blockIdx.x == 0 && warp == 0, &at, &total);
+    } else {
+        share = share_out<kWarps * 32>(a, e, blockIdx.x * teams, teams, starts, &total);
+        at = starts[team_id];
+    }
     unsigned long long x = worker * share;
     const unsigned long long x1 = min(total, x + share);
-    if (x >= x1) return;                          // no barrier of the whole block follows
-    PageCursor at = starts[team_id];
+    if (x >= x1) {                                // no barrier of the whole block follows
+        if (a.tc.on) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ring_bytes(D, kF8);
     float *mine = reinterpret_cast<float *>(smem + warp * ring_bytes(D, kF8));
@@ -568,6 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
         }
         team_sync(team, team_id);                 // rings are free again
     }
+    if (a.tc.on) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------- the join
@@ -583,13 +495,13 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int qh = kW == 1 ? blockIdx.x * 4 + warp : blockIdx.x, part = kW == 1 ? 0 : warp;
     const int i = blockIdx.y, r = blockIdx.z, group = (int)a.group;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (qh >= (int)a.q_heads) return;
+    // the call's inputs were there before the kernels in front of this one began
     const PageSeg own = own_seg(a, r);
-    if (i >= own.n) return;
+    const int in = group_of(a, r, own.q0, own.n);
     const int64_t tok = own.q0 + i;
     const int head = qh / group, j = qh - head * group;
-    const int in = group_of(a, r, own.q0, own.n);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (qh >= (int)a.q_heads || i >= own.n) return;
     if (a.rows.on && a.rows.seg_units[seg_count(a, a.rows)] > a.rows.units) return;
     if (a.tc.on && a.tc.seg_units[seg_count(a, a.tc)] > a.tc.units) return;
     float top = kNoMax, sum = 0.0f, acc[NV];
@@ -597,7 +509,7 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
     for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
     for (int side = in >= 0 ? 0 : 1; side < 2; ++side) {
         const PageSeg s = side == 0 ? prefix_seg(a, in) : own;
-        const PageEngine &e = (side == 0 ? a.tc.prefix : a.tc.own) && a.tc.on ? a.tc : a.rows;
+        const PageEngine &e = (side == 0 ? a.tc.prefix : a.tc.own) ? a.tc : a.rows;
         if (s.len == 0) continue;
         const uint32_t at = side == 0 ? (uint32_t)in : (e.prefix ? a.groups : 0) + (uint32_t)r;
         const RowPieces p = row_pieces(a, e, s, at, (int)(tok - s.q0), head, j);
@@ -732,23 +644,41 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
     const bool picked = budget != 0;
     const uint32_t prefix_rows = (uint32_t)std::min<uint64_t>((uint64_t)max_group * group, 1u << 30);
     const uint32_t own_rows = picked ? group : max_q * group;
-    PageEngine &e = p.rows;
-    e.on = 1;
-    e.prefix = groups != 0;
-    e.own = 1;
-    e.row_tile = kRowsP;
-    e.slot_rows = std::min<uint32_t>(kRowsP, std::max(own_rows, groups != 0 ? prefix_rows : 0));
-    const uint64_t units = most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
-    const Variant *v = find_variant(D, fp8, false);
-    const uint32_t blocks = (uint32_t)(sms * v->blocks);
-    // A warp works by itself where units are many and short; where there are few of them a
-    // block's four warps share one, so that fewer pieces have to be joined.
-    e.team = units >= 2ull * blocks ? 1 : kWarps;
-    e.kv_tile = kTile * e.team;
-    e.workers = blocks * (kWarps / e.team);
+    // More rows than one tile of mma.sync: tcgen05.
+    const bool tc_prefix = groups != 0 && max_prefix != 0 && prefix_rows > kRowsP, tc_own = !picked && own_rows > kRowsP;
     uint64_t at = 0;
-    place(&e, &at, units, (uint64_t)groups + requests, D);
-    p.wide_join = e.workers > 6 * units;
+    const uint64_t segs = (uint64_t)groups + requests;
+    if (tc_prefix || tc_own) {
+        PageEngine &e = p.tc;
+        const uint32_t most = std::max(tc_prefix ? prefix_rows : 0, tc_own ? own_rows : 0);
+        e.on = 1;
+        e.prefix = tc_prefix;
+        e.own = tc_own;
+        e.row_tile = pages_tc_rows(D, most);
+        e.kv_shift = pages_tc_shift();
+        e.slot_rows = std::min(e.row_tile, most);
+        e.team = 1;
+        e.workers = (uint32_t)sms;
+        place(&e, &at, most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads), segs, D);
+    }
+    if (!(tc_prefix || groups == 0) || !tc_own) {
+        PageEngine &e = p.rows;
+        e.on = 1;
+        e.prefix = groups != 0 && !tc_prefix;
+        e.own = !tc_own;
+        e.row_tile = kRowsP;
+        e.slot_rows = std::min<uint32_t>(kRowsP, std::max(e.own ? own_rows : 0, e.prefix ? prefix_rows : 0));
+        const uint64_t units = most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
+        const uint32_t blocks = (uint32_t)(sms * find_variant(D, fp8, false)->blocks);
+        // A warp works by itself where units are many and short; where there are few of them a
+        // block's four warps share one, so that fewer pieces have to be joined.
+        e.team = units >= 2ull * blocks ? 1 : kWarps;
+        e.kv_shift = e.team == 1 ? 4 : 6;
+        e.workers = blocks * (kWarps / e.team);
+        place(&e, &at, units, segs, D);
+        p.wide_join = e.workers > 6 * units;
+    }
+    if (p.tc.on && p.tc.workers > 6 * p.tc.units) p.wide_join = true;
     p.bytes = at;
     return p;
 }
@@ -758,10 +688,18 @@ cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D,
     (void)cudaGetLastError();
     const Variant *v = find_variant(D, fp8, fp16);
     if (v == nullptr) return cudaErrorInvalidValue;
-    const uint32_t teams = kWarps / a.rows.team;
-    cudaError_t e = launch(v->rows_fn, dim3(a.rows.workers / teams), kWarps * 32, v->smem, stream, pdl, a);
-    if (e != cudaSuccess) return e;
-    ++*launches;
+    cudaError_t e;
+    if (a.tc.on) {
+        e = launch_pages_tc(a, D, fp8, fp16, pdl, stream);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    if (a.rows.on) {
+        const uint32_t teams = kWarps / a.rows.team;
+        e = launch(v->rows_fn, dim3(a.rows.workers / teams), kWarps * 32, v->smem, stream, pdl, a);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
     if (p.wide_join) e = launch(v->join4_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
     else e = launch(v->join_fn, dim3((a.q_heads + 3) / 4, a.max_q, a.requests), 128, 0, stream, pdl, a);
     if (e == cudaSuccess) ++*launches;
@@ -778,7 +716,7 @@ cudaError_t preload_pages_kernels() {
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
+    return preload_pages_tc_kernels();
 }
 
 }  // namespace kvb

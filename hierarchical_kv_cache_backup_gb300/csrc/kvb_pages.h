@@ -12,7 +12,7 @@ namespace kvb {
 //
 // A segment is a run of cached tokens with the queries that see it: the prefix of a group
 // of requests, or the own tokens of one request.  A unit is one KV head and one tile of
-// query rows of a segment; its cached tokens are counted in tiles of kv_tile.  All tiles
+// query rows of a segment; its cached tokens are counted in tiles of 2^kv_shift.  All tiles
 // of a call, in the order segment, row tile, head, cached tokens, are cut into equal runs,
 // one a worker, so that ragged lengths leave nobody idle; what a worker holds of a unit is a
 // piece, and a kernel behind joins the pieces of each query row.  Unit u's piece at worker
@@ -23,7 +23,7 @@ namespace kvb {
 struct PageEngine {
     uint32_t on;              // launched for this call
     uint32_t prefix, own;     // which segments it takes: groups' prefixes first, then requests
-    uint32_t row_tile, kv_tile;
+    uint32_t row_tile, kv_shift;   // query rows of a unit, log2 of the cached tokens of a tile
     uint32_t workers;
     uint32_t slot_rows;       // query rows of a slot
     uint32_t team;            // warps of a worker (kernel for few rows)
@@ -58,40 +58,33 @@ struct PageSeg {
     uint32_t index;           // of the group or request
 };
 
-// Request r's queries and cached tokens, brought into range.
-KVB_HD PageSeg own_seg(const PageAttendArgs &a, uint32_t r) {
-    const int q0 = a.q_start[r], q1 = a.q_start[r + 1], len = a.lens[r];
-    const bool out = q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_q;
-    PageSeg s;
-    s.bad = out || len < 0 || len > (int)a.max_len;
-    s.q0 = out ? 0 : q0;
-    s.n = out ? 0 : q1 - q0;
-    s.len = len < 0 ? 0 : len > (int)a.max_len ? (int)a.max_len : len;
-    s.prefix = false;
-    s.index = r;
-    return s;
+// A group's prefix with all query tokens of its requests (none where the group is out of order
+// or holds more than max_group), or a request's own tokens with its queries (none where they are
+// out of range); lengths brought into range.
+KVB_HD PageSeg seg_of(const PageAttendArgs &a, bool prefix, uint32_t index) {
+    PageSeg g;
+    g.prefix = prefix;
+    g.index = index;
+    const int32_t *lens = g.prefix ? a.prefix_lens : a.lens;
+    const int len = lens[g.index];
+    int r0 = (int)g.index, r1 = r0 + 1;
+    if (g.prefix) {
+        r0 = a.group_start[g.index];
+        r1 = a.group_start[g.index + 1];
+    }
+    bool out = r0 < 0 || r1 < r0 || r1 > (int)a.requests;
+    const int q0 = out ? 0 : a.q_start[r0], q1 = out ? 0 : a.q_start[r1];
+    const int most = (int)(g.prefix ? a.max_group : a.max_q), longest = (int)(g.prefix ? a.max_prefix : a.max_len);
+    out = out || q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > most;
+    g.bad = out || len < 0 || len > longest;
+    g.q0 = out ? 0 : q0;
+    g.n = out ? 0 : q1 - q0;
+    g.len = len < 0 ? 0 : len > longest ? longest : len;
+    return g;
 }
 
-// Group g's: all query tokens of its requests.  A group that is out of order or holds more
-// than max_group query tokens has none.
-KVB_HD PageSeg prefix_seg(const PageAttendArgs &a, uint32_t g) {
-    const int r0 = a.group_start[g], r1 = a.group_start[g + 1], len = a.prefix_lens[g];
-    bool out = r0 < 0 || r1 < r0 || r1 > (int)a.requests;
-    int q0 = 0, q1 = 0;
-    if (!out) {
-        q0 = a.q_start[r0];
-        q1 = a.q_start[r1];
-        out = q0 < 0 || q1 < q0 || q1 > (int)a.tokens || q1 - q0 > (int)a.max_group;
-    }
-    PageSeg s;
-    s.bad = out || len < 0 || len > (int)a.max_prefix;
-    s.q0 = out ? 0 : q0;
-    s.n = out ? 0 : q1 - q0;
-    s.len = len < 0 ? 0 : len > (int)a.max_prefix ? (int)a.max_prefix : len;
-    s.prefix = true;
-    s.index = g;
-    return s;
-}
+KVB_HD PageSeg own_seg(const PageAttendArgs &a, uint32_t r) { return seg_of(a, false, r); }
+KVB_HD PageSeg prefix_seg(const PageAttendArgs &a, uint32_t g) { return seg_of(a, true, g); }
 
 // The group whose prefix request r's queries q0 .. q0 + n - 1 see, or -1.  Groups are in
 // order; where they are not, whichever the search meets.
@@ -114,16 +107,17 @@ KVB_HD uint32_t seg_count(const PageAttendArgs &a, const PageEngine &e) {
     return (e.prefix ? a.groups : 0) + (e.own ? a.requests : 0);
 }
 
+// Segment s of an engine's.
 KVB_HD PageSeg seg_at(const PageAttendArgs &a, const PageEngine &e, uint32_t s) {
     const uint32_t before = e.prefix ? a.groups : 0;
-    return s < before ? prefix_seg(a, s) : own_seg(a, s - before);
+    return seg_of(a, s < before, s < before ? s : s - before);
 }
 
 // Row tiles of a segment.  Rows are (query token, head of the group); where every token
 // has pages of its own, a tile holds rows of one token.
 KVB_HD int row_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s) {
     const int rt = (int)e.row_tile, g = (int)a.group;
-    return a.picks != nullptr ? s.n * ((g + rt - 1) / rt) : (int)(((int64_t)s.n * g + rt - 1) / rt);
+    return a.picks != nullptr ? s.n * ((g + rt - 1) / rt) : (s.n * g + rt - 1) / rt;    // at most 2^30 rows
 }
 
 // Cached tokens that some row of a tile sees: [0, that).
@@ -131,17 +125,17 @@ KVB_HD int seen_tokens(const PageAttendArgs &a, const PageEngine &e, const PageS
     if (s.prefix) return s.len;
     if (a.picks != nullptr) {
         // whole pages of the list, as many as the request's last token may have
-        const uint32_t all = (uint32_t)(((uint64_t)s.len + a.pool.T - 1) / a.pool.T);
+        const uint32_t all = div_T(a.pool, (uint32_t)s.len + a.pool.T - 1);
         return (int)((all < a.budget ? all : a.budget) * a.pool.T);
     }
-    int64_t last = (((int64_t)rt + 1) * e.row_tile - 1) / a.group;
+    int last = (int)((((uint32_t)rt + 1) * e.row_tile - 1) / a.group);
     if (last > s.n - 1) last = s.n - 1;
-    const int64_t hi = (int64_t)s.len - s.n + last + 1;
-    return hi < 0 ? 0 : (int)hi;                 // at most len
+    const int hi = s.len - s.n + last + 1;
+    return hi < 0 ? 0 : hi;                      // at most len
 }
 
 KVB_HD uint32_t unit_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
-    return ((uint32_t)seen_tokens(a, e, s, rt) + e.kv_tile - 1) / e.kv_tile;
+    return ((uint32_t)seen_tokens(a, e, s, rt) + (1u << e.kv_shift) - 1) >> e.kv_shift;
 }
 
 // Tiles of the row tiles before rt, for one head.
@@ -157,8 +151,11 @@ KVB_HD uint64_t seg_tiles(const PageAttendArgs &a, const PageEngine &e, const Pa
     return s.n == 0 || s.len == 0 ? 0 : tiles_before(a, e, s, row_tiles(a, e, s)) * a.pool.H;
 }
 
+// Division, in 32 bits where that does.
+KVB_HD uint64_t quotient(uint64_t a, uint64_t b) { return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b; }
+
 // Tiles of a worker.
-KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : (tiles + workers - 1) / workers; }
+KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : quotient(tiles + workers - 1, workers); }
 
 // Where a worker stands: a segment, and tiles and units before it.
 struct PageCursor {
@@ -190,7 +187,7 @@ KVB_HD PagePiece piece_at(const PageAttendArgs &a, const PageEngine &e, PageCurs
     uint32_t n = unit_tiles(a, e, p.s, 0);
     p.rt = 0;
     if (p.s.prefix || a.picks != nullptr) {
-        p.rt = (int)(rel / ((uint64_t)n * a.pool.H));
+        p.rt = (int)quotient(rel, (uint64_t)n * a.pool.H);
         rel -= (uint64_t)p.rt * n * a.pool.H;
     } else {
         while (rel >= (uint64_t)n * a.pool.H) {
@@ -199,8 +196,8 @@ KVB_HD PagePiece piece_at(const PageAttendArgs &a, const PageEngine &e, PageCurs
         }
     }
     p.n_tiles = (int)n;
-    p.head = (int)(rel / n);
-    p.k0 = (int)(rel % n);
+    p.head = (int)quotient(rel, n);
+    p.k0 = (int)(rel - (uint64_t)p.head * n);
     const uint64_t left = p.k0 + (x1 - x);
     p.k1 = left < n ? (int)left : (int)n;
     p.slot = at->units + (uint64_t)p.rt * a.pool.H + p.head + worker;
@@ -219,15 +216,15 @@ struct RowPieces {
 KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint32_t at, int i, int head, int j) {
     RowPieces p;
     const int rt_n = (int)e.row_tile, g = (int)a.group;
-    const int64_t row = (int64_t)i * g + j;
-    const int rt = a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + j / rt_n : (int)(row / rt_n);
+    const int row = i * g + j;
+    const int rt = a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + j / rt_n : row / rt_n;
     const uint32_t n = unit_tiles(a, e, s, rt);
     p.any = n != 0;
-    p.row = a.picks != nullptr ? j % rt_n : (int)(row % rt_n);
+    p.row = a.picks != nullptr ? j % rt_n : row % rt_n;
     const uint64_t share = share_of(e.seg_tiles[seg_count(a, e)], e.workers);
     const uint64_t t0 = e.seg_tiles[at] + tiles_before(a, e, s, rt) * a.pool.H + (uint64_t)head * n;
-    p.w0 = t0 / share;
-    p.w1 = (t0 + (n != 0 ? n : 1) - 1) / share;
+    p.w0 = quotient(t0, share);
+    p.w1 = quotient(t0 + (n != 0 ? n : 1) - 1, share);
     p.unit = e.seg_units[at] + (uint64_t)rt * a.pool.H + head;
     return p;
 }

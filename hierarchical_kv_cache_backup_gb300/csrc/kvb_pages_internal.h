@@ -19,6 +19,11 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
 cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D, bool fp8, bool fp16, bool pdl,
                          cudaStream_t stream, int *launches);
 cudaError_t preload_pages_kernels();
+// The kernel on tcgen05: query rows of its units, cached tokens of its tiles.
+uint32_t pages_tc_rows(uint32_t D, uint64_t rows);
+uint32_t pages_tc_shift();
+cudaError_t launch_pages_tc(const PageAttendArgs &a, uint32_t D, bool fp8, bool fp16, bool pdl, cudaStream_t stream);
+cudaError_t preload_pages_tc_kernels();
 
 cudaError_t launch_bound(const BoundArgs &a, uint32_t D, bool fp8, bool fp16, bool pdl, int sms, cudaStream_t stream);
 cudaError_t launch_select(const SelectArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream, int *launches);

@@ -280,8 +280,8 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
     if (a.format != KV_CACHE_SAME && a.format != KV_CACHE_E4M3)
         return fail(KV_ERR_INVALID_ARG, "format %u: SAME and E4M3 pages are taken (Q4 by kv_attend)", a.format);
     TRY(pool_layer(p, a.format, a.head_dim, layer));
-    if (!vector_index_fits(*layer))
-        return fail(KV_ERR_LAYOUT, "the pool's pages span 2^32 head vectors or more");
+    if (!vector_index_fits(*layer) || (a.format == KV_CACHE_SAME && (uint64_t)layer->P * layer->v_page > 0x7fffffffull))
+        return fail(KV_ERR_LAYOUT, "the pool's pages span too many head vectors (2^31 of 16-bit values, 2^32 of fp8)");
     TRY(check_counts(a.requests, a.tokens, a.max_q, a.max_len, a.q_heads, layer->H, layer->T));
     if (a.groups > 65535 || a.max_prefix > kMostTokens)
         return fail(KV_ERR_INVALID_ARG, "groups %u or max_prefix %u too large", a.groups, a.max_prefix);

@@ -693,8 +693,8 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  * tokens may make all of the call be left out (BAD_LENGTH).
  * A row of a page table holds ceil(max_len / T) (ceil(max_prefix / T)) entries that
  * may be read.  q and out hold `tokens` vectors.  head_dim: 64, 96, 128, 192 or
- * 256; fewer than 2^32 head vectors between the layer's first and the pool's
- * last; T at most 2^20 (LAYOUT otherwise).  Errors: as kv_attend. */
+ * 256; fewer than 2^31 head vectors (2^32 of fp8) between the layer's first and the
+ * pool's last; T at most 2^20 (LAYOUT otherwise).  Errors: as kv_attend. */
 typedef struct {
     kv_vecs q, out;
     float *lse;

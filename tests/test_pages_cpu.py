@@ -29,7 +29,9 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
     int picked = 0;
     a.picks = in[10] ? &picked : nullptr;
     PageEngine &e = a.rows;
-    e.row_tile = in[11]; e.kv_tile = in[12]; e.workers = in[13]; e.prefix = in[14]; e.own = in[15];
+    while ((1ull << a.pool.t_shift) < (unsigned)in[9]) ++a.pool.t_shift;      // division by T, as the library's
+    a.pool.t_mul = (uint32_t)(((1ull << 32) * ((1ull << a.pool.t_shift) - in[9])) / in[9] + 1);
+    e.row_tile = in[11]; e.kv_shift = in[12] == 16 ? 4 : 6; e.workers = in[13]; e.prefix = in[14]; e.own = in[15];
     const uint32_t n = seg_count(a, e);
     std::vector<uint64_t> st(n + 1), su(n + 1);
     uint64_t t = 0, u = 0;
@@ -55,7 +57,7 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
         while (x < x1) {
             const PagePiece p = piece_at(a, e, &c, x, x1, w);
             if (p.k1 <= p.k0 || p.k1 > p.n_tiles || p.head >= (int)a.pool.H || p.rt >= row_tiles(a, e, p.s)) return 2;
-            if ((uint64_t)(p.n_tiles - 1) * e.kv_tile >= (uint64_t)seen_tokens(a, e, p.s, p.rt)) return 3;
+            if (((uint64_t)(p.n_tiles - 1) << e.kv_shift) >= (uint64_t)seen_tokens(a, e, p.s, p.rt)) return 3;
             if (p.slot >= units + e.workers || !slots.emplace(p.slot, p).second) return 4;
             done += p.k1 - p.k0;
             x += p.k1 - p.k0;
@@ -84,7 +86,7 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
                         }
                     // all that the row sees is in its pieces
                     const int sees = g.prefix ? g.len : a.picks ? 0 : g.len - g.n + i + 1;
-                    if ((int64_t)at * e.kv_tile < sees) return 10;
+                    if (((int64_t)at << e.kv_shift) < sees) return 10;
                 }
     }
     return 0;
