@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 
 namespace kvb {
 
@@ -30,18 +31,21 @@ constexpr float kNoMax = -3.0e38f;
 __host__ __device__ constexpr int row_bytes(int D, bool f8) { return f8 ? D : 2 * D; }
 __host__ __device__ constexpr int smem_stride(int D, bool f8) { return row_bytes(D, f8) + 16; }
 __host__ __device__ constexpr int stage_bytes(int D, bool f8) { return 2 * kTile * smem_stride(D, f8); }
-__host__ __device__ constexpr int stages_of(int D, bool f8) { return row_bytes(D, f8) >= 256 ? 3 : 4; }
+// Stages: few, for as many warps as registers allow (D = 128 of 16 bits: two stages and 12 warps of 168
+// registers an SM).
+__host__ __device__ constexpr int stages_of(int D, bool f8) { return row_bytes(D, f8) >= 256 ? 2 : row_bytes(D, f8) >= 128 ? 3 : 4; }
 __host__ __device__ constexpr int ring_bytes(int D, bool f8) {
     const int ring = stages_of(D, f8) * stage_bytes(D, f8), join = kRowsP * (D + 4) * 4;
     return ring > join ? ring : join;
 }
-__host__ __device__ constexpr int blocks_per_sm(int D, bool f8) {
-    const int by_smem = 227 * 1024 / (kWarps * ring_bytes(D, f8) + 2048), by_regs = D <= 64 ? 4 : D <= 128 ? 3 : 2;
-    return by_smem < 1 ? 1 : by_smem < by_regs ? by_smem : by_regs;
-}
+// Blocks of an SM that the registers are kept for.
+__host__ __device__ constexpr int blocks_wanted(int D) { return D <= 64 ? 4 : D <= 128 ? 3 : 1; }
 
 __device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 __device__ __forceinline__ void ldm(uint32_t addr, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -73,6 +77,59 @@ __device__ __forceinline__ void team_sync(uint32_t team, uint32_t id) {
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + id), "r"(team * 32) : "memory");
 }
 
+// ------------------------------------------------------------------- the plan
+//
+// Tiles and units before each segment, where a block's table cannot hold them: one block an engine
+// (0: few rows, 1: tcgen05), 1,024 segments at a time.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __grid_constant__ PageAttendArgs a) {
+    __shared__ unsigned long long sums[2][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const PageEngine &e = blockIdx.x == 0 ? a.rows : a.tc;
+    if (!e.on || e.small) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t n = seg_count(a, e);
+    unsigned long long run_t = 0, run_u = 0;
+    for (uint32_t s0 = 0; s0 < n; s0 += kPlanThreads) {
+        const uint32_t s = s0 + tid;
+        unsigned long long t = 0, u = 0;
+        if (s < n) {
+            const PageSeg g = seg_at(a, e, s);
+            t = seg_tiles(a, e, g);
+            u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
+            if (g.bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+        }
+        const unsigned long long it = scan_add(t, lane), iu = scan_add(u, lane);
+        __syncthreads();
+        if (lane == 31) {
+            sums[0][warp] = it;
+            sums[1][warp] = iu;
+        }
+        __syncthreads();
+        unsigned long long bt = run_t + it - t, bu = run_u + iu - u;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) {
+                bt += sums[0][w];
+                bu += sums[1][w];
+            }
+            run_t += sums[0][w];
+            run_u += sums[1][w];
+        }
+        if (s < n) {
+            e.seg_tiles[s] = bt;
+            e.seg_units[s] = bu;
+            put_seg(e.seg_table + (uint64_t)s * kSegWords, seg_at(a, e, s));
+        }
+    }
+    if (tid == 0) {
+        e.seg_tiles[n] = run_t;
+        e.seg_units[n] = run_u;
+        if (run_u > e.units && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+    }
+}
+
 // ------------------------------------------------------------- few query rows
 //
 // A worker is a team of 1 or 4 warps.  Warps take 16 cached tokens in turn, each with a
@@ -80,7 +137,7 @@ __device__ __forceinline__ void team_sync(uint32_t team, uint32_t id) {
 // mma.sync m16n8k16, cached tokens the 8 columns of the first product and the 16 k of the
 // second, so that weights go from one to the other in registers.
 template <int D, bool kF8, bool kHalf>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
+__global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
     kv_pages_rows_kernel(const __grid_constant__ PageAttendArgs a) {
     constexpr bool kBf = !kF8 && !kHalf;          // type of the products' operands
     // Weights in two parts: bf16 (8 bits) alone errs as much as the output's rounding again, and
@@ -92,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
     constexpr int KS = D / 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float join_m[kWarps][kRowsP], join_l[kWarps][kRowsP];
-    __shared__ PageCursor starts[kWarps];
+    __shared__ PageTableSpace space;
     __shared__ uint32_t masks[kWarps][kStages];
     // Behind the kernel on tcgen05, which lets this one start once what came before it is done, the two
     // have nothing to wait for in each other; this one ends after it, so that the join finds both done.
@@ -103,20 +160,13 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t team = e.team, team_id = warp / team, w_in = warp % team, teams = kWarps / team;
     const uint32_t worker = blockIdx.x * teams + team_id;
-    unsigned long long total, share;
-    PageCursor at{};
-    if (seg_count(a, e) <= kWarpSegs) {
-        share = warp_share(a, e, worker, blockIdx.x == 0 && warp == 0, &at, &total);
-    } else {
-        share = share_out<kWarps * 32>(a, e, blockIdx.x * teams, teams, starts, &total);
-        at = starts[team_id];
-    }
-    unsigned long long x = worker * share;
-    const unsigned long long x1 = min(total, x + share);
+    unsigned long long x, x1;
+    const PageTable table_of = table_and_share(a, e, blockIdx.x == 0, worker, space, &x, &x1);
     if (x >= x1) {                                // no barrier of the whole block follows
         if (a.tc.on) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
+    uint32_t seg = find_segment(table_of.tiles, seg_count(a, e), x);
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ring_bytes(D, kF8);
     float *mine = reinterpret_cast<float *>(smem + warp * ring_bytes(D, kF8));
@@ -129,7 +179,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
     const uint32_t to = ring + lane_tok * SV + piece16 * 16;
 
     while (x < x1) {
-        const PagePiece piece = piece_at(a, e, &at, x, x1, worker);
+        const PagePiece piece = piece_of(a, e, table_of, &seg, x, x1, worker);
         const PageSeg &s = piece.s;
         const int rt = piece.rt, head = piece.head, k0 = piece.k0, k1 = piece.k1;
         x += k1 - k0;
@@ -139,32 +189,66 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
         const int per = (group + kRowsP - 1) / kRowsP;
         const int tok0 = picked ? rt / per : 0, row0 = picked ? rt % per * kRowsP : rt * kRowsP;
         const int rows = min(kRowsP, (picked ? group : s.n * group) - row0);
-        auto new_token = [&](int row) { return picked ? tok0 : (row0 + row) / group; };
-        auto head_of = [&](int row) { return picked ? row0 + row : (row0 + row) % group; };
+        const bool single = picked || (s.n == 1 && !s.prefix);       // rows of one token: no division
+        auto new_token = [&](int row) { return single ? tok0 : (row0 + row) / group; };
+        auto head_of = [&](int row) { return single ? row0 + row : (row0 + row) % group; };
         const int32_t *table = s.prefix ? a.prefix_pages + (int64_t)s.index * a.prefix_stride
                                         : a.pages + (int64_t)s.index * a.pages_stride;
         const int32_t *list = picked ? a.picks + ((int64_t)(s.q0 + tok0) * H + head) * a.budget : nullptr;
         const int pos0 = s.len - s.n + tok0;      // picked: the query's position
         const int pages0 = pages_seen(s.len, s.n, tok0, a.pool.T);
-        const bool alone = !s.prefix && group_of(a, s.index, s.q0, s.n) < 0;
-        const bool whole = alone && k0 == 0 && k1 == piece.n_tiles;
+        const bool whole = !s.prefix && s.in < 0 && k0 == 0 && k1 == piece.n_tiles;
 
-        // Token of this lane in tile k (-1: none that is seen), and its page.
+        // Token of this lane in tile k (-1: none that is seen), and its page.  Where there is a list of pages,
+        // its entry is read a tile before it is looked at.
         bool wrong_pick = false;
-        auto token_of = [&](int k) {
-            const int t = (k * (int)team + (int)w_in) * kTile + (lane & 15);
+        auto place_in = [&](int k) { return (k * (int)team + (int)w_in) * kTile + (lane & 15); };
+        auto entry_of = [&](int k) {
+            const int t = place_in(k);
+            return picked && k < k1 && t < end ? list[div_T(a.pool, (uint32_t)t)] : -1;
+        };
+        auto token_of = [&](int k, int p) {
+            const int t = place_in(k);
             if (k >= k1 || t >= end) return -1;
             if (!picked) return t;
-            const uint32_t i = div_T(a.pool, (uint32_t)t);
-            const int p = list[i];
             if ((uint32_t)p >= (uint32_t)pages0) {
                 wrong_pick |= p != -1;
                 return -1;
             }
-            const int real = p * (int)a.pool.T + (t - (int)i * (int)a.pool.T);
+            const int real = p * (int)a.pool.T + (t - (int)(div_T(a.pool, (uint32_t)t) * a.pool.T));
             return real <= pos0 ? real : -1;
         };
         auto page_of = [&](int t) { return t >= 0 ? table[div_T(a.pool, (uint32_t)t)] : 0; };
+        int tk[kStages + 1], entry[kStages + 2];
+        int32_t pg[kStages + 1];
+#pragma unroll
+        for (int i = 0; i < kStages + 2; ++i) entry[i] = entry_of(k0 + i);
+#pragma unroll
+        for (int i = 0; i < kStages + 1; ++i) {
+            tk[i] = token_of(k0 + i, entry[i]);
+            pg[i] = page_of(tk[i]);
+        }
+        // Query rows first, so that they are there when the first tiles are.
+        constexpr int SQ = 2 * D + 16;
+        static_assert(kRowsP * SQ <= stage_bytes(D, kF8), "queries fit a stage");
+        const uint32_t place = ring + (kStages - 1) * stage_bytes(D, kF8);
+        int pos;
+        {
+            // through the last stage's place, neighbouring lanes a row's 16-byte pieces
+            constexpr int PQ = D / 8, AQ = PQ <= 8 ? 4 : PQ <= 16 ? 2 : 1;
+            const int sub = lane / PQ, ch = lane - sub * PQ;
+            const bool on = (lane & 15) < rows;
+            const int i = on ? new_token(lane & 15) : 0, j = on ? head_of(lane & 15) : 0;
+            const long long mine_at = (long long)(s.q0 + i) * a.q.s_tok + (long long)(head * group + j) * a.q.s_head;
+            pos = s.prefix || picked || !on ? end - 1 : s.len - s.n + i;
+#pragma unroll
+            for (int r0 = 0; r0 < kRowsP; r0 += AQ) {
+                const int r = r0 + sub;
+                const long long from = __shfl_sync(0xffffffffu, mine_at, r & 15);
+                if (sub < AQ) copy16(place + r * SQ + ch * 16, a.q.data + from + ch * 16, r < rows);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         const uint64_t from_k = a.pool.base[0] + (uint64_t)head * a.pool.s_head + piece16 * 16;
         const uint64_t from_v = a.pool.base[1] + (uint64_t)head * a.pool.s_head + piece16 * 16;
         auto load = [&](int stage, int k, int t, int32_t page) {
@@ -174,25 +258,30 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
                 const uint32_t good = __ballot_sync(0xffffffffu, ok), bads = __ballot_sync(0xffffffffu, bad);
                 if (lane == 0) masks[warp][stage] = (good & 0xffffu) | bads << 16;
                 const uint32_t dst = to + stage * stage_bytes(D, kF8);
+                if ((good & 0xffffu) == 0xffffu) {
 #pragma unroll
-                for (int i = 0; i < (kTile + kAtOnce - 1) / kAtOnce; ++i) {
-                    const int tok = i * kAtOnce + lane_tok;
-                    const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, where, tok & 15) * (uint32_t)RB;
-                    if (lane_tok < kAtOnce && (kTile % kAtOnce == 0 || tok < kTile)) {
-                        copy16(dst + i * kAtOnce * SV, from_k + off, good >> (tok & 15) & 1);
-                        copy16(dst + (i * kAtOnce + kTile) * SV, from_v + off, good >> (tok & 15) & 1);
+                    for (int i = 0; i < (kTile + kAtOnce - 1) / kAtOnce; ++i) {
+                        const int tok = i * kAtOnce + lane_tok;
+                        const uint32_t w = __shfl_sync(0xffffffffu, where, tok & 15);
+                        if (lane_tok < kAtOnce && (kTile % kAtOnce == 0 || tok < kTile)) {
+                            copy16(dst + i * kAtOnce * SV, from_k + (uint64_t)w * (uint32_t)RB);
+                            copy16(dst + (i * kAtOnce + kTile) * SV, from_v + (uint64_t)w * (uint32_t)RB);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < (kTile + kAtOnce - 1) / kAtOnce; ++i) {
+                        const int tok = i * kAtOnce + lane_tok;
+                        const uint32_t w = __shfl_sync(0xffffffffu, where, tok & 15);
+                        if (lane_tok < kAtOnce && (kTile % kAtOnce == 0 || tok < kTile)) {
+                            copy16(dst + i * kAtOnce * SV, from_k + (uint64_t)w * (uint32_t)RB, good >> (tok & 15) & 1);
+                            copy16(dst + (i * kAtOnce + kTile) * SV, from_v + (uint64_t)w * (uint32_t)RB, good >> (tok & 15) & 1);
+                        }
                     }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        int tk[kStages + 2];
-        int32_t pg[kStages + 1];
-#pragma unroll
-        for (int i = 0; i < kStages + 2; ++i) tk[i] = token_of(k0 + i);
-#pragma unroll
-        for (int i = 0; i < kStages + 1; ++i) pg[i] = page_of(tk[i]);
-
         // Query rows as A fragments.  fp8 keys meet fp16 queries: a bf16 row is scaled by
         // the power of two that brings its largest value to 2^14..2^15 (values under 2^-22
         // of it lose bits), which its scores undo.
@@ -200,25 +289,31 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
         float sc[2];
         int lim[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            const bool on = row < rows;
-            const int i = on ? new_token(row) : 0, j = on ? head_of(row) : 0;
-            const uint64_t src = a.q.data + (int64_t)(s.q0 + i) * a.q.s_tok + (int64_t)(head * group + j) * a.q.s_head;
-            lim[r] = s.prefix || picked || !on ? end - 1 : s.len - s.n + i;
+        for (int i = 0; i < kStages - 1; ++i) load(i, k0 + i, tk[i], pg[i]);
+        {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int r = 0; r < 2; ++r) lim[r] = __shfl_sync(0xffffffffu, pos, g + 8 * r);
+            if (kF8) {
+                // fragments of fp8 come 4 values a lane: 4 c and 4 c + 2 of a run of 16 are the lane's pairs
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // the lane's pairs of dims: 2 c and 2 c + 8 of a run of 16, or with fp8, whose
-                    // fragments come 4 values a lane, 4 c and 4 c + 2
-                    const int d = 16 * ks + (kF8 ? 4 * c + 2 * h : 2 * c + 8 * h);
-                    qf[ks][r + 2 * h] = on ? *reinterpret_cast<const uint32_t *>(src + d * 2) : 0u;
-                }
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t w[2];
+                        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(place + (g + 8 * r) * SQ + 32 * ks + 8 * c) : "memory");
+                        qf[ks][r] = w[0];
+                        qf[ks][r + 2] = w[1];
+                    }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) ldm(place + (lane & 15) * SQ + ks * 32 + (lane >> 4) * 16, qf[ks]);
+            }
+            __syncwarp();
         }
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) load(i, k0 + i, tk[i], pg[i]);
-        int t_ahead = tk[kStages + 1];
+        load(kStages - 1, k0 + kStages - 1, tk[kStages - 1], pg[kStages - 1]);
+        int entry_next = entry[kStages + 1];
         int t_next = tk[kStages];
         int32_t page_next = pg[kStages];
 #pragma unroll
@@ -410,15 +505,56 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
             }
             __syncwarp();
             load(stage, k + kStages, t_next, page_next);
-            t_next = t_ahead;
+            t_next = token_of(k + kStages + 1, entry_next);
             page_next = page_of(t_next);
-            t_ahead = token_of(k + kStages + 2);
+            entry_next = entry_of(k + kStages + 2);
             if (++stage == kStages) stage = 0;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
         if (wrong_pick && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
 
+        const uint64_t to_row = piece.slot * e.slot_rows;
+        if (team == 1) {
+            // a warp's rows go out of its registers, pairs of neighbouring dims a lane (fp8: four)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float t = l[r];
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                t += __shfl_xor_sync(0xffffffffu, t, 2);
+                const int row = g + 8 * r;
+                if (row >= rows) continue;
+                const int64_t tok = s.q0 + new_token(row);
+                const int qh = head * group + head_of(row);
+                if (whole) {
+                    const float inv = t != 0.0f ? a.v_scale / t : 0.0f;
+                    const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head;
+#pragma unroll
+                    for (int n = 0; n < 2 * KS; ++n) {
+                        if (!kF8)
+                            *reinterpret_cast<uint32_t *>(dst + 16 * n + 4 * c) = pack2<!kHalf>(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+                        else if ((n & 1) == 0)
+                            *reinterpret_cast<uint2 *>(dst + 16 * n + 8 * c) =
+                                make_uint2(pack2<!kHalf>(o[n][2 * r] * inv, o[n + 1][2 * r] * inv), pack2<!kHalf>(o[n][2 * r + 1] * inv, o[n + 1][2 * r + 1] * inv));
+                    }
+                    if (c == 0 && a.lse != nullptr)
+                        a.lse[tok * a.q_heads + qh] = t != 0.0f ? (m[r] + log2f(t)) * 0.693147180559945f : -INFINITY;
+                } else {
+                    float *dst = e.part_o + (to_row + row) * D;
+#pragma unroll
+                    for (int n = 0; n < 2 * KS; ++n) {
+                        if (!kF8)
+                            *reinterpret_cast<float2 *>(dst + 8 * n + 2 * c) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                        else if ((n & 1) == 0)
+                            *reinterpret_cast<float4 *>(dst + 8 * n + 4 * c) =
+                                make_float4(o[n][2 * r], o[n + 1][2 * r], o[n][2 * r + 1], o[n + 1][2 * r + 1]);
+                    }
+                    if (c == 0) *reinterpret_cast<float2 *>(e.part_ml + (to_row + row) * 2) = make_float2(m[r], t);
+                }
+            }
+            __syncwarp();                         // the ring is free again
+            continue;
+        }
         // Join the team's warps: accumulators go to the warp's own ring as [row][D + 4].
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -472,9 +608,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(D, kF8))
                 if (d4 == 0 && a.lse != nullptr)
                     a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
             } else {
-                const uint64_t to_row = piece.slot * e.slot_rows + row;
-                *reinterpret_cast<float4 *>(e.part_o + to_row * D + d4 * 4) = acc;
-                if (d4 == 0) *reinterpret_cast<float2 *>(e.part_ml + to_row * 2) = make_float2(top, sum);
+                *reinterpret_cast<float4 *>(e.part_o + (to_row + row) * D + d4 * 4) = acc;
+                if (d4 == 0) *reinterpret_cast<float2 *>(e.part_ml + (to_row + row) * 2) = make_float2(top, sum);
             }
         }
         team_sync(team, team_id);                 // rings are free again
@@ -491,16 +626,16 @@ template <int D, bool kHalf, int kW>
 __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constant__ PageAttendArgs a) {
     constexpr int NV = D / 32;
     __shared__ float acc_s[kW][D], m_s[kW], l_s[kW];
-    asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int qh = kW == 1 ? blockIdx.x * 4 + warp : blockIdx.x, part = kW == 1 ? 0 : warp;
     const int i = blockIdx.y, r = blockIdx.z, group = (int)a.group;
     // the call's inputs were there before the kernels in front of this one began
     const PageSeg own = own_seg(a, r);
-    const int in = group_of(a, r, own.q0, own.n);
+    const int in = a.joined ? -1 : own.in;
     const int64_t tok = own.q0 + i;
     const int head = qh / group, j = qh - head * group;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     if (qh >= (int)a.q_heads || i >= own.n) return;
     if (a.rows.on && a.rows.seg_units[seg_count(a, a.rows)] > a.rows.units) return;
     if (a.tc.on && a.tc.seg_units[seg_count(a, a.tc)] > a.tc.units) return;
@@ -510,7 +645,6 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
     for (int side = in >= 0 ? 0 : 1; side < 2; ++side) {
         const PageSeg s = side == 0 ? prefix_seg(a, in) : own;
         const PageEngine &e = (side == 0 ? a.tc.prefix : a.tc.own) ? a.tc : a.rows;
-        if (s.len == 0) continue;
         const uint32_t at = side == 0 ? (uint32_t)in : (e.prefix ? a.groups : 0) + (uint32_t)r;
         const RowPieces p = row_pieces(a, e, s, at, (int)(tok - s.q0), head, j);
         if (!p.any) continue;
@@ -573,18 +707,18 @@ struct Variant {
     uint32_t D;
     bool fp8, fp16;
     PagesFn *rows_fn, *join_fn, *join4_fn;
-    int smem, blocks;
+    int smem, blocks;      // blocks of an SM: set when the kernels are loaded
 };
 template <int D, bool kF8, bool kHalf>
 constexpr Variant variant() {
     return Variant{(uint32_t)D, kF8, kHalf, kv_pages_rows_kernel<D, kF8, kHalf>, kv_pages_join_kernel<D, kHalf, 1>,
-                   kv_pages_join_kernel<D, kHalf, 4>, kWarps * ring_bytes(D, kF8), blocks_per_sm(D, kF8)};
+                   kv_pages_join_kernel<D, kHalf, 4>, kWarps * ring_bytes(D, kF8), 1};
 }
 #define KVB_PAGES(D) variant<D, false, false>(), variant<D, false, true>(), variant<D, true, false>(), variant<D, true, true>()
-const Variant kVariants[] = {KVB_PAGES(64), KVB_PAGES(96), KVB_PAGES(128), KVB_PAGES(192), KVB_PAGES(256)};
+Variant g_variants[] = {KVB_PAGES(64), KVB_PAGES(96), KVB_PAGES(128), KVB_PAGES(192), KVB_PAGES(256)};
 
 const Variant *find_variant(uint32_t D, bool fp8, bool fp16) {
-    for (const Variant &v : kVariants)
+    for (const Variant &v : g_variants)
         if (v.D == D && v.fp8 == fp8 && v.fp16 == fp16) return &v;
     return nullptr;
 }
@@ -625,8 +759,12 @@ uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t tokens, uin
     return u * H;
 }
 
-void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint32_t D) {
+// `span`: the most cached tokens of a unit.
+void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t span, uint32_t D) {
     e->units = units;
+    const uint64_t tiles = units * ((span >> e->kv_shift) + 2);      // at most
+    e->small = segs <= kPlanSegs && units < (1ull << 31) && tiles < (1ull << 31);
+    if (!e->small) e->seg_table = (int32_t *)take(at, segs * kSegWords * 4);
     const uint64_t rows = (units + e->workers) * e->slot_rows;
     e->seg_tiles = (uint64_t *)take(at, (segs + 1) * 8);
     e->seg_units = (uint64_t *)take(at, (segs + 1) * 8);
@@ -645,39 +783,57 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
     const uint32_t prefix_rows = (uint32_t)std::min<uint64_t>((uint64_t)max_group * group, 1u << 30);
     const uint32_t own_rows = picked ? group : max_q * group;
     // More rows than one tile of mma.sync: tcgen05.
-    const bool tc_prefix = groups != 0 && max_prefix != 0 && prefix_rows > kRowsP, tc_own = !picked && own_rows > kRowsP;
+    const bool tc_own = !picked && own_rows > kRowsP;
+    // Where a request fills a unit on its own, reading its prefix with it costs nothing and saves the joining.
+    p.joined = groups != 0 && tc_own && own_rows >= 256;
+    const bool tc_prefix = groups != 0 && max_prefix != 0 && prefix_rows > kRowsP && !p.joined;
+    const uint64_t span = picked ? (uint64_t)max_len + T : p.joined ? (uint64_t)max_prefix + max_len : std::max(max_len, groups != 0 ? max_prefix : 0);
     uint64_t at = 0;
     const uint64_t segs = (uint64_t)groups + requests;
+    PageEngine &t = p.tc, &e = p.rows;
+    uint64_t t_units = 0, e_units = 0;
+    const Variant *v = find_variant(D, fp8, false);
     if (tc_prefix || tc_own) {
-        PageEngine &e = p.tc;
         const uint32_t most = std::max(tc_prefix ? prefix_rows : 0, tc_own ? own_rows : 0);
-        e.on = 1;
-        e.prefix = tc_prefix;
-        e.own = tc_own;
-        e.row_tile = pages_tc_rows(D, most);
-        e.kv_shift = pages_tc_shift();
-        e.slot_rows = std::min(e.row_tile, most);
-        e.team = 1;
-        e.workers = (uint32_t)sms;
-        place(&e, &at, most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads), segs, D);
+        t.on = 1;
+        t.prefix = tc_prefix;
+        t.own = tc_own;
+        t.row_tile = pages_tc_rows(D, most);
+        t.kv_shift = pages_tc_shift();
+        t.slot_rows = std::min(t.row_tile, most);
+        t.team = 1;
+        t.workers = (uint32_t)sms;
+        t_units = most_units(t, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
     }
-    if (!(tc_prefix || groups == 0) || !tc_own) {
-        PageEngine &e = p.rows;
+    if (!(tc_prefix || p.joined || groups == 0) || !tc_own) {
         e.on = 1;
-        e.prefix = groups != 0 && !tc_prefix;
+        e.prefix = groups != 0 && !tc_prefix && !p.joined;
         e.own = !tc_own;
         e.row_tile = kRowsP;
         e.slot_rows = std::min<uint32_t>(kRowsP, std::max(e.own ? own_rows : 0, e.prefix ? prefix_rows : 0));
-        const uint64_t units = most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
-        const uint32_t blocks = (uint32_t)(sms * find_variant(D, fp8, false)->blocks);
-        // A warp works by itself where units are many and short; where there are few of them a
-        // block's four warps share one, so that fewer pieces have to be joined.
-        e.team = units >= 2ull * blocks ? 1 : kWarps;
+        e_units = most_units(e, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
+        uint32_t e_sms = (uint32_t)sms;
+        if (t.on) {
+            // The two kernels run side by side, each on SMs of its own, so that neither waits for the other's
+            // beginning and end: as many for tcgen05 as its share of the cycles, about 12 D a tile of 64
+            // cached tokens (twice that from fp8) against 20 D a warp's tile of 16.  64 requests of up to 1,000
+            // tokens behind 8,192: 96 us one after the other on all SMs.
+            const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * 12.0 * D * (fp8 ? 2 : 1);
+            const double rows_cost = (double)e_units * (max_len / 16 + 1) * 20.0 * D / (kWarps * v->blocks);
+            const double part = (double)sms * tc_cost / (tc_cost + rows_cost);
+            t.workers = (uint32_t)std::min<double>(sms - 1, std::max(1.0, std::floor(part + 0.5)));
+            e_sms = (uint32_t)sms - t.workers;
+        }
+        const uint32_t blocks = e_sms * (uint32_t)v->blocks;
+        // A warp works by itself (what a unit takes to begin and end is paid once); where that would make
+        // more than 16 pieces of a unit, a block's four warps share one, so that fewer pieces have to be joined.
+        e.team = 4 * e_units >= blocks ? 1 : kWarps;
         e.kv_shift = e.team == 1 ? 4 : 6;
         e.workers = blocks * (kWarps / e.team);
-        place(&e, &at, units, segs, D);
-        p.wide_join = e.workers > 6 * units;
+        place(&e, &at, e_units, segs, span, D);
+        p.wide_join = e.workers > 6 * e_units;
     }
+    if (t.on) place(&t, &at, t_units, segs, span, D);
     if (p.tc.on && p.tc.workers > 6 * p.tc.units) p.wide_join = true;
     p.bytes = at;
     return p;
@@ -689,6 +845,11 @@ cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D,
     const Variant *v = find_variant(D, fp8, fp16);
     if (v == nullptr) return cudaErrorInvalidValue;
     cudaError_t e;
+    if ((a.rows.on && !a.rows.small) || (a.tc.on && !a.tc.small)) {
+        e = launch(kv_pages_plan_kernel, dim3(2), kPlanThreads, 0, stream, pdl, a);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
     if (a.tc.on) {
         e = launch_pages_tc(a, D, fp8, fp16, pdl, stream);
         if (e != cudaSuccess) return e;
@@ -708,12 +869,22 @@ cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D,
 
 cudaError_t preload_pages_kernels() {
     cudaFuncAttributes at;
-    for (const Variant &v : kVariants) {
+    const cudaError_t e0 = cudaFuncGetAttributes(&at, (const void *)kv_pages_plan_kernel);
+    if (e0 != cudaSuccess) return e0;
+    for (Variant &v : g_variants) {
         cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.rows_fn);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute((const void *)v.rows_fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v.blocks, (const void *)v.rows_fn, kWarps * 32, (size_t)v.smem);
+        if (e == cudaSuccess && v.blocks < 1) e = cudaErrorInvalidConfiguration;
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
+        // The same split of an SM's memory for all: an SM has to be empty to change it, and blocks of the next
+        // kernel, launched early, would find no place beside the join's.
+        for (PagesFn *fn : {v.rows_fn, v.join_fn, v.join4_fn})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
     }
     return preload_pages_tc_kernels();

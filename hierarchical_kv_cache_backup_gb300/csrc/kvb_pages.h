@@ -28,10 +28,12 @@ struct PageEngine {
     uint32_t slot_rows;       // query rows of a slot
     uint32_t team;            // warps of a worker (kernel for few rows)
     uint64_t units;           // that the workspace has room for
+    uint32_t small;           // the segments fit a block's table, and tiles and units 31 bits
     float *part_o;            // [slot][slot_rows][D] sums
     float *part_ml;           // [slot][slot_rows][2] maxima (base 2), sums of weights
-    uint64_t *seg_tiles;      // [segments + 1] tiles before each segment (written by worker 0)
+    uint64_t *seg_tiles;      // [segments + 1] tiles before each segment (written on the GPU)
     uint64_t *seg_units;      // [segments + 1]
+    int32_t *seg_table;       // [segments][kSegWords], not where they are few
 };
 
 struct PageAttendArgs {
@@ -49,6 +51,7 @@ struct PageAttendArgs {
     uint32_t q_heads, group;  // group: query heads of a KV head
     float scale_log2;         // scale * log2(e), the keys' scale included
     float v_scale;
+    uint32_t joined;          // a request's units take its group's prefix in front of its own tokens
     PageEngine rows, tc;      // kernel for few rows, kernel on tcgen05
 };
 
@@ -56,6 +59,8 @@ struct PageSeg {
     int q0, n, len;           // first query token, query tokens, cached tokens
     bool prefix, bad;
     uint32_t index;           // of the group or request
+    int in;                   // a request: the group whose prefix its queries see, or -1
+    int before;               // tokens of that prefix where they are in front of its own (joined)
 };
 
 // A group's prefix with all query tokens of its requests (none where the group is out of order
@@ -80,10 +85,11 @@ KVB_HD PageSeg seg_of(const PageAttendArgs &a, bool prefix, uint32_t index) {
     g.q0 = out ? 0 : q0;
     g.n = out ? 0 : q1 - q0;
     g.len = len < 0 ? 0 : len > longest ? longest : len;
+    g.in = -1;
+    g.before = 0;
     return g;
 }
 
-KVB_HD PageSeg own_seg(const PageAttendArgs &a, uint32_t r) { return seg_of(a, false, r); }
 KVB_HD PageSeg prefix_seg(const PageAttendArgs &a, uint32_t g) { return seg_of(a, true, g); }
 
 // The group whose prefix request r's queries q0 .. q0 + n - 1 see, or -1.  Groups are in
@@ -103,6 +109,14 @@ KVB_HD int group_of(const PageAttendArgs &a, uint32_t r, int q0, int n) {
     return (int)lo;
 }
 
+KVB_HD PageSeg own_seg(const PageAttendArgs &a, uint32_t r) {
+    PageSeg s = seg_of(a, false, r);
+    if (a.groups == 0 || s.n == 0) return s;
+    s.in = group_of(a, r, s.q0, s.n);
+    if (a.joined && s.in >= 0) s.before = prefix_seg(a, (uint32_t)s.in).len;
+    return s;
+}
+
 KVB_HD uint32_t seg_count(const PageAttendArgs &a, const PageEngine &e) {
     return (e.prefix ? a.groups : 0) + (e.own ? a.requests : 0);
 }
@@ -110,7 +124,7 @@ KVB_HD uint32_t seg_count(const PageAttendArgs &a, const PageEngine &e) {
 // Segment s of an engine's.
 KVB_HD PageSeg seg_at(const PageAttendArgs &a, const PageEngine &e, uint32_t s) {
     const uint32_t before = e.prefix ? a.groups : 0;
-    return seg_of(a, s < before, s < before ? s : s - before);
+    return s < before ? prefix_seg(a, s) : own_seg(a, s - before);
 }
 
 // Row tiles of a segment.  Rows are (query token, head of the group); where every token
@@ -120,7 +134,7 @@ KVB_HD int row_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg
     return a.picks != nullptr ? s.n * ((g + rt - 1) / rt) : (s.n * g + rt - 1) / rt;    // at most 2^30 rows
 }
 
-// Cached tokens that some row of a tile sees: [0, that).
+// Cached tokens of the segment's own that some row of a tile sees: [0, that).
 KVB_HD int seen_tokens(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
     if (s.prefix) return s.len;
     if (a.picks != nullptr) {
@@ -134,8 +148,9 @@ KVB_HD int seen_tokens(const PageAttendArgs &a, const PageEngine &e, const PageS
     return hi < 0 ? 0 : hi;                      // at most len
 }
 
+KVB_HD uint32_t tiles_of(const PageEngine &e, int tokens) { return ((uint32_t)tokens + (1u << e.kv_shift) - 1) >> e.kv_shift; }
 KVB_HD uint32_t unit_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
-    return ((uint32_t)seen_tokens(a, e, s, rt) + (1u << e.kv_shift) - 1) >> e.kv_shift;
+    return tiles_of(e, s.before) + tiles_of(e, seen_tokens(a, e, s, rt));
 }
 
 // Tiles of the row tiles before rt, for one head.
@@ -148,7 +163,7 @@ KVB_HD uint64_t tiles_before(const PageAttendArgs &a, const PageEngine &e, const
 }
 
 KVB_HD uint64_t seg_tiles(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s) {
-    return s.n == 0 || s.len == 0 ? 0 : tiles_before(a, e, s, row_tiles(a, e, s)) * a.pool.H;
+    return s.n == 0 ? 0 : tiles_before(a, e, s, row_tiles(a, e, s)) * a.pool.H;
 }
 
 // Division, in 32 bits where that does.
@@ -157,12 +172,6 @@ KVB_HD uint64_t quotient(uint64_t a, uint64_t b) { return ((a | b) >> 32) == 0 ?
 // Tiles of a worker.
 KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : quotient(tiles + workers - 1, workers); }
 
-// Where a worker stands: a segment, and tiles and units before it.
-struct PageCursor {
-    uint64_t tiles, units;
-    uint32_t seg;
-};
-
 // A worker's tiles [k0, k1) of the n_tiles of a unit.
 struct PagePiece {
     PageSeg s;
@@ -170,37 +179,72 @@ struct PagePiece {
     uint64_t slot;
 };
 
-// The piece of `worker` that begins with tile x (x < x1, its last tile), from a cursor at
-// its segment or before.
-KVB_HD PagePiece piece_at(const PageAttendArgs &a, const PageEngine &e, PageCursor *at, uint64_t x, uint64_t x1,
-                          uint32_t worker) {
-    PagePiece p;
-    p.s = seg_at(a, e, at->seg);
-    uint64_t tiles = seg_tiles(a, e, p.s);
-    while (x >= at->tiles + tiles) {
-        if (tiles != 0) at->units += (uint64_t)row_tiles(a, e, p.s) * a.pool.H;
-        at->tiles += tiles;
-        p.s = seg_at(a, e, ++at->seg);
-        tiles = seg_tiles(a, e, p.s);
+// The segments of a call: what comes before each, and its members.  A block holds up to kPlanSegs of
+// them in shared memory; a kernel of its own writes more to the workspace.
+constexpr uint32_t kPlanSegs = 128;
+struct PageTable {
+    const uint64_t *tiles, *units;        // [segments + 1]
+    const int32_t *seg;                   // [segments][kSegWords]: q0, n, len, in, before
+};
+constexpr uint32_t kSegWords = 5;
+struct PageTableSpace {
+    uint64_t tiles[kPlanSegs + 1], units[kPlanSegs + 1];
+    int32_t seg[kPlanSegs * kSegWords];
+};
+
+KVB_HD void put_seg(int32_t *to, const PageSeg &s) {
+    to[0] = s.q0;
+    to[1] = s.n;
+    to[2] = s.len;
+    to[3] = s.in;
+    to[4] = s.before;
+}
+
+// The segment that holds tile x.
+KVB_HD uint32_t find_segment(const uint64_t *tiles, uint32_t n, uint64_t x) {
+    uint32_t lo = 0, hi = n;              // tiles[lo] <= x < tiles[hi]
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (tiles[mid] <= x) lo = mid;
+        else hi = mid;
     }
-    uint64_t rel = x - at->tiles;
-    uint32_t n = unit_tiles(a, e, p.s, 0);
+    return lo;
+}
+
+// The piece of `worker` that begins with tile x (x < x1, its last tile); *seg: a segment at x or before.
+// A segment has fewer than 2^31 tiles.
+KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const PageTable &t, uint32_t *seg, uint64_t x, uint64_t x1,
+                          uint32_t worker) {
+    uint32_t i = *seg;
+    while (x >= t.tiles[i + 1]) ++i;
+    *seg = i;
+    const uint32_t before = e.prefix ? a.groups : 0, H = a.pool.H;
+    const int32_t *w = t.seg + (uint64_t)i * kSegWords;
+    PagePiece p;
+    p.s.q0 = w[0];
+    p.s.n = w[1];
+    p.s.len = w[2];
+    p.s.in = w[3];
+    p.s.before = w[4];
+    p.s.bad = false;
+    p.s.prefix = i < before;
+    p.s.index = i < before ? i : i - before;
+    uint32_t rel = (uint32_t)(x - t.tiles[i]), n = unit_tiles(a, e, p.s, 0);
     p.rt = 0;
     if (p.s.prefix || a.picks != nullptr) {
-        p.rt = (int)quotient(rel, (uint64_t)n * a.pool.H);
-        rel -= (uint64_t)p.rt * n * a.pool.H;
+        p.rt = (int)(rel / (n * H));
+        rel -= (uint32_t)p.rt * n * H;
     } else {
-        while (rel >= (uint64_t)n * a.pool.H) {
-            rel -= (uint64_t)n * a.pool.H;
+        while (rel >= n * H) {
+            rel -= n * H;
             n = unit_tiles(a, e, p.s, ++p.rt);
         }
     }
     p.n_tiles = (int)n;
-    p.head = (int)quotient(rel, n);
-    p.k0 = (int)(rel - (uint64_t)p.head * n);
-    const uint64_t left = p.k0 + (x1 - x);
-    p.k1 = left < n ? (int)left : (int)n;
-    p.slot = at->units + (uint64_t)p.rt * a.pool.H + p.head + worker;
+    p.head = (int)(rel / n);
+    p.k0 = (int)(rel - (uint32_t)p.head * n);
+    p.k1 = x1 - x < n - (uint32_t)p.k0 ? p.k0 + (int)(x1 - x) : (int)n;
+    p.slot = t.units[i] + (uint64_t)p.rt * H + p.head + worker;
     return p;
 }
 

@@ -37,9 +37,6 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return __vcmpeq2(w & e, e);
 }
 
-// Up to this many segments a warp finds its worker's first tile by itself.
-constexpr uint32_t kWarpSegs = 128;
-
 __device__ __forceinline__ unsigned long long scan_add(unsigned long long x, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -49,133 +46,54 @@ __device__ __forceinline__ unsigned long long scan_add(unsigned long long x, int
     return x;
 }
 
-// A warp sums tiles and units of all segments and finds the segment of `worker`'s first tile;
-// with `record` it writes the sums before each segment to the workspace, for the join, and
-// reports what is out of range.  Returns the tiles of a worker, *total the tiles of all (0 where
-// the units pass the workspace's room).
-__device__ __forceinline__ unsigned long long warp_share(const PageAttendArgs &a, const PageEngine &e, uint32_t worker, bool record,
-                                                         PageCursor *start, unsigned long long *total) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t n = seg_count(a, e);
-    unsigned long long all_t = 0, all_u = 0, t = 0, u = 0;
-    auto segment = [&](uint32_t s, bool report) {
-        t = u = 0;
-        if (s >= n) return;
-        const PageSeg g = seg_at(a, e, s);
-        t = seg_tiles(a, e, g);
-        u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
-        if (g.bad && report && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-    };
-    for (uint32_t s0 = 0; s0 < n; s0 += 32) {
-        segment(s0 + lane, record);
-        all_t += t;
-        all_u += u;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        all_t += __shfl_xor_sync(0xffffffffu, all_t, d);
-        all_u += __shfl_xor_sync(0xffffffffu, all_u, d);
-    }
-    if (record && lane == 0) {
-        e.seg_tiles[n] = all_t;
-        e.seg_units[n] = all_u;
-        if (all_u > e.units && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-    }
-    if (all_u > e.units) all_t = 0;
-    *total = all_t;
-    const unsigned long long share = share_of(all_t, e.workers), x = worker * share;
-    unsigned long long before_t = 0, before_u = 0;
-    for (uint32_t s0 = 0; s0 < n; s0 += 32) {
-        if (n > 32) segment(s0 + lane, false);
-        const unsigned long long it = scan_add(t, lane), iu = scan_add(u, lane);
-        const unsigned long long bt = before_t + it - t, bu = before_u + iu - u;
-        if (record && s0 + lane < n) {
-            e.seg_tiles[s0 + lane] = bt;
-            e.seg_units[s0 + lane] = bu;
-        }
-        const uint32_t in = __ballot_sync(0xffffffffu, x >= bt && x < bt + t);
-        if (in != 0) {
-            const int l = __ffs(in) - 1;
-            start->tiles = __shfl_sync(0xffffffffu, bt, l);
-            start->units = __shfl_sync(0xffffffffu, bu, l);
-            start->seg = s0 + l;
-            if (!record) break;
-        }
-        before_t += __shfl_sync(0xffffffffu, it, 31);
-        before_u += __shfl_sync(0xffffffffu, iu, 31);
-    }
-    return share;
-}
-
-// The same over a block, for any number of segments and the block's workers, worker0 and the
-// next; worker 0's block records.
-template <int kThreads>
-__device__ __forceinline__ unsigned long long share_out(const PageAttendArgs &a, const PageEngine &e, uint32_t worker0,
-                                                        uint32_t workers_here, PageCursor *starts, unsigned long long *total) {
-    constexpr int kW = kThreads / 32;
-    __shared__ unsigned long long sums[2][kW];
+// Fills a block's table of the call's segments: one thread a segment, one sum over four warps.  Block 0
+// (`record`) writes what comes before each segment to the workspace, for the join, and reports what
+// is out of range.  The table is there for all threads when it returns.
+__device__ __forceinline__ void fill_table(const PageAttendArgs &a, const PageEngine &e, bool record, PageTableSpace &t) {
+    __shared__ unsigned long long sums[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t n = seg_count(a, e);
-    unsigned long long share = 0, all_t = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        unsigned long long run_t = 0, run_u = 0;
-        for (uint32_t s0 = 0; s0 < n; s0 += kThreads) {
-            const uint32_t s = s0 + tid;
-            unsigned long long t = 0, u = 0;
-            if (s < n) {
-                const PageSeg g = seg_at(a, e, s);
-                t = seg_tiles(a, e, g);
-                u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
-                if (g.bad && pass == 0 && worker0 == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-            }
-            unsigned long long it = t, iu = u;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long xt = __shfl_up_sync(0xffffffffu, it, d), xu = __shfl_up_sync(0xffffffffu, iu, d);
-                if (lane >= d) {
-                    it += xt;
-                    iu += xu;
-                }
-            }
-            __syncthreads();
-            if (lane == 31) {
-                sums[0][warp] = it;
-                sums[1][warp] = iu;
-            }
-            __syncthreads();
-            unsigned long long bt = run_t, bu = run_u;
-#pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                if (w < warp) {
-                    bt += sums[0][w];
-                    bu += sums[1][w];
-                }
-                run_t += sums[0][w];
-                run_u += sums[1][w];
-            }
-            if (pass == 1 && s < n) {
-                const unsigned long long before = bt + it - t;
-                for (uint32_t k = 0; k < workers_here; ++k) {
-                    const unsigned long long x = (worker0 + k) * share;
-                    if (x >= before && x < before + t) starts[k] = PageCursor{before, bu + iu - u, s};
-                }
-                if (worker0 == 0) {
-                    e.seg_tiles[s] = before;
-                    e.seg_units[s] = bu + iu - u;
-                }
-            }
+    unsigned long long x = 0, sum = 0;           // tiles, and units in the high word
+    if (tid < (int)kPlanSegs) {
+        if (tid < (int)n) {
+            const PageSeg s = seg_at(a, e, tid);
+            const uint32_t tiles = (uint32_t)seg_tiles(a, e, s);
+            x = tiles | (unsigned long long)(tiles != 0 ? (uint32_t)row_tiles(a, e, s) * a.pool.H : 0) << 32;
+            put_seg(t.seg + tid * kSegWords, s);
+            if (s.bad && record && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }
-        all_t = run_u > e.units ? 0 : run_t;
-        share = share_of(all_t, e.workers);
-        if (run_u > e.units && worker0 == 0 && tid == 0 && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
-        if (pass == 1 && worker0 == 0 && tid == 0) {
-            e.seg_tiles[n] = run_t;
-            e.seg_units[n] = run_u;
+        sum = scan_add(x, lane);
+        if (lane == 31) sums[warp] = sum;
+    }
+    __syncthreads();
+    if (tid < (int)kPlanSegs) {
+        for (int w = 0; w < warp; ++w) sum += sums[w];
+        t.tiles[tid + 1] = (uint32_t)sum;
+        t.units[tid + 1] = sum >> 32;
+        if (tid == 0) t.tiles[0] = t.units[0] = 0;
+        if (record && tid < (int)n) {
+            e.seg_tiles[tid + 1] = (uint32_t)sum;
+            e.seg_units[tid + 1] = sum >> 32;
+            if (tid == 0) e.seg_tiles[0] = e.seg_units[0] = 0;
+            if (tid + 1 == (int)n && (sum >> 32) > e.units && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }
     }
     __syncthreads();
-    *total = all_t;
-    return share;
+}
+
+// The table of a call, a worker's first tile *x and its end *x1 (nothing where the units pass the workspace's room).
+__device__ __forceinline__ PageTable table_and_share(const PageAttendArgs &a, const PageEngine &e, bool record, uint32_t worker,
+                                                     PageTableSpace &space, unsigned long long *x, unsigned long long *x1) {
+    PageTable t{e.seg_tiles, e.seg_units, e.seg_table};
+    if (e.small) {
+        fill_table(a, e, record, space);
+        t = PageTable{space.tiles, space.units, space.seg};
+    }
+    const uint32_t n = seg_count(a, e);
+    const unsigned long long total = t.units[n] > e.units ? 0 : t.tiles[n], share = share_of(total, e.workers);
+    *x = worker * share;
+    *x1 = min(total, *x + share);
+    return t;
 }
 
 }  // namespace kvb

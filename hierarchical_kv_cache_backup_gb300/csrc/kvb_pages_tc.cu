@@ -63,7 +63,9 @@ struct Shared {
     uint2 place[4][kTileK];     // fp8: of a tile's tokens: vector count, and 0 past the end, 1 in the pool, 2 outside
     unsigned long long bad[8];  // 16-bit: tokens of a tile in pages outside the pool
     // the piece in hand, kept here so that no role carries what it does not use in registers
-    PageCursor at;
+    PageTableSpace space;
+    PageTable table;
+    uint32_t seg;
     PagePiece piece;
     uint64_t x, x1;
     int seen, whole, none;
@@ -77,7 +79,7 @@ __device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
 
 template <int D, bool kF8, bool kHalf>
 __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const __grid_constant__ PageAttendArgs a) {
-    constexpr int kLoadWarps = load_warps(kF8), kLoadThreads = 32 * kLoadWarps, kThreads = threads_of(kF8);
+    constexpr int kLoadWarps = load_warps(kF8), kLoadThreads = 32 * kLoadWarps;
     constexpr bool kBf = !kF8 && !kHalf;              // type of the operands
     constexpr float kBits = kBf ? 0.0f : 7.0f;        // fp16 weights stand 2^7 higher
     constexpr int NB = blocks_of(D), NQ = q_tiles_of(D), kStages = stages_of(D);
@@ -97,14 +99,13 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
     const PageEngine &e = a.tc;
     if (tid == 0) sh.gave_up = 0;
     {
-        // One warp finds the block's work while another takes tensor memory.
-        const bool few = seg_count(a, e) <= kWarpSegs;
-        unsigned long long total = 0, share = 0;
-        if (!few) share = share_out<kThreads>(a, e, blockIdx.x, 1, &sh.at, &total);
-        else if (warp == 0) share = warp_share(a, e, blockIdx.x, blockIdx.x == 0, &sh.at, &total);
+        unsigned long long x, x1;
+        const PageTable t = table_and_share(a, e, blockIdx.x == 0, blockIdx.x, sh.space, &x, &x1);
         if (tid == 0) {
-            sh.x = blockIdx.x * share;
-            sh.x1 = min(total, sh.x + share);
+            sh.table = t;
+            sh.x = x;
+            sh.x1 = x1;
+            sh.seg = x < x1 ? find_segment(t.tiles, seg_count(a, e), x) : 0;
         }
         if (warp == kSoftWarps + kLoadWarps) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
@@ -115,11 +116,11 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
 
     for (bool first = true;; first = false) {
         if (tid == 0 && sh.x < sh.x1) {
-            sh.piece = piece_at(a, e, &sh.at, sh.x, sh.x1, blockIdx.x);
+            sh.piece = piece_of(a, e, sh.table, &sh.seg, sh.x, sh.x1, blockIdx.x);
             sh.x += sh.piece.k1 - sh.piece.k0;
             const PageSeg &g = sh.piece.s;
             sh.seen = seen_tokens(a, e, g, sh.piece.rt);
-            sh.whole = !g.prefix && sh.piece.k0 == 0 && sh.piece.k1 == sh.piece.n_tiles && group_of(a, g.index, g.q0, g.n) < 0;
+            sh.whole = !g.prefix && sh.piece.k0 == 0 && sh.piece.k1 == sh.piece.n_tiles && (g.in < 0 || a.joined);
             if (!first)
                 for (int i = 0; i < 28; ++i) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bars + 8 * i) : "memory");
             for (int i = 0; i < 4; ++i) {
@@ -151,14 +152,20 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
         const int head = piece.head, end = sh.seen;
         const int row0 = piece.rt * (int)e.row_tile;
         const int rows = (int)min((int64_t)e.row_tile, (int64_t)s.n * group - row0);
-        const int c0 = piece.k0 * kTileK, c1 = min(end, piece.k1 * kTileK);
+        // tiles of the prefix come first (all of them, or those in front of a request's own)
+        const int k0 = piece.k0, pre = s.prefix ? s.len : s.before, pre_tiles = s.prefix ? piece.n_tiles : (int)tiles_of(e, pre);
+        // tile t: its first token, and the end of the tokens that it may hold
+        auto first_of = [&](int t) { return (k0 + t < pre_tiles ? k0 + t : k0 + t - pre_tiles) * kTileK; };
+        auto end_of = [&](int t) { return k0 + t < pre_tiles ? pre : end; };
         const int q_tiles = rows > kTileQ ? 2 : 1;
         // after a wait that ran out the rest of the block's rows are NaN
         const int tiles = sh.gave_up != 0 ? 0 : piece.k1 - piece.k0;
-        const int32_t *table = s.prefix ? a.prefix_pages + (int64_t)s.index * a.prefix_stride
-                                        : a.pages + (int64_t)s.index * a.pages_stride;
+        const int32_t *table = a.pages + (int64_t)s.index * a.pages_stride;
+        const int32_t *pre_table = a.prefix_pages + (int64_t)(s.prefix ? (int)s.index : max(s.in, 0)) * a.prefix_stride;
         const int64_t head_off = (int64_t)head * a.pool.s_head;
-        const int all_see = s.prefix ? end : s.len - s.n + row0 / group + 1;    // tokens that every row sees
+        const int all_see = s.len - s.n + row0 / group + 1;    // own tokens that every row sees
+        // rows see different tokens of tile t
+        auto edge = [&](int t) { return k0 + t >= pre_tiles && min(first_of(t) + kTileK, end) > all_see; };
 
         if (warp < kSoftWarps) {
             // -------------------------------------------------------- softmax
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
             }
             sc = fmaxf(sc, 1.2e-38f);       // never 0, so that a masked score of -infinity stays one
 
-            const int lim = !on || s.prefix ? c1 - 1 : min(s.len - s.n + i, c1 - 1);     // sees tokens 0..lim
+            const int own_lim = on ? min(s.len - s.n + i, end - 1) : end - 1;     // sees own tokens 0..that
             const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
             const uint32_t o = mine + 256 + q * D;
             float m = kNoMax, l = 0.0f;
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                 uint32_t y[64];
                 tmem_ld32(sp, y);
                 tmem_ld32(sp + 32, y + 32);
-                const int t0 = c0 + t * kTileK;
+                const int t0 = first_of(t), lim = k0 + t < pre_tiles ? pre - 1 : own_lim;
                 const bool inside = __all_sync(0xffffffffu, t0 + kTileK - 1 <= lim);
                 tmem_ld_wait();
                 if (!kF8) {
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                     for (int k = 0; k < 64; ++k)
                         if (t0 + k > lim) y[k] = 0xff800000u;      // -infinity
                 }
-                if (!kF8 && min(t0 + kTileK, c1) > all_see) {
+                if (!kF8 && edge(t)) {
                     // Rows see different tokens: a value that is not finite would reach all (0 x NaN).  It
                     // leaves the tile, and the rows that see it are put right at the end.
                     const uint32_t st = t % kStages;
@@ -315,12 +322,24 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                 const unsigned long long sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
                 const unsigned long long less2 = pair(__float_as_uint(less), __float_as_uint(less));
                 unsigned long long sum[2] = {0, 0};
-#pragma unroll
+#pragma unroll(kF8 ? 1 : 2)
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t p[16];
+                    uint32_t p[16], z[32];
+                    if (kF8) {                  // read again: its warps have few registers
+                        tmem_ld32(sp + 32 * h, z);
+                        tmem_ld_wait();
+                        if (!inside) {
+#pragma unroll
+                            for (int b = 0; b < 32; ++b)
+                                if (t0 + 32 * h + b > lim) z[b] = 0xff800000u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 32; ++b) z[b] = y[32 * (kF8 ? 0 : h) + b];
+                    }
 #pragma unroll
                     for (int b = 0; b < 32; b += 2) {
-                        float2 u = unpair(fma2(pair(y[32 * h + b], y[32 * h + b + 1]), sc2, less2));
+                        float2 u = unpair(fma2(pair(z[b], z[b + 1]), sc2, less2));
                         u.x = ex2(u.x);
                         u.y = ex2(u.y);
                         sum[b >> 1 & 1] = add2(sum[b >> 1 & 1], pair(__float_as_uint(u.x), __float_as_uint(u.y)));
@@ -360,7 +379,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                         if (spoiled) {
                             // values that are not finite were left out of tiles that rows see in part
                             uint32_t bad = 0;
-                            for (int t = max(c0, all_see / kTileK * kTileK); t <= lim; ++t) {
+                            for (int t = max(max(0, k0 - pre_tiles) * kTileK, max(0, all_see) / kTileK * kTileK); t <= own_lim; ++t) {
                                 bool wrong;
                                 const int64_t off = token_offset(a.pool, table, (uint32_t)t, &wrong);
                                 if (wrong) continue;
@@ -429,8 +448,8 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                 auto pages_of = [&](int t, int32_t *pg) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int tk = c0 + t * kTileK + 32 * h + lane;
-                        pg[h] = tk < c1 ? table[div_T(a.pool, (uint32_t)tk)] : 0;
+                        const int tk = first_of(t) + 32 * h + lane;
+                        pg[h] = t < tiles && tk < end_of(t) ? (k0 + t < pre_tiles ? pre_table : table)[div_T(a.pool, (uint32_t)tk)] : 0;
                     }
                 };
                 int32_t pg[3][2];
@@ -444,8 +463,8 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                         unsigned long long bads = 0;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int tk = c0 + t * kTileK + 32 * h + lane;
-                            const bool in = tk < c1, bad = in && (uint32_t)pg[0][h] >= a.pool.P;
+                            const int tk = first_of(t) + 32 * h + lane;
+                            const bool in = tk < end_of(t), bad = in && (uint32_t)pg[0][h] >= a.pool.P;
                             where[h] = in && !bad ? vector_index(a.pool, (uint32_t)pg[0][h], (uint32_t)tk) : 0;
                             good[h] = __ballot_sync(0xffffffffu, in && !bad);
                             bads |= (unsigned long long)__ballot_sync(0xffffffffu, bad) << (32 * h);
@@ -477,13 +496,13 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
             const int d = tid - 32 * kSoftWarps, ch = d % PW, tk0 = d / PW;
             const bool idle = ch >= PV;
             auto page_of = [&](int t) {
-                const int tk = c0 + t * kTileK + d;
-                return d < kTileK && tk < c1 ? table[div_T(a.pool, (uint32_t)tk)] : 0;
+                const int tk = first_of(t) + d;
+                return d < kTileK && t < tiles && tk < end_of(t) ? (k0 + t < pre_tiles ? pre_table : table)[div_T(a.pool, (uint32_t)tk)] : 0;
             };
             auto place = [&](int t, int32_t page) {
                 if (d >= kTileK) return;
-                const int tk = c0 + t * kTileK + d;
-                const bool in = tk < c1, bad = in && (uint32_t)page >= a.pool.P;
+                const int tk = first_of(t) + d;
+                const bool in = t < tiles && tk < end_of(t), bad = in && (uint32_t)page >= a.pool.P;
                 sh.place[t & 3][d] = make_uint2(in && !bad ? vector_index(a.pool, (uint32_t)page, (uint32_t)tk) : 0, bad ? 2 : in ? 1 : 0);
                 if (bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
             };
@@ -510,7 +529,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
                     const uint32_t st = t % kStages;
                     bar_wait((comp ? v_free : k_free) + 8 * st, ((t / kStages) & 1) ^ 1, &sh.gave_up);
                     const uint32_t tile = (comp ? v_tile : k_tile) + st * kBytesK;
-                    const bool look = comp == 1 && min(c0 + (t + 1) * kTileK, c1) > all_see;
+                    const bool look = comp == 1 && edge(t);
                     if (!idle)
 #pragma unroll
                         for (int it = 0; it < NI; ++it) {
@@ -672,6 +691,8 @@ cudaError_t preload_pages_tc_kernels() {
     for (const VariantTc &v : kVariantsTc) {
         cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
         if (e == cudaSuccess) e = cudaFuncSetAttribute((const void *)v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute((const void *)v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -294,6 +294,11 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
     if (!empty_call(a))
         *plan = plan_pages(a.requests, a.tokens, a.max_q, a.max_len, a.groups, std::min(a.max_group, a.tokens), a.max_prefix, c.budget,
                            layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms);
+    // the kernels count a request's (or group's) pieces of work in 31 bits, and so the blocks of a launch
+    const uint64_t rows = std::max<uint64_t>((uint64_t)a.max_q, a.groups != 0 ? std::min(a.max_group, a.tokens) : 0) * (a.q_heads / layer->H);
+    if ((rows / 16 + a.max_q + 1) * layer->H * (((uint64_t)a.max_len + a.max_prefix) / 16 + layer->T / 16 + 3) >= (1ull << 31))
+        return fail(KV_ERR_INVALID_ARG, "max_q %u, max_len %u, max_group %u and max_prefix %u make too much work for one request", a.max_q,
+                    a.max_len, a.max_group, a.max_prefix);
     return KV_OK;
 }
 
@@ -313,6 +318,7 @@ void at_workspace(PageEngine *e, void *workspace) {
     e->part_ml = (float *)((uint64_t)(uintptr_t)e->part_ml + w);
     e->seg_tiles = (uint64_t *)((uint64_t)(uintptr_t)e->seg_tiles + w);
     e->seg_units = (uint64_t *)((uint64_t)(uintptr_t)e->seg_units + w);
+    e->seg_table = (int32_t *)((uint64_t)(uintptr_t)e->seg_table + w);
 }
 
 kv_status attend_pages(kv_pool pool, const PagesCall &c, bool selected, void *stream) {
@@ -381,6 +387,7 @@ kv_status attend_pages(kv_pool pool, const PagesCall &c, bool selected, void *st
     const bool fp8 = a.format == KV_CACHE_E4M3;
     k.scale_log2 = a.scale * (fp8 ? a.k_scale : 1.0f) * 1.44269504088896340736f;
     k.v_scale = fp8 ? a.v_scale : 1.0f;
+    k.joined = plan.joined;
     k.rows = plan.rows;
     k.tc = plan.tc;
     at_workspace(&k.rows, a.workspace);
