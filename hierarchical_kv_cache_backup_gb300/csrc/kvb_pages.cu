@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
         const PagePiece piece = piece_of(a, e, table_of, &seg, x, x1, worker);
         const PageSeg &s = piece.s;
         const int rt = piece.rt, head = piece.head, k0 = piece.k0, k1 = piece.k1;
-        x += k1 - k0;
+        x += piece.span;
+        if (k0 >= k1) continue;
 
         const int end = seen_tokens(a, e, s, rt);
         // rows of the tile: new token and head of the group
@@ -634,34 +635,68 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
     const int in = a.joined ? -1 : own.in;
     const int64_t tok = own.q0 + i;
     const int head = qh / group, j = qh - head * group;
+    const PageSeg pre = in >= 0 ? prefix_seg(a, (uint32_t)in) : own;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (qh >= (int)a.q_heads || i >= own.n) return;
-    if (a.rows.on && a.rows.seg_units[seg_count(a, a.rows)] > a.rows.units) return;
-    if (a.tc.on && a.tc.seg_units[seg_count(a, a.tc)] > a.tc.units) return;
+    // all that says where the row's pieces are, in one go
+    const PageEngine &e0 = a.tc.prefix ? a.tc : a.rows, &e1 = a.tc.own ? a.tc : a.rows;
+    const uint32_t at1 = (e1.prefix ? a.groups : 0) + (uint32_t)r, n0 = seg_count(a, e0), n1 = seg_count(a, e1);
+    unsigned long long tiles0 = 0, units0 = 0, total0 = 0, all0 = 0;
+    if (in >= 0) {
+        tiles0 = e0.seg_tiles[in];
+        units0 = e0.seg_units[in];
+        total0 = e0.seg_tiles[n0];
+        all0 = e0.seg_units[n0];
+    }
+    const unsigned long long tiles1 = e1.seg_tiles[at1], units1 = e1.seg_units[at1], total1 = e1.seg_tiles[n1], all1 = e1.seg_units[n1];
+    if ((in >= 0 && all0 > e0.units) || all1 > e1.units) return;
+    const RowPieces p1 = row_pieces(a, e1, own, tiles1, units1, total1, i, head, j);
+    if (in < 0 && p1.any && p1.w0 == p1.w1) return;
+    int c0 = 0, c1 = p1.any ? (int)(p1.w1 - p1.w0) + 1 : 0;       // pieces of the prefix and of its own tokens
+    unsigned long long from0 = 0;
+    if (in >= 0) {
+        const RowPieces p0 = row_pieces(a, e0, pre, tiles0, units0, total0, (int)(tok - pre.q0), head, j);
+        c0 = p0.any ? (int)(p0.w1 - p0.w0) + 1 : 0;
+        from0 = (p0.unit + p0.w0) * e0.slot_rows + p0.row;
+    }
+    const unsigned long long from1 = (p1.unit + p1.w0) * e1.slot_rows + p1.row;
     float top = kNoMax, sum = 0.0f, acc[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] = 0.0f;
-    for (int side = in >= 0 ? 0 : 1; side < 2; ++side) {
-        const PageSeg s = side == 0 ? prefix_seg(a, in) : own;
-        const PageEngine &e = (side == 0 ? a.tc.prefix : a.tc.own) ? a.tc : a.rows;
-        const uint32_t at = side == 0 ? (uint32_t)in : (e.prefix ? a.groups : 0) + (uint32_t)r;
-        const RowPieces p = row_pieces(a, e, s, at, (int)(tok - s.q0), head, j);
-        if (!p.any) continue;
-        if (side == 1 && in < 0 && p.w0 == p.w1) return;
+    // A lane looks after a piece's maximum and sum, 32 pieces at a time; then all take the sums of each.
+    for (int p = part; p < c0 + c1; p += 32 * kW) {
+        const int mine = p + lane * kW, count = min(32, (c0 + c1 - p + kW - 1) / kW);
+        float2 ml = make_float2(kNoMax, 0.0f);
+        unsigned long long o_at = 0;
+        if (mine < c0 + c1) {
+            const bool one = mine < c0;
+            const unsigned long long at = one ? from0 + (unsigned long long)mine * e0.slot_rows : from1 + (unsigned long long)(mine - c0) * e1.slot_rows;
+            ml = *reinterpret_cast<const float2 *>((one ? e0.part_ml : e1.part_ml) + at * 2);
+            o_at = reinterpret_cast<unsigned long long>((one ? e0.part_o : e1.part_o) + at * D);
+        }
+        float most = ml.y != 0.0f ? ml.x : kNoMax;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        most = fmaxf(most, top);
+        const float u = exp2_fast(top - most), f = ml.y != 0.0f ? exp2_fast(ml.x - most) : 0.0f;
+        float add = ml.y * f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+        top = most;
+        sum = sum * u + add;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc[v] *= u;
 #pragma unroll 4
-        for (uint64_t w = p.w0 + part; w <= p.w1; w += kW) {
-            const uint64_t from = (p.unit + w) * e.slot_rows + p.row;
-            const float2 ml = *reinterpret_cast<const float2 *>(e.part_ml + from * 2);
+        for (int k = 0; k < count; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *o = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, o_at, k)) + lane;
             float x[NV];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) x[v] = e.part_o[from * D + v * 32 + lane];
-            if (ml.y == 0.0f) continue;
-            const float t = fmaxf(top, ml.x), u = exp2_fast(top - t), f = exp2_fast(ml.x - t);
-            top = t;
-            sum = sum * u + ml.y * f;
+            for (int v = 0; v < NV; ++v) x[v] = o[v * 32];
+            if (fk == 0.0f) continue;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) acc[v] = acc[v] * u + x[v] * f;
+            for (int v = 0; v < NV; ++v) acc[v] += x[v] * fk;
         }
     }
     if (kW > 1) {
@@ -762,7 +797,7 @@ uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t tokens, uin
 // `span`: the most cached tokens of a unit.
 void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t span, uint32_t D) {
     e->units = units;
-    const uint64_t tiles = units * ((span >> e->kv_shift) + 2);      // at most
+    const uint64_t tiles = units * ((span >> e->kv_shift) + 2 + e->unit_cost);      // at most
     e->small = segs <= kPlanSegs && units < (1ull << 31) && tiles < (1ull << 31);
     if (!e->small) e->seg_table = (int32_t *)take(at, segs * kSegWords * 4);
     const uint64_t rows = (units + e->workers) * e->slot_rows;
@@ -802,6 +837,7 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
         t.kv_shift = pages_tc_shift();
         t.slot_rows = std::min(t.row_tile, most);
         t.team = 1;
+        t.unit_cost = 10;                        // 27,000 cycles
         t.workers = (uint32_t)sms;
         t_units = most_units(t, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
     }
@@ -818,17 +854,20 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
             // beginning and end: as many for tcgen05 as its share of the cycles, about 12 D a tile of 64
             // cached tokens (twice that from fp8) against 20 D a warp's tile of 16.  64 requests of up to 1,000
             // tokens behind 8,192: 96 us one after the other on all SMs.
-            const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * 12.0 * D * (fp8 ? 2 : 1);
-            const double rows_cost = (double)e_units * (max_len / 16 + 1) * 20.0 * D / (kWarps * v->blocks);
+            const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * (fp8 ? 18.0 : 20.0) * D;
+            const double rows_cost = (double)e_units * (max_len / 16 + 1) * 25.0 * D / (kWarps * v->blocks);
             const double part = (double)sms * tc_cost / (tc_cost + rows_cost);
             t.workers = (uint32_t)std::min<double>(sms - 1, std::max(1.0, std::floor(part + 0.5)));
             e_sms = (uint32_t)sms - t.workers;
         }
-        const uint32_t blocks = e_sms * (uint32_t)v->blocks;
+        // A few places are left free: a block that found none at the start (the kernel in front still in it) would
+        // begin when the others end (selected decode of 48 requests: 48 us, 80 where that happened).
+        const uint32_t places = e_sms * (uint32_t)v->blocks, blocks = places - places / 32;
         // A warp works by itself (what a unit takes to begin and end is paid once); where that would make
         // more than 16 pieces of a unit, a block's four warps share one, so that fewer pieces have to be joined.
         e.team = 4 * e_units >= blocks ? 1 : kWarps;
         e.kv_shift = e.team == 1 ? 4 : 6;
+        e.unit_cost = e.team == 1 ? 5 : 4;       // 12,000 cycles
         e.workers = blocks * (kWarps / e.team);
         place(&e, &at, e_units, segs, span, D);
         p.wide_join = e.workers > 6 * e_units;

@@ -23,6 +23,7 @@ namespace kvb {
 struct PageEngine {
     uint32_t on;              // launched for this call
     uint32_t prefix, own;     // which segments it takes: groups' prefixes first, then requests
+    uint32_t unit_cost;       // what a unit takes to begin and end, in tiles
     uint32_t row_tile, kv_shift;   // query rows of a unit, log2 of the cached tokens of a tile
     uint32_t workers;
     uint32_t slot_rows;       // query rows of a slot
@@ -153,12 +154,18 @@ KVB_HD uint32_t unit_tiles(const PageAttendArgs &a, const PageEngine &e, const P
     return tiles_of(e, s.before) + tiles_of(e, seen_tokens(a, e, s, rt));
 }
 
-// Tiles of the row tiles before rt, for one head.
+// What a unit counts when work is shared out: its tiles, and in front of them unit_cost.
+KVB_HD uint32_t unit_span(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
+    const uint32_t n = unit_tiles(a, e, s, rt);
+    return n == 0 ? 0 : n + e.unit_cost;
+}
+
+// The spans of the row tiles before rt, for one head.
 KVB_HD uint64_t tiles_before(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt) {
     if (rt == 0) return 0;
-    if (s.prefix || a.picks != nullptr) return (uint64_t)rt * unit_tiles(a, e, s, 0);
+    if (s.prefix || a.picks != nullptr) return (uint64_t)rt * unit_span(a, e, s, 0);
     uint64_t sum = 0;
-    for (int i = 0; i < rt; ++i) sum += unit_tiles(a, e, s, i);
+    for (int i = 0; i < rt; ++i) sum += unit_span(a, e, s, i);
     return sum;
 }
 
@@ -172,10 +179,12 @@ KVB_HD uint64_t quotient(uint64_t a, uint64_t b) { return ((a | b) >> 32) == 0 ?
 // Tiles of a worker.
 KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : quotient(tiles + workers - 1, workers); }
 
-// A worker's tiles [k0, k1) of the n_tiles of a unit.
+// A worker's tiles [k0, k1) of the n_tiles of a unit (none where its run ends in front of them), and how much of
+// the run that is.
 struct PagePiece {
     PageSeg s;
     int rt, head, k0, k1, n_tiles;
+    uint32_t span;
     uint64_t slot;
 };
 
@@ -211,8 +220,8 @@ KVB_HD uint32_t find_segment(const uint64_t *tiles, uint32_t n, uint64_t x) {
     return lo;
 }
 
-// The piece of `worker` that begins with tile x (x < x1, its last tile); *seg: a segment at x or before.
-// A segment has fewer than 2^31 tiles.
+// The piece of `worker` that begins at x of its run (x < x1, the run's end); *seg: a segment at x or before.
+// A segment counts fewer than 2^31.
 KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const PageTable &t, uint32_t *seg, uint64_t x, uint64_t x1,
                           uint32_t worker) {
     uint32_t i = *seg;
@@ -229,7 +238,7 @@ KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const Pa
     p.s.bad = false;
     p.s.prefix = i < before;
     p.s.index = i < before ? i : i - before;
-    uint32_t rel = (uint32_t)(x - t.tiles[i]), n = unit_tiles(a, e, p.s, 0);
+    uint32_t rel = (uint32_t)(x - t.tiles[i]), n = unit_span(a, e, p.s, 0);
     p.rt = 0;
     if (p.s.prefix || a.picks != nullptr) {
         p.rt = (int)(rel / (n * H));
@@ -237,13 +246,16 @@ KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const Pa
     } else {
         while (rel >= n * H) {
             rel -= n * H;
-            n = unit_tiles(a, e, p.s, ++p.rt);
+            n = unit_span(a, e, p.s, ++p.rt);
         }
     }
-    p.n_tiles = (int)n;
+    const uint32_t c = e.unit_cost;
+    p.n_tiles = (int)(n - c);
     p.head = (int)(rel / n);
-    p.k0 = (int)(rel - (uint32_t)p.head * n);
-    p.k1 = x1 - x < n - (uint32_t)p.k0 ? p.k0 + (int)(x1 - x) : (int)n;
+    const uint32_t v0 = rel - (uint32_t)p.head * n, v1 = x1 - x < n - v0 ? v0 + (uint32_t)(x1 - x) : n;
+    p.k0 = v0 > c ? (int)(v0 - c) : 0;
+    p.k1 = v1 > c ? (int)(v1 - c) : 0;
+    p.span = v1 - v0;
     p.slot = t.units[i] + (uint64_t)p.rt * H + p.head + worker;
     return p;
 }
@@ -255,21 +267,22 @@ struct RowPieces {
     bool any;
 };
 
-// Row (query token i of segment s, head j of the KV head's group) of a segment that is number
-// `at` of the engine's.
-KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint32_t at, int i, int head, int j) {
+// Row (query token i of segment s, head j of the KV head's group) of a segment that `tiles_at` tiles and
+// `units_at` units of all the engine's `total` tiles come before.
+KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint64_t tiles_at, uint64_t units_at,
+                            uint64_t total, int i, int head, int j) {
     RowPieces p;
     const int rt_n = (int)e.row_tile, g = (int)a.group;
     const int row = i * g + j;
     const int rt = a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + j / rt_n : row / rt_n;
-    const uint32_t n = unit_tiles(a, e, s, rt);
+    const uint32_t n = unit_span(a, e, s, rt);
     p.any = n != 0;
     p.row = a.picks != nullptr ? j % rt_n : row % rt_n;
-    const uint64_t share = share_of(e.seg_tiles[seg_count(a, e)], e.workers);
-    const uint64_t t0 = e.seg_tiles[at] + tiles_before(a, e, s, rt) * a.pool.H + (uint64_t)head * n;
-    p.w0 = quotient(t0, share);
+    const uint64_t share = share_of(total, e.workers);
+    const uint64_t t0 = tiles_at + tiles_before(a, e, s, rt) * a.pool.H + (uint64_t)head * n;
+    p.w0 = quotient(t0 + (n != 0 ? e.unit_cost : 0), share);      // the first that holds tiles
     p.w1 = quotient(t0 + (n != 0 ? n : 1) - 1, share);
-    p.unit = e.seg_units[at] + (uint64_t)rt * a.pool.H + head;
+    p.unit = units_at + (uint64_t)rt * a.pool.H + head;
     return p;
 }
 

@@ -8,9 +8,9 @@
 //   2 warps  16-bit pages: bring keys and values into swizzled tiles in shared memory by
 //            cp.async.  TMA gathers of four tokens were measured: a warp issues one in 70 cycles, so
 //            that the 64 of a tile took 4,300 cycles from one warp, 2,500 from three
-//   4 warps  fp8 pages: the same through registers, as fp16, exact
+//   4 warps  (8 for heads over 128) fp8 pages: the same through registers, as fp16, exact
 //   1 warp   issues tcgen05.mma: scores S = Q K^T and sums O += P V
-//   4 + 4    softmax of the two tiles, one row a thread: scores come from tensor
+//   4 + 4    softmax of the two tiles (4 of one), one row a thread: scores come from tensor
 //            memory, weights go back there, the A operand of P V
 // Tensor memory holds two buffers of 64 scores a row for each tile (P overwrites S) and
 // O0, O1 (D columns each; one of up to 256).
@@ -32,15 +32,17 @@ using namespace tc;
 namespace {
 
 constexpr int kTileQ = 128, kTileK = 64;
-constexpr int kSoftWarps = 8;
-__host__ __device__ constexpr int load_warps(bool f8) { return f8 ? 4 : 2; }
-__host__ __device__ constexpr int threads_of(bool f8) { return 32 * (kSoftWarps + load_warps(f8) + 1); }
 constexpr float kNoMax = -3.0e38f;
 // 64 values (128 bytes, swizzled) of every row of a tile
 constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
 __host__ __device__ constexpr int q_tiles_of(int D) { return D > 128 ? 1 : 2; }
+// Softmax warps, and those that bring keys and values: 13 warps of fp8 (128 registers a thread), 11 or 7 of
+// 16 bits.
+__host__ __device__ constexpr int soft_warps(int D) { return 4 * q_tiles_of(D); }
+__host__ __device__ constexpr int load_warps(int D, bool f8) { return f8 ? 12 - soft_warps(D) : 2; }
+__host__ __device__ constexpr int threads_of(int D, bool f8) { return 32 * (soft_warps(D) + load_warps(D, f8) + 1); }
 // Stages of keys, and as many of values.
 __host__ __device__ constexpr int stages_of(int D) { return D > 192 ? 2 : D > 64 ? 3 : 4; }
 __host__ __device__ constexpr int smem_of(int D) {
@@ -78,8 +80,8 @@ __device__ __forceinline__ void copy16(uint32_t smem, uint64_t gmem, bool on) {
 }
 
 template <int D, bool kF8, bool kHalf>
-__global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const __grid_constant__ PageAttendArgs a) {
-    constexpr int kLoadWarps = load_warps(kF8), kLoadThreads = 32 * kLoadWarps;
+__global__ void __launch_bounds__(threads_of(D, kF8), 1) kv_pages_tc_kernel(const __grid_constant__ PageAttendArgs a) {
+    constexpr int kSoftWarps = soft_warps(D), kLoadWarps = load_warps(D, kF8), kLoadThreads = 32 * kLoadWarps;
     constexpr bool kBf = !kF8 && !kHalf;              // type of the operands
     constexpr float kBits = kBf ? 0.0f : 7.0f;        // fp16 weights stand 2^7 higher
     constexpr int NB = blocks_of(D), NQ = q_tiles_of(D), kStages = stages_of(D);
@@ -115,9 +117,13 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
     const int group = (int)a.group;
 
     for (bool first = true;; first = false) {
-        if (tid == 0 && sh.x < sh.x1) {
+        bool found = false;
+        while (tid == 0 && !found && sh.x < sh.x1) {
             sh.piece = piece_of(a, e, sh.table, &sh.seg, sh.x, sh.x1, blockIdx.x);
-            sh.x += sh.piece.k1 - sh.piece.k0;
+            sh.x += sh.piece.span;
+            found = sh.piece.k0 < sh.piece.k1;
+        }
+        if (found) {
             const PageSeg &g = sh.piece.s;
             sh.seen = seen_tokens(a, e, g, sh.piece.rt);
             sh.whole = !g.prefix && sh.piece.k0 == 0 && sh.piece.k1 == sh.piece.n_tiles && (g.in < 0 || a.joined);
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(threads_of(kF8), 1) kv_pages_tc_kernel(const _
             // the scale's sign goes into the queries; a scale of 0 takes zeros
             const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.0f ? 0u : 0xffffffffu;
             float sc = fabsf(a.scale_log2);
-            if (q < NQ && tiles > 0) {
+            if (tiles > 0) {
                 // A warp brings its 32 rows, neighbouring lanes a row's 16-byte pieces.
                 constexpr int PQ = D / 8, AT = PQ <= 8 ? 4 : PQ <= 16 ? 2 : 1, kBatch = 8;
                 const int sub = lane / PQ, ch = lane - sub * PQ;
@@ -653,11 +659,11 @@ struct VariantTc {
     uint32_t D;
     bool fp8, fp16;
     PagesTcFn *fn;
-    int smem;
+    int smem, threads;
 };
 template <int D, bool kF8, bool kHalf>
 constexpr VariantTc variant_tc() {
-    return VariantTc{(uint32_t)D, kF8, kHalf, kv_pages_tc_kernel<D, kF8, kHalf>, smem_of(D)};
+    return VariantTc{(uint32_t)D, kF8, kHalf, kv_pages_tc_kernel<D, kF8, kHalf>, smem_of(D), threads_of(D, kF8)};
 }
 #define KVB_PAGES_TC(D) \
     variant_tc<D, false, false>(), variant_tc<D, false, true>(), variant_tc<D, true, false>(), variant_tc<D, true, true>()
@@ -673,7 +679,7 @@ cudaError_t launch_pages_tc(const PageAttendArgs &a, uint32_t D, bool fp8, bool 
         if (v.D != D || v.fp8 != fp8 || v.fp16 != fp16) continue;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.tc.workers);
-        cfg.blockDim = dim3((unsigned)threads_of(fp8));
+        cfg.blockDim = dim3((unsigned)v.threads);
         cfg.dynamicSmemBytes = (size_t)v.smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32) kv_bound_kernel(const __grid
 constexpr int kScoreWarps = 8, kHeads = 4;
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kScoreWarps * 32) kv_score_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __grid_constant__ SelectArgs a) {
     using P = Pair16<!kHalf>;
     constexpr int NG = D / 32, LG = NG <= 2 ? 2 : NG <= 4 ? 4 : 8, SLOTS = 32 / LG;
     constexpr uint32_t kRec = (2 * D + D / 8 + 15) / 16 * 16;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv_score_kernel(const __grid
     const int seen = pages_seen(len, q1 - q0, i, a.T);
     if (seen <= (int)a.budget || p0 >= seen) return;
     const int64_t tok = q0 + i;
-    const int p1 = min(seen, p0 + (int)a.block_pages);
+    const int p1 = min(seen, p0 + (int)a.block_pages);      // block_pages: at most 64 a warp
     const int slot = lane / LG, gr = lane % LG;
     const int32_t *table = a.pages + (int64_t)r * a.pages_stride;
     float *scores = a.scores + (tok * a.H + head) * (int64_t)a.max_pages;
@@ -236,62 +236,93 @@ __global__ void __launch_bounds__(kScoreWarps * 32) kv_score_kernel(const __grid
             neg[h][4] = x.x; neg[h][5] = x.y; neg[h][6] = x.z; neg[h][7] = x.w;
             t[h] = unit[h][gu];
         }
-#pragma unroll 2
-        for (int p = p0 + warp * SLOTS; p < p1; p += kScoreWarps * SLOTS) {
-            const int mine = p + slot;
-            const bool on = mine < p1;
-            const uint32_t page = on ? (uint32_t)table[mine] : 0;
-            const bool bad = on && page >= a.P;
-            int lo[8], hi[8];
-            float step = 0.0f;
+        // A warp takes a run of the block's pages; it reads their ids at once, and a record while it
+        // multiplies the one before.
+        const int w0 = p0 + warp * ((int)a.block_pages / kScoreWarps), w1 = min(p1, w0 + (int)a.block_pages / kScoreWarps);
+        uint32_t ids[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) lo[k] = hi[k] = 0;
-            if (on && !bad && gr < NG) {
+        for (int k = 0; k < 2; ++k) ids[k] = w0 + 32 * k + lane < w1 ? (uint32_t)table[w0 + 32 * k + lane] : 0;
+        struct Record {
+            int4 lo[2], hi[2];
+            float step;
+            bool on, bad;
+        };
+        auto fetch = [&](int p) {
+            Record c;
+            const int at = p - w0 + slot;
+            const uint32_t i0 = __shfl_sync(0xffffffffu, ids[0], at & 31), i1 = __shfl_sync(0xffffffffu, ids[1], at & 31);
+            const uint32_t page = at < 32 ? i0 : i1;
+            c.on = p + slot < w1;
+            c.bad = c.on && page >= a.P;
+            c.lo[0] = c.lo[1] = c.hi[0] = c.hi[1] = make_int4(0, 0, 0, 0);
+            c.step = 0.0f;
+            if (c.on && !c.bad && gr < NG) {
                 const uint8_t *rec = a.bounds + ((uint64_t)page * a.H + head) * kRec + 32 * gr;
-                const int4 u = *reinterpret_cast<const int4 *>(rec), v = *reinterpret_cast<const int4 *>(rec + 16);
-                const int4 w = *reinterpret_cast<const int4 *>(rec + D), x = *reinterpret_cast<const int4 *>(rec + D + 16);
-                step = *reinterpret_cast<const float *>(rec + 2 * D - 32 * gr + 4 * gr);
-                lo[0] = u.x; lo[1] = u.y; lo[2] = u.z; lo[3] = u.w; lo[4] = v.x; lo[5] = v.y; lo[6] = v.z; lo[7] = v.w;
-                hi[0] = w.x; hi[1] = w.y; hi[2] = w.z; hi[3] = w.w; hi[4] = x.x; hi[5] = x.y; hi[6] = x.z; hi[7] = x.w;
+                c.lo[0] = *reinterpret_cast<const int4 *>(rec);
+                c.lo[1] = *reinterpret_cast<const int4 *>(rec + 16);
+                c.hi[0] = *reinterpret_cast<const int4 *>(rec + D);
+                c.hi[1] = *reinterpret_cast<const int4 *>(rec + D + 16);
+                c.step = *reinterpret_cast<const float *>(rec + 2 * D - 32 * gr + 4 * gr);
             }
+            return c;
+        };
+        Record next = fetch(w0);
+        for (int p = w0; p < w1; p += SLOTS) {
+            const Record c = next;
+            if (p + SLOTS < w1) next = fetch(p + SLOTS);
+            const int lo[8] = {c.lo[0].x, c.lo[0].y, c.lo[0].z, c.lo[0].w, c.lo[1].x, c.lo[1].y, c.lo[1].z, c.lo[1].w};
+            const int hi[8] = {c.hi[0].x, c.hi[0].y, c.hi[0].z, c.hi[0].w, c.hi[1].x, c.hi[1].y, c.hi[1].z, c.hi[1].w};
             float best = -INFINITY;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 int dot = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) dot = __dp4a(neg[h][k], lo[k], __dp4a(pos[h][k], hi[k], dot));
-                const float term = __fmul_rn((float)dot, __fmul_rn(step, t[h]));
+                const float term = __fmul_rn((float)dot, __fmul_rn(c.step, t[h]));
                 float sum = __shfl_sync(0xffffffffu, term, slot * LG);
 #pragma unroll
                 for (int g = 1; g < NG; ++g) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, term, slot * LG + g));
                 if (!(fabsf(sum) <= kMostScore)) sum = kMostScore;
                 if (h < heads) best = fmaxf(best, sum);
             }
-            if (on && gr == 0) {
-                if (bad) best = -kMostScore;                 // nothing to be found there
-                if (h0 != 0) best = fmaxf(best, scores[mine]);
-                scores[mine] = best;
-                if (bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
+            if (c.on && gr == 0) {
+                if (c.bad) best = -kMostScore;               // nothing to be found there
+                if (h0 != 0) best = fmaxf(best, scores[p + slot]);
+                scores[p + slot] = best;
+                if (c.bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_PAGE);
             }
         }
     }
 }
 
-// Picks: a block takes one query and KV head.  The least key that is selected is found by
-// histograms over the range of keys that is left, 2,048 bins at a time (the first over the keys'
-// own range, so that scores of one size spread over the bins); then every thread looks at a run
-// of pages, and a sum over the block says where its picks go, in the order of the pages.
-constexpr int kPickThreads = 1024, kBins = 2048, kHeld = 8;
+// Picks: a block takes one query and KV head, a thread a run of pages.  The least key that is selected is
+// found by a histogram over the range of the keys (so that scores of one size spread over the
+// bins); what is in its bin is ranked, key against key, or, if too much, spread over bins again.  A sum
+// over the block then says where a thread's picks go, in the order of the pages.  Rows of up to 2,048 pages
+// take 256 threads, longer ones 1,024.
+constexpr int kHeld = 8, kRanked = 256, kShortRow = 2048;
+
+__device__ __forceinline__ unsigned long long scan_up(unsigned long long x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
 
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __float_as_uint(x);
     return u ^ ((u >> 31) != 0 ? 0xffffffffu : 0x80000000u);
 }
 
+template <int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ uint32_t bins[kBins];
-    __shared__ unsigned long long sums[32];
-    __shared__ uint32_t least_s[32], most_s[32], found[3];
+    constexpr int kBins = 2 * kPickThreads, kBinBits = kPickThreads == 1024 ? 11 : 9, kWarps = kPickThreads / 32;
+    static_assert(kBins == 1 << kBinBits && kRanked <= kPickThreads, "two bins a thread");
+    __shared__ uint32_t bins[kBins], ranked[kRanked];
+    __shared__ uint32_t sums[kWarps], least_s[kWarps], most_s[kWarps], found[3], listed;
+    __shared__ unsigned long long wide[kWarps];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.x, i = blockIdx.y, r = blockIdx.z;
@@ -320,19 +351,22 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) held[j] = j < per && candidate(b0 + j) ? order_key(scores[b0 + j]) : 0u;
     }
+    // every page of the run in turn: its number, and its key if it is a candidate (else it is kept)
     auto each = [&](auto &&f) {
         if (per <= kHeld) {
 #pragma unroll
             for (int j = 0; j < kHeld; ++j)
-                if (j < per && candidate(b0 + j)) f(held[j]);
+                if (j < per && b0 + j < n) f(b0 + j, held[j], candidate(b0 + j));
         } else {
-            for (int p = c0 + tid; p < c1; p += kPickThreads) f(order_key(scores[p]));
+            for (int p = b0; p < min(n, b0 + per); ++p) f(p, candidate(p) ? order_key(scores[p]) : 0u, candidate(p));
         }
     };
     uint32_t lo = 0xffffffffu, hi = 0;
-    each([&](uint32_t u) {
-        lo = min(lo, u);
-        hi = max(hi, u);
+    each([&](int, uint32_t u, bool c) {
+        if (c) {
+            lo = min(lo, u);
+            hi = max(hi, u);
+        }
     });
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
@@ -340,19 +374,20 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_cons
         least_s[warp] = lo;
         most_s[warp] = hi;
     }
+    if (tid == 0) listed = 0;
     __syncthreads();
-    lo = __reduce_min_sync(0xffffffffu, least_s[lane]);
-    hi = __reduce_max_sync(0xffffffffu, most_s[lane]);
+    lo = __reduce_min_sync(0xffffffffu, least_s[lane % kWarps]);
+    hi = __reduce_max_sync(0xffffffffu, most_s[lane % kWarps]);
     uint32_t need = k;                                       // of the keys equal to the least one selected
     while (k != 0 && lo != hi) {
-        const int shift = max(0, 32 - __clz(hi - lo) - 11);
-        for (int b = tid; b < kBins; b += kPickThreads) bins[b] = 0;
+        const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
+        bins[tid] = bins[tid + kPickThreads] = 0;
         __syncthreads();
-        each([&](uint32_t u) {
-            if (u >= lo && u <= hi) atomicAdd(&bins[(u - lo) >> shift], 1u);
+        each([&](int, uint32_t u, bool c) {
+            if (c && u >= lo && u <= hi) atomicAdd(&bins[(u - lo) >> shift], 1u);
         });
         __syncthreads();
-        // keys in the bins above: thread t looks after bins 2046 - 2 t and the next
+        // keys in the bins above: thread t looks after the last bins but 2 t and 2 t + 1
         const uint32_t x1 = bins[kBins - 1 - 2 * tid], x0 = bins[kBins - 2 - 2 * tid];
         uint32_t s = x0 + x1;
 #pragma unroll
@@ -360,9 +395,9 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_cons
             const uint32_t y = __shfl_up_sync(0xffffffffu, s, d);
             if (lane >= d) s += y;
         }
-        if (lane == 31) least_s[warp] = s;
+        if (lane == 31) sums[warp] = s;
         __syncthreads();
-        uint32_t before = lane < warp ? least_s[lane] : 0;
+        uint32_t before = lane < warp ? sums[lane % kWarps] : 0;
         before = __reduce_add_sync(0xffffffffu, before) + s - x0 - x1;
         if (before < k && before + x1 >= k) {
             found[0] = (uint32_t)(kBins - 1 - 2 * tid);
@@ -383,45 +418,54 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(const __grid_cons
             need = 0xffffffffu;
             break;
         }
+        if (inside <= kRanked && lo != hi) {
+            each([&](int, uint32_t u, bool c) {
+                if (c && u >= lo && u <= hi) ranked[atomicAdd(&listed, 1u)] = u;
+            });
+            __syncthreads();
+            if (tid < (int)inside) {
+                const uint32_t mine = ranked[tid];
+                uint32_t above = 0, same = 0;
+                for (uint32_t j = 0; j < inside; ++j) {
+                    above += ranked[j] > mine;
+                    same += ranked[j] == mine;
+                }
+                if (above < k && above + same >= k) {        // equal keys write the same
+                    found[0] = mine;
+                    found[1] = k - above;
+                }
+            }
+            __syncthreads();
+            lo = found[0];
+            need = found[1];
+            break;
+        }
     }
     if (k == 0) {                                            // the pages that are kept fill the budget
         lo = 0xffffffffu;
         need = 0;
     }
     // key > lo is selected, key == lo for the first `need` of them, and with need without bound all from lo on
-    auto above = [&](int p, uint32_t u) { return !candidate(p) || u > lo; };
-    unsigned long long mine = 0;                             // above, and equal in the high word
-    for (int j = 0; j < per; ++j) {
-        const int p = b0 + j;
-        if (p >= n) break;
-        const uint32_t u = candidate(p) ? order_key(scores[p]) : 0;
-        if (above(p, u)) mine += 1;
+    unsigned long long mine = 0;                             // selected, and equal in the high word
+    each([&](int, uint32_t u, bool c) {
+        if (!c || u > lo) mine += 1;
         else if (u == lo) mine += 1ull << 32;
-    }
-    unsigned long long s = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += y;
-    }
+    });
+    const unsigned long long sum = scan_up(mine, lane);
+    if (lane == 31) wide[warp] = sum;
     __syncthreads();
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    unsigned long long before = s - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
+    unsigned long long before = sum - mine;
+    for (int w = 0; w < warp; ++w) before += wide[w];
     uint32_t gt = (uint32_t)before, eq = (uint32_t)(before >> 32);
-    for (int j = 0; j < per; ++j) {
-        const int p = b0 + j;
-        if (p >= n) break;
-        const uint32_t u = candidate(p) ? order_key(scores[p]) : 0;
-        if (above(p, u)) {
+    each([&](int p, uint32_t u, bool c) {
+        if (!c || u > lo) {
             picks[gt + min(eq, need)] = p;
             ++gt;
         } else if (u == lo) {
             if (eq < need) picks[gt + eq] = p;
             ++eq;
         }
-    }
+    });
 }
 
 typedef void(BoundFn)(BoundArgs);
@@ -471,9 +515,9 @@ cudaError_t launch_bound(const BoundArgs &a, uint32_t D, bool fp8, bool fp16, bo
 }
 
 uint32_t select_block_pages(uint64_t pages, int sms) {
-    // about four blocks an SM, of 64 pages at least (a step of the block's warps at heads of 128) and 1,024 at most
-    const uint64_t want = pages / (4ull * (uint64_t)sms);
-    return (uint32_t)std::min<uint64_t>(1024, std::max<uint64_t>(64, (want + 63) / 64 * 64));
+    // two blocks an SM, all at once (one request of 8,192 pages: 13.9 us; with four an SM 16.0), of 64 pages at least (a step of the block's warps at heads of 128) and 512 at most
+    const uint64_t want = pages / (2ull * (uint64_t)sms);
+    return (uint32_t)std::min<uint64_t>(64 * kScoreWarps, std::max<uint64_t>(64, (want + 63) / 64 * 64));
 }
 
 cudaError_t launch_select(const SelectArgs &a, uint32_t D, bool fp16, bool pdl, cudaStream_t stream, int *launches) {
@@ -486,7 +530,9 @@ cudaError_t launch_select(const SelectArgs &a, uint32_t D, bool fp16, bool pdl, 
             if (e != cudaSuccess) return e;
             ++*launches;
         }
-        const cudaError_t e = launch(kv_pick_kernel, dim3(a.H, a.max_q, a.requests), kPickThreads, stream, pdl, a);
+        const dim3 grid(a.H, a.max_q, a.requests);
+        const cudaError_t e = a.max_pages <= (uint32_t)kShortRow ? launch(kv_pick_kernel<256>, grid, 256, stream, pdl, a)
+                                                                 : launch(kv_pick_kernel<1024>, grid, 1024, stream, pdl, a);
         if (e == cudaSuccess) ++*launches;
         return e;
     }
@@ -503,7 +549,8 @@ cudaError_t preload_select_kernels() {
         const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
         if (e != cudaSuccess) return e;
     }
-    return cudaFuncGetAttributes(&at, (const void *)kv_pick_kernel);
+    const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)kv_pick_kernel<256>);
+    return e != cudaSuccess ? e : cudaFuncGetAttributes(&at, (const void *)kv_pick_kernel<1024>);
 }
 
 }  // namespace kvb

@@ -296,7 +296,7 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
                            layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms);
     // the kernels count a request's (or group's) pieces of work in 31 bits, and so the blocks of a launch
     const uint64_t rows = std::max<uint64_t>((uint64_t)a.max_q, a.groups != 0 ? std::min(a.max_group, a.tokens) : 0) * (a.q_heads / layer->H);
-    if ((rows / 16 + a.max_q + 1) * layer->H * (((uint64_t)a.max_len + a.max_prefix) / 16 + layer->T / 16 + 3) >= (1ull << 31))
+    if ((rows / 16 + a.max_q + 1) * layer->H * (((uint64_t)a.max_len + a.max_prefix) / 16 + layer->T / 16 + 16) >= (1ull << 31))
         return fail(KV_ERR_INVALID_ARG, "max_q %u, max_len %u, max_group %u and max_prefix %u make too much work for one request", a.max_q,
                     a.max_len, a.max_group, a.max_prefix);
     return KV_OK;

@@ -19,7 +19,7 @@ HARNESS = r"""
 using namespace kvb;
 // Cuts a call among workers and takes every row's pieces back together.  Returns 0, or the number of
 // the check that failed.  in: requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group,
-// T, budget, row_tile, kv_tile, workers, prefix, own, joined; units: room in the workspace.
+// T, budget, row_tile, kv_tile, workers, prefix, own, joined, unit_cost; units: room in the workspace.
 extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const int *group_start, const int *prefix_lens,
                      unsigned long long units, unsigned long long *total) {
     PageAttendArgs a{};
@@ -31,7 +31,7 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
     PageEngine &e = a.rows;
     while ((1ull << a.pool.t_shift) < (unsigned)in[9]) ++a.pool.t_shift;      // division by T, as the library's
     a.pool.t_mul = (uint32_t)(((1ull << 32) * ((1ull << a.pool.t_shift) - in[9])) / in[9] + 1);
-    e.row_tile = in[11]; e.kv_shift = in[12] == 16 ? 4 : 6; e.workers = in[13]; e.prefix = in[14]; e.own = in[15]; a.joined = in[16];
+    e.row_tile = in[11]; e.kv_shift = in[12] == 16 ? 4 : 6; e.workers = in[13]; e.prefix = in[14]; e.own = in[15]; a.joined = in[16]; e.unit_cost = in[17];
     const uint32_t n = seg_count(a, e);
     std::vector<uint64_t> st(n + 1), su(n + 1);
     uint64_t t = 0, u = 0;
@@ -59,11 +59,13 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
         if (x < st[seg] || x >= st[seg + 1]) return 11;
         while (x < x1) {
             const PagePiece p = piece_of(a, e, table, &seg, x, x1, w);
-            if (p.k1 <= p.k0 || p.k1 > p.n_tiles || p.head >= (int)a.pool.H || p.rt >= row_tiles(a, e, p.s)) return 2;
+            done += p.span;
+            x += p.span;
+            if (p.span == 0) return 12;
+            if (p.k1 <= p.k0) continue;
+            if ( p.k1 > p.n_tiles || p.head >= (int)a.pool.H || p.rt >= row_tiles(a, e, p.s)) return 2;
             if ((uint32_t)p.n_tiles != unit_tiles(a, e, p.s, p.rt)) return 3;
             if (p.slot >= units + e.workers || !slots.emplace(p.slot, p).second) return 4;
-            done += p.k1 - p.k0;
-            x += p.k1 - p.k0;
         }
     }
     if (done != t) return 5;
@@ -72,7 +74,7 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
         for (int i = 0; i < g.n; ++i)
             for (uint32_t h = 0; h < a.pool.H; ++h)
                 for (uint32_t j = 0; j < a.group; ++j) {
-                    const RowPieces r = row_pieces(a, e, g, s, i, h, j);
+                    const RowPieces r = row_pieces(a, e, g, st[s], su[s], t, i, h, j);
                     int at = 0;
                     if (r.any)
                         for (uint64_t w = r.w0; w <= r.w1; ++w) {
@@ -129,7 +131,7 @@ def most_units(segs, tokens, most, group, row_tile, picked):
     return min(segs * -(-most * group // row_tile), tokens * group // row_tile + segs)
 
 
-def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, budget, row_tile, kv_tile, workers, prefix, own, joined=0):
+def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, budget, row_tile, kv_tile, workers, prefix, own, joined=0, cost=0):
     n_q = [rng.choice((0, 1, max_q, rng.randint(0, max_q))) for _ in range(requests)]
     q_start = np.cumsum([0] + n_q)
     lens = [rng.choice((0, 1, max_len, rng.randint(0, max_len))) for _ in range(requests)]
@@ -140,7 +142,7 @@ def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, bu
     units = H * ((most_units(groups, tokens, max_group, group, row_tile, False) if prefix else 0) +
                  (most_units(requests, tokens, max_q, group, row_tile, budget > 0) if own else 0))
     arrays = [i32(x) for x in ([requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group, T, budget,
-                                row_tile, kv_tile, workers, prefix, own, joined], q_start, lens, marks, prefix_lens or [0])]
+                                row_tile, kv_tile, workers, prefix, own, joined, cost], q_start, lens, marks, prefix_lens or [0])]
     total = ctypes.c_uint64()
     got = host.h_cut(*(x.ctypes.data for x in arrays), units, ctypes.byref(total))
     assert got == 0, (got, n_q, lens, marks, prefix_lens)
@@ -156,7 +158,7 @@ def test_pieces_cover_every_row_once(host, seed):
     cut(host, rng, rng.choice((1, 3, 40, 150)), rng.choice((1, 5, 33)), rng.choice((1, 17, 500)), groups, rng.choice((0, 1, 900)),
         rng.choice((1, 2, 8)), rng.choice((1, 4, 5, 16, 17, 40)), rng.choice((1, 16, 17, 64)),
         rng.choice((1, 3, 100)) if picked else 0, rng.choice((16, 128, 256)), rng.choice((16, 64)),
-        rng.choice((1, 7, 152, 1216)), *which)
+        rng.choice((1, 7, 152, 1216)), *which, cost=rng.choice((0, 1, 10)))
 
 
 def test_nothing_to_do_is_nothing(host):
@@ -168,7 +170,7 @@ def test_overlapping_queries_pass_the_room(host):
     """Ranges that overlap (every other one out of order) may hold more units than the workspace has room for."""
     requests, tokens = 64, 100
     q_start, lens = i32([100 * (i % 2) for i in range(requests + 1)]), i32([300] * requests)
-    args = i32([requests, tokens, 100, 300, 0, 0, 0, 2, 4, 16, 0, 16, 16, 152, 0, 1, 0])
+    args = i32([requests, tokens, 100, 300, 0, 0, 0, 2, 4, 16, 0, 16, 16, 152, 0, 1, 0, 0])
     none = i32([0, 0])
     room = 2 * most_units(requests, tokens, 100, 4, 16, False)
     got = host.h_cut(args.ctypes.data, q_start.ctypes.data, lens.ctypes.data, none.ctypes.data, none.ctypes.data, room,
