@@ -1,6 +1,7 @@
 """Attention over 16-bit and fp8 pages, bounds and selection without a GPU: how a call's work is
 cut and joined, compiled for the host, and refusals that need no device."""
 import ctypes
+import os
 import random
 import shutil
 import subprocess
@@ -11,6 +12,7 @@ import pytest
 from hierarchical_kv_cache_backup_gb300 import build as kbuild
 
 kbuild.build_library()
+from hierarchical_kv_cache_backup_gb300 import kvb  # noqa: E402
 
 HARNESS = r"""
 #include <map>
@@ -204,3 +206,57 @@ def test_step_of_bounds(host, m):
     else:
         assert np.frexp(s)[0] == 0.5 and s * inv.value == 1
         assert float(np.float32(m)) <= 127 * s and float(np.float32(m)) > 63.5 * s
+
+
+V16 = kvb.kv_vecs(1 << 20, 128, 64)
+
+
+@pytest.mark.parametrize("pool,status", [(None, kvb.KV_ERR_INVALID_ARG), (987654321, kvb.KV_ERR_CLOSED)])
+def test_calls_without_a_pool(pool, status):
+    at = dict(q_start=1 << 21, lens=1 << 21, pages=1 << 21, pages_stride=1, requests=1, tokens=1, max_q=1, max_len=1, q_heads=1, head_dim=64, dtype=0)
+    sh = kvb.make_attend_shared_args(V16, V16, format=0, layer=0, scale=1.0, **at)
+    se = kvb.make_select_args(1 << 22, V16, 1 << 23, budget=1, **at)
+    sd = kvb.make_attend_selected_args(V16, V16, picks=1 << 23, budget=1, format=0, layer=0, scale=1.0, **at)
+    bo = kvb.make_bound_args(1 << 22, lens=1 << 21, pages=1 << 21, pages_stride=1, requests=1, max_len=1, max_new=1, head_dim=64, dtype=0, format=0, layer=0)
+    for call in (lambda: kvb.kv_attend_shared(pool, sh), lambda: kvb.kv_attend_shared_workspace(pool, sh), lambda: kvb.kv_select(pool, se),
+                 lambda: kvb.kv_select_workspace(pool, se), lambda: kvb.kv_attend_selected(pool, sd),
+                 lambda: kvb.kv_attend_selected_workspace(pool, sd), lambda: kvb.kv_bound(pool, bo)):
+        with pytest.raises(kvb.KvError) as e:
+            call()
+        assert e.value.status == status
+
+
+def test_null_blocks():
+    lib, out = kvb.library(), ctypes.c_uint64()
+    for call in (lambda: lib.kv_attend_shared(None, None, None), lambda: lib.kv_attend_shared_workspace(None, None, out),
+                 lambda: lib.kv_attend_selected(None, None, None), lambda: lib.kv_attend_selected_workspace(None, None, out),
+                 lambda: lib.kv_select(None, None, None), lambda: lib.kv_select_workspace(None, None, out), lambda: lib.kv_bound(None, None, None),
+                 lambda: lib.kv_bound_bytes(128, None)):
+        assert call() == kvb.KV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dim,want", [(64, 144), (96, 208), (128, 272), (192, 416), (256, 544)])
+def test_record_sizes(dim, want):
+    assert kvb.kv_bound_bytes(dim) == want
+
+
+@pytest.mark.parametrize("dim", [0, 8, 32, 80, 160, 320])
+def test_record_sizes_refused(dim):
+    with pytest.raises(kvb.KvError) as e:
+        kvb.kv_bound_bytes(dim)
+    assert e.value.status == kvb.KV_ERR_LAYOUT
+
+
+def test_block_sizes_match_the_header():
+    """sizeof of every argument block, from the C compiler."""
+    names = ["kv_attend_shared_args", "kv_bound_args", "kv_select_args", "kv_attend_selected_args"]
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = '#include "kvb.h"\n#include <stdio.h>\nint main(void) {' + \
+        "".join('printf("%%zu\\n", sizeof(%s));' % n for n in names) + "return 0;}"
+    exe = os.path.join(kbuild.BUILD, "page_block_sizes")
+    os.makedirs(kbuild.BUILD, exist_ok=True)
+    subprocess.run([cc, "-std=c99", "-x", "c", "-I", kbuild.INCLUDE, "-o", exe, "-"], input=src.encode(), check=True)
+    got = [int(v) for v in subprocess.run([exe], capture_output=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(getattr(kvb, n)) for n in names]
