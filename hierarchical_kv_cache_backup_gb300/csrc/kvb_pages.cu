@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __gri
     asm volatile("griddepcontrol.launch_dependents;");
     const PageEngine &e = blockIdx.x == 0 ? a.rows : a.tc;
     if (!e.on || e.small) return;
+    report_groups(a);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t n = seg_count(a, e);
     unsigned long long run_t = 0, run_u = 0;
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __gri
         if (s < n) {
             const PageSeg g = seg_at(a, e, s);
             t = seg_tiles(a, e, g);
-            u = t != 0 ? (unsigned long long)row_tiles(a, e, g) * a.pool.H : 0;
+            u = seg_units(a, e, g, t);
             if (g.bad && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }
         const unsigned long long it = scan_add(t, lane), iu = scan_add(u, lane);
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
         if (a.tc.on) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    uint32_t seg = find_segment(table_of.tiles, seg_count(a, e), x);
+    uint32_t seg = find_segment(e.whole ? table_of.units : table_of.tiles, seg_count(a, e), x);
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ring_bytes(D, kF8);
     float *mine = reinterpret_cast<float *>(smem + warp * ring_bytes(D, kF8));
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
         const PageSeg &s = piece.s;
         const int rt = piece.rt, head = piece.head, k0 = piece.k0, k1 = piece.k1;
         x += piece.span;
-        if (k0 >= k1) continue;
+        if (k0 >= k1 && !e.whole) continue;
 
         const int end = seen_tokens(a, e, s, rt);
         // rows of the tile: new token and head of the group
@@ -193,24 +194,28 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
         const bool single = picked || (s.n == 1 && !s.prefix);       // rows of one token: no division
         auto new_token = [&](int row) { return single ? tok0 : (row0 + row) / group; };
         auto head_of = [&](int row) { return single ? row0 + row : (row0 + row) % group; };
+        // tiles of the prefix come first where it stands in front of a request's own tokens
+        const int pre = s.before, pre_tiles = (int)tiles_of(e, pre);
         const int32_t *table = s.prefix ? a.prefix_pages + (int64_t)s.index * a.prefix_stride
                                         : a.pages + (int64_t)s.index * a.pages_stride;
+        const int32_t *pre_table = a.prefix_pages + (int64_t)max(s.in, 0) * a.prefix_stride;
         const int32_t *list = picked ? a.picks + ((int64_t)(s.q0 + tok0) * H + head) * a.budget : nullptr;
         const int pos0 = s.len - s.n + tok0;      // picked: the query's position
         const int pages0 = pages_seen(s.len, s.n, tok0, a.pool.T);
-        const bool whole = !s.prefix && s.in < 0 && k0 == 0 && k1 == piece.n_tiles;
+        const bool whole = !s.prefix && (s.in < 0 || a.joined) && k0 == 0 && k1 == piece.n_tiles;
 
         // Token of this lane in tile k (-1: none that is seen), and its page.  Where there is a list of pages,
         // its entry is read a tile before it is looked at.
         bool wrong_pick = false;
-        auto place_in = [&](int k) { return (k * (int)team + (int)w_in) * kTile + (lane & 15); };
+        auto first_of = [&](int k) { return ((k < pre_tiles ? k : k - pre_tiles) * (int)team + (int)w_in) * kTile; };
+        auto place_in = [&](int k) { return first_of(k) + (lane & 15); };
         auto entry_of = [&](int k) {
             const int t = place_in(k);
             return picked && k < k1 && t < end ? list[div_T(a.pool, (uint32_t)t)] : -1;
         };
         auto token_of = [&](int k, int p) {
             const int t = place_in(k);
-            if (k >= k1 || t >= end) return -1;
+            if (k >= k1 || t >= (k < pre_tiles ? pre : end)) return -1;
             if (!picked) return t;
             if ((uint32_t)p >= (uint32_t)pages0) {
                 wrong_pick |= p != -1;
@@ -219,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
             const int real = p * (int)a.pool.T + (t - (int)(div_T(a.pool, (uint32_t)t) * a.pool.T));
             return real <= pos0 ? real : -1;
         };
-        auto page_of = [&](int t) { return t >= 0 ? table[div_T(a.pool, (uint32_t)t)] : 0; };
+        auto page_of = [&](int k, int t) { return t >= 0 ? (k < pre_tiles ? pre_table : table)[div_T(a.pool, (uint32_t)t)] : 0; };
         int tk[kStages + 1], entry[kStages + 2];
         int32_t pg[kStages + 1];
 #pragma unroll
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
 #pragma unroll
         for (int i = 0; i < kStages + 1; ++i) {
             tk[i] = token_of(k0 + i, entry[i]);
-            pg[i] = page_of(tk[i]);
+            pg[i] = page_of(k0 + i, tk[i]);
         }
         // Query rows first, so that they are there when the first tiles are.
         constexpr int SQ = 2 * D + 16;
@@ -361,8 +366,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
             __syncwarp();
             const uint32_t tile = ring + stage * stage_bytes(D, kF8);
             const uint32_t mask = masks[warp][stage];
-            const int t0 = (k * (int)team + (int)w_in) * kTile;
-            const bool edge = !picked && min(t0 + kTile, end) > all_see;      // rows see different tokens
+            const int t0 = first_of(k);
+            const bool edge = !picked && k >= pre_tiles && min(t0 + kTile, end) > all_see;      // rows see different tokens
             if (mask != 0) {                      // a token that some row sees
                 float y[2][4];
 #pragma unroll
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
                         for (int i = 0; i < 4; ++i) {
                             const int in = 8 * n + 2 * c + (i & 1);
                             if (mask >> 16 >> in & 1) y[n][i] = __uint_as_float(kNanWord);
-                            if (!((mask | mask >> 16) >> in & 1) || (!picked && t0 + in > lim[i >> 1])) y[n][i] = -INFINITY;
+                            if (!((mask | mask >> 16) >> in & 1) || (edge && t0 + in > lim[i >> 1])) y[n][i] = -INFINITY;
                         }
                     if (mask >> 16 != 0 && a.status != nullptr && lane == 0) atomicOr(a.status, KV_STATUS_BAD_PAGE);
                     if (edge) {
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
             __syncwarp();
             load(stage, k + kStages, t_next, page_next);
             t_next = token_of(k + kStages + 1, entry_next);
-            page_next = page_of(t_next);
+            page_next = page_of(k + kStages + 1, t_next);
             entry_next = entry_of(k + kStages + 2);
             if (++stage == kStages) stage = 0;
         }
@@ -800,9 +805,12 @@ void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t 
     const uint64_t tiles = units * ((span >> e->kv_shift) + 2 + e->unit_cost);      // at most
     e->small = segs <= kPlanSegs && units < (1ull << 31) && tiles < (1ull << 31);
     if (!e->small) e->seg_table = (int32_t *)take(at, segs * kSegWords * 4);
+    if (!e->small || !e->whole) {
+        e->seg_tiles = (uint64_t *)take(at, (segs + 1) * 8);
+        e->seg_units = (uint64_t *)take(at, (segs + 1) * 8);
+    }
+    if (e->whole) return;                 // nothing is joined
     const uint64_t rows = (units + e->workers) * e->slot_rows;
-    e->seg_tiles = (uint64_t *)take(at, (segs + 1) * 8);
-    e->seg_units = (uint64_t *)take(at, (segs + 1) * 8);
     e->part_ml = (float *)take(at, rows * 8);
     e->part_o = (float *)take(at, rows * D * 4);
 }
@@ -818,6 +826,7 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
     const uint32_t prefix_rows = (uint32_t)std::min<uint64_t>((uint64_t)max_group * group, 1u << 30);
     const uint32_t own_rows = picked ? group : max_q * group;
     // More rows than one tile of mma.sync: tcgen05.
+    const Variant *v0 = find_variant(D, fp8, false);
     const bool tc_own = !picked && own_rows > kRowsP;
     // Where a request fills a unit on its own, reading its prefix with it costs nothing and saves the joining.
     p.joined = groups != 0 && tc_own && own_rows >= 256;
@@ -826,6 +835,34 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
     uint64_t at = 0;
     const uint64_t segs = (uint64_t)groups + requests;
     PageEngine &t = p.tc, &e = p.rows;
+    if (own_rows <= (uint32_t)kRowsP) {
+        // A block a request (or query with a list) and head, the prefix in front of its own tokens, and nothing to join:
+        // where that ends sooner.  In rounds of a block's four warps (64 tokens, 1.3 us at heads of 128): a unit begins
+        // and ends in 4; cut in equal shares the join takes 4 more, and tcgen05 begins in 8.  Two requests of 30 behind
+        // 150 tokens: 13.1 us cut.
+        PageEngine w{};
+        w.own = 1;
+        w.row_tile = kRowsP;
+        w.kv_shift = 6;
+        const uint64_t units = most_units(w, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
+        const uint64_t all = picked ? std::min<uint64_t>((uint64_t)budget * T, (uint64_t)max_len + T) : (uint64_t)max_len + (groups != 0 ? max_prefix : 0);
+        const double rounds = (double)(all / 64 + 1), places = (double)sms * v0->blocks;
+        const double by_units = std::ceil((double)units / places) * (rounds + 4.0);
+        const double own_rounds = picked ? rounds : (double)(max_len / 64 + 1);
+        const double cut = ((double)units * (own_rounds + 4.0) + (groups != 0 && !tc_prefix ? (double)groups * kv_heads * (max_prefix / 64.0 + 4.0) : 0.0)) / places;
+        if (by_units <= std::max(cut, 5.0) + 4.0 + (tc_prefix ? 8.0 : 0.0)) {
+            e = w;
+            e.on = 1;
+            e.whole = 1;
+            e.team = kWarps;
+            e.slot_rows = 1;
+            e.workers = (uint32_t)units;
+            p.joined = groups != 0;
+            place(&e, &at, units, segs, (uint64_t)max_len + max_prefix, D);
+            p.bytes = at;
+            return p;
+        }
+    }
     uint64_t t_units = 0, e_units = 0;
     const Variant *v = find_variant(D, fp8, false);
     if (tc_prefix || tc_own) {
@@ -896,10 +933,11 @@ cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D,
     }
     if (a.rows.on) {
         const uint32_t teams = kWarps / a.rows.team;
-        e = launch(v->rows_fn, dim3(a.rows.workers / teams), kWarps * 32, v->smem, stream, pdl, a);
+        e = launch(v->rows_fn, dim3((a.rows.workers + teams - 1) / teams), kWarps * 32, v->smem, stream, pdl, a);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
+    if (a.rows.whole) return cudaSuccess;
     if (p.wide_join) e = launch(v->join4_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
     else e = launch(v->join_fn, dim3((a.q_heads + 3) / 4, a.max_q, a.requests), 128, 0, stream, pdl, a);
     if (e == cudaSuccess) ++*launches;

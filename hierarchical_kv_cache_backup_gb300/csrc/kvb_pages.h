@@ -23,6 +23,7 @@ namespace kvb {
 struct PageEngine {
     uint32_t on;              // launched for this call
     uint32_t prefix, own;     // which segments it takes: groups' prefixes first, then requests
+    uint32_t whole;           // a worker takes one unit, and nothing is joined
     uint32_t unit_cost;       // what a unit takes to begin and end, in tiles
     uint32_t row_tile, kv_shift;   // query rows of a unit, log2 of the cached tokens of a tile
     uint32_t workers;
@@ -179,6 +180,11 @@ KVB_HD uint64_t quotient(uint64_t a, uint64_t b) { return ((a | b) >> 32) == 0 ?
 // Tiles of a worker.
 KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ? 1 : quotient(tiles + workers - 1, workers); }
 
+// Units of a segment.  Those without a token to see are left to the join, where there is one.
+KVB_HD uint64_t seg_units(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint64_t tiles) {
+    return tiles != 0 || e.whole ? (uint64_t)row_tiles(a, e, s) * a.pool.H : 0;
+}
+
 // A worker's tiles [k0, k1) of the n_tiles of a unit (none where its run ends in front of them), and how much of
 // the run that is.
 struct PagePiece {
@@ -221,11 +227,12 @@ KVB_HD uint32_t find_segment(const uint64_t *tiles, uint32_t n, uint64_t x) {
 }
 
 // The piece of `worker` that begins at x of its run (x < x1, the run's end); *seg: a segment at x or before.
-// A segment counts fewer than 2^31.
+// A segment counts fewer than 2^31.  Where workers take whole units, x counts those.
 KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const PageTable &t, uint32_t *seg, uint64_t x, uint64_t x1,
                           uint32_t worker) {
     uint32_t i = *seg;
-    while (x >= t.tiles[i + 1]) ++i;
+    const uint64_t *counts = e.whole ? t.units : t.tiles;
+    while (x >= counts[i + 1]) ++i;
     *seg = i;
     const uint32_t before = e.prefix ? a.groups : 0, H = a.pool.H;
     const int32_t *w = t.seg + (uint64_t)i * kSegWords;
@@ -238,7 +245,18 @@ KVB_HD PagePiece piece_of(const PageAttendArgs &a, const PageEngine &e, const Pa
     p.s.bad = false;
     p.s.prefix = i < before;
     p.s.index = i < before ? i : i - before;
-    uint32_t rel = (uint32_t)(x - t.tiles[i]), n = unit_span(a, e, p.s, 0);
+    uint32_t rel = (uint32_t)(x - counts[i]);
+    if (e.whole) {
+        p.rt = (int)(rel / H);
+        p.head = (int)(rel - (uint32_t)p.rt * H);
+        p.n_tiles = (int)unit_tiles(a, e, p.s, p.rt);
+        p.k0 = 0;
+        p.k1 = p.n_tiles;
+        p.span = 1;
+        p.slot = 0;
+        return p;
+    }
+    uint32_t n = unit_span(a, e, p.s, 0);
     p.rt = 0;
     if (p.s.prefix || a.picks != nullptr) {
         p.rt = (int)(rel / (n * H));

@@ -46,6 +46,13 @@ __device__ __forceinline__ unsigned long long scan_add(unsigned long long x, int
     return x;
 }
 
+// Groups that are out of range, where no segment of their own tells (a block's threads, one of all blocks).
+__device__ __forceinline__ void report_groups(const PageAttendArgs &a) {
+    if (!a.joined || a.status == nullptr) return;
+    for (uint32_t g = threadIdx.x; g < a.groups; g += blockDim.x)
+        if (prefix_seg(a, g).bad) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
+}
+
 // Fills a block's table of the call's segments: one thread a segment, one sum over four warps.  Block 0
 // (`record`) writes what comes before each segment to the workspace, for the join, and reports what
 // is out of range.  The table is there for all threads when it returns.
@@ -54,11 +61,12 @@ __device__ __forceinline__ void fill_table(const PageAttendArgs &a, const PageEn
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t n = seg_count(a, e);
     unsigned long long x = 0, sum = 0;           // tiles, and units in the high word
+    if (record) report_groups(a);
     if (tid < (int)kPlanSegs) {
         if (tid < (int)n) {
             const PageSeg s = seg_at(a, e, tid);
             const uint32_t tiles = (uint32_t)seg_tiles(a, e, s);
-            x = tiles | (unsigned long long)(tiles != 0 ? (uint32_t)row_tiles(a, e, s) * a.pool.H : 0) << 32;
+            x = tiles | (unsigned long long)seg_units(a, e, s, tiles) << 32;
             put_seg(t.seg + tid * kSegWords, s);
             if (s.bad && record && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }
@@ -72,16 +80,18 @@ __device__ __forceinline__ void fill_table(const PageAttendArgs &a, const PageEn
         t.units[tid + 1] = sum >> 32;
         if (tid == 0) t.tiles[0] = t.units[0] = 0;
         if (record && tid < (int)n) {
-            e.seg_tiles[tid + 1] = (uint32_t)sum;
-            e.seg_units[tid + 1] = sum >> 32;
-            if (tid == 0) e.seg_tiles[0] = e.seg_units[0] = 0;
+            if (!e.whole) {
+                e.seg_tiles[tid + 1] = (uint32_t)sum;
+                e.seg_units[tid + 1] = sum >> 32;
+                if (tid == 0) e.seg_tiles[0] = e.seg_units[0] = 0;
+            }
             if (tid + 1 == (int)n && (sum >> 32) > e.units && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }
     }
     __syncthreads();
 }
 
-// The table of a call, a worker's first tile *x and its end *x1 (nothing where the units pass the workspace's room).
+// The table of a call, and a worker's run from *x to *x1, of tiles or whole units (nothing where the units pass the workspace's room).
 __device__ __forceinline__ PageTable table_and_share(const PageAttendArgs &a, const PageEngine &e, bool record, uint32_t worker,
                                                      PageTableSpace &space, unsigned long long *x, unsigned long long *x1) {
     PageTable t{e.seg_tiles, e.seg_units, e.seg_table};
@@ -90,7 +100,8 @@ __device__ __forceinline__ PageTable table_and_share(const PageAttendArgs &a, co
         t = PageTable{space.tiles, space.units, space.seg};
     }
     const uint32_t n = seg_count(a, e);
-    const unsigned long long total = t.units[n] > e.units ? 0 : t.tiles[n], share = share_of(total, e.workers);
+    const unsigned long long units = t.units[n], total = units > e.units ? 0 : e.whole ? units : t.tiles[n];
+    const unsigned long long share = e.whole ? 1 : share_of(total, e.workers);
     *x = worker * share;
     *x1 = min(total, *x + share);
     return t;

@@ -216,6 +216,8 @@ class Batch:
     def __exit__(self, *a):
         torch.cuda.synchronize()
         self.p.close()
+        for work, behind in self.works:                    # not a byte past the workspace
+            assert torch.equal(work[work.numel() - 4096:], behind)
 
     def common(self, q=None, out=None):
         kvb, p = self.kvb, self.p
@@ -228,8 +230,9 @@ class Batch:
             k_scale=p.k_scale, v_scale=p.v_scale, status=self.status.data_ptr())
 
     def space(self, a, need):
-        self.works.append(torch.randint(0, 256, (max(16, need),), device="cuda", dtype=torch.uint8))   # whatever it held before
-        a.workspace, a.workspace_bytes = self.works[-1].data_ptr(), need
+        work = torch.randint(0, 256, (need + 4096,), device="cuda", dtype=torch.uint8)   # whatever it held before
+        self.works.append((work, work[need:].clone()))
+        a.workspace, a.workspace_bytes = work.data_ptr(), need
         return a
 
     def max_group(self):

@@ -21,7 +21,7 @@ HARNESS = r"""
 using namespace kvb;
 // Cuts a call among workers and takes every row's pieces back together.  Returns 0, or the number of
 // the check that failed.  in: requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group,
-// T, budget, row_tile, kv_tile, workers, prefix, own, joined, unit_cost; units: room in the workspace.
+// T, budget, row_tile, kv_tile, workers, prefix, own, joined, unit_cost, whole; units: room in the workspace.
 extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const int *group_start, const int *prefix_lens,
                      unsigned long long units, unsigned long long *total) {
     PageAttendArgs a{};
@@ -33,7 +33,7 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
     PageEngine &e = a.rows;
     while ((1ull << a.pool.t_shift) < (unsigned)in[9]) ++a.pool.t_shift;      // division by T, as the library's
     a.pool.t_mul = (uint32_t)(((1ull << 32) * ((1ull << a.pool.t_shift) - in[9])) / in[9] + 1);
-    e.row_tile = in[11]; e.kv_shift = in[12] == 16 ? 4 : 6; e.workers = in[13]; e.prefix = in[14]; e.own = in[15]; a.joined = in[16]; e.unit_cost = in[17];
+    e.row_tile = in[11]; e.kv_shift = in[12] == 16 ? 4 : 6; e.workers = in[13]; e.prefix = in[14]; e.own = in[15]; a.joined = in[16]; e.unit_cost = in[17]; e.whole = in[18];
     const uint32_t n = seg_count(a, e);
     std::vector<uint64_t> st(n + 1), su(n + 1);
     uint64_t t = 0, u = 0;
@@ -42,35 +42,44 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
         const PageSeg g = seg_at(a, e, s);
         const uint64_t x = seg_tiles(a, e, g);
         t += x;
-        if (x) u += (uint64_t)row_tiles(a, e, g) * a.pool.H;
+        u += seg_units(a, e, g, x);
     }
     st[n] = t; su[n] = u;
     e.seg_tiles = st.data(); e.seg_units = su.data();
     *total = t;
     if (u > units) return 1;
-    const uint64_t share = share_of(t, e.workers);
+    if (e.whole) e.workers = (uint32_t)units;
+    const uint64_t run = e.whole ? u : t, share = e.whole ? 1 : share_of(t, e.workers);
+    const std::vector<uint64_t> &counts = e.whole ? su : st;
+    std::map<std::vector<uint64_t>, int> alone;
     std::vector<int32_t> segs(n * kSegWords + 1);
     for (uint32_t s = 0; s < n; ++s) put_seg(segs.data() + s * kSegWords, seg_at(a, e, s));
     const PageTable table{st.data(), su.data(), segs.data()};
     std::map<uint64_t, PagePiece> slots;
     uint64_t done = 0;
     for (uint32_t w = 0; w < e.workers; ++w) {
-        uint64_t x = w * share, x1 = x + share < t ? x + share : t;
+        uint64_t x = w * share, x1 = x + share < run ? x + share : run;
         if (x >= x1) continue;
-        uint32_t seg = find_segment(st.data(), n, x);
-        if (x < st[seg] || x >= st[seg + 1]) return 11;
+        uint32_t seg = find_segment(counts.data(), n, x);
+        if (x < counts[seg] || x >= counts[seg + 1]) return 11;
         while (x < x1) {
             const PagePiece p = piece_of(a, e, table, &seg, x, x1, w);
             done += p.span;
             x += p.span;
             if (p.span == 0) return 12;
+            if (e.whole) {
+                if (p.k0 != 0 || p.k1 != p.n_tiles || (uint32_t)p.n_tiles != unit_tiles(a, e, p.s, p.rt) || p.rt >= row_tiles(a, e, p.s)) return 13;
+                if (!alone.emplace(std::vector<uint64_t>{p.s.index, (uint64_t)p.rt, (uint64_t)p.head}, 1).second) return 14;
+                continue;
+            }
             if (p.k1 <= p.k0) continue;
             if ( p.k1 > p.n_tiles || p.head >= (int)a.pool.H || p.rt >= row_tiles(a, e, p.s)) return 2;
             if ((uint32_t)p.n_tiles != unit_tiles(a, e, p.s, p.rt)) return 3;
             if (p.slot >= units + e.workers || !slots.emplace(p.slot, p).second) return 4;
         }
     }
-    if (done != t) return 5;
+    if (done != run) return 5;
+    if (e.whole) return 0;
     for (uint32_t s = 0; s < n; ++s) {
         const PageSeg g = seg_at(a, e, s);
         for (int i = 0; i < g.n; ++i)
@@ -133,7 +142,7 @@ def most_units(segs, tokens, most, group, row_tile, picked):
     return min(segs * -(-most * group // row_tile), tokens * group // row_tile + segs)
 
 
-def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, budget, row_tile, kv_tile, workers, prefix, own, joined=0, cost=0):
+def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, budget, row_tile, kv_tile, workers, prefix, own, joined=0, cost=0, whole=0):
     n_q = [rng.choice((0, 1, max_q, rng.randint(0, max_q))) for _ in range(requests)]
     q_start = np.cumsum([0] + n_q)
     lens = [rng.choice((0, 1, max_len, rng.randint(0, max_len))) for _ in range(requests)]
@@ -144,7 +153,7 @@ def cut(host, rng, requests, max_q, max_len, groups, max_prefix, H, group, T, bu
     units = H * ((most_units(groups, tokens, max_group, group, row_tile, False) if prefix else 0) +
                  (most_units(requests, tokens, max_q, group, row_tile, budget > 0) if own else 0))
     arrays = [i32(x) for x in ([requests, tokens, max_q, max_len, groups, max_group, max_prefix, H, group, T, budget,
-                                row_tile, kv_tile, workers, prefix, own, joined, cost], q_start, lens, marks, prefix_lens or [0])]
+                                row_tile, kv_tile, workers, prefix, own, joined, cost, whole], q_start, lens, marks, prefix_lens or [0])]
     total = ctypes.c_uint64()
     got = host.h_cut(*(x.ctypes.data for x in arrays), units, ctypes.byref(total))
     assert got == 0, (got, n_q, lens, marks, prefix_lens)
@@ -172,7 +181,7 @@ def test_overlapping_queries_pass_the_room(host):
     """Ranges that overlap (every other one out of order) may hold more units than the workspace has room for."""
     requests, tokens = 64, 100
     q_start, lens = i32([100 * (i % 2) for i in range(requests + 1)]), i32([300] * requests)
-    args = i32([requests, tokens, 100, 300, 0, 0, 0, 2, 4, 16, 0, 16, 16, 152, 0, 1, 0, 0])
+    args = i32([requests, tokens, 100, 300, 0, 0, 0, 2, 4, 16, 0, 16, 16, 152, 0, 1, 0, 0, 0])
     none = i32([0, 0])
     room = 2 * most_units(requests, tokens, 100, 4, 16, False)
     got = host.h_cut(args.ctypes.data, q_start.ctypes.data, lens.ctypes.data, none.ctypes.data, none.ctypes.data, room,
@@ -260,3 +269,11 @@ def test_block_sizes_match_the_header():
     subprocess.run([cc, "-std=c99", "-x", "c", "-I", kbuild.INCLUDE, "-o", exe, "-"], input=src.encode(), check=True)
     got = [int(v) for v in subprocess.run([exe], capture_output=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(getattr(kvb, n)) for n in names]
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_whole_units_are_taken_once(host, seed):
+    rng = random.Random(1000 + seed)
+    picked = seed % 2
+    cut(host, rng, rng.choice((1, 7, 60)), rng.choice((1, 3)), rng.choice((0, 1, 90)), 0 if picked else rng.choice((0, 3)), 70, rng.choice((1, 8)),
+        rng.choice((1, 4, 5)), rng.choice((1, 16, 17)), rng.choice((1, 9)) if picked else 0, 16, 64, 1, 0, 1, joined=0 if picked else 1, whole=1)
