@@ -32,8 +32,9 @@ __host__ __device__ constexpr int row_bytes(int D, bool f8) { return f8 ? D : 2 
 __host__ __device__ constexpr int smem_stride(int D, bool f8) { return row_bytes(D, f8) + 16; }
 __host__ __device__ constexpr int stage_bytes(int D, bool f8) { return 2 * kTile * smem_stride(D, f8); }
 // Stages: few, for as many warps as registers allow (D = 128 of 16 bits: two stages and 12 warps of 168
-// registers an SM).
-__host__ __device__ constexpr int stages_of(int D, bool f8) { return row_bytes(D, f8) >= 256 ? 2 : row_bytes(D, f8) >= 128 ? 3 : 4; }
+// registers an SM; D = 64, 300 queries with 1,024 selected tokens each: 62 us with three stages and 12
+// warps, 54 with two and 16).
+__host__ __device__ constexpr int stages_of(int D, bool f8) { return row_bytes(D, f8) >= 128 ? 2 : 3; }
 __host__ __device__ constexpr int ring_bytes(int D, bool f8) {
     const int ring = stages_of(D, f8) * stage_bytes(D, f8), join = kRowsP * (D + 4) * 4;
     return ring > join ? ring : join;
@@ -888,10 +889,11 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
         uint32_t e_sms = (uint32_t)sms;
         if (t.on) {
             // The two kernels run side by side, each on SMs of its own, so that neither waits for the other's
-            // beginning and end: as many for tcgen05 as its share of the cycles, about 12 D a tile of 64
-            // cached tokens (twice that from fp8) against 20 D a warp's tile of 16.  64 requests of up to 1,000
-            // tokens behind 8,192: 96 us one after the other on all SMs.
-            const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * (fp8 ? 18.0 : 20.0) * D;
+            // beginning and end: as many for tcgen05 as its share of the cycles, 26 D a tile of 64
+            // cached tokens against 25 D a warp's tile of 16, waits included.  64 requests of up to 1,000
+            // tokens behind 8,192: 96 us one after the other on all SMs, side by side 72 / 66 / 68 with
+            // 20 / 26 / 32 D.
+            const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * (fp8 ? 24.0 : 26.0) * D;
             const double rows_cost = (double)e_units * (max_len / 16 + 1) * 25.0 * D / (kWarps * v->blocks);
             const double part = (double)sms * tc_cost / (tc_cost + rows_cost);
             t.workers = (uint32_t)std::min<double>(sms - 1, std::max(1.0, std::floor(part + 0.5)));

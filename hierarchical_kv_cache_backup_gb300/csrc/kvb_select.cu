@@ -182,6 +182,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __g
     using P = Pair16<!kHalf>;
     constexpr int NG = D / 32, LG = NG <= 2 ? 2 : NG <= 4 ? 4 : 8, SLOTS = 32 / LG;
     constexpr uint32_t kRec = (2 * D + D / 8 + 15) / 16 * 16;
+    constexpr int kStages = 4;
+    extern __shared__ __align__(16) uint8_t records[];       // [warp][stage][SLOTS] records
+    __shared__ int32_t ids[kScoreWarps][64];
     __shared__ __align__(16) int8_t code[kHeads][2][D];
     __shared__ float unit[kHeads][NG];
     asm volatile("griddepcontrol.launch_dependents;");
@@ -236,42 +239,49 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __g
             neg[h][4] = x.x; neg[h][5] = x.y; neg[h][6] = x.z; neg[h][7] = x.w;
             t[h] = unit[h][gu];
         }
-        // A warp takes a run of the block's pages; it reads their ids at once, and a record while it
-        // multiplies the one before.
+        // A warp takes a run of the block's pages.  It reads their ids at once; records come by cp.async, a step
+        // of SLOTS pages a stage, kStages - 1 of them under way.
         const int w0 = p0 + warp * ((int)a.block_pages / kScoreWarps), w1 = min(p1, w0 + (int)a.block_pages / kScoreWarps);
-        uint32_t ids[2];
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) ids[k] = w0 + 32 * k + lane < w1 ? (uint32_t)table[w0 + 32 * k + lane] : 0;
-        struct Record {
-            int4 lo[2], hi[2];
-            float step;
-            bool on, bad;
+        for (int k = 0; k < 2; ++k)
+            if (w0 + 32 * k + lane < w1) ids[warp][32 * k + lane] = table[w0 + 32 * k + lane];
+        __syncwarp();
+        const uint32_t ring = (uint32_t)__cvta_generic_to_shared(records) + warp * (kStages * SLOTS * kRec);
+        const uint8_t *from = a.bounds + (uint64_t)head * kRec;
+        auto load = [&](int p, int stage) {
+            if (p < w1)
+#pragma unroll
+                for (int c = 0; c < (SLOTS * (int)kRec / 16 + 31) / 32; ++c) {
+                    const int piece = 32 * c + lane, at = piece / ((int)kRec / 16);
+                    const uint32_t page = at < SLOTS && p + at < w1 ? (uint32_t)ids[warp][p - w0 + at] : 0xffffffffu;
+                    if (page < a.P)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + stage * (SLOTS * kRec) + piece * 16),
+                                     "l"(from + (uint64_t)page * a.H * kRec + (piece - at * ((int)kRec / 16)) * 16) : "memory");
+                }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto fetch = [&](int p) {
-            Record c;
-            const int at = p - w0 + slot;
-            const uint32_t i0 = __shfl_sync(0xffffffffu, ids[0], at & 31), i1 = __shfl_sync(0xffffffffu, ids[1], at & 31);
-            const uint32_t page = at < 32 ? i0 : i1;
-            c.on = p + slot < w1;
-            c.bad = c.on && page >= a.P;
-            c.lo[0] = c.lo[1] = c.hi[0] = c.hi[1] = make_int4(0, 0, 0, 0);
-            c.step = 0.0f;
-            if (c.on && !c.bad && gr < NG) {
-                const uint8_t *rec = a.bounds + ((uint64_t)page * a.H + head) * kRec + 32 * gr;
-                c.lo[0] = *reinterpret_cast<const int4 *>(rec);
-                c.lo[1] = *reinterpret_cast<const int4 *>(rec + 16);
-                c.hi[0] = *reinterpret_cast<const int4 *>(rec + D);
-                c.hi[1] = *reinterpret_cast<const int4 *>(rec + D + 16);
-                c.step = *reinterpret_cast<const float *>(rec + 2 * D - 32 * gr + 4 * gr);
-            }
-            return c;
-        };
-        Record next = fetch(w0);
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) load(w0 + k * SLOTS, k);
+        int stage = 0;
         for (int p = w0; p < w1; p += SLOTS) {
-            const Record c = next;
-            if (p + SLOTS < w1) next = fetch(p + SLOTS);
-            const int lo[8] = {c.lo[0].x, c.lo[0].y, c.lo[0].z, c.lo[0].w, c.lo[1].x, c.lo[1].y, c.lo[1].z, c.lo[1].w};
-            const int hi[8] = {c.hi[0].x, c.hi[0].y, c.hi[0].z, c.hi[0].w, c.hi[1].x, c.hi[1].y, c.hi[1].z, c.hi[1].w};
+            load(p + (kStages - 1) * SLOTS, stage == 0 ? kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
+            struct {
+                bool on, bad;
+                float step;
+            } c;
+            c.on = p + slot < w1;
+            c.bad = c.on && (uint32_t)ids[warp][p - w0 + slot] >= a.P;
+            const uint8_t *rec = records + (uint32_t)(warp * kStages + stage) * (SLOTS * kRec) + slot * kRec + 32 * gu;
+            const int4 l0 = *reinterpret_cast<const int4 *>(rec), l1 = *reinterpret_cast<const int4 *>(rec + 16);
+            const int4 h0v = *reinterpret_cast<const int4 *>(rec + D), h1v = *reinterpret_cast<const int4 *>(rec + D + 16);
+            c.step = *reinterpret_cast<const float *>(rec + 2 * D - 32 * gu + 4 * gu);
+            const int lo[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+            const int hi[8] = {h0v.x, h0v.y, h0v.z, h0v.w, h1v.x, h1v.y, h1v.z, h1v.w};
+            __syncwarp();
+            if (++stage == kStages) stage = 0;
             float best = -INFINITY;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
@@ -479,20 +489,23 @@ struct ScoreVariant {
     uint32_t D;
     bool fp16;
     SelectFn *fn;
+    int smem;
 };
+constexpr int score_smem(int D) { return kScoreWarps * 4 * (D <= 64 ? 16 : D <= 128 ? 8 : 4) * ((2 * D + D / 8 + 15) / 16 * 16); }
 // fp8 values are the same whatever the queries' type
 #define KVB_BOUND(D)                                                                              \
     BoundVariant{D, false, false, kv_bound_kernel<D, false, false>},                              \
         BoundVariant{D, false, true, kv_bound_kernel<D, false, true>}, BoundVariant{D, true, true, kv_bound_kernel<D, true, true>}
-#define KVB_SCORE(D) ScoreVariant{D, false, kv_score_kernel<D, false>}, ScoreVariant{D, true, kv_score_kernel<D, true>}
+#define KVB_SCORE(D) ScoreVariant{D, false, kv_score_kernel<D, false>, score_smem(D)}, ScoreVariant{D, true, kv_score_kernel<D, true>, score_smem(D)}
 const BoundVariant kBounds[] = {KVB_BOUND(64), KVB_BOUND(96), KVB_BOUND(128), KVB_BOUND(192), KVB_BOUND(256)};
 const ScoreVariant kScores[] = {KVB_SCORE(64), KVB_SCORE(96), KVB_SCORE(128), KVB_SCORE(192), KVB_SCORE(256)};
 
 template <class Args>
-cudaError_t launch(void (*fn)(Args), dim3 grid, int threads, cudaStream_t stream, bool pdl, const Args &a) {
+cudaError_t launch(void (*fn)(Args), dim3 grid, int threads, cudaStream_t stream, bool pdl, const Args &a, int smem = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -526,7 +539,7 @@ cudaError_t launch_select(const SelectArgs &a, uint32_t D, bool fp16, bool pdl, 
         if (v.D != D || v.fp16 != fp16) continue;
         if (a.max_pages > a.budget) {             // otherwise every page is picked
             const uint32_t chunks = (a.max_pages + a.block_pages - 1) / a.block_pages;
-            const cudaError_t e = launch(v.fn, dim3(chunks * a.H, a.max_q, a.requests), kScoreWarps * 32, stream, pdl, a);
+            const cudaError_t e = launch(v.fn, dim3(chunks * a.H, a.max_q, a.requests), kScoreWarps * 32, stream, pdl, a, v.smem);
             if (e != cudaSuccess) return e;
             ++*launches;
         }
@@ -546,7 +559,8 @@ cudaError_t preload_select_kernels() {
         if (e != cudaSuccess) return e;
     }
     for (const ScoreVariant &v : kScores) {
-        const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        cudaError_t e = cudaFuncGetAttributes(&at, (const void *)v.fn);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute((const void *)v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
         if (e != cudaSuccess) return e;
     }
     const cudaError_t e = cudaFuncGetAttributes(&at, (const void *)kv_pick_kernel<256>);
