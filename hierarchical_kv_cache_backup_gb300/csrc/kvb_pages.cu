@@ -81,7 +81,8 @@ __device__ __forceinline__ void team_sync(uint32_t team, uint32_t id) {
 // ------------------------------------------------------------------- the plan
 //
 // Tiles and units before each segment, where a block's table cannot hold them: one block an engine
-// (0: few rows, 1: tcgen05), 1,024 segments at a time.
+// (0: few rows, 1: tcgen05), 1,024 segments at a time.  Bound: a launch and two dependent reads; smaller calls go
+// without (every block sums up to 128 segments itself).
 constexpr int kPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __grid_constant__ PageAttendArgs a) {
@@ -137,7 +138,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __gri
 // A worker is a team of 1 or 4 warps.  Warps take 16 cached tokens in turn, each with a
 // private ring of cp.async stages (no barrier in the loop); query rows are the 16 rows of
 // mma.sync m16n8k16, cached tokens the 8 columns of the first product and the 16 k of the
-// second, so that weights go from one to the other in registers.
+// second, so that weights go from one to the other in registers.  tcgen05 would leave 112 or more of
+// its 128 rows empty here.  Bound: the latency of one warp's chain (a tile of 16 tokens of 128 values takes
+// 2,700 cycles: load 500, scores 700, softmax 200, weights and sums 850, the rest waits) with the 12 warps that
+// 168 registers leave an SM; 64 requests of up to 1,000 tokens of their own behind 8,192 common ones, with
+// the kernel on tcgen05 beside it: 67 us, floor 34.6 by bytes.
 template <int D, bool kF8, bool kHalf>
 __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
     kv_pages_rows_kernel(const __grid_constant__ PageAttendArgs a) {
@@ -628,7 +633,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
 //
 // A row (query token and head) takes the pieces of its prefix and of its own tokens, kW
 // warps a row, each every kW-th piece, a lane D / 32 values.  Rows that one worker held alone
-// were written by it.
+// were written by it.  Bound: a chain of three dependent reads (plan, maxima, sums), 3 to 7 us; several heads
+// a warp were no faster.
 template <int D, bool kHalf, int kW>
 __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constant__ PageAttendArgs a) {
     constexpr int NV = D / 32;
@@ -851,7 +857,7 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
         const double by_units = std::ceil((double)units / places) * (rounds + 4.0);
         const double own_rounds = picked ? rounds : (double)(max_len / 64 + 1);
         const double cut = ((double)units * (own_rounds + 4.0) + (groups != 0 && !tc_prefix ? (double)groups * kv_heads * (max_prefix / 64.0 + 4.0) : 0.0)) / places;
-        if (by_units <= std::max(cut, 5.0) + 4.0 + (tc_prefix ? 8.0 : 0.0)) {
+        if (units < (1ull << 31) && by_units <= std::max(cut, 5.0) + 4.0 + (tc_prefix ? 8.0 : 0.0)) {
             e = w;
             e.on = 1;
             e.whole = 1;

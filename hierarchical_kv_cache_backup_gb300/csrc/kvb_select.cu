@@ -37,7 +37,8 @@ struct Pair16<false> {
 //
 // A warp takes one page and KV head: 16 bytes of a token a lane, several tokens at once where
 // a vector is short, least and largest values two at a time in their own type (fp8 as fp16,
-// exact).  Bound: memory, keys read once.
+// exact).  Bound: memory, keys read once (four prompts of 32,768 tokens, 8 heads of 128: 36 to 42 us, floor 33.6).
+// One page a request is a launch: 3.6 us.
 constexpr int kBoundWarps = 8;
 
 template <int D, bool kF8, bool kHalf>
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __g
 // found by a histogram over the range of the keys (so that scores of one size spread over the
 // bins); what is in its bin is ranked, key against key, or, if too much, spread over bins again.  A sum
 // over the block then says where a thread's picks go, in the order of the pages.  Rows of up to 2,048 pages
-// take 256 threads, longer ones 1,024.
+// take 256 threads, longer ones 1,024.  Bound: barriers and the latency of shared memory, 8 us for 256 rows of
+// up to 1,024 pages.
 constexpr int kHeld = 8, kRanked = 256, kShortRow = 2048;
 
 __device__ __forceinline__ unsigned long long scan_up(unsigned long long x, int lane) {

@@ -294,11 +294,16 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
     if (!empty_call(a))
         *plan = plan_pages(a.requests, a.tokens, a.max_q, a.max_len, a.groups, std::min(a.max_group, a.tokens), a.max_prefix, c.budget,
                            layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms);
-    // the kernels count a request's (or group's) pieces of work in 31 bits, and so the blocks of a launch
-    const uint64_t rows = std::max<uint64_t>((uint64_t)a.max_q, a.groups != 0 ? std::min(a.max_group, a.tokens) : 0) * (a.q_heads / layer->H);
-    if ((rows / 16 + a.max_q + 1) * layer->H * (((uint64_t)a.max_len + a.max_prefix) / 16 + layer->T / 16 + 16) >= (1ull << 31))
-        return fail(KV_ERR_INVALID_ARG, "max_q %u, max_len %u, max_group %u and max_prefix %u make too much work for one request", a.max_q,
-                    a.max_len, a.max_group, a.max_prefix);
+    // the kernels count the tiles of one request (or group) in 31 bits
+    const double group = a.q_heads / layer->H, own = (double)a.max_q * group, all = (double)std::min(a.max_group, a.tokens) * group;
+    for (const PageEngine *e : {&plan->rows, &plan->tc}) {
+        if (!e->on) continue;
+        const double units = layer->H * (selected ? a.max_q * (group / e->row_tile + 1) : std::max(own, e->prefix ? all : 0.0) / e->row_tile + 1);
+        const double tiles = ((double)a.max_len + a.max_prefix + layer->T) / (1u << e->kv_shift) + 2 + e->unit_cost;
+        if (units * tiles >= 2147483648.0)
+            return fail(KV_ERR_INVALID_ARG, "tokens %u, max_q %u, max_len %u, max_group %u and max_prefix %u make too much work", a.tokens,
+                        a.max_q, a.max_len, a.max_group, a.max_prefix);
+    }
     return KV_OK;
 }
 
@@ -417,6 +422,8 @@ kv_status check_select(const kv_select_args *a, const VecPool &p, SelectArgs *k,
     k->H = l.num_heads;
     k->max_pages = (a->max_len + l.page_tokens - 1) / l.page_tokens;
     const uint64_t rows = (uint64_t)a->tokens * l.num_heads;
+    if (k->max_pages != 0 && rows > (1ull << 58) / k->max_pages)
+        return fail(KV_ERR_INVALID_ARG, "tokens %u and max_len %u make too many scores", a->tokens, a->max_len);
     k->block_pages = select_block_pages(rows * k->max_pages, p.sms);
     const uint64_t chunks = (k->max_pages + k->block_pages - 1) / k->block_pages;
     if (chunks * l.num_heads > 0x7fffffffull)

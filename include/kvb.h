@@ -711,7 +711,7 @@ typedef struct {
     uint32_t *status;
     uint32_t requests;           /* at most 65535                                 */
     uint32_t tokens;             /* query tokens of all requests                  */
-    uint32_t max_q;              /* the most of one request                       */
+    uint32_t max_q;              /* the most of one request, at most 65535        */
     uint32_t max_len;            /* the most own tokens, 0..2^29                  */
     uint32_t groups;             /* at most 65535                                 */
     uint32_t max_group;          /* the most query tokens of one group            */
@@ -736,8 +736,8 @@ KVB_API kv_status kv_attend_shared_workspace(kv_pool pool, const kv_attend_share
  * and codes 0; a value that is not finite: s = infinity, codes 0.  E4M3 keys are
  * taken before their scale.  The call writes the records of all pages that hold one of the tokens
  * first[r]..lens[r] - 1 of a request (first = NULL: 0), each over all of the page's tokens below
- * lens[r]; no other byte changes.  A page that two requests name holds the same tokens for
- * both, or its record is one of the two.
+ * lens[r]; no other byte changes.  A page that two requests name must end at the same token
+ * for both (a full page of a prefix, say); otherwise its record may mix the two.
  * A request with lens[r] outside [0, max_len], first[r] outside [0, lens[r]] or more than
  * max_new tokens between them is left out (BAD_LENGTH); so is a page outside the pool (BAD_PAGE).
  * head_dim: 64, 96, 128, 192 or 256.  Errors: as kv_append. */
@@ -769,7 +769,7 @@ KVB_API kv_status kv_bound_bytes(uint32_t head_dim, uint32_t *out);
  * code x b) x (s x t), and the score the sum of the terms in the order of the groups,
  * each product and sum rounded in float32; one that is not finite counts as
  * the largest float32.  The score for a KV head is the largest of its query heads'.
- * A page id outside the pool sets BAD_PAGE and is picked last.  Requests are checked as
+ * Where there are more, a page id outside the pool sets BAD_PAGE and is picked last.  Requests are checked as
  * by kv_attend_shared (BAD_LENGTH; what is left out has its picks left as they were, and so
  * has a request whose length is outside [0, max_len]).  The
  * bounds of every page that is seen must be those of its keys.  Errors: as kv_attend. */

@@ -492,6 +492,25 @@ def test_bound_refusals():
     assert [kvb.kv_bound_bytes(d) for d in (64, 96, 128, 192, 256)] == [ref.record_bytes(d) for d in (64, 96, 128, 192, 256)]
 
 
+def test_sizes_whose_products_pass_64_bits():
+    """Counts that are in range one by one, and whose blocks or bytes are not."""
+    with Batch(kvb, [4], [1], (), 64, 1, 64, T=1) as b:
+        bounds, picks = bound(b), torch.zeros(1, 64, 1, dtype=torch.int32, device="cuda")
+        big = dict(tokens=2 ** 30, max_len=2 ** 29, pages_stride=2 ** 29)
+        a = select_args(b, bounds, picks, 1)
+        for call in (lambda x: kvb.kv_select(b.p.pool, x), lambda x: kvb.kv_select_workspace(b.p.pool, x)):
+            refused(INV, call, a, **big)
+        a, s = b.shared_args(), b.selected_args(picks)
+        for call, x in ((kvb.kv_attend_shared_workspace, a), (kvb.kv_attend_shared, a), (kvb.kv_attend_selected_workspace, s)):
+            refused(INV, lambda y: call(b.p.pool, y), x, tokens=2 ** 30, max_q=65535, max_len=2 ** 29, pages_stride=2 ** 29)
+        s.tokens = 2 ** 30                              # more units than a launch has blocks: cut in shares
+        assert kvb.kv_attend_selected_workspace(b.p.pool, s) > 2 ** 36
+        for kw in (dict(tokens=65535, max_q=65535, max_len=131072), dict(tokens=1 << 20, max_q=1, max_len=1 << 20, requests=65535)):
+            for key, value in kw.items():
+                setattr(a, key, value)
+            assert kvb.kv_attend_shared_workspace(b.p.pool, a) >= 0
+
+
 # ------------------------------------------------------------------ selection
 
 def select_args(b, bounds, picks, budget, **kw):
