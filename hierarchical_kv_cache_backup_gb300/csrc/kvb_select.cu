@@ -195,6 +195,10 @@ __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t *r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// 1.5 x 2^23 as a float's bits: added to a whole number below 2^22 it is the bits of the number's float
+// but for 1.5 x 2^23.
+constexpr int kWhole = 0x4b400000;
+
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __grid_constant__ SelectArgs a) {
     using P = Pair16<!kHalf>;
@@ -240,16 +244,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __g
     __syncwarp();
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(records) + warp * (kStages * kStage);
     const uint8_t *from = a.bounds + (uint64_t)head * kRec;
+    // Codes: neighbouring lanes a record's 16-byte pieces, which its page's lane hands them; steps: a lane a record.
+    constexpr int PC = 2 * D / 16, kAtOnce = 32 / PC, kStepPieces = (kRec - 2 * D) / 16;
+    static_assert(kStepPieces <= 2, "a half warp a piece");
+    const int sub = lane / PC, of = (lane - sub * PC) * 16, tail = 2 * D + (lane >> 4) * 16;
+    const uint32_t to = ring + sub * kRec + of, to_tail = ring + (lane & 15) * kRec + tail, row = a.H * (uint32_t)kRec;
+    auto copy16 = [](uint32_t smem, const uint8_t *gmem) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+    };
     auto load = [&](int p, int stage) {
-        if (p < w1)
+        if (p < w1) {
+            const uint32_t at = stage * kStage;
+            const uint32_t mine = p + (lane & 15) < w1 ? (uint32_t)ids[warp][p - w0 + (lane & 15)] : 0xffffffffu;
 #pragma unroll
-            for (int k = 0; k < (kStage / 16 + 31) / 32; ++k) {
-                const int piece = 32 * k + lane, at = piece / (kRec / 16);
-                const uint32_t page = at < kScorePages && p + at < w1 ? (uint32_t)ids[warp][p - w0 + at] : 0xffffffffu;
-                if (page < a.P)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + stage * kStage + piece * 16),
-                                 "l"(from + (uint64_t)page * a.H * kRec + (piece - at * (kRec / 16)) * 16) : "memory");
+            for (int k = 0; k < kScorePages / kAtOnce; ++k) {
+                const uint32_t page = __shfl_sync(0xffffffffu, mine, (k * kAtOnce + sub) & 15);
+                if (sub < kAtOnce && page < a.P) copy16(to + at + k * kAtOnce * kRec, from + (uint64_t)page * row + of);
             }
+            if (lane < 16 * kStepPieces && mine < a.P) copy16(to_tail + at, from + (uint64_t)mine * row + tail);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int h0 = 0; h0 < (int)a.group; h0 += kHeads) {
@@ -296,13 +309,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) kv_score_kernel(const __g
                 uint32_t lo[4], hi[4];
                 ldm4(rows + 32 * gr, lo);
                 ldm4(rows + D + 32 * gr, hi);
-                int dot[4] = {0, 0, 0, 0};
+                int dot[4] = {kWhole, kWhole, kWhole, kWhole};
                 imma(dot, hi, pos[gr][0], pos[gr][1]);
                 imma(dot, lo, neg[gr][0], neg[gr][1]);
                 const float s[2] = {step[gr], step[gr + 8 * kRec / 4]};          // of pages g and g + 8
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float term = __fmul_rn((float)dot[k], __fmul_rn(s[k >> 1], t[gr][k & 1]));
+                    const float term = __fmul_rn(__fsub_rn(__int_as_float(dot[k]), __int_as_float(kWhole)), __fmul_rn(s[k >> 1], t[gr][k & 1]));
                     sum[k] = gr == 0 ? term : __fadd_rn(sum[k], term);
                 }
             }
