@@ -635,6 +635,15 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
 // warps a row, each every kW-th piece, a lane D / 32 values.  Rows that one worker held alone
 // were written by it.  Bound: a chain of three dependent reads (plan, maxima, sums), 3 to 7 us; several heads
 // a warp were no faster.
+
+// Pieces of head j of a KV head's group and query token i of a segment: `tiles` and `units` of the engine's come before it.
+__device__ __forceinline__ RowPieces find_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint64_t tiles, uint64_t units,
+                                                 uint64_t total, int i, int head, int j) {
+    int row;
+    const int rt = row_tile_of(a, e, i, j, &row);
+    return row_pieces(a, e, share_of(total, e.workers), tiles + tiles_before(a, e, s, rt) * a.pool.H, units, unit_span(a, e, s, rt), rt, row, head);
+}
+
 template <int D, bool kHalf, int kW>
 __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constant__ PageAttendArgs a) {
     constexpr int NV = D / 32;
@@ -663,12 +672,12 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
     }
     const unsigned long long tiles1 = e1.seg_tiles[at1], units1 = e1.seg_units[at1], total1 = e1.seg_tiles[n1], all1 = e1.seg_units[n1];
     if ((in >= 0 && all0 > e0.units) || all1 > e1.units) return;
-    const RowPieces p1 = row_pieces(a, e1, own, tiles1, units1, total1, i, head, j);
+    const RowPieces p1 = find_pieces(a, e1, own, tiles1, units1, total1, i, head, j);
     if (in < 0 && p1.any && p1.w0 == p1.w1) return;
     int c0 = 0, c1 = p1.any ? (int)(p1.w1 - p1.w0) + 1 : 0;       // pieces of the prefix and of its own tokens
     unsigned long long from0 = 0;
     if (in >= 0) {
-        const RowPieces p0 = row_pieces(a, e0, pre, tiles0, units0, total0, (int)(tok - pre.q0), head, j);
+        const RowPieces p0 = find_pieces(a, e0, pre, tiles0, units0, total0, (int)(tok - pre.q0), head, j);
         c0 = p0.any ? (int)(p0.w1 - p0.w0) + 1 : 0;
         from0 = (p0.unit + p0.w0) * e0.slot_rows + p0.row;
     }
@@ -749,17 +758,150 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
         a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
 }
 
+// The same for calls with many rows, 8 lanes a row: a warp takes join_heads rows of a token, four at once, and
+// works out once where their pieces are; sums are asked for together with the maxima that weigh them.  A
+// token's rows lie in at most two row tiles of a segment (kManyGroup heads of a group), or have a list of pages.
+// Bound: latency of the reads.  Four chunks of 500 tokens of 32 heads of 128 behind 8,192: the call takes 233 us, 259 with the
+// kernel above, 252 where that takes its rows in turn.
+constexpr uint32_t kManyGroup = 128;
+
+// What comes before row tile rt of a segment, by a warp.
+__device__ __forceinline__ uint64_t warp_tiles_before(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, int rt, int lane) {
+    if (s.prefix || a.picks != nullptr) return rt == 0 ? 0 : (uint64_t)rt * unit_span(a, e, s, 0);
+    unsigned long long sum = 0;
+    for (int k = lane; k < rt; k += 32) sum += unit_span(a, e, s, k);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    return sum;
+}
+
+// A segment with the row tiles of one of its tokens.
+struct JoinSide {
+    unsigned long long tiles, units, share, at[2];
+    uint32_t span[2];
+    int i, rt;
+    __device__ __forceinline__ void begin(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, unsigned long long total, int token,
+                                          int lane) {
+        int row;
+        i = token;
+        share = share_of(total, e.workers);
+        rt = row_tile_of(a, e, i, 0, &row);
+        const int rt1 = row_tile_of(a, e, i, (int)a.group - 1, &row);
+        at[0] = tiles + warp_tiles_before(a, e, s, rt, lane) * a.pool.H;
+        span[0] = unit_span(a, e, s, rt);
+        at[1] = at[0] + (uint64_t)span[0] * a.pool.H;
+        span[1] = rt1 != rt ? unit_span(a, e, s, rt1) : 0;
+    }
+    __device__ __forceinline__ RowPieces find(const PageAttendArgs &a, const PageEngine &e, int head, int j) const {
+        int row;
+        const int t = row_tile_of(a, e, i, j, &row);
+        // with lists all units of a token are of one span
+        if (a.picks != nullptr)
+            return row_pieces(a, e, share, at[0] + (uint64_t)(t - rt) * span[0] * a.pool.H, units, span[0], t, row, head);
+        return row_pieces(a, e, share, t != rt ? at[1] : at[0], units, t != rt ? span[1] : span[0], t, row, head);
+    }
+};
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(128) kv_pages_join_many_kernel(const __grid_constant__ PageAttendArgs a) {
+    constexpr int NV = D / 32, kAtOnce = D <= 128 ? 2 : 1;
+    const int lane = threadIdx.x & 31, in8 = lane & 7;
+    const int i = blockIdx.y, r = blockIdx.z, group = (int)a.group;
+    const int first = (blockIdx.x * 4 + (threadIdx.x >> 5)) * (int)a.join_heads, last = min((int)a.q_heads, first + (int)a.join_heads);
+    // the call's inputs were there before the kernels in front of this one began
+    const PageSeg own = own_seg(a, r);
+    const int in = a.joined ? -1 : own.in;
+    const int64_t tok = own.q0 + i;
+    const PageSeg pre = in >= 0 ? prefix_seg(a, (uint32_t)in) : own;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (first >= last || i >= own.n) return;
+    const PageEngine &e0 = a.tc.prefix ? a.tc : a.rows, &e1 = a.tc.own ? a.tc : a.rows;
+    const uint32_t at1 = (e1.prefix ? a.groups : 0) + (uint32_t)r, n0 = seg_count(a, e0), n1 = seg_count(a, e1);
+    JoinSide d0{}, d1{};
+    unsigned long long total0 = 0, all0 = 0;
+    if (in >= 0) {
+        d0.tiles = e0.seg_tiles[in];
+        d0.units = e0.seg_units[in];
+        total0 = e0.seg_tiles[n0];
+        all0 = e0.seg_units[n0];
+    }
+    d1.tiles = e1.seg_tiles[at1];
+    d1.units = e1.seg_units[at1];
+    const unsigned long long total1 = e1.seg_tiles[n1], all1 = e1.seg_units[n1];
+    if ((in >= 0 && all0 > e0.units) || all1 > e1.units) return;
+    d1.begin(a, e1, own, total1, i, lane);
+    if (in >= 0) d0.begin(a, e0, pre, total0, (int)(tok - pre.q0), lane);
+    for (int q = first; q < last; q += 4) {
+        const int qh = q + (lane >> 3);
+        if (qh >= last) continue;                 // no shuffle follows
+        const int head = qh / group, j = qh - head * group;
+        const RowPieces p1 = d1.find(a, e1, head, j);
+        if (in < 0 && p1.any && p1.w0 == p1.w1) continue;
+        const int c1 = p1.any ? (int)(p1.w1 - p1.w0) + 1 : 0;
+        int c0 = 0;
+        unsigned long long from0 = 0;
+        if (in >= 0) {
+            const RowPieces p0 = d0.find(a, e0, head, j);
+            c0 = p0.any ? (int)(p0.w1 - p0.w0) + 1 : 0;
+            from0 = (p0.unit + p0.w0) * e0.slot_rows + p0.row;
+        }
+        const unsigned long long from1 = (p1.unit + p1.w0) * e1.slot_rows + p1.row;
+        float top = kNoMax, sum = 0.0f;
+        float4 acc[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = 0; p < c0 + c1; p += kAtOnce) {
+            float2 ml[kAtOnce];
+            float4 x[kAtOnce][NV];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                ml[k] = make_float2(kNoMax, 0.0f);
+                if (p + k >= c0 + c1) continue;
+                const bool one = p + k < c0;
+                const unsigned long long at = one ? from0 + (unsigned long long)(p + k) * e0.slot_rows : from1 + (unsigned long long)(p + k - c0) * e1.slot_rows;
+                ml[k] = *reinterpret_cast<const float2 *>((one ? e0.part_ml : e1.part_ml) + at * 2);
+                const float4 *o = reinterpret_cast<const float4 *>((one ? e0.part_o : e1.part_o) + at * D) + in8;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) x[k][v] = o[8 * v];
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (ml[k].y == 0.0f) continue;    // nothing seen
+                const float most = fmaxf(top, ml[k].x), u = exp2_fast(top - most), f = exp2_fast(ml[k].x - most);
+                top = most;
+                sum = sum * u + ml[k].y * f;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    acc[v].x = acc[v].x * u + x[k][v].x * f;
+                    acc[v].y = acc[v].y * u + x[k][v].y * f;
+                    acc[v].z = acc[v].z * u + x[k][v].z * f;
+                    acc[v].w = acc[v].w * u + x[k][v].w * f;
+                }
+            }
+        }
+        const float inv = sum != 0.0f ? a.v_scale / sum : 0.0f;
+        const uint64_t dst = a.out.data + tok * a.out.s_tok + (int64_t)qh * a.out.s_head;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            *reinterpret_cast<uint2 *>(dst + 2 * (v * 32 + in8 * 4)) =
+                make_uint2(pack2<!kHalf>(acc[v].x * inv, acc[v].y * inv), pack2<!kHalf>(acc[v].z * inv, acc[v].w * inv));
+        if (in8 == 0 && a.lse != nullptr)
+            a.lse[tok * a.q_heads + qh] = sum != 0.0f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
+    }
+}
+
 typedef void(PagesFn)(PageAttendArgs);
 struct Variant {
     uint32_t D;
     bool fp8, fp16;
-    PagesFn *rows_fn, *join_fn, *join4_fn;
+    PagesFn *rows_fn, *join_fn, *join4_fn, *join_many_fn;
     int smem, blocks;      // blocks of an SM: set when the kernels are loaded
 };
 template <int D, bool kF8, bool kHalf>
 constexpr Variant variant() {
     return Variant{(uint32_t)D, kF8, kHalf, kv_pages_rows_kernel<D, kF8, kHalf>, kv_pages_join_kernel<D, kHalf, 1>,
-                   kv_pages_join_kernel<D, kHalf, 4>, kWarps * ring_bytes(D, kF8), 1};
+                   kv_pages_join_kernel<D, kHalf, 4>, kv_pages_join_many_kernel<D, kHalf>, kWarps * ring_bytes(D, kF8), 1};
 }
 #define KVB_PAGES(D) variant<D, false, false>(), variant<D, false, true>(), variant<D, true, false>(), variant<D, true, true>()
 Variant g_variants[] = {KVB_PAGES(64), KVB_PAGES(96), KVB_PAGES(128), KVB_PAGES(192), KVB_PAGES(256)};
@@ -919,6 +1061,10 @@ PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t
     }
     if (t.on) place(&t, &at, t_units, segs, span, D);
     if (p.tc.on && p.tc.workers > 6 * p.tc.units) p.wide_join = true;
+    // Rows of a token that a warp of the join takes: as many as make about two rounds of 32 warps an SM, four at
+    // least where it is more than one.
+    const uint64_t rounds = (uint64_t)tokens * q_heads / ((uint64_t)sms * 64);
+    p.join_heads = rounds < 2 || group > kManyGroup ? 1 : (uint32_t)std::min<uint64_t>((rounds + 3) / 4 * 4, (q_heads + 3) / 4);
     p.bytes = at;
     return p;
 }
@@ -947,7 +1093,8 @@ cudaError_t launch_pages(const PageAttendArgs &a, const PagePlan &p, uint32_t D,
     }
     if (a.rows.whole) return cudaSuccess;
     if (p.wide_join) e = launch(v->join4_fn, dim3(a.q_heads, a.max_q, a.requests), 128, 0, stream, pdl, a);
-    else e = launch(v->join_fn, dim3((a.q_heads + 3) / 4, a.max_q, a.requests), 128, 0, stream, pdl, a);
+    else e = launch(a.join_heads > 1 ? v->join_many_fn : v->join_fn,
+                    dim3((a.q_heads + 4 * a.join_heads - 1) / (4 * a.join_heads), a.max_q, a.requests), 128, 0, stream, pdl, a);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
@@ -965,9 +1112,10 @@ cudaError_t preload_pages_kernels() {
         if (e == cudaSuccess && v.blocks < 1) e = cudaErrorInvalidConfiguration;
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_fn);
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join4_fn);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, (const void *)v.join_many_fn);
         // The same split of an SM's memory for all: an SM has to be empty to change it, and blocks of the next
         // kernel, launched early, would find no place beside the join's.
-        for (PagesFn *fn : {v.rows_fn, v.join_fn, v.join4_fn})
+        for (PagesFn *fn : {v.rows_fn, v.join_fn, v.join4_fn, v.join_many_fn})
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return e;

@@ -53,6 +53,7 @@ struct PageAttendArgs {
     uint32_t q_heads, group;  // group: query heads of a KV head
     float scale_log2;         // scale * log2(e), the keys' scale included
     float v_scale;
+    uint32_t join_heads;      // query heads that a warp of the join takes in turn
     uint32_t joined;          // a request's units take its group's prefix in front of its own tokens
     PageEngine rows, tc;      // kernel for few rows, kernel on tcgen05
 };
@@ -285,21 +286,23 @@ struct RowPieces {
     bool any;
 };
 
-// Row (query token i of segment s, head j of the KV head's group) of a segment that `tiles_at` tiles and
-// `units_at` units of all the engine's `total` tiles come before.
-KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint64_t tiles_at, uint64_t units_at,
-                            uint64_t total, int i, int head, int j) {
+// The row tile of query token i and head j of the KV head's group, and which row of it that is.
+KVB_HD int row_tile_of(const PageAttendArgs &a, const PageEngine &e, int i, int j, int *row) {
+    const int rt_n = (int)e.row_tile, g = (int)a.group, at = a.picks != nullptr ? j : i * g + j;
+    *row = at % rt_n;
+    return a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + at / rt_n : at / rt_n;
+}
+
+// Pieces of row `row` of row tile rt, whose units (one a KV head, each of `span`) begin `at` into the engine's run of
+// shares; units_at units come before the segment's.
+KVB_HD RowPieces row_pieces(const PageAttendArgs &a, const PageEngine &e, uint64_t share, uint64_t at, uint64_t units_at, uint32_t span,
+                            int rt, int row, int head) {
     RowPieces p;
-    const int rt_n = (int)e.row_tile, g = (int)a.group;
-    const int row = i * g + j;
-    const int rt = a.picks != nullptr ? i * ((g + rt_n - 1) / rt_n) + j / rt_n : row / rt_n;
-    const uint32_t n = unit_span(a, e, s, rt);
-    p.any = n != 0;
-    p.row = a.picks != nullptr ? j % rt_n : row % rt_n;
-    const uint64_t share = share_of(total, e.workers);
-    const uint64_t t0 = tiles_at + tiles_before(a, e, s, rt) * a.pool.H + (uint64_t)head * n;
-    p.w0 = quotient(t0 + (n != 0 ? e.unit_cost : 0), share);      // the first that holds tiles
-    p.w1 = quotient(t0 + (n != 0 ? n : 1) - 1, share);
+    p.any = span != 0;
+    p.row = row;
+    const uint64_t t0 = at + (uint64_t)head * span;
+    p.w0 = quotient(t0 + (span != 0 ? e.unit_cost : 0), share);      // the first that holds tiles
+    p.w1 = quotient(t0 + (span != 0 ? span : 1) - 1, share);
     p.unit = units_at + (uint64_t)rt * a.pool.H + head;
     return p;
 }

@@ -12,6 +12,7 @@ struct PagePlan {
     PageEngine rows, tc;      // pointers are offsets from the workspace's start
     uint64_t bytes;
     bool wide_join;           // a row may have many pieces
+    uint32_t join_heads;      // rows that a warp of the join takes in turn
     bool joined;              // units of own tokens take the prefix too
 };
 PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t max_len, uint32_t groups,

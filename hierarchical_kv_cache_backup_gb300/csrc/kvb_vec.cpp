@@ -392,6 +392,7 @@ kv_status attend_pages(kv_pool pool, const PagesCall &c, bool selected, void *st
     const bool fp8 = a.format == KV_CACHE_E4M3;
     k.scale_log2 = a.scale * (fp8 ? a.k_scale : 1.0f) * 1.44269504088896340736f;
     k.v_scale = fp8 ? a.v_scale : 1.0f;
+    k.join_heads = plan.join_heads;
     k.joined = plan.joined;
     k.rows = plan.rows;
     k.tc = plan.tc;

@@ -85,7 +85,10 @@ extern "C" int h_cut(const int *in, const int *q_start, const int *lens, const i
         for (int i = 0; i < g.n; ++i)
             for (uint32_t h = 0; h < a.pool.H; ++h)
                 for (uint32_t j = 0; j < a.group; ++j) {
-                    const RowPieces r = row_pieces(a, e, g, st[s], su[s], t, i, h, j);
+                    int row;
+                    const int rt = row_tile_of(a, e, i, j, &row);
+                    const uint64_t from = st[s] + tiles_before(a, e, g, rt) * a.pool.H;
+                    const RowPieces r = row_pieces(a, e, share_of(t, e.workers), from, su[s], unit_span(a, e, g, rt), rt, row, h);
                     int at = 0;
                     if (r.any)
                         for (uint64_t w = r.w0; w <= r.w1; ++w) {

@@ -88,6 +88,20 @@ def test_more_segments_than_a_table(n, groups):
         no_status(b)
 
 
+@pytest.mark.parametrize("fmt,dtype,dim", [("same", "bf16", 64), ("same", "fp16", 96), ("same", "bf16", 128), ("e4m3", "bf16", 192), ("e4m3", "fp16", 256)])
+@pytest.mark.parametrize("lens,n_q,groups,H,group", [
+    ([400, 350], [300, 280], (), 4, 9), ([400, 350], [300, 280], ((0, 2, 150),), 4, 9),          # a token's rows in two row tiles
+    ([5 + 3 * i for i in range(40)], [20] * 40, ((0, 25, 200), (25, 40, 90)), 8, 5),             # prefix and own tokens apart
+    ([7 + i % 40 for i in range(300)], [3] * 300, ((0, 300, 2000),), 8, 4),                      # few own rows, many requests
+    ([30, 90], [90, 110], ((0, 1, 100),), 1, 150)])                                              # a token of more rows than a tile
+def test_more_rows_than_places(fmt, dtype, dim, lens, n_q, groups, H, group):
+    """So many rows that a warp of the join takes several."""
+    with Batch(kvb, lens, n_q, groups, H, group, dim, fmt, dtype, T=16) as b:
+        b.run()
+        b.check()
+        no_status(b)
+
+
 @pytest.mark.parametrize("sign", [-1.0, 0.0])
 @pytest.mark.parametrize("n_q", [1, 40])
 def test_scale_signs(sign, n_q):
@@ -656,6 +670,16 @@ def some_picks(b, budget, holes=True):
                 if holes and len(some) > 2:
                     picks[a + r, h, 1] = -1
     return picks.cuda()
+
+
+@pytest.mark.parametrize("dim,H,group,budget", [(128, 2, 17, 20), (64, 1, 40, 90)])
+def test_selected_more_rows_than_places(dim, H, group, budget):
+    """So many rows that a warp of the join takes several; heads of a group in two and three row tiles."""
+    with Batch(kvb, [900, 700], [310, 290], (), H, group, dim, T=8) as b:
+        picks = some_picks(b, budget)
+        run_selected(b, picks)
+        check_selected(b, picks)
+        no_status(b)
 
 
 @pytest.mark.parametrize("fmt,dtype", [("same", "bf16"), ("same", "fp16"), ("e4m3", "bf16"), ("e4m3", "fp16")])
