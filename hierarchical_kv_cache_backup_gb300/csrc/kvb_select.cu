@@ -175,10 +175,10 @@ __global__ void __launch_bounds__(kBoundWarps * 32) kv_bound_kernel(const __grid
 // Scores: a block takes some pages of one query and KV head, a warp 16 pages at a time.  A group of 32 dims is
 // the k of one mma.sync m16n8k32 of 8-bit integers: 16 pages by 8 query heads, the codes of the largest
 // against the queries' positive ones and of the least against the negative ones into the same sums.  (With
-// dp4a, a page's group a lane, 64 instructions stood where 2 do now, at the same time: what bounds this is the
-// chain of loads at a block's beginning and records of 272 bytes in any order.  With the query's values asked
-// for first, 32 requests of up to 1,024 pages go from 29.1 to 26.7 us with the picks; floor 8.1.)  The float
-// terms are added in the order of the groups.
+// dp4a, a page's group a lane, 64 instructions stood where 2 do now, at the same time.)  The float terms are
+// added in the order of the groups.  Bound: the chain of a warp's instructions, 16 warps an SM, behind the loads
+// at a block's beginning.  With the query's values asked for first, 32 requests of up to 1,024 pages went
+// from 29.1 to 26.7 us with the picks, and to 25.5 with records handed out by their page's lane; floor 8.1.
 constexpr int kScoreWarps = 8, kHeads = 8, kScorePages = 16, kWarpPages = 64;
 
 __host__ __device__ constexpr int record_of(int D) { return (2 * D + D / 8 + 15) / 16 * 16; }
