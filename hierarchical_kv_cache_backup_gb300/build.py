@@ -30,7 +30,7 @@ SOURCES = ["kvb_api.cpp", "kvb_kernels.cu", "kvb_noalloc.cu", "kvb_ring.cpp", "k
 HEADERS = [os.path.join(CSRC, "kvb_internal.h"), os.path.join(CSRC, "kvb_ring_internal.h"),
            os.path.join(CSRC, "kvb_vec.h"), os.path.join(CSRC, "kvb_vec_internal.h"),
            os.path.join(CSRC, "kvb_pages.h"), os.path.join(CSRC, "kvb_pages_internal.h"),
-           os.path.join(CSRC, "kvb_pages_device.h"), os.path.join(CSRC, "kvb_tc.h"),
+           os.path.join(CSRC, "kvb_pages_device.h"), os.path.join(CSRC, "kvb_pages_plan.h"), os.path.join(CSRC, "kvb_tc.h"),
            os.path.join(INCLUDE, "kvb.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

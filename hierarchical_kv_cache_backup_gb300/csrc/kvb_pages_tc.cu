@@ -35,22 +35,21 @@ using namespace tc;
 
 namespace {
 
-constexpr int kTileQ = 128, kTileK = 64;
+constexpr int kTileQ = kTcTileQ, kTileK = 1 << kTcShift;
 constexpr float kNoMax = -3.0e38f;
 // 64 values (128 bytes, swizzled) of every row of a tile
 constexpr uint32_t kBlockQ = kTileQ * 128, kBlockK = kTileK * 128;
 
 __host__ __device__ constexpr int blocks_of(int D) { return (D + 63) / 64; }
-__host__ __device__ constexpr int q_tiles_of(int D) { return D > 128 ? 1 : 2; }
 // Softmax warps, and those that bring keys and values: 13 warps of fp8 (128 registers a thread), 11 or 7 of
 // 16 bits.
-__host__ __device__ constexpr int soft_warps(int D) { return 4 * q_tiles_of(D); }
+__host__ __device__ constexpr int soft_warps(int D) { return 4 * tc_q_tiles(D); }
 __host__ __device__ constexpr int load_warps(int D, bool f8) { return f8 ? 12 - soft_warps(D) : 2; }
 __host__ __device__ constexpr int threads_of(int D, bool f8) { return 32 * (soft_warps(D) + load_warps(D, f8) + 1); }
 // Stages of keys, and as many of values.
 __host__ __device__ constexpr int stages_of(int D) { return D > 192 ? 2 : D > 64 ? 3 : 4; }
 __host__ __device__ constexpr int smem_of(int D) {
-    return blocks_of(D) * (int)(q_tiles_of(D) * kBlockQ + 2 * stages_of(D) * kBlockK) + 1024;
+    return blocks_of(D) * (int)(tc_q_tiles(D) * kBlockQ + 2 * stages_of(D) * kBlockK) + 1024;
 }
 static_assert(smem_of(128) <= 226 * 1024 && smem_of(192) <= 226 * 1024 && smem_of(256) <= 226 * 1024, "fits an SM");
 
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(threads_of(D, kF8), 1) kv_pages_tc_kernel(cons
     constexpr int kSoftWarps = soft_warps(D), kLoadWarps = load_warps(D, kF8), kLoadThreads = 32 * kLoadWarps;
     constexpr bool kBf = !kF8 && !kHalf;              // type of the operands
     constexpr float kBits = kBf ? 0.0f : 7.0f;        // fp16 weights stand 2^7 higher
-    constexpr int NB = blocks_of(D), NQ = q_tiles_of(D), kStages = stages_of(D);
+    constexpr int NB = blocks_of(D), NQ = tc_q_tiles(D), kStages = stages_of(D);
     constexpr uint32_t kBytesQ = NB * kBlockQ, kBytesK = NB * kBlockK;
     constexpr int RB = kF8 ? D : 2 * D;
     extern __shared__ unsigned char smem_raw[];
@@ -675,9 +674,6 @@ constexpr VariantTc variant_tc() {
 const VariantTc kVariantsTc[] = {KVB_PAGES_TC(64), KVB_PAGES_TC(96), KVB_PAGES_TC(128), KVB_PAGES_TC(192), KVB_PAGES_TC(256)};
 
 }  // namespace
-
-uint32_t pages_tc_rows(uint32_t D, uint64_t rows) { return q_tiles_of((int)D) == 1 || rows <= kTileQ ? kTileQ : 2 * kTileQ; }
-uint32_t pages_tc_shift() { return 6; }
 
 cudaError_t launch_pages_tc(const PageAttendArgs &a, uint32_t D, bool fp8, bool fp16, bool pdl, cudaStream_t stream) {
     for (const VariantTc &v : kVariantsTc) {

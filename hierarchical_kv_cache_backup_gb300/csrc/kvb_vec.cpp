@@ -293,7 +293,8 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
     *plan = PagePlan{};
     if (!empty_call(a))
         *plan = plan_pages(a.requests, a.tokens, a.max_q, a.max_len, a.groups, std::min(a.max_group, a.tokens), a.max_prefix, c.budget,
-                           layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms);
+                           layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms,
+                           pages_blocks(a.head_dim, a.format == KV_CACHE_E4M3));
     // the kernels count the tiles of one request (or group) in 31 bits
     const double group = a.q_heads / layer->H, own = (double)a.max_q * group, all = (double)std::min(a.max_group, a.tokens) * group;
     for (const PageEngine *e : {&plan->rows, &plan->tc}) {

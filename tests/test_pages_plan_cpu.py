@@ -1,0 +1,122 @@
+"""Which kernel takes what of a call of attention over 16-bit and fp8 pages, and the room it has for that: the
+library's own plan, compiled for the host."""
+import ctypes
+import random
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+from hierarchical_kv_cache_backup_gb300 import build as kbuild
+
+HARNESS = r"""
+#include "kvb_pages_plan.h"
+using namespace kvb;
+// in: requests, tokens, max_q, max_len, groups, max_group, max_prefix, budget, T, q_heads, kv_heads, D, fp8, sms, per_sm
+static PagePlan plan_of(const uint32_t *in) {
+    return plan_pages(in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], in[9], in[10], in[11], in[12] != 0, (int)in[13], in[14]);
+}
+extern "C" void h_plan(const uint32_t *in, uint64_t *out) {
+    const PagePlan p = plan_of(in);
+    for (const PageEngine *e : {&p.rows, &p.tc}) {
+        const uint64_t v[] = {e->on, e->prefix, e->own, e->whole, e->unit_cost, e->row_tile, e->kv_shift, e->workers, e->slot_rows, e->team, e->units, e->small};
+        for (uint64_t x : v) *out++ = x;
+    }
+    *out++ = p.joined;
+    *out++ = p.bytes;
+    *out++ = p.join_heads;
+    *out++ = p.wide_join;
+}
+// Tiles and units of all segments, of the kernel for few rows and of that on tcgen05.
+extern "C" void h_work(const uint32_t *in, const int *q_start, const int *lens, const int *group_start, const int *prefix_lens, uint64_t *out) {
+    const PagePlan p = plan_of(in);
+    PageAttendArgs a{};
+    a.q_start = q_start; a.lens = lens; a.group_start = group_start; a.prefix_lens = prefix_lens;
+    a.requests = in[0]; a.tokens = in[1]; a.max_q = in[2]; a.max_len = in[3]; a.groups = in[4]; a.max_group = in[5]; a.max_prefix = in[6];
+    a.budget = in[7]; a.pool.T = in[8]; a.q_heads = in[9]; a.pool.H = in[10]; a.group = in[9] / in[10];
+    int picked = 0;
+    a.picks = in[7] ? &picked : nullptr;
+    while ((1ull << a.pool.t_shift) < a.pool.T) ++a.pool.t_shift;             // division by T, as the library's
+    a.pool.t_mul = (uint32_t)(((1ull << 32) * ((1ull << a.pool.t_shift) - a.pool.T)) / a.pool.T + 1);
+    a.joined = p.joined; a.rows = p.rows; a.tc = p.tc;
+    for (const PageEngine *e : {&a.rows, &a.tc}) {
+        out[0] = out[1] = 0;
+        for (uint32_t s = 0; e->on && s < seg_count(a, *e); ++s) {
+            const PageSeg g = seg_at(a, *e, s);
+            const uint64_t tiles = seg_tiles(a, *e, g);
+            out[0] += tiles;
+            out[1] += seg_units(a, *e, g, tiles);
+        }
+        out += 2;
+    }
+}
+"""
+ENGINE = ("on", "prefix", "own", "whole", "unit_cost", "row_tile", "kv_shift", "workers", "slot_rows", "team", "units", "small")
+IN = ("requests", "tokens", "max_q", "max_len", "groups", "max_group", "max_prefix", "budget", "T", "q_heads", "kv_heads", "D", "fp8", "sms", "per_sm")
+SHAPE = dict(groups=0, max_group=0, max_prefix=0, budget=0, T=16, q_heads=32, kv_heads=8, D=128, fp8=0, sms=152, per_sm=3)
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    cc = shutil.which("g++")
+    if cc is None:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("plan")
+    (d / "h.cpp").write_text(HARNESS)
+    subprocess.run([cc, "-O1", "-std=c++17", "-shared", "-fPIC", "-I", kbuild.CSRC, str(d / "h.cpp"), "-o", str(d / "h.so")], check=True)
+    return ctypes.CDLL(str(d / "h.so"))
+
+
+class Plan:
+    def __init__(self, host, **kw):
+        shape = dict(SHAPE, **kw)
+        self.args = np.array([shape[k] for k in IN], dtype=np.uint32)
+        self.host, out = host, np.zeros(2 * len(ENGINE) + 4, dtype=np.uint64)
+        host.h_plan(ctypes.c_void_p(self.args.ctypes.data), ctypes.c_void_p(out.ctypes.data))
+        out = [int(x) for x in out]
+        n = len(ENGINE)
+        self.rows, self.tc = dict(zip(ENGINE, out[:n])), dict(zip(ENGINE, out[n:2 * n]))
+        self.joined, self.bytes, self.join_heads, self.wide_join = out[2 * n:]
+
+    def work(self, q_start, lens, group_start=(0,), prefix_lens=(0,)):
+        """(tiles, units) of the kernel for few rows and of that on tcgen05."""
+        at = [np.array(x, dtype=np.int32) for x in (q_start, lens, group_start, prefix_lens)]
+        out = np.zeros(4, dtype=np.uint64)
+        self.host.h_work(*(ctypes.c_void_p(x.ctypes.data) for x in (self.args, *at, out)))
+        return [(int(out[0]), int(out[1])), (int(out[2]), int(out[3]))]
+
+
+def test_plans(host):
+    """A call of each kind: who takes the prefixes, who the requests' own tokens."""
+    p = Plan(host, requests=2, tokens=2, max_q=1, max_len=30, groups=1, max_group=2, max_prefix=150)
+    assert p.rows["on"] and p.rows["whole"] and p.joined and not p.tc["on"] and p.bytes == 0
+    p = Plan(host, requests=64, tokens=64, max_q=1, max_len=1000, groups=1, max_group=64, max_prefix=8192)
+    assert p.tc["prefix"] and not p.tc["own"] and p.rows["own"] and not p.rows["prefix"] and not p.joined
+    p = Plan(host, requests=4, tokens=2000, max_q=500, max_len=1000, groups=1, max_group=2000, max_prefix=8192)
+    assert p.tc["own"] and not p.tc["prefix"] and not p.rows["on"] and p.joined
+    p = Plan(host, requests=2, tokens=100, max_q=50, max_len=1000, groups=1, max_group=100, max_prefix=8192)
+    assert p.tc["own"] and p.tc["prefix"] and not p.rows["on"] and not p.joined
+    p = Plan(host, requests=1, tokens=1, max_q=1, max_len=131072, budget=256)
+    assert p.rows["own"] and not p.rows["whole"] and not p.tc["on"]
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_room_for_the_work(host, seed):
+    """What valid ranges hold is never more than the plan has room for, and counts that are said to be small are."""
+    rng = random.Random(seed)
+    requests, q, length, prefix = rng.choice((1, 3, 60, 127)), rng.choice((1, 4, 30, 600)), rng.choice((0, 1, 90, 5000)), rng.choice((0, 40, 9000))
+    picked = seed % 3 == 0
+    groups = 0 if picked else rng.choice((0, 1, 4))
+    n_q = [rng.choice((1, q, rng.randint(0, q))) for _ in range(requests)]
+    q_start = np.cumsum([0] + n_q)
+    marks = sorted(rng.randint(0, requests) for _ in range(groups + 1))
+    max_group = max([int(q_start[b] - q_start[a]) for a, b in zip(marks, marks[1:])], default=0)
+    kv_heads, group = rng.choice((1, 4, 8)), rng.choice((1, 4, 16, 40))
+    p = Plan(host, requests=requests, tokens=max(1, sum(n_q)), max_q=max(1, max(n_q)), max_len=length, groups=groups, max_group=max_group, max_prefix=prefix if groups else 0,
+             budget=rng.choice((1, 30, 2000)) if picked else 0, T=rng.choice((1, 16, 17, 256)), q_heads=kv_heads * group, kv_heads=kv_heads,
+             D=rng.choice((64, 128, 256)))
+    lens = [rng.choice((0, length, rng.randint(0, length))) for _ in range(requests)]
+    for e, (tiles, units) in zip((p.rows, p.tc), p.work(q_start, lens, marks, [prefix] * max(1, groups))):
+        if e["on"]:
+            assert units <= e["units"] and (not e["small"] or tiles < 2 ** 31)
