@@ -51,7 +51,7 @@ inline uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t toke
     return u * H;
 }
 
-// `span`: the most cached tokens of a unit.
+// `span`: the most cached tokens of a unit (a list counts whole pages, so up to a page more than a request may have).
 inline void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t span, uint32_t D) {
     e->units = units;
     const uint64_t tiles = units * ((span >> e->kv_shift) + 2 + e->unit_cost);      // at most
@@ -108,7 +108,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
             e.slot_rows = 1;
             e.workers = (uint32_t)units;
             p.joined = groups != 0;
-            place(&e, &at, units, segs, (uint64_t)max_len + max_prefix, D);
+            place(&e, &at, units, segs, picked ? (uint64_t)max_len + T : (uint64_t)max_len + (groups != 0 ? max_prefix : 0), D);
             p.bytes = at;
             return p;
         }

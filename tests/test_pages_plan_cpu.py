@@ -120,3 +120,13 @@ def test_room_for_the_work(host, seed):
     for e, (tiles, units) in zip((p.rows, p.tc), p.work(q_start, lens, marks, [prefix] * max(1, groups))):
         if e["on"]:
             assert units <= e["units"] and (not e["small"] or tiles < 2 ** 31)
+
+
+def test_lists_of_large_pages(host):
+    """A list counts whole pages, of up to 2^20 tokens, however short the request is."""
+    tokens = 6 * 54720
+    p = Plan(host, requests=6, tokens=tokens, max_q=54720, max_len=64, budget=1, T=1 << 20, q_heads=1, kv_heads=1, D=64, per_sm=4)
+    (tiles, units), _ = p.work([54720 * i for i in range(7)], [64] * 6)
+    assert p.rows["on"] and units == p.rows["units"] == tokens
+    assert tiles == tokens << 14 and not p.rows["small"]
+    assert tiles + (units << 32) >> 32 != units                  # what a sum of 32-bit words would have said
