@@ -30,7 +30,7 @@ struct PageEngine {
     uint32_t slot_rows;       // query rows of a slot
     uint32_t team;            // warps of a worker (kernel for few rows)
     uint64_t units;           // that the workspace has room for
-    uint32_t small;           // the segments fit a block's table, and tiles and units 31 bits
+    uint32_t small;           // the segments fit a block's table, units 24 bits and tiles 31
     float *part_o;            // [slot][slot_rows][D] sums
     float *part_ml;           // [slot][slot_rows][2] maxima (base 2), sums of weights
     uint64_t *seg_tiles;      // [segments + 1] tiles before each segment (written on the GPU)
@@ -184,6 +184,14 @@ KVB_HD uint64_t share_of(uint64_t tiles, uint32_t workers) { return tiles == 0 ?
 // Units of a segment.  Those without a token to see are left to the join, where there is one.
 KVB_HD uint64_t seg_units(const PageAttendArgs &a, const PageEngine &e, const PageSeg &s, uint64_t tiles) {
     return tiles != 0 || e.whole ? (uint64_t)row_tiles(a, e, s) * a.pool.H : 0;
+}
+
+// Where a block sums up the segments itself (PageEngine::small): a segment's tiles, and its units in the high word.  Valid
+// ranges make fewer than kSmallUnits units and 2^31 tiles in all; of ranges that overlap, each counts for one more
+// than there is room for at most, so that kPlanSegs of them do not wrap the high word.
+constexpr uint64_t kSmallUnits = 1u << 24;
+KVB_HD uint64_t pack_work(const PageEngine &e, uint64_t tiles, uint64_t units) {
+    return (uint32_t)tiles | (units > e.units ? e.units + 1 : units) << 32;
 }
 
 // A worker's tiles [k0, k1) of the n_tiles of a unit (none where its run ends in front of them), and how much of

@@ -65,8 +65,8 @@ __device__ __forceinline__ void fill_table(const PageAttendArgs &a, const PageEn
     if (tid < (int)kPlanSegs) {
         if (tid < (int)n) {
             const PageSeg s = seg_at(a, e, tid);
-            const uint32_t tiles = (uint32_t)seg_tiles(a, e, s);
-            x = tiles | (unsigned long long)seg_units(a, e, s, tiles) << 32;
+            const uint64_t tiles = seg_tiles(a, e, s);
+            x = pack_work(e, tiles, seg_units(a, e, s, tiles));
             put_seg(t.seg + tid * kSegWords, s);
             if (s.bad && record && a.status != nullptr) atomicOr(a.status, KV_STATUS_BAD_LENGTH);
         }

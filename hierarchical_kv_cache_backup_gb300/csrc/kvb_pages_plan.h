@@ -55,7 +55,7 @@ inline uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t toke
 inline void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t span, uint32_t D) {
     e->units = units;
     const uint64_t tiles = units * ((span >> e->kv_shift) + 2 + e->unit_cost);      // at most
-    e->small = segs <= kPlanSegs && units < (1ull << 31) && tiles < (1ull << 31);
+    e->small = segs <= kPlanSegs && units < kSmallUnits && tiles < (1ull << 31);
     if (!e->small) e->seg_table = (int32_t *)take(at, segs * kSegWords * 4);
     if (!e->small || !e->whole) {
         e->seg_tiles = (uint64_t *)take(at, (segs + 1) * 8);

@@ -51,6 +51,13 @@ extern "C" void h_work(const uint32_t *in, const int *q_start, const int *lens, 
         out += 2;
     }
 }
+// The kernel for few rows: what a block's table sums up of `segs` segments of these tiles and units.
+extern "C" uint64_t h_packed(const uint32_t *in, uint32_t segs, uint64_t tiles, uint64_t units) {
+    const PagePlan p = plan_of(in);
+    uint64_t sum = 0;
+    for (uint32_t s = 0; s < segs; ++s) sum += pack_work(p.rows, tiles, units);
+    return sum;
+}
 """
 ENGINE = ("on", "prefix", "own", "whole", "unit_cost", "row_tile", "kv_shift", "workers", "slot_rows", "team", "units", "small")
 IN = ("requests", "tokens", "max_q", "max_len", "groups", "max_group", "max_prefix", "budget", "T", "q_heads", "kv_heads", "D", "fp8", "sms", "per_sm")
@@ -130,3 +137,17 @@ def test_lists_of_large_pages(host):
     assert p.rows["on"] and units == p.rows["units"] == tokens
     assert tiles == tokens << 14 and not p.rows["small"]
     assert tiles + (units << 32) >> 32 != units                  # what a sum of 32-bit words would have said
+
+
+@pytest.mark.parametrize("heads", [1, 255, 256, 1025])
+def test_overlapping_ranges_do_not_wrap_the_tables_sums(host, heads):
+    """64 requests of the same 65,535 query tokens (every other range out of order): more units than there is room for,
+    whether a block's table sums them in 32 bits or a kernel of its own in 64."""
+    n = 65535
+    p = Plan(host, requests=127, tokens=n, max_q=n, max_len=16, budget=1, T=16, q_heads=heads, kv_heads=heads, D=64)
+    (tiles, units), _ = p.work([n * (i % 2) for i in range(128)], [16] * 127)
+    assert units == 64 * n * heads > p.rows["units"]
+    if p.rows["small"]:
+        host.h_packed.restype, host.h_packed.argtypes = ctypes.c_uint64, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64]
+        assert host.h_packed(p.args.ctypes.data, 64, tiles // 64, units // 64) >> 32 > p.rows["units"]
+        assert host.h_packed(p.args.ctypes.data, 1, tiles // 64, units // 64) == tiles // 64 | (units // 64) << 32
