@@ -36,6 +36,11 @@ inline uint64_t take(uint64_t *at, uint64_t bytes) {
     return p;
 }
 
+// The most cached tokens that a list of pages stands for (whole pages of it, as many as the request has).
+inline uint64_t list_tokens(uint32_t budget, uint32_t T, uint32_t max_len) {
+    return std::min((uint64_t)budget * T, (uint64_t)max_len + T);
+}
+
 // The most units that an engine may meet.
 inline uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t tokens, uint32_t max_q, uint32_t groups, uint32_t max_group,
                            uint32_t group, bool picked, uint32_t H) {
@@ -51,7 +56,7 @@ inline uint64_t most_units(const PageEngine &e, uint32_t requests, uint32_t toke
     return u * H;
 }
 
-// `span`: the most cached tokens of a unit (a list counts whole pages, so up to a page more than a request may have).
+// `span`: the most cached tokens of a unit.
 inline void place(PageEngine *e, uint64_t *at, uint64_t units, uint64_t segs, uint64_t span, uint32_t D) {
     e->units = units;
     const uint64_t tiles = units * ((span >> e->kv_shift) + 2 + e->unit_cost);      // at most
@@ -81,7 +86,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
     // Where a request fills a unit on its own, reading its prefix with it costs nothing and saves the joining.
     p.joined = groups != 0 && tc_own && own_rows >= 256;
     const bool tc_prefix = groups != 0 && max_prefix != 0 && prefix_rows > kRowsP && !p.joined;
-    const uint64_t span = picked ? (uint64_t)max_len + T : p.joined ? (uint64_t)max_prefix + max_len : std::max(max_len, groups != 0 ? max_prefix : 0);
+    const uint64_t span = picked ? list_tokens(budget, T, max_len) : p.joined ? (uint64_t)max_prefix + max_len : std::max(max_len, groups != 0 ? max_prefix : 0);
     uint64_t at = 0;
     const uint64_t segs = (uint64_t)groups + requests;
     PageEngine &t = p.tc, &e = p.rows;
@@ -95,7 +100,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
         w.row_tile = kRowsP;
         w.kv_shift = 6;
         const uint64_t units = most_units(w, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
-        const uint64_t all = picked ? std::min<uint64_t>((uint64_t)budget * T, (uint64_t)max_len + T) : (uint64_t)max_len + (groups != 0 ? max_prefix : 0);
+        const uint64_t all = picked ? list_tokens(budget, T, max_len) : (uint64_t)max_len + (groups != 0 ? max_prefix : 0);
         const double rounds = (double)(all / 64 + 1), places = (double)sms * per_sm;
         const double by_units = std::ceil((double)units / places) * (rounds + 4.0);
         const double own_rounds = picked ? rounds : (double)(max_len / 64 + 1);
@@ -108,7 +113,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
             e.slot_rows = 1;
             e.workers = (uint32_t)units;
             p.joined = groups != 0;
-            place(&e, &at, units, segs, picked ? (uint64_t)max_len + T : (uint64_t)max_len + (groups != 0 ? max_prefix : 0), D);
+            place(&e, &at, units, segs, all, D);
             p.bytes = at;
             return p;
         }
@@ -167,6 +172,22 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
     p.join_heads = rounds < 2 || group > kManyGroup ? 1 : (uint32_t)std::min<uint64_t>((rounds + 3) / 4 * 4, (q_heads + 3) / 4);
     p.bytes = at;
     return p;
+}
+
+// The kernels count the tiles of one segment, all its units with what each takes to begin and end, in 31 bits.
+inline bool plan_counts_fit(const PagePlan &p, uint32_t max_q, uint32_t max_len, uint32_t max_group, uint32_t max_prefix,
+                            uint32_t budget, uint32_t T, uint32_t q_heads, uint32_t kv_heads) {
+    const double group = q_heads / kv_heads;
+    // a list is taken for at most what the request has, and both stay far from 64 bits
+    if (budget != 0 && (double)max_q * kv_heads * max_len >= 281474976710656.0) return false;
+    for (const PageEngine *e : {&p.rows, &p.tc}) {
+        if (!e->on) continue;
+        const double rows = std::max(max_q * group, e->prefix ? max_group * group : 0.0);
+        const double units = kv_heads * (budget != 0 ? max_q * std::ceil(group / e->row_tile) : rows / e->row_tile + 1);
+        const double tokens = budget != 0 ? (double)list_tokens(budget, T, max_len) : (double)max_len + max_prefix;
+        if (units * (tokens / (1u << e->kv_shift) + 2 + e->unit_cost) >= 2147483648.0) return false;
+    }
+    return true;
 }
 
 }  // namespace kvb

@@ -295,16 +295,9 @@ kv_status check_pages(const PagesCall &c, bool selected, const VecPool &p, PoolL
         *plan = plan_pages(a.requests, a.tokens, a.max_q, a.max_len, a.groups, std::min(a.max_group, a.tokens), a.max_prefix, c.budget,
                            layer->T, a.q_heads, layer->H, a.head_dim, a.format == KV_CACHE_E4M3, p.sms,
                            pages_blocks(a.head_dim, a.format == KV_CACHE_E4M3));
-    // the kernels count the tiles of one request (or group) in 31 bits
-    const double group = a.q_heads / layer->H, own = (double)a.max_q * group, all = (double)std::min(a.max_group, a.tokens) * group;
-    for (const PageEngine *e : {&plan->rows, &plan->tc}) {
-        if (!e->on) continue;
-        const double units = layer->H * (selected ? a.max_q * (group / e->row_tile + 1) : std::max(own, e->prefix ? all : 0.0) / e->row_tile + 1);
-        const double tiles = ((double)a.max_len + a.max_prefix + layer->T) / (1u << e->kv_shift) + 2 + e->unit_cost;
-        if (units * tiles >= 2147483648.0)
-            return fail(KV_ERR_INVALID_ARG, "tokens %u, max_q %u, max_len %u, max_group %u and max_prefix %u make too much work", a.tokens,
-                        a.max_q, a.max_len, a.max_group, a.max_prefix);
-    }
+    if (!plan_counts_fit(*plan, a.max_q, a.max_len, std::min(a.max_group, a.tokens), a.max_prefix, c.budget, layer->T, a.q_heads, layer->H))
+        return fail(KV_ERR_INVALID_ARG, "tokens %u, max_q %u, max_len %u, max_group %u, max_prefix %u and budget %u make too much work",
+                    a.tokens, a.max_q, a.max_len, a.max_group, a.max_prefix, c.budget);
     return KV_OK;
 }
 

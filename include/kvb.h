@@ -694,7 +694,9 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  * A row of a page table holds ceil(max_len / T) (ceil(max_prefix / T)) entries that
  * may be read.  q and out hold `tokens` vectors.  head_dim: 64, 96, 128, 192 or
  * 256; fewer than 2^31 head vectors (2^32 of fp8) between the layer's first and the
- * pool's last; T at most 2^20 (LAYOUT otherwise).  Errors: as kv_attend. */
+ * pool's last; T at most 2^20 (LAYOUT otherwise).  One request or group makes fewer
+ * than 2^31 tiles of work, of 256 query rows by 64 cached tokens and KV head, 16 by 16 with
+ * few rows (INVALID_ARG).  Errors: as kv_attend. */
 typedef struct {
     kv_vecs q, out;
     float *lse;
@@ -799,7 +801,9 @@ KVB_API kv_status kv_select_workspace(kv_pool pool, const kv_select_args *args, 
  * indices stand in its picks[token][h][0..budget).  An entry of -1 is skipped; one outside
  * [-1, pages that the query sees) is too and sets BAD_PAGE.  Of a list, as many entries
  * are looked at as the request has pages.  An index that stands twice counts twice.
- * Weights are rounded as in calls with few rows.  Errors: as kv_attend. */
+ * Weights are rounded as in calls with few rows.  One request makes fewer than 2^31 tiles of
+ * work, of a token's 16 query heads by 16 tokens of a list (those past the request's pages do not
+ * count), and max_q x H x max_len is below 2^48 (INVALID_ARG).  Errors: as kv_attend. */
 typedef struct {
     kv_vecs q, out;
     float *lse;

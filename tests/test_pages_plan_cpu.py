@@ -28,6 +28,10 @@ extern "C" void h_plan(const uint32_t *in, uint64_t *out) {
     *out++ = p.join_heads;
     *out++ = p.wide_join;
 }
+// Whether the kernels' 32-bit counts hold the call.
+extern "C" int h_fits(const uint32_t *in) {
+    return plan_counts_fit(plan_of(in), in[2], in[3], in[5], in[6], in[7], in[8], in[9], in[10]);
+}
 // Tiles and units of all segments, of the kernel for few rows and of that on tcgen05.
 extern "C" void h_work(const uint32_t *in, const int *q_start, const int *lens, const int *group_start, const int *prefix_lens, uint64_t *out) {
     const PagePlan p = plan_of(in);
@@ -85,6 +89,9 @@ class Plan:
         n = len(ENGINE)
         self.rows, self.tc = dict(zip(ENGINE, out[:n])), dict(zip(ENGINE, out[n:2 * n]))
         self.joined, self.bytes, self.join_heads, self.wide_join = out[2 * n:]
+
+    def fits(self):
+        return bool(self.host.h_fits(ctypes.c_void_p(self.args.ctypes.data)))
 
     def work(self, q_start, lens, group_start=(0,), prefix_lens=(0,)):
         """(tiles, units) of the kernel for few rows and of that on tcgen05."""
@@ -151,3 +158,31 @@ def test_overlapping_ranges_do_not_wrap_the_tables_sums(host, heads):
         host.h_packed.restype, host.h_packed.argtypes = ctypes.c_uint64, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64]
         assert host.h_packed(p.args.ctypes.data, 64, tiles // 64, units // 64) >> 32 > p.rows["units"]
         assert host.h_packed(p.args.ctypes.data, 1, tiles // 64, units // 64) == tiles // 64 | (units // 64) << 32
+
+
+@pytest.mark.parametrize("chunk,length,budget,T", [(4096, 1 << 20, 64, 16), (32768, 1 << 17, 64, 16), (65535, 1 << 20, 512, 32), (8192, 1 << 22, 2048, 1)])
+def test_chunks_over_long_caches_count_their_lists(host, chunk, length, budget, T):
+    """What a list stands for is the work, not all that the request has cached."""
+    p = Plan(host, requests=1, tokens=chunk, max_q=chunk, max_len=length, budget=budget, T=T)
+    (tiles, units), _ = p.work([0, chunk], [length])
+    assert p.fits() and tiles < 2 ** 31 and units == chunk * 8
+    assert p.rows["small"] and tiles <= units * ((budget * T >> p.rows["kv_shift"]) + 2 + p.rows["unit_cost"])
+
+
+@pytest.mark.parametrize("kw", [dict(max_q=65535, max_len=1 << 24, budget=1 << 24), dict(max_q=65535, max_len=1 << 29, budget=1, kv_heads=64, q_heads=64),
+                                dict(max_q=65535, max_len=1 << 29)])
+def test_work_past_32_bits_does_not_fit(host, kw):
+    assert not Plan(host, **dict(dict(requests=2, tokens=70000, T=1), **kw)).fits()
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_what_fits_is_counted_in_31_bits(host, seed):
+    rng = random.Random(seed)
+    picked = seed % 2
+    q, kv_heads, group = rng.choice((1, 500, 65535)), rng.choice((1, 8, 64)), rng.choice((1, 5, 16, 17))
+    length, prefix, groups = rng.choice((1, 5000, 1 << 20, 1 << 29)), rng.choice((0, 1 << 20, 1 << 29)), 0 if picked else rng.choice((0, 1))
+    p = Plan(host, requests=1, tokens=q, max_q=q, max_len=length, groups=groups, max_group=q if groups else 0, max_prefix=prefix if groups else 0,
+             budget=rng.choice((1, 64, 1 << 24)) if picked else 0, T=rng.choice((1, 16, 1 << 20)), q_heads=kv_heads * group, kv_heads=kv_heads)
+    if p.fits():
+        for tiles, _ in (p.work([0, q], [length], [0, 1], [prefix]) if length * q < 2 ** 45 else ()):
+            assert tiles < 2 ** 32 if groups else tiles < 2 ** 31
