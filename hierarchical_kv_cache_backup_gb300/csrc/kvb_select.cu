@@ -361,8 +361,9 @@ __device__ __forceinline__ unsigned long long scan_up(unsigned long long x, int 
     return x;
 }
 
+// Keys in the order of the scores.  -0, a negative sum whose steps' product underflows, is 0: the two tie.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(__fadd_rn(x, 0.0f));
     return u ^ ((u >> 31) != 0 ? 0xffffffffu : 0x80000000u);
 }
 
