@@ -673,7 +673,7 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  * pool's H; query head j reads KV head j / (q_heads / H).  With x_t = scale q . k_t
  * over the tokens it sees: out = sum exp(x_t) v_t / sum exp(x_t), lse (float32
  * [tokens][q_heads], NULL: not wanted) = ln sum exp(x_t).  A query that sees
- * nothing gets out = 0 and lse = -infinity.  k_scale and v_scale: of E4M3 pages.
+ * nothing, or scores of -infinity alone, gets out = 0 and lse = -infinity.  k_scale and v_scale: of E4M3 pages.
  * Scores, softmax statistics and sums are float32.  Rounded to fewer bits are:
  *   a weight      exp(x_t - largest) to two parts of 8 bits (bf16 pages), to two
  *                 parts of 11 bits (fp16 outputs), to 11 bits (fp8 pages, bf16
@@ -682,8 +682,11 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  *                 Those under 2^-21 of the query's largest lose bits (not on bf16 pages)
  *   a query       of bf16 against fp8 pages: values under 2^-22 of the vector's
  *                 largest
- * A key or value that is not finite makes outputs of the queries that see it not
- * finite (a value: of its dim), and no others.
+ * A score of -infinity has weight 0 (an infinite key against a query value of the other
+ * sign, say); one of +infinity or NaN makes all of the query's outputs and its lse NaN.  A
+ * value that is not finite makes its dim of the outputs of the queries that see it not
+ * finite (where its score is -infinity: that or nothing).  Queries that do not see a token
+ * are the same whatever it holds.
  * A page id outside the pool inside a length sets BAD_PAGE, and the queries that
  * see the page get NaN.  lens[r] and prefix_lens[g] are taken as at most max_len
  * and max_prefix and at least 0; a request whose q_start values are out of order,

@@ -1,5 +1,6 @@
 """Corners of kv_attend_shared, kv_bound, kv_select and kv_attend_selected, against plain implementations in 64
 bits (pages_ref.py, where the tolerances are derived)."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -9,7 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from hierarchical_kv_cache_backup_gb300 import kvb  # noqa: E402
-from pages_ref import Batch  # noqa: E402
+from pages_ref import Batch, softmax_rows, tolerance  # noqa: E402
 from test_pages_gpu import bound, check_picks, check_selected, no_status, run_selected, select, some_picks  # noqa: E402
 
 
@@ -40,3 +41,58 @@ def test_zeros_of_both_signs_tie(pages):
             check_picks(b, bounds, picks, budget, first, last)
             want = list(range(budget - last)) + list(range(pages - last, pages))
             assert picks[0].tolist() == [want, want]
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("fp16", 64), ("bf16", 96), ("fp16", 256)])
+@pytest.mark.parametrize("n_q,groups", [(1, ()), (3, ((0, 1, 30),)), (20, ((0, 1, 30),)), (90, ())])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_keys(dtype, dim, n_q, groups, bad, sign):
+    """A score of -infinity has weight 0, one of +infinity makes the query's outputs NaN, and nobody else's."""
+    H, group, own, h, d = 2, 4, 150, 1, 37
+    with Batch(kvb, [own], [n_q], groups, H, group, dim, "same", dtype, T=16) as b:
+        b.scale *= sign
+        at = own - n_q + n_q // 2                              # query n_q // 2 is the first that sees it
+        b.run()
+        clean, clean_lse = b.out.clone(), b.lse.clone()
+        x = torch.from_numpy(b.p.held(b.table[0], own, 0)).cuda().float()
+        x[at, h, d] = bad
+        b.p.put(b.table[0], x, 0)
+        b.run()
+        no_status(b)
+        pre = groups[0][2] if groups else 0
+        k, v = (np.concatenate(([b.p.held(b.prefix_table[0], pre, c)] if pre else []) + [b.p.held(b.table[0], own, c)]) for c in (0, 1))
+        k[pre + at, h, d] = 0.0                                # not looked at below
+        q, out, lse = (y.double().cpu().numpy() for y in (b.q, b.out, b.lse))
+        pos = own - n_q + np.arange(n_q)
+        seen = np.concatenate((np.ones((n_q, pre), bool), np.arange(own)[None] <= pos[:, None]), 1)
+        hit = np.arange(n_q) >= n_q // 2
+        for j in range(H * group):
+            if j // group != h:
+                assert torch.equal(b.out[:, j], clean[:, j]) and torch.equal(b.lse[:, j], clean_lse[:, j])
+                continue
+            up = hit & (sign * bad * q[:, j, d] > 0)
+            low = hit & (sign * bad * q[:, j, d] < 0)
+            assert np.isnan(out[up, j]).all() and np.isnan(lse[up, j]).all()
+            assert torch.equal(b.out[~torch.from_numpy(hit).cuda(), j], clean[~torch.from_numpy(hit).cuda(), j])
+            if low.any():
+                sees = seen[low].copy()
+                sees[:, pre + at] = False
+                want, wl, w, s = softmax_rows(q[low, j], k[:, h], v[:, h], sees, b.scale)
+                tol, tl = tolerance(q[low, j], k[:, h], v[:, h], w, s, want, b.scale, b.p.dt, False, b.many())
+                assert (np.abs(out[low, j] - want) <= tol).all() and (np.abs(lse[low, j] - wl) <= tl + 2.0 ** -21 * np.abs(wl)).all()
+
+
+@pytest.mark.parametrize("n_q", [1, 20])
+def test_scores_of_minus_infinity_alone(n_q):
+    """Such a query gets what one that sees nothing gets."""
+    with Batch(kvb, [40], [n_q], [(0, 1, 70)], 1, 4, 64) as b:
+        b.q[:, 1] = 1.0
+        b.q[:, 0] = b.q[:, 2:] = 0.0
+        for table, n in ((b.table[0], 40), (b.prefix_table[0], 70)):
+            x = torch.zeros(n, 1, 64, device="cuda")
+            x[..., 5] = -float("inf")
+            b.p.put(table, x, 0)
+        b.run()
+        assert not b.out[:, 1].any() and torch.isneginf(b.lse[:, 1]).all()
+        assert torch.isnan(b.out[:, [0, 2, 3]]).all() and torch.isnan(b.lse[:, [0, 2, 3]]).all()       # 0 x infinity
