@@ -699,8 +699,9 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
         most = fmaxf(most, top);
-        const float u = exp2_fast(top - most), f = ml.y != 0.0f ? exp2_fast(ml.x - most) : 0.0f;
-        float add = ml.y * f;
+        // -1: nothing seen.  A weight that underflows still multiplies: 0 x NaN is what such a value gives.
+        const float u = exp2_fast(top - most), f = ml.y != 0.0f ? exp2_fast(ml.x - most) : -1.0f;
+        float add = ml.y != 0.0f ? ml.y * f : 0.0f;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
         top = most;
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
             float x[NV];
 #pragma unroll
             for (int v = 0; v < NV; ++v) x[v] = o[v * 32];
-            if (fk == 0.0f) continue;
+            if (fk < 0.0f) continue;
 #pragma unroll
             for (int v = 0; v < NV; ++v) acc[v] += x[v] * fk;
         }

@@ -96,3 +96,24 @@ def test_scores_of_minus_infinity_alone(n_q):
         b.run()
         assert not b.out[:, 1].any() and torch.isneginf(b.lse[:, 1]).all()
         assert torch.isnan(b.out[:, [0, 2, 3]]).all() and torch.isnan(b.lse[:, [0, 2, 3]]).all()       # 0 x infinity
+
+
+@pytest.mark.parametrize("fmt,bad", [("same", float("nan")), ("same", -float("inf")), ("e4m3", float("nan"))])
+@pytest.mark.parametrize("requests,n_q,H,prefix", [(1, 1, 2, 9000), (8, 1, 2, 9000), (2, 40, 2, 3000), (300, 3, 8, 1000)])
+def test_values_of_no_weight(fmt, bad, requests, n_q, H, prefix):
+    """A value that is not finite reaches the queries that see it, even where its piece of the tokens weighs nothing in the end."""
+    with Batch(kvb, [60] * requests, [n_q] * requests, [(0, requests, prefix)], H, 4, 128, fmt, T=16) as b:
+        b.q.fill_(1.0)
+        b.p.put(b.prefix_table[0], torch.full((prefix, H, 128), -20.0 if fmt == "same" else -300.0, device="cuda"), 0)     # scores under -200
+        for i in range(requests):
+            b.p.put(b.table[i], torch.zeros(60, H, 128, device="cuda"), 0)
+        b.run()
+        b.check()
+        clean, lse = b.out.clone(), b.lse.clone()
+        size = b.p.B // 128
+        word = torch.tensor([bad], device="cuda").to(torch.float8_e4m3fn if fmt == "e4m3" else b.p.dt).view(torch.uint8)
+        b.p.view(1)[b.prefix_table[0, 700 // 16].long(), 700 % 16, 1, 5 * size:6 * size] = word
+        b.run()
+        assert not torch.isfinite(b.out[:, 4:8, 5]).any() and torch.equal(b.lse, lse)
+        b.out[:, 4:8, 5] = clean[:, 4:8, 5]
+        assert torch.equal(b.out, clean)
