@@ -84,11 +84,12 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
     // More rows than one tile of mma.sync: tcgen05.
     const bool tc_own = !picked && own_rows > kRowsP;
     // Where a request fills a unit on its own, reading its prefix with it costs nothing and saves the joining.
-    p.joined = groups != 0 && tc_own && own_rows >= 256;
-    const bool tc_prefix = groups != 0 && max_prefix != 0 && prefix_rows > kRowsP && !p.joined;
+    // Groups without any prefix are the same: nothing is in front, and no kernel is kept for them.
+    p.joined = groups != 0 && (max_prefix == 0 || (tc_own && own_rows >= 256));
+    const bool tc_prefix = groups != 0 && prefix_rows > kRowsP && !p.joined;
     const uint64_t span = picked ? list_tokens(budget, T, max_len) : p.joined ? (uint64_t)max_prefix + max_len : std::max(max_len, groups != 0 ? max_prefix : 0);
     uint64_t at = 0;
-    const uint64_t segs = (uint64_t)groups + requests;
+    const uint64_t segs = (p.joined ? 0 : (uint64_t)groups) + requests;
     PageEngine &t = p.tc, &e = p.rows;
     if (own_rows <= (uint32_t)kRowsP) {
         // A block a request (or query with a list) and head, the prefix in front of its own tokens, and nothing to join:
@@ -104,7 +105,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
         const double rounds = (double)(all / 64 + 1), places = (double)sms * per_sm;
         const double by_units = std::ceil((double)units / places) * (rounds + 4.0);
         const double own_rounds = picked ? rounds : (double)(max_len / 64 + 1);
-        const double cut = ((double)units * (own_rounds + 4.0) + (groups != 0 && !tc_prefix ? (double)groups * kv_heads * (max_prefix / 64.0 + 4.0) : 0.0)) / places;
+        const double cut = ((double)units * (own_rounds + 4.0) + (groups != 0 && max_prefix != 0 && !tc_prefix ? (double)groups * kv_heads * (max_prefix / 64.0 + 4.0) : 0.0)) / places;
         if (units < (1ull << 31) && by_units <= std::max(cut, 5.0) + 4.0 + (tc_prefix ? 8.0 : 0.0)) {
             e = w;
             e.on = 1;

@@ -117,3 +117,30 @@ def test_values_of_no_weight(fmt, bad, requests, n_q, H, prefix):
         assert not torch.isfinite(b.out[:, 4:8, 5]).any() and torch.equal(b.lse, lse)
         b.out[:, 4:8, 5] = clean[:, 4:8, 5]
         assert torch.equal(b.out, clean)
+
+
+@pytest.mark.parametrize("n_q", [1, 3, 10, 70])
+@pytest.mark.parametrize("own", [60, 6000])
+def test_groups_without_prefixes(n_q, own):
+    """No launch is made for them, and groups or lengths that are wrong are still said to be."""
+    with Batch(kvb, [own, 30, own], [n_q] * 3, [(0, 2, 0), (2, 3, 0)], 2, 4, 64, T=16) as b:
+        a, alone = b.shared_args(), b.shared_args(groups=0)
+        n = kvb.kv_launch_count()
+        kvb.kv_attend_shared(b.p.pool, alone)
+        n, m = kvb.kv_launch_count(), kvb.kv_launch_count() - n
+        torch.cuda.synchronize()
+        want = b.out.clone()
+        b.out.fill_(7.0)
+        kvb.kv_attend_shared(b.p.pool, a)
+        assert kvb.kv_launch_count() - n == m and a.workspace_bytes == alone.workspace_bytes
+        torch.cuda.synchronize()
+        b.check()
+        no_status(b)
+        assert torch.equal(b.out, want)
+        for wrong in (b.prefix_lens, b.group_start):
+            wrong[1] = 5
+            kvb.kv_attend_shared(b.p.pool, a)
+            torch.cuda.synchronize()
+            assert int(b.status) == kvb.KV_STATUS_BAD_LENGTH and torch.equal(b.out, want)
+            wrong[1] = 0 if wrong is b.prefix_lens else 2
+            b.status.zero_()

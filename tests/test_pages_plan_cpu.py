@@ -186,3 +186,12 @@ def test_what_fits_is_counted_in_31_bits(host, seed):
     if p.fits():
         for tiles, _ in (p.work([0, q], [length], [0, 1], [prefix]) if length * q < 2 ** 45 else ()):
             assert tiles < 2 ** 32 if groups else tiles < 2 ** 31
+
+
+@pytest.mark.parametrize("max_q", [1, 4, 10, 100])
+@pytest.mark.parametrize("max_len", [50, 20000])
+def test_groups_without_prefixes(host, max_q, max_len):
+    """They are planned as no groups are: no kernel is launched, given SMs or room for prefixes of no tokens."""
+    kw = dict(requests=6, tokens=6 * max_q, max_q=max_q, max_len=max_len)
+    p, alone = Plan(host, groups=2, max_group=3 * max_q, **kw), Plan(host, **kw)
+    assert p.joined and (p.rows, p.tc, p.bytes) == (alone.rows, alone.tc, alone.bytes)
