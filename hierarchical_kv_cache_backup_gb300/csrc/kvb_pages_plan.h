@@ -148,7 +148,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
             // tokens behind 8,192: 96 us one after the other on all SMs, side by side 72 / 66 / 68 with
             // 20 / 26 / 32 D.
             const double tc_cost = (double)t_units * ((t.prefix ? max_prefix : max_len) / 64 + 1) * (fp8 ? 24.0 : 26.0) * D;
-            const double rows_cost = (double)e_units * (max_len / 16 + 1) * 25.0 * D / (kWarps * per_sm);
+            const double rows_cost = (double)e_units * ((e.prefix ? max_prefix : max_len) / 16 + 1) * 25.0 * D / (kWarps * per_sm);
             const double part = (double)sms * tc_cost / (tc_cost + rows_cost);
             t.workers = (uint32_t)std::min<double>(sms - 1, std::max(1.0, std::floor(part + 0.5)));
             e_sms = (uint32_t)sms - t.workers;

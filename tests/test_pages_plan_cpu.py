@@ -195,3 +195,12 @@ def test_groups_without_prefixes(host, max_q, max_len):
     kw = dict(requests=6, tokens=6 * max_q, max_q=max_q, max_len=max_len)
     p, alone = Plan(host, groups=2, max_group=3 * max_q, **kw), Plan(host, **kw)
     assert p.joined and (p.rows, p.tc, p.bytes) == (alone.rows, alone.tc, alone.bytes)
+
+
+def test_the_sms_go_where_the_work_is(host):
+    """A few queries over a long prefix beside a chunk of another request, and the other way round."""
+    kw = dict(requests=5, tokens=54, max_q=50, groups=1, max_group=4)
+    far, near = Plan(host, max_len=100, max_prefix=100000, **kw), Plan(host, max_len=100000, max_prefix=100, **kw)
+    for p in (far, near):
+        assert p.rows["prefix"] and not p.rows["own"] and p.tc["own"] and not p.tc["prefix"]
+    assert far.tc["workers"] < 20 and near.tc["workers"] > 130
