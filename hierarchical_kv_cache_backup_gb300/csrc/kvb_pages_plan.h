@@ -83,9 +83,18 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
     const uint32_t own_rows = picked ? group : max_q * group;
     // More rows than one tile of mma.sync: tcgen05.
     const bool tc_own = !picked && own_rows > kRowsP;
-    // Where a request fills a unit on its own, reading its prefix with it costs nothing and saves the joining.
+    // Where requests fill units on their own, reading the prefix with them saves the joining: where the call has at
+    // most a third more units so than all its rows fill.  Units that a few single tokens take for themselves would
+    // each read the prefix again.  Behind 8,192 tokens (us, prefix in front / apart): four chunks of 500 237 / 286, with
+    // 8 single tokens beside them 288 / 301, 16 343 / 315, 32 451 / 343; a chunk of 512 beside 63 732 / 434; 8-bit
+    // pages and heads of 256, chunks of 500 with 4, 8 and 16 beside them 231 / 232, 245 / 239 and 277 / 251.
     // Groups without any prefix are the same: nothing is in front, and no kernel is kept for them.
-    p.joined = groups != 0 && (max_prefix == 0 || (tc_own && own_rows >= 256));
+    PageEngine alone{};
+    alone.own = 1;
+    alone.row_tile = pages_tc_rows(D, own_rows);
+    const uint64_t filled = ((uint64_t)tokens * group + alone.row_tile - 1) / alone.row_tile;
+    const uint64_t most = most_units(alone, requests, tokens, max_q, 0, 0, group, false, 1);
+    p.joined = groups != 0 && (max_prefix == 0 || (tc_own && own_rows >= 256 && 3 * most <= 4 * filled));
     const bool tc_prefix = groups != 0 && prefix_rows > kRowsP && !p.joined;
     const uint64_t span = picked ? list_tokens(budget, T, max_len) : p.joined ? (uint64_t)max_prefix + max_len : std::max(max_len, groups != 0 ? max_prefix : 0);
     uint64_t at = 0;

@@ -667,7 +667,8 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  * Group g is the requests group_start[g]..group_start[g + 1] - 1 (groups in
  * order, a request in one at most); in front of each one's own tokens stand the
  * prefix_lens[g] tokens of its pages prefix_pages[g x prefix_stride + t / T], which
- * are read once for all of the group's queries.  Query i of request r sees its
+ * are read once for all of the group's queries, or about once for 256 rows (a query token and a
+ * query head of a KV head; 128 for heads over 128 values) where there are more.  Query i of request r sees its
  * group's whole prefix and the own tokens t <= lens[r] - n + i.  groups = 0: no
  * prefixes, attention of each request by itself.  q_heads is a multiple of the
  * pool's H; query head j reads KV head j / (q_heads / H).  With x_t = scale q . k_t

@@ -204,3 +204,15 @@ def test_the_sms_go_where_the_work_is(host):
     for p in (far, near):
         assert p.rows["prefix"] and not p.rows["own"] and p.tc["own"] and not p.tc["prefix"]
     assert far.tc["workers"] < 20 and near.tc["workers"] > 130
+
+
+@pytest.mark.parametrize("n_q,joined", [([500] * 4, 1), ([64] * 16, 1), ([500, 300, 200, 120], 1), ([512], 1), ([500] * 4 + [1], 1), ([2048] + [1] * 8, 1),
+                                        ([1] * 63 + [512], 0), ([500] * 4 + [1] * 16, 0), ([2048] + [1] * 30, 0), ([1] * 7 + [64], 0), ([63] * 16, 0)])
+def test_a_prefix_is_read_again_only_by_requests_that_fill_units(host, n_q, joined):
+    """A chunk among single tokens leaves the prefix to be read for all of them together."""
+    p = Plan(host, requests=len(n_q), tokens=sum(n_q), max_q=max(n_q), max_len=1000, groups=1, max_group=sum(n_q), max_prefix=8192)
+    assert p.joined == joined and p.tc["prefix"] == 1 - joined
+    q_start = np.cumsum([0] + n_q)
+    _, (tiles, units) = p.work(q_start, [1000] * len(n_q), [0, len(n_q)], [8192])
+    filled = -(-sum(n_q) * 4 // 256)
+    assert tiles <= 8 * ((4 * filled // 3 if joined else filled) * (8192 // 64 + 10) + (filled + len(n_q)) * (1000 // 64 + 1 + 10))
