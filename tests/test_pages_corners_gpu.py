@@ -156,3 +156,26 @@ def test_a_chunk_among_single_tokens(fmt, dtype, dim, H, n_q):
             b.run()
             b.check()
             no_status(b)
+
+
+@pytest.mark.parametrize("own", [500, 20000])
+@pytest.mark.parametrize("selected", [False, True])
+def test_requests_that_share_query_tokens_are_left_out(selected, own):
+    """More units than valid ranges can make: not an output is written, by calls that are cut, of whole units, and on
+    tcgen05.  (The ranges between, out of order, are said to be wrong as well: fewer requests of the same ranges are answered.)"""
+    n, q = 40, 400
+    with Batch(kvb, [own] * n, [q // n] * n, (), 1, 4, 64, T=64) as b:
+        b.q_start.copy_(torch.tensor([q * (i % 2) for i in range(n + 1)], dtype=torch.int32))
+        picks = torch.arange(200 if own > 500 else 1, dtype=torch.int32, device="cuda").expand(q, 1, -1).contiguous()
+        for requests in (2, n):
+            kw = dict(max_q=q, requests=requests)
+            a = b.selected_args(picks, **kw) if selected else b.shared_args(**kw)
+            assert (a.workspace_bytes == 0) == (selected and own == 500)         # whole units
+            b.out.fill_(7.0)
+            b.lse.fill_(7.0)
+            b.status.zero_()
+            (kvb.kv_attend_selected if selected else kvb.kv_attend_shared)(b.p.pool, a)
+            torch.cuda.synchronize()
+            assert int(b.status) == kvb.KV_STATUS_BAD_LENGTH
+            left = (b.out == 7.0).all() and (b.lse == 7.0).all()
+            assert left if requests == n else not (b.lse == 7.0).any()
