@@ -678,11 +678,13 @@ KVB_API kv_status kv_attend_workspace(kv_pool pool, const kv_attend_args *args, 
  * Scores, softmax statistics and sums are float32.  Rounded to fewer bits are:
  *   a weight      exp(x_t - largest) to two parts of 8 bits (bf16 pages), to two
  *                 parts of 11 bits (fp16 outputs), to 11 bits (fp8 pages, bf16
- *                 outputs); in calls with many rows (more than 16 query rows, tokens x
- *                 q_heads / H, in a prefix or request) to one part of these.
+ *                 outputs); of prefixes with more than 16 query rows (max_group x
+ *                 q_heads / H) and of own tokens with more (max_q x q_heads / H) to one
+ *                 part of these.
  *                 Those under 2^-21 of the query's largest lose bits (not on bf16 pages)
  *   a query       of bf16 against fp8 pages: values under 2^-22 of the vector's
  *                 largest
+ * q . k and x_t log2(e) are below 2^126 in magnitude; of more, outputs may be anything.
  * A score of -infinity has weight 0 (an infinite key against a query value of the other
  * sign, say); one of +infinity or NaN makes all of the query's outputs and its lse NaN.  A
  * value that is not finite makes its dim of the outputs of the queries that see it not

@@ -11,6 +11,7 @@ if not torch.cuda.is_available():
 
 from hierarchical_kv_cache_backup_gb300 import kvb  # noqa: E402
 from pages_ref import Batch, softmax_rows, tolerance  # noqa: E402
+from vec_ref import half_step  # noqa: E402
 from test_pages_gpu import bound, check_picks, check_selected, no_status, run_selected, select, some_picks  # noqa: E402
 
 
@@ -179,3 +180,50 @@ def test_requests_that_share_query_tokens_are_left_out(selected, own):
             assert int(b.status) == kvb.KV_STATUS_BAD_LENGTH
             left = (b.out == 7.0).all() and (b.lse == 7.0).all()
             assert left if requests == n else not (b.lse == 7.0).any()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("same", "bf16"), ("same", "fp16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("requests,n_q,prefix", [(1, 1, 30), (1, 1, 9000), (12, 1, 3000), (2, 40, 3000), (200, 3, 900)])
+def test_two_runs_give_the_same_bits(fmt, dtype, requests, n_q, prefix):
+    """Nothing that is written depends on which block ends first."""
+    with Batch(kvb, [70 + 7 * (i % 9) for i in range(requests)], [n_q] * requests, [(0, requests, prefix)], 4, 4, 128, fmt, dtype) as b:
+        b.run()
+        out, lse = b.out.clone(), b.lse.clone()
+        for _ in range(3):
+            b.out.fill_(7.0)
+            b.run()
+            assert torch.equal(b.out, out) and torch.equal(b.lse, lse)
+        picks = some_picks(b, 3)
+        run_selected(b, picks)
+        out = b.out.clone()
+        run_selected(b, picks)
+        assert torch.equal(b.out, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [22, 25, 28, 40, 125])
+@pytest.mark.parametrize("n_q,own,prefix", [(1, 60, 50), (1, 60, 9000), (40, 60, 900), (90, 100, 300)])
+def test_scores_as_far_as_float32_goes(dtype, sign, power, n_q, own, prefix):
+    """Scores of up to 2^125: the largest alone has weight, and its value comes out."""
+    with Batch(kvb, [own], [n_q], [(0, 1, prefix)], 1, 4, 64, "same", dtype) as b:
+        q = b.q.double().cpu().numpy()
+        k, v = (np.concatenate((b.p.held(b.prefix_table[0], prefix, c), b.p.held(b.table[0], own, c)))[:, 0] for c in (0, 1))
+        x = np.einsum("ijd,kd->ijk", q, k) * sign
+        b.scale = float(sign * 2.0 ** (power - 1) / np.abs(x).max())                 # times log2(e): under 2^power
+        b.run()
+        out, lse = b.out.double().cpu().numpy(), b.lse.double().cpu().numpy()
+        for i in range(n_q):
+            x[i, :, prefix + own - n_q + i + 1:] = -np.inf
+        two = np.sort(x, -1)[..., -2:]
+        # far past the scores' roundings, and 2^32 or more apart in weight (n 2^-32 is under half a step of fp16)
+        gap = (two[..., 1] - two[..., 0]) * abs(b.scale)
+        clear = (gap > 2.0 ** -16 * np.abs(two[..., 1]) * abs(b.scale)) & (gap > 23)
+        assert clear.mean() > 0.9
+        top = x.argmax(-1)
+        # With few rows weights have 2^-17 and the sums 2^-20: rounded, the value itself.  With many rows the largest
+        # weight is 2^r, r the rounding of its score, and goes in rounded once (half a step) over a sum that is not;
+        # then the output's own half a step, of a value up to that much larger.
+        h = half_step(b.p.dt) if b.many() else 0.0
+        assert (np.abs(out[clear] - v[top[clear]]) <= (2 * h + h * h) * np.abs(v[top[clear]])).all()
+        assert np.allclose(lse, two[..., 1] * abs(b.scale), rtol=2.0 ** -18, atol=0)
