@@ -138,9 +138,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_pages_plan_kernel(const __gri
 // private ring of cp.async stages (no barrier in the loop); query rows are the 16 rows of
 // mma.sync m16n8k16, cached tokens the 8 columns of the first product and the 16 k of the
 // second, so that weights go from one to the other in registers.  tcgen05 would leave 112 or more of
-// its 128 rows empty here.  Bound: the latency of one warp's chain (a tile of 16 tokens of 128 values takes
-// 2,700 cycles: load 500, scores 700, softmax 200, weights and sums 850, the rest waits) with the 12 warps that
-// 168 registers leave an SM; 64 requests of up to 1,000 tokens of their own behind 8,192 common ones, with
+// its 128 rows empty here.  Bound: the latency of one warp's chain (of a tile of 16 tokens of 128 values
+// 3,450 cycles with stamps of the clock in it: wait 150, scores 730, maximum 200, weights and sums 940, asking for the
+// next tile 1,400) with the 12 warps that 168 registers leave an SM; 64 requests of up to 1,000 tokens of their own behind 8,192 common ones, with
 // the kernel on tcgen05 beside it: 67 us, floor 34.6 by bytes.
 template <int D, bool kF8, bool kHalf>
 __global__ void __launch_bounds__(kWarps * 32, blocks_wanted(D))
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(128) kv_pages_join_kernel(const __grid_constan
 // The same for calls with many rows, 8 lanes a row: a warp takes join_heads rows of a token, four at once, and
 // works out once where their pieces are; sums are asked for together with the maxima that weigh them.  A
 // token's rows lie in at most two row tiles of a segment (kManyGroup heads of a group), or have a list of pages.
-// Bound: latency of the reads.  Four chunks of 500 tokens of 32 heads of 128 behind 8,192: the call takes 233 us, 259 with the
+// Bound: latency of the reads.  Four chunks of 500 tokens of 32 heads of 128 behind 8,192: the call took 233 us, 259 with the
 // kernel above, 252 where that takes its rows in turn.
 
 // What comes before row tile rt of a segment, by a warp.

@@ -138,7 +138,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
         t.kv_shift = kTcShift;
         t.slot_rows = std::min(t.row_tile, most);
         t.team = 1;
-        t.unit_cost = 10;                        // 27,000 cycles
+        t.unit_cost = 10;                        // 14,000 cycles, 27,000 of a block's first piece
         t.workers = (uint32_t)sms;
         t_units = most_units(t, requests, tokens, max_q, groups, max_group, group, picked, kv_heads);
     }
@@ -169,7 +169,7 @@ inline PagePlan plan_pages(uint32_t requests, uint32_t tokens, uint32_t max_q, u
         // more than 16 pieces of a unit, a block's four warps share one, so that fewer pieces have to be joined.
         e.team = 4 * e_units >= blocks ? 1 : kWarps;
         e.kv_shift = e.team == 1 ? 4 : 6;
-        e.unit_cost = e.team == 1 ? 5 : 4;       // 12,000 cycles
+        e.unit_cost = e.team == 1 ? 5 : 4;       // 10,000 cycles
         e.workers = blocks * (kWarps / e.team);
         place(&e, &at, e_units, segs, span, D);
         p.wide_join = e.workers > 6 * e_units;

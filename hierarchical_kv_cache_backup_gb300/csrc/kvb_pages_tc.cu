@@ -16,8 +16,8 @@
 // O0, O1 (D columns each; one of up to 256).
 //
 // Bound: a product of 64 keys reads 6 KB of shared memory for 32 cycles of arithmetic, 1,280 cycles a tile for
-// both row tiles; measured are 1,560 to 1,800, and 27,000 for the beginning and end of a piece.  Four chunks of
-// 500 tokens behind 8,192: 233 us with the join, floor 147.4 by operations (1.21 PFLOP/s).
+// both row tiles; measured are 1,640, and 14,000 for the beginning and end of a piece (27,000 of a block's first
+// piece, cold).  Four chunks of 500 tokens behind 8,192: 238 us with the join, floor 147.4 by operations (1.17 PFLOP/s).
 //
 // What is rounded: a weight, to the operands' type (bf16: 2^-9 of itself at most, 2^-8 in
 // steps of the type; fp16: 2^-11), once; a bf16 query against fp8 pages below 2^-22 of

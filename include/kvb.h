@@ -615,6 +615,7 @@ KVB_API kv_status kv_fetch(kv_pool pool, const kv_fetch_args *args, void *stream
  *   a value       to fp16, 2^-11 of itself; two parts (2^-19) for fp16 outputs
  *   a key         to fp16 for bf16 outputs without lse, two parts otherwise: with
  *                 lse the last bits of bf16 outputs may be other ones
+ * (x_t log2(e) is below 2^22 in magnitude there; of more, outputs may be NaN)
  * in requests (and KV heads) whose steps are less than 2^16 apart in every group;
  * others take the way of few rows, about four times as long.  What a query does
  * not see, or gives no weight, takes no bits from it: steps may differ by any
