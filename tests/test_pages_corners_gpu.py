@@ -227,3 +227,55 @@ def test_scores_as_far_as_float32_goes(dtype, sign, power, n_q, own, prefix):
         h = half_step(b.p.dt) if b.many() else 0.0
         assert (np.abs(out[clear] - v[top[clear]]) <= (2 * h + h * h) * np.abs(v[top[clear]])).all()
         assert np.allclose(lse, two[..., 1] * abs(b.scale), rtol=2.0 ** -18, atol=0)
+
+
+@pytest.mark.parametrize("dim,H", [(64, 4), (128, 2)])
+def test_two_calls_at_once(dim, H):
+    """Calls on two streams, each with a workspace of its own, among them two that want all tensor memory of an SM."""
+    made = [([70, 200, 90], [40, 60, 3], [(0, 3, 700)]), ([300] * 3, [100] * 3, ()), ([90] * 30, [1] * 30, [(0, 30, 2000)]), ([4000], [1], ())]
+    batches = [Batch(kvb, lens, n_q, groups, H, 4, dim, seed=20 + i) for i, (lens, n_q, groups) in enumerate(made)]
+    picks = [some_picks(b, 4) for b in batches]
+    args = [(b.shared_args(), b.selected_args(p)) for b, p in zip(batches, picks)]
+    want = []
+    for b, (shared, selected) in zip(batches, args):
+        kvb.kv_attend_selected(b.p.pool, selected)
+        torch.cuda.synchronize()
+        one = b.out.clone()
+        kvb.kv_attend_shared(b.p.pool, shared)
+        torch.cuda.synchronize()
+        b.check()
+        want.append((b.out.clone(), one))
+    streams = [torch.cuda.Stream() for _ in batches]
+    for k in range(40):
+        for b, (shared, selected), stream in zip(batches, args, streams):
+            if k % 3:
+                kvb.kv_attend_shared(b.p.pool, shared, stream.cuda_stream)
+            else:
+                kvb.kv_attend_selected(b.p.pool, selected, stream.cuda_stream)
+        if k % 3 != 1:
+            torch.cuda.synchronize()
+            for b, (shared, selected) in zip(batches, want):
+                assert torch.equal(b.out, shared if k % 3 else selected)
+    for b in batches:
+        no_status(b)
+        b.__exit__()
+
+
+def test_rows_of_tables_apart():
+    """Page tables inside wider ones, whose other entries are anything."""
+    with Batch(kvb, [90, 33, 150], [1, 20, 3], [(0, 2, 100), (2, 3, 60)], 2, 4, 64, T=16) as b:
+        b.run()
+        want, picks = b.out.clone(), some_picks(b, 4)
+        run_selected(b, picks)
+        chosen = b.out.clone()
+        own, pre = (torch.full((3, 40), 2 ** 31 - 1, dtype=torch.int32, device="cuda"), torch.full((2, 30), -9, dtype=torch.int32, device="cuda"))
+        own[:, 7:7 + b.per], pre[:, 3:3 + b.pre] = b.table, b.prefix_table
+        at = dict(pages=own.data_ptr() + 28, pages_stride=40)
+        b.run(**at, prefix_pages=pre.data_ptr() + 12, prefix_stride=30)
+        assert torch.equal(b.out, want)
+        run_selected(b, picks, **at)
+        assert torch.equal(b.out, chosen)
+        bounds = bound(b)
+        assert torch.equal(bound(b, pages=at["pages"], pages_stride=40), bounds)
+        assert torch.equal(select(b, bounds, 3), select(b, bounds, 3, keep_first=0))
+        no_status(b)
